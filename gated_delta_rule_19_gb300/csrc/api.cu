@@ -233,7 +233,9 @@ const char* const kKernelNames[gdn::KID_COUNT] = {
     "prep_fwd_tc", "scan_fwd_tc", "prep_fwd_tc(bwd)", "scan_fwd_tc(state-only)",
     "scan_bwd_tc", "grad_qk_tc", "grad_wy_tc", "decode_kernel", "prologue_fwd_kernel",
     "prologue_bwd_kernel", "varlen_offsets", "varlen_gather", "varlen_scatter", "scan_fwd_tc(split pass 1)",
-    "scan_bwd_tc(split pass 1)", "scan_fwd_tc(transitions)", "split_combine", "count_nonfinite_kernel"};
+    "scan_bwd_tc(split pass 1)", "scan_fwd_tc(transitions)", "split_combine", "count_nonfinite_kernel",
+    "la_states", "la_scan", "la_decode_kernel", "qk_norm_rope_fwd_kernel", "qk_norm_rope_bwd_kernel",
+    "gated_norm_fwd_kernel", "gated_norm_bwd_kernel", "weight_sum_kernel"};
 
 template <typename F>
 cudaError_t timed(int kid, cudaStream_t st, F&& launch) {
@@ -1605,6 +1607,463 @@ gdn_status gdn_profiler_summary(int id, int* launches, double* total_ms) {
 void gdn_profiler_release(void) {
     for (cudaEvent_t e : g_prof.ev) cudaEventDestroy(e);
     g_prof = Profiler();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The linear-attention layer: linear attention with a decay per head, the norm and
+// rotation of its q and k rows, the gated norm of its output.
+
+namespace {
+
+size_t elem_size(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
+gdn::InType elem_type(int32_t dtype) { return dtype == GDN_BF16 ? gdn::InType::BF16 : gdn::InType::F32; }
+
+gdn_status check_layer_sizes(int64_t B, int64_t T, int64_t H, int32_t dtype) {
+    if (B < 0 || T < 0 || H < 0)
+        return fail(GDN_ERR_INVALID_ARG, "negative size (B=%lld T=%lld H=%lld)", (long long)B, (long long)T,
+                    (long long)H);
+    if (dtype != GDN_F32 && dtype != GDN_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_F32 or GDN_BF16", (int)dtype);
+    if (B > 65535 || H > 65535 || B * H > (int64_t)1 << 24)
+        return fail(GDN_ERR_UNSUPPORTED, "B=%lld H=%lld: each must be <= 65535, B*H <= 2^24", (long long)B,
+                    (long long)H);
+    if (T > (int64_t)1 << 30) return fail(GDN_ERR_UNSUPPORTED, "T=%lld exceeds 2^30", (long long)T);
+    return GDN_OK;
+}
+
+// The token stride of [B, T, H, D] rows (0: dense): checked and filled in.
+gdn_status row_stride(const char* name, int64_t stride, int64_t H, int64_t D, int32_t dtype, int64_t* out) {
+    *out = stride ? stride : H * D;
+    if (*out < H * D || *out > (int64_t)1 << 40)
+        return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld does not cover a token's %lld elements", name,
+                    (long long)stride, (long long)(H * D));
+    if (*out * elem_size(dtype) % 16 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld is not a multiple of 16 bytes", name, (long long)stride);
+    return GDN_OK;
+}
+
+// Bytes from a strided tensor's first to its last element.
+size_t row_span(int64_t tokens, int64_t stride, int64_t width, int32_t dtype) {
+    return tokens ? (size_t)((tokens - 1) * stride + width) * elem_size(dtype) : 0;
+}
+
+gdn_status check_word_ptr(const void* p, const char* name) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "%s is NULL", name);
+    if ((uintptr_t)p % 4 != 0) return fail(GDN_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+    return GDN_OK;
+}
+
+gdn_status check_spans(const Span* ins, int nin, unsigned optional_ins, const Span* outs, int nout,
+                       unsigned optional_outs, const void* same_out, const void* same_in) {
+    gdn_status st;
+    for (int i = 0; i < nin; ++i)
+        if ((st = check_ptr(ins[i], !(optional_ins >> i & 1))) != GDN_OK) return st;
+    for (int i = 0; i < nout; ++i)
+        if ((st = check_ptr(outs[i], !(optional_outs >> i & 1))) != GDN_OK) return st;
+    const bool same = same_out && same_out == same_in;  // the very same buffer, not a part of it
+    return check_overlaps(ins, nin, outs, nout, same ? same_out : nullptr, same ? same_in : nullptr);
+}
+
+struct LaCall {
+    gdn::LaDims d{};
+    int64_t sq, sk, sv;
+    int64_t tokens;
+    size_t state;  // floats of all streams' states
+    size_t sums;   // floats of all segments' sums
+};
+
+gdn_status la_problem(const gdn_la_problem* p, LaCall* c) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    gdn_status st = check_layer_sizes(p->B, p->T, p->H, p->dtype);
+    if (st != GDN_OK) return st;
+    if (!supported_dim(p->K) || !supported_dim(p->V))
+        return fail(GDN_ERR_UNSUPPORTED, "K=%lld V=%lld: each must be 16, 32, 64 or 128", (long long)p->K,
+                    (long long)p->V);
+    if ((st = row_stride("q", p->q_stride, p->H, p->K, p->dtype, &c->sq)) != GDN_OK) return st;
+    if ((st = row_stride("k", p->k_stride, p->H, p->K, p->dtype, &c->sk)) != GDN_OK) return st;
+    if ((st = row_stride("v", p->v_stride, p->H, p->V, p->dtype, &c->sv)) != GDN_OK) return st;
+    c->d.B = (int)p->B;
+    c->d.T = (int)p->T;
+    c->d.H = (int)p->H;
+    c->d.K = (int)p->K;
+    c->d.V = (int)p->V;
+    c->d.wait_ns = g_wait_limit_ns;
+    gdn::la_segments(&c->d);
+    c->tokens = p->B * p->T;
+    c->state = (size_t)c->d.NS() * p->V * p->K;
+    c->sums = c->state * (c->d.nseg - 1);
+    return GDN_OK;
+}
+
+struct LaBufs {
+    int* err;
+    float* copy;  // of a state that is read and overwritten by the same call
+    float* fwd;   // the segments' sums in the order of time
+    float* rev;   // and against it
+};
+size_t carve_la(const LaCall& c, Carver& cv, LaBufs* b, bool bwd) {
+    b->err = cv.take<int>(64);
+    b->copy = bwd || c.d.nseg > 1 ? cv.take<float>(c.state) : nullptr;
+    b->fwd = cv.take<float>(c.sums);
+    b->rev = bwd ? cv.take<float>(c.sums) : nullptr;
+    return cv.off;
+}
+size_t la_workspace(const gdn_la_problem* p, bool bwd) {
+    LaCall c;
+    if (la_problem(p, &c) != GDN_OK) return 0;
+    Carver cv{nullptr};
+    LaBufs b;
+    return carve_la(c, cv, &b, bwd);
+}
+
+// The state of an empty sequence, or a NULL one's zeros.
+gdn_status copy_state(float* dst, const float* src, size_t n, cudaStream_t cs) {
+    if (!dst || dst == src) return GDN_OK;
+    cudaError_t e = src ? cudaMemcpyAsync(dst, src, n * sizeof(float), cudaMemcpyDeviceToDevice, cs)
+                        : cudaMemsetAsync(dst, 0, n * sizeof(float), cs);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "state copy");
+}
+
+gdn_status run_la(const LaCall& c, gdn::InType ty, const gdn::LaRoles& sums, const gdn::LaRoles& outs,
+                  cudaStream_t cs) {
+    cudaError_t e = cudaSuccess;
+    if (c.d.nseg > 1 && sums.n)
+        e = timed(gdn::KID_LA_STATES, cs, [&] { return gdn::launch_la_states(c.d, ty, sums, cs); });
+    if (e == cudaSuccess) e = timed(gdn::KID_LA_SCAN, cs, [&] { return gdn::launch_la_scan(c.d, ty, outs, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear-attention kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_la_fwd_workspace_bytes(const gdn_la_problem* p) { return la_workspace(p, false); }
+size_t gdn_la_bwd_workspace_bytes(const gdn_la_problem* p) { return la_workspace(p, true); }
+size_t gdn_la_saved_bytes(const gdn_la_problem* p) {
+    LaCall c;
+    return la_problem(p, &c) == GDN_OK ? c.sums * sizeof(float) : 0;
+}
+
+gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, const void* v, const float* log_decay,
+                      const float* initial_state, void* o, float* final_state, void* saved, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    LaCall c;
+    gdn_status st = la_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const size_t need = la_workspace(p, false), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
+    const int64_t wk = p->H * p->K, wv = p->H * p->V;
+    const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},
+                        {k, row_span(c.tokens, c.sk, wk, p->dtype), "k"},
+                        {v, row_span(c.tokens, c.sv, wv, p->dtype), "v"},
+                        {initial_state, nstate, "initial_state"}};
+    const Span outs[] = {{o, (size_t)c.tokens * wv * es, "o"},
+                         {final_state, nstate, "final_state"},
+                         {saved, c.sums * sizeof(float), "saved"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 1u << 1 | 1u << 2, final_state, initial_state)) != GDN_OK)
+        return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    if (c.d.NS() == 0) return GDN_OK;
+    if ((st = check_word_ptr(log_decay, "log_decay")) != GDN_OK) return st;
+    cudaStream_t cs = (cudaStream_t)stream;
+    if (c.d.T == 0) return copy_state(final_state, initial_state, c.state, cs);
+    Carver cv{(char*)workspace};
+    LaBufs b;
+    carve_la(c, cv, &b, false);
+    c.d.err = b.err;
+    c.d.log_decay = log_decay;
+    float* sums = saved ? (float*)saved : b.fwd;
+    // with several segments the CTA that writes the final state is not the only one
+    // that reads the initial state
+    if (final_state && final_state == initial_state && c.d.nseg > 1) {
+        if ((st = copy_state(b.copy, initial_state, c.state, cs)) != GDN_OK) return st;
+        initial_state = b.copy;
+    }
+    gdn::LaRoles r;
+    r.n = 1;
+    r.r[0] = {q, k, v, o, c.sq, c.sk, c.sv, c.d.K, c.d.V, initial_state, final_state, sums, c.d.K, 1, 0};
+    return run_la(c, elem_type(p->dtype), r, r, cs);
+}
+
+gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, const void* v, const float* log_decay,
+                      const float* initial_state, const void* saved, const void* d_o, const float* d_final_state,
+                      void* dq, void* dk, void* dv, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    g_err[0] = 0;
+    LaCall c;
+    gdn_status st = la_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const size_t need = la_workspace(p, true), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
+    const int64_t wk = p->H * p->K, wv = p->H * p->V;
+    const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},
+                        {k, row_span(c.tokens, c.sk, wk, p->dtype), "k"},
+                        {v, row_span(c.tokens, c.sv, wv, p->dtype), "v"},
+                        {d_o, (size_t)c.tokens * wv * es, "d_o"},
+                        {initial_state, nstate, "initial_state"},
+                        {saved, c.sums * sizeof(float), "saved"},
+                        {d_final_state, nstate, "d_final_state"}};
+    const Span outs[] = {{dq, (size_t)c.tokens * wk * es, "dq"},
+                         {dk, (size_t)c.tokens * wk * es, "dk"},
+                         {dv, (size_t)c.tokens * wv * es, "dv"},
+                         {d_initial_state, nstate, "d_initial_state"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 7, 1u << 4 | 1u << 5 | 1u << 6, outs, 5, 1u << 3, d_initial_state, d_final_state)) !=
+        GDN_OK)
+        return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    if (c.d.NS() == 0) return GDN_OK;
+    if ((st = check_word_ptr(log_decay, "log_decay")) != GDN_OK) return st;
+    cudaStream_t cs = (cudaStream_t)stream;
+    if (c.d.T == 0) return copy_state(d_initial_state, d_final_state, c.state, cs);
+    Carver cv{(char*)workspace};
+    LaBufs b;
+    carve_la(c, cv, &b, true);
+    c.d.err = b.err;
+    c.d.log_decay = log_decay;
+    if (d_initial_state && d_initial_state == d_final_state) {  // two scans read what one of them overwrites
+        if ((st = copy_state(b.copy, d_final_state, c.state, cs)) != GDN_OK) return st;
+        d_final_state = b.copy;
+    }
+    const int K = c.d.K, V = c.d.V;
+    const int64_t so = wv;  // d_o is dense
+    const float* fwd = saved ? (const float*)saved : b.fwd;
+    gdn::LaRoles sums, outs3;
+    sums.r[sums.n++] = {nullptr, q, d_o, nullptr, 0, c.sq, so, K, V, nullptr, nullptr, b.rev, K, 1, 1};
+    if (!saved) sums.r[sums.n++] = {nullptr, k, v, nullptr, 0, c.sk, c.sv, K, V, nullptr, nullptr, b.fwd, K, 1, 0};
+    outs3.n = 3;
+    outs3.r[0] = {d_o, v, k, dq, so, c.sv, c.sk, V, K, initial_state, nullptr, fwd, 1, K, 0};
+    outs3.r[1] = {v, d_o, q, dk, c.sv, so, c.sq, V, K, d_final_state, nullptr, b.rev, 1, K, 1};
+    outs3.r[2] = {k, q, d_o, dv, c.sk, c.sq, so, K, V, d_final_state, d_initial_state, b.rev, K, 1, 1};
+    return run_la(c, elem_type(p->dtype), sums, outs3, cs);
+}
+
+gdn_status gdn_la_decode(const gdn_la_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, float* state, void* o, void* stream) {
+    g_err[0] = 0;
+    LaCall c;
+    gdn_status st = la_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const int64_t wk = p->H * p->K, wv = p->H * p->V;
+    const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},
+                        {k, row_span(c.tokens, c.sk, wk, p->dtype), "k"},
+                        {v, row_span(c.tokens, c.sv, wv, p->dtype), "v"}};
+    const Span outs[] = {{o, (size_t)c.tokens * wv * elem_size(p->dtype), "o"},
+                         {state, c.state * sizeof(float), "state"}};
+    if ((st = check_spans(ins, 3, 0, outs, 2, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (c.d.NS() == 0 || c.d.T == 0) return GDN_OK;
+    if ((st = check_word_ptr(log_decay, "log_decay")) != GDN_OK) return st;
+    cudaStream_t cs = (cudaStream_t)stream;
+    c.d.log_decay = log_decay;
+    cudaError_t e = timed(gdn::KID_LA_DECODE, cs, [&] {
+        return gdn::launch_la_decode(c.d, elem_type(p->dtype), q, k, v, c.sq, c.sk, c.sv, state, o, cs);
+    });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear-attention decode kernel");
+}
+
+}  // extern "C"
+
+namespace {
+
+gdn_status check_row_width(const char* name, int64_t D, int32_t dtype, int64_t least) {
+    const int64_t step = 32 / (int64_t)elem_size(dtype);
+    if (D < least || D > 256 || D % step != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "%s=%lld: must be a multiple of %lld, %lld to 256", name, (long long)D,
+                    (long long)step, (long long)least);
+    return GDN_OK;
+}
+
+gdn_status rope_problem(const gdn_rope_problem* p, gdn::RopeCall* c) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    gdn_status st = check_layer_sizes(p->B, p->T, p->Hq, p->dtype);
+    if (st != GDN_OK || (st = check_layer_sizes(p->B, p->T, p->Hk, p->dtype)) != GDN_OK) return st;
+    if ((st = check_row_width("D", p->D, p->dtype, 1)) != GDN_OK) return st;
+    if ((st = check_row_width("R", p->R, p->dtype, 0)) != GDN_OK) return st;
+    if (p->R > p->D) return fail(GDN_ERR_INVALID_ARG, "R=%lld exceeds D=%lld", (long long)p->R, (long long)p->D);
+    if (p->table_rows < 0 || p->table_rows > (int64_t)1 << 30)
+        return fail(GDN_ERR_INVALID_ARG, "table_rows=%lld", (long long)p->table_rows);
+    if (!(p->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps=%g is negative", (double)p->eps);
+    if (p->B * p->T > ((int64_t)1 << 33) / (p->Hq + p->Hk > 0 ? p->Hq + p->Hk : 1))
+        return fail(GDN_ERR_UNSUPPORTED, "B*T*(Hq+Hk) exceeds 2^33");
+    if ((st = row_stride("q", p->q_stride, p->Hq, p->D, p->dtype, &c->q_stride)) != GDN_OK) return st;
+    if ((st = row_stride("k", p->k_stride, p->Hk, p->D, p->dtype, &c->k_stride)) != GDN_OK) return st;
+    c->tokens = p->B * p->T;
+    c->T = (int)p->T;
+    c->Hq = (int)p->Hq;
+    c->Hk = (int)p->Hk;
+    c->D = (int)p->D;
+    c->R = (int)p->R;
+    c->rows = (int)p->table_rows;
+    c->eps = p->eps;
+    c->interleaved = p->interleaved != 0;
+    c->blocks = gdn::rows_bwd_blocks(c->tokens * (p->Hq > p->Hk ? p->Hq : p->Hk));
+    return GDN_OK;
+}
+
+gdn_status rope_tables(const gdn_rope_problem* p, const float* cos, const float* sin, const int32_t* positions) {
+    gdn_status st;
+    if (p->R == 0) return GDN_OK;
+    const Span tables[] = {{cos, 1, "cos"}, {sin, 1, "sin"}};
+    for (const Span& s : tables)
+        if ((st = check_ptr(s, true)) != GDN_OK) return st;
+    if (positions && (uintptr_t)positions % 4 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+    if (!positions && p->table_rows < p->T)
+        return fail(GDN_ERR_INVALID_ARG, "table_rows=%lld: without positions at least T=%lld rows are needed",
+                    (long long)p->table_rows, (long long)p->T);
+    return GDN_OK;
+}
+
+gdn_status gated_problem(const gdn_gated_norm_problem* p, gdn::GatedCall* c) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    gdn_status st = check_layer_sizes(p->B, p->T, p->H, p->dtype);
+    if (st != GDN_OK || (st = check_row_width("D", p->D, p->dtype, 1)) != GDN_OK) return st;
+    if (!(p->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps=%g is negative", (double)p->eps);
+    if (p->B * p->T > ((int64_t)1 << 33) / (p->H > 0 ? p->H : 1))
+        return fail(GDN_ERR_UNSUPPORTED, "B*T*H exceeds 2^33");
+    if ((st = row_stride("x", p->x_stride, p->H, p->D, p->dtype, &c->x_stride)) != GDN_OK) return st;
+    if ((st = row_stride("gate", p->gate_stride, p->H, p->D, p->dtype, &c->z_stride)) != GDN_OK) return st;
+    c->rows = p->B * p->T * p->H;
+    c->H = (int)p->H;
+    c->D = (int)p->D;
+    c->eps = p->eps;
+    c->blocks = gdn::rows_bwd_blocks(c->rows);
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                void* q_out, void* k_out, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    gdn_status st = rope_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
+    const int64_t wq = p->Hq * p->D, wk = p->Hk * p->D;
+    const Span ins[] = {{q, row_span(c.tokens, c.q_stride, wq, p->dtype), "q"},
+                        {k, row_span(c.tokens, c.k_stride, wk, p->dtype), "k"},
+                        {q_weight, p->D * es, "q_weight"},
+                        {k_weight, p->D * es, "k_weight"},
+                        {cos, table, "cos"},
+                        {sin, table, "sin"}};
+    const Span outs[] = {{q_out, (size_t)c.tokens * wq * es, "q_out"}, {k_out, (size_t)c.tokens * wk * es, "k_out"}};
+    if ((st = check_spans(ins, 6, 1u << 4 | 1u << 5, outs, 2, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (c.tokens == 0 || p->Hq + p->Hk == 0) return GDN_OK;
+    if ((st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
+    c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
+    c.qo = q_out, c.ko = k_out;
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = timed(gdn::KID_NORM_ROPE_FWD, cs,
+                          [&] { return gdn::launch_qk_norm_rope(c, elem_type(p->dtype), false, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "q, k norm and rotation kernel");
+}
+
+size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p) {
+    gdn::RopeCall c{};
+    return rope_problem(p, &c) == GDN_OK ? (size_t)2 * c.blocks * c.D * sizeof(float) : 0;
+}
+
+gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                const void* dq_out, const void* dk_out, void* dq, void* dk, void* dq_weight,
+                                void* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    gdn_status st = rope_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
+    const size_t need = gdn_qk_norm_rope_bwd_workspace_bytes(p);
+    const int64_t wq = p->Hq * p->D, wk = p->Hk * p->D;
+    const size_t nq = (size_t)c.tokens * wq * es, nk = (size_t)c.tokens * wk * es;
+    const Span ins[] = {{q, row_span(c.tokens, c.q_stride, wq, p->dtype), "q"},
+                        {k, row_span(c.tokens, c.k_stride, wk, p->dtype), "k"},
+                        {q_weight, p->D * es, "q_weight"},
+                        {k_weight, p->D * es, "k_weight"},
+                        {dq_out, nq, "dq_out"},
+                        {dk_out, nk, "dk_out"},
+                        {cos, table, "cos"},
+                        {sin, table, "sin"}};
+    const Span outs[] = {{dq, nq, "dq"},
+                         {dk, nk, "dk"},
+                         {dq_weight, p->D * es, "dq_weight"},
+                         {dk_weight, p->D * es, "dk_weight"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 8, 1u << 6 | 1u << 7, outs, 5, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    if (c.tokens && (st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
+    c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
+    c.qo = dq, c.ko = dk, c.dqo = dq_out, c.dko = dk_out, c.part = (float*)workspace;
+    cudaStream_t cs = (cudaStream_t)stream;
+    const gdn::InType ty = elem_type(p->dtype);
+    cudaError_t e = timed(gdn::KID_NORM_ROPE_BWD, cs, [&] { return gdn::launch_qk_norm_rope(c, ty, true, cs); });
+    if (e == cudaSuccess)
+        e = timed(gdn::KID_WEIGHT_SUM, cs,
+                  [&] { return gdn::launch_weight_sum(2, c.blocks, c.D, ty, c.part, dq_weight, dk_weight, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "q, k norm and rotation gradient kernel");
+}
+
+gdn_status gdn_gated_norm_fwd(const gdn_gated_norm_problem* p, const void* x, const void* gate, const void* weight,
+                              void* y, void* stream) {
+    g_err[0] = 0;
+    gdn::GatedCall c{};
+    gdn_status st = gated_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const int64_t tokens = p->B * p->T, w = p->H * p->D;
+    const size_t es = elem_size(p->dtype);
+    const Span ins[] = {{x, row_span(tokens, c.x_stride, w, p->dtype), "x"},
+                        {gate, row_span(tokens, c.z_stride, w, p->dtype), "gate"},
+                        {weight, p->D * es, "weight"}};
+    const Span outs[] = {{y, (size_t)tokens * w * es, "y"}};
+    if ((st = check_spans(ins, 3, 0, outs, 1, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (c.rows == 0) return GDN_OK;
+    c.x = x, c.z = gate, c.w = weight, c.y = y;
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = timed(gdn::KID_GATED_NORM_FWD, cs,
+                          [&] { return gdn::launch_gated_norm(c, elem_type(p->dtype), false, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gated norm kernel");
+}
+
+size_t gdn_gated_norm_bwd_workspace_bytes(const gdn_gated_norm_problem* p) {
+    gdn::GatedCall c{};
+    return gated_problem(p, &c) == GDN_OK ? (size_t)c.blocks * c.D * sizeof(float) : 0;
+}
+
+gdn_status gdn_gated_norm_bwd(const gdn_gated_norm_problem* p, const void* x, const void* gate, const void* weight,
+                              const void* dy, void* dx, void* dgate, void* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    gdn::GatedCall c{};
+    gdn_status st = gated_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const int64_t tokens = p->B * p->T, w = p->H * p->D;
+    const size_t es = elem_size(p->dtype), n = (size_t)tokens * w * es;
+    const size_t need = gdn_gated_norm_bwd_workspace_bytes(p);
+    const Span ins[] = {{x, row_span(tokens, c.x_stride, w, p->dtype), "x"},
+                        {gate, row_span(tokens, c.z_stride, w, p->dtype), "gate"},
+                        {weight, p->D * es, "weight"},
+                        {dy, n, "dy"}};
+    const Span outs[] = {
+        {dx, n, "dx"}, {dgate, n, "dgate"}, {dweight, p->D * es, "dweight"}, {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 4, 0, outs, 4, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    c.x = x, c.z = gate, c.w = weight, c.dy = dy, c.dx = dx, c.dz = dgate, c.part = (float*)workspace;
+    cudaStream_t cs = (cudaStream_t)stream;
+    const gdn::InType ty = elem_type(p->dtype);
+    cudaError_t e = timed(gdn::KID_GATED_NORM_BWD, cs, [&] { return gdn::launch_gated_norm(c, ty, true, cs); });
+    if (e == cudaSuccess)
+        e = timed(gdn::KID_WEIGHT_SUM, cs,
+                  [&] { return gdn::launch_weight_sum(1, c.blocks, c.D, ty, c.part, dweight, dweight, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gated norm gradient kernel");
 }
 
 }  // extern "C"

@@ -142,6 +142,14 @@ enum KernelId {
     KID_SPLIT_TRANS,     // scan_fwd_tc, transitions only (backward with saved)
     KID_SPLIT_COMBINE,   // pieces_kernel, combine_fwd_kernel, combine_bwd_kernel
     KID_COUNT_NONFINITE, // count_nonfinite_kernel
+    KID_LA_STATES,       // la_chunk_kernel, the segments' sums
+    KID_LA_SCAN,         // la_chunk_kernel, outputs or gradients
+    KID_LA_DECODE,       // la_decode_kernel
+    KID_NORM_ROPE_FWD,   // qk_norm_rope_fwd_kernel
+    KID_NORM_ROPE_BWD,   // qk_norm_rope_bwd_kernel
+    KID_GATED_NORM_FWD,  // gated_norm_fwd_kernel
+    KID_GATED_NORM_BWD,  // gated_norm_bwd_kernel
+    KID_WEIGHT_SUM,      // weight_sum_kernel
     KID_COUNT
 };
 
@@ -300,5 +308,81 @@ cudaError_t launch_grad_wy_tc(const Dims& d, const void* k, const void* v, const
                               const void* beta, const TcBufs& tb, const TcBwdBufs& bb,
                               void* dk, void* dv, void* dalpha, void* dbeta, cudaStream_t st,
                               const RawPrologue* raw = nullptr);
+
+// ---- the linear-attention layer (la.cu, norm_rope.cu, gated_norm.cu) ----
+
+// Linear attention with a decay per head: a sequence is cut into nseg segments of L
+// tokens (a multiple of 128), the last one shorter.
+struct LaDims {
+    int B, T, H, K, V;
+    int L, nseg;
+    const float* log_decay;  // [H]
+    uint32_t wait_ns = 0;    // as Dims::wait_ns
+    int* err = nullptr;      // the workspace's error word
+    __host__ __device__ int64_t NS() const { return (int64_t)B * H; }
+};
+constexpr int kLaMaxSeg = 16;
+void la_segments(LaDims* d);
+
+// One scan (see la.cu): out_r = sum of gamma^|r-s| (a_r . b_s) c_s, a and b of Db columns,
+// c and out of Dc; token strides in elements (out is dense).  M's element (c, b) is at
+// c * m_sc + b * m_sb of the caller's [V, K] matrices: m0 enters (or NULL), mT receives
+// the state that leaves (or NULL), R [stream][nseg - 1][V][K] holds the segments' sums.
+struct LaRole {
+    const void *a, *b, *c;
+    void* out;
+    int64_t sa, sb, sc;
+    int Db, Dc;
+    const float* m0;
+    float* mT;
+    const float* R;
+    int m_sc, m_sb, rev;
+};
+struct LaRoles {
+    LaRole r[3];
+    int n = 0;
+};
+// The segments' sums into R (nseg > 1), then the outputs.
+cudaError_t launch_la_states(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
+cudaError_t launch_la_scan(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
+cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const void* k, const void* v, int64_t sq,
+                             int64_t sk, int64_t sv, float* state, void* o, cudaStream_t st);
+
+// RMS norm and rotation of q and k rows; backward: qo, ko are dq, dk, dqo, dko the
+// gradients of the outputs, part [2][blocks][D] the blocks' sums for the weights.
+struct RopeCall {
+    int64_t tokens;
+    int T, Hq, Hk, D, R, rows;
+    float eps;
+    bool interleaved;
+    int64_t q_stride, k_stride;
+    const void *q, *k, *wq, *wk;
+    const float *cos, *sin;
+    const int32_t* pos;
+    void *qo, *ko;
+    const void *dqo = nullptr, *dko = nullptr;
+    float* part = nullptr;
+    int blocks = 0;
+};
+cudaError_t launch_qk_norm_rope(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
+
+// RMS norm of x times silu(z); backward: part [blocks][D].
+struct GatedCall {
+    int64_t rows;
+    int H, D;
+    int64_t x_stride, z_stride;
+    float eps;
+    const void *x, *z, *w;
+    void* y = nullptr;
+    const void* dy = nullptr;
+    void *dx = nullptr, *dz = nullptr;
+    float* part = nullptr;
+    int blocks = 0;
+};
+cudaError_t launch_gated_norm(const GatedCall& c, InType ty, bool bwd, cudaStream_t st);
+// dw of `sides` weights from their blocks' sums, in a fixed order.
+cudaError_t launch_weight_sum(int sides, int blocks, int D, InType ty, const float* part, void* dw0, void* dw1,
+                              cudaStream_t st);
+int rows_bwd_blocks(int64_t rows);
 
 }  // namespace gdn

@@ -33,6 +33,25 @@ class gdn_problem(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class gdn_la_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("V", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class gdn_rope_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("R", ctypes.c_int64),
+                ("table_rows", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class gdn_gated_norm_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
 
@@ -88,6 +107,18 @@ def load_library():
     lib.gdn_varlen_fwd.restype = ctypes.c_int
     lib.gdn_varlen_bwd.argtypes = [P, ctypes.c_int64] + [_vp] * 17 + [ctypes.c_size_t, _vp]
     lib.gdn_varlen_bwd.restype = ctypes.c_int
+    PL, PR, PG = (ctypes.POINTER(t) for t in (gdn_la_problem, gdn_rope_problem, gdn_gated_norm_problem))
+    for fn, prob, ptrs, sized in (("gdn_la_fwd", PL, 9, True), ("gdn_la_bwd", PL, 13, True),
+                                  ("gdn_la_decode", PL, 6, False), ("gdn_qk_norm_rope_fwd", PR, 9, False),
+                                  ("gdn_qk_norm_rope_bwd", PR, 14, True), ("gdn_gated_norm_fwd", PG, 4, False),
+                                  ("gdn_gated_norm_bwd", PG, 8, True)):
+        getattr(lib, fn).argtypes = [prob] + [_vp] * ptrs + ([ctypes.c_size_t] if sized else []) + [_vp]
+        getattr(lib, fn).restype = ctypes.c_int
+    for fn, prob in (("gdn_la_fwd_workspace_bytes", PL), ("gdn_la_saved_bytes", PL),
+                     ("gdn_la_bwd_workspace_bytes", PL), ("gdn_qk_norm_rope_bwd_workspace_bytes", PR),
+                     ("gdn_gated_norm_bwd_workspace_bytes", PG)):
+        getattr(lib, fn).argtypes = [prob]
+        getattr(lib, fn).restype = ctypes.c_size_t
     lib.gdn_count_nonfinite.argtypes = [_vp, ctypes.c_int64, ctypes.c_int, _vp, _vp]
     lib.gdn_count_nonfinite.restype = ctypes.c_int
     lib.gdn_set_sequence_split.argtypes = [ctypes.c_int]
@@ -116,7 +147,10 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_last_error", "gdn_fwd_works
             "gdn_prologue_fwd", "gdn_prologue_bwd", "gdn_varlen_fwd_workspace_bytes",
             "gdn_varlen_bwd_workspace_bytes", "gdn_varlen_saved_bytes", "gdn_varlen_fwd", "gdn_varlen_bwd",
             "gdn_set_sequence_split", "gdn_get_sequence_split", "gdn_count_nonfinite",
-            "gdn_test_set_wait_limit")
+            "gdn_test_set_wait_limit", "gdn_la_fwd_workspace_bytes", "gdn_la_saved_bytes",
+            "gdn_la_bwd_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode",
+            "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_bytes", "gdn_qk_norm_rope_bwd",
+            "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd")
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -843,3 +877,279 @@ def gdn_fwd_noalloc(q, k, v, alpha, beta, initial_state, o, final_state=None, *,
                                  _stream_handle(dev, stream))
     _check(st)
     return o, final_state
+
+
+# ---- The linear-attention layer: linear attention with a decay per head, the norm and
+# rotation of its q and k rows, the gated norm of its output (see include/gdn.h).
+
+def _rows(t, name, shape, dtype, device):
+    """Checks a [B, T, H, D] tensor whose tokens lie a fixed stride apart (a slice of a
+    fused projection, say) and returns that stride in elements (0: dense)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.is_contiguous() or t.numel() == 0:
+        return 0
+    B, T, H, D = shape
+    sb, st, sh, sd = t.stride()
+    token = st if T > 1 else sb
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 1 and sb != T * st) or (B * T > 1 and token < H * D):
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be dense in its last two dimensions and its tokens a fixed "
+                                            f"stride apart, got strides {t.stride()}")
+    return token if B * T > 1 else 0
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise GdnError(GDN_ERR_INVALID_ARG, "inputs must be CUDA tensors")
+    if t.dim() != 4:
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected four dimensions")
+    return t.device
+
+
+def _la_inputs(q, k, v, log_decay):
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    _cuda_device(v, "v")
+    B, T, H, K = q.shape
+    V = v.shape[-1]
+    p = gdn_la_problem(B, T, H, K, V, _rows(q, "q", q.shape, dt, dev), _rows(k, "k", q.shape, dt, dev),
+                       _rows(v, "v", (B, T, H, V), dt, dev), _dtype_code(dt))
+    if log_decay is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "log_decay is required")
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    return p, dev, dt, (B, T, H, V), (B, H, V, K)
+
+
+def _scratch(nbytes, dev):
+    return torch.empty(nbytes if nbytes else 1, dtype=torch.uint8, device=dev)
+
+
+def _bytes_of(t, name, dev):
+    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a contiguous tensor on {dev}")
+    return t.numel() * t.element_size()
+
+
+def _out_state(t, name, shape, dev):
+    if t is True:
+        return torch.empty(shape, dtype=torch.float32, device=dev)
+    if t is False or t is None:
+        return None
+    _need(t, name, shape, torch.float32, dev)
+    return t
+
+
+def gdn_la_fwd(q, k, v, log_decay, initial_state=None, *, o=None, final_state=True, saved=False, workspace=None,
+               stream=None):
+    """Linear attention with a fixed decay per head (``gdn_la_fwd``), per (b, h):
+
+        S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T,   o_t = S_t q_t.
+
+    q, k [B,T,H,K]; v [B,T,H,V] (float32 or bfloat16; tokens may lie a fixed stride
+    apart, as in a slice of a fused projection); log_decay float32 [H], <= 0;
+    initial_state float32 [B,H,V,K] or None.  ``final_state``: True (allocate), a
+    float32 tensor to fill (may be initial_state itself), or False/None.  ``saved``:
+    True to allocate and return what :func:`gdn_la_bwd` then need not compute again,
+    or a buffer of at least gdn_la_saved_bytes() bytes.
+    Returns ``(o, final_state or None, saved or None)``."""
+    lib = load_library()
+    p, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
+    _need(initial_state, "initial_state", sshape, torch.float32, dev)
+    if o is None:
+        o = torch.empty(oshape, dtype=dt, device=dev)
+    else:
+        _need(o, "o", oshape, dt, dev)
+    final_state = _out_state(final_state, "final_state", sshape, dev)
+    ref = ctypes.byref(p)
+    if saved is True:
+        saved = _scratch(lib.gdn_la_saved_bytes(ref), dev)
+    elif saved is False:
+        saved = None
+    elif saved is not None and _bytes_of(saved, "saved", dev) < lib.gdn_la_saved_bytes(ref):
+        raise GdnError(GDN_ERR_INVALID_ARG, "saved buffer is smaller than gdn_la_saved_bytes()")
+    if workspace is None:
+        workspace = _scratch(lib.gdn_la_fwd_workspace_bytes(ref), dev)
+    _check(lib.gdn_la_fwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(o),
+                          _ptr(final_state), _ptr(saved), _ptr(workspace), _bytes_of(workspace, "workspace", dev),
+                          _stream_handle(dev, stream)))
+    return o, final_state, saved
+
+
+def gdn_la_bwd(q, k, v, log_decay, initial_state, d_o, d_final_state=None, *, saved=None, grads=None,
+               d_initial_state=True, workspace=None, stream=None):
+    """Gradients of ``sum(d_o * o) + sum(d_final_state * final_state)`` of
+    :func:`gdn_la_fwd` (``gdn_la_bwd``); ``saved`` is what the forward returned for
+    the same inputs, or None.  Returns ``(dq, dk, dv, d_initial_state or None)``."""
+    lib = load_library()
+    p, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
+    _need(initial_state, "initial_state", sshape, torch.float32, dev)
+    if d_o is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "d_o is required")
+    _need(d_o, "d_o", oshape, dt, dev)
+    _need(d_final_state, "d_final_state", sshape, torch.float32, dev)
+    if grads is None:
+        dq, dk = (torch.empty(q.shape, dtype=dt, device=dev) for _ in range(2))
+        dv = torch.empty(oshape, dtype=dt, device=dev)
+    else:
+        dq, dk, dv = grads
+        for t, n, s in ((dq, "dq", q.shape), (dk, "dk", q.shape), (dv, "dv", oshape)):
+            _need(t, n, s, dt, dev)
+    d_initial_state = _out_state(d_initial_state, "d_initial_state", sshape, dev)
+    ref = ctypes.byref(p)
+    if saved is not None and _bytes_of(saved, "saved", dev) < lib.gdn_la_saved_bytes(ref):
+        raise GdnError(GDN_ERR_INVALID_ARG, "saved buffer is smaller than gdn_la_saved_bytes()")
+    if workspace is None:
+        workspace = _scratch(lib.gdn_la_bwd_workspace_bytes(ref), dev)
+    _check(lib.gdn_la_bwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(saved),
+                          _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(d_initial_state),
+                          _ptr(workspace), _bytes_of(workspace, "workspace", dev), _stream_handle(dev, stream)))
+    return dq, dk, dv, d_initial_state
+
+
+def gdn_la_decode(q, k, v, log_decay, state, *, o=None, stream=None):
+    """The same recurrence token by token (``gdn_la_decode``, usually T = 1):
+    ``state`` [B,H,V,K] float32 is updated in place.  Returns ``(o, state)``."""
+    lib = load_library()
+    p, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
+    if o is None:
+        o = torch.empty(oshape, dtype=dt, device=dev)
+    else:
+        _need(o, "o", oshape, dt, dev)
+    if state is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "state is required")
+    _need(state, "state", sshape, torch.float32, dev)
+    _check(lib.gdn_la_decode(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o),
+                             _stream_handle(dev, stream)))
+    return o, state
+
+
+def _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    _cuda_device(k, "k")
+    B, T, Hq, D = q.shape
+    kshape = (B, T, k.shape[2], D)
+    R = rows = 0
+    if cos is not None or sin is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise GdnError(GDN_ERR_INVALID_ARG, "cos must be a [table_rows, R/2] tensor")
+        rows, R = cos.shape[0], 2 * cos.shape[1]
+        if sin is None:
+            raise GdnError(GDN_ERR_INVALID_ARG, "sin is required with cos")
+        _need(cos, "cos", (rows, R // 2), torch.float32, dev)
+        _need(sin, "sin", (rows, R // 2), torch.float32, dev)
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            raise GdnError(GDN_ERR_INVALID_ARG, f"{n} is required")
+        _need(w, n, (D,), dt, dev)
+    _need(positions, "positions", (B, T), torch.int32, dev)
+    p = gdn_rope_problem(B, T, Hq, kshape[2], D, R, rows, _rows(q, "q", q.shape, dt, dev),
+                         _rows(k, "k", kshape, dt, dev), eps, 1 if interleaved else 0, _dtype_code(dt))
+    return p, dev, dt, kshape
+
+
+def gdn_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, *, eps: float = 1e-6,
+                         interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head's q and k row, then the rotation by its token's position,
+    in one pass (``gdn_qk_norm_rope_fwd``).  q [B,T,Hq,D], k [B,T,Hk,D] (tokens may lie
+    a fixed stride apart); q_weight, k_weight [D]; cos, sin float32 [table_rows, R/2]
+    (None: no rotation); positions int32 [B,T], rows of the tables (None: 0 .. T-1).
+    Pairs are (i, i + R/2), or (2i, 2i+1) with ``interleaved``.  A position outside the
+    tables makes its token's rows NaN.  Returns ``(q_out, k_out)``, dense."""
+    lib = load_library()
+    p, dev, dt, kshape = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    else:
+        _need(q_out, "q_out", q.shape, dt, dev)
+    if k_out is None:
+        k_out = torch.empty(kshape, dtype=dt, device=dev)
+    else:
+        _need(k_out, "k_out", kshape, dt, dev)
+    _check(lib.gdn_qk_norm_rope_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+                                    _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out),
+                                    _stream_handle(dev, stream)))
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, *, eps: float = 1e-6,
+                         interleaved: bool = False, grads=None, workspace=None, stream=None):
+    """Backward of :func:`gdn_qk_norm_rope_fwd` (``gdn_qk_norm_rope_bwd``) from the
+    gradients of its outputs.  Returns ``(dq, dk, dq_weight, dk_weight)``."""
+    lib = load_library()
+    p, dev, dt, kshape = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    shapes = (q.shape, kshape, q_weight.shape, k_weight.shape)
+    for t, n, s in ((dq_out, "dq_out", q.shape), (dk_out, "dk_out", kshape)):
+        if t is None:
+            raise GdnError(GDN_ERR_INVALID_ARG, f"{n} is required")
+        _need(t, n, s, dt, dev)
+    if grads is None:
+        grads = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes)
+    else:
+        for t, n, s in zip(grads, ("dq", "dk", "dq_weight", "dk_weight"), shapes):
+            _need(t, n, s, dt, dev)
+    dq, dk, dwq, dwk = grads
+    ref = ctypes.byref(p)
+    if workspace is None:
+        workspace = _scratch(lib.gdn_qk_norm_rope_bwd_workspace_bytes(ref), dev)
+    _check(lib.gdn_qk_norm_rope_bwd(ref, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                                    _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
+                                    _ptr(dwk), _ptr(workspace), _bytes_of(workspace, "workspace", dev),
+                                    _stream_handle(dev, stream)))
+    return dq, dk, dwq, dwk
+
+
+def _gated_inputs(x, gate, weight, eps):
+    dev, dt = _cuda_device(x, "x"), x.dtype
+    B, T, H, D = x.shape
+    if weight is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "weight is required")
+    _need(weight, "weight", (D,), dt, dev)
+    p = gdn_gated_norm_problem(B, T, H, D, _rows(x, "x", x.shape, dt, dev), _rows(gate, "gate", x.shape, dt, dev),
+                               eps, _dtype_code(dt))
+    return p, dev, dt
+
+
+def gdn_gated_norm_fwd(x, gate, weight, *, eps: float = 1e-6, y=None, stream=None):
+    """``y = x weight silu(gate) / sqrt(mean(x^2) + eps)`` for every row of x, gate
+    [B,T,H,D] (tokens may lie a fixed stride apart), weight [D]
+    (``gdn_gated_norm_fwd``).  Returns ``y``, dense."""
+    lib = load_library()
+    p, dev, dt = _gated_inputs(x, gate, weight, eps)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _need(y, "y", x.shape, dt, dev)
+    _check(lib.gdn_gated_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(y),
+                                  _stream_handle(dev, stream)))
+    return y
+
+
+def gdn_gated_norm_bwd(x, gate, weight, dy, *, eps: float = 1e-6, grads=None, workspace=None, stream=None):
+    """Backward of :func:`gdn_gated_norm_fwd` (``gdn_gated_norm_bwd``).
+    Returns ``(dx, dgate, dweight)``."""
+    lib = load_library()
+    p, dev, dt = _gated_inputs(x, gate, weight, eps)
+    if dy is None:
+        raise GdnError(GDN_ERR_INVALID_ARG, "dy is required")
+    _need(dy, "dy", x.shape, dt, dev)
+    shapes = (x.shape, x.shape, weight.shape)
+    if grads is None:
+        grads = tuple(torch.empty(s, dtype=dt, device=dev) for s in shapes)
+    else:
+        for t, n, s in zip(grads, ("dx", "dgate", "dweight"), shapes):
+            _need(t, n, s, dt, dev)
+    dx, dgate, dw = grads
+    ref = ctypes.byref(p)
+    if workspace is None:
+        workspace = _scratch(lib.gdn_gated_norm_bwd_workspace_bytes(ref), dev)
+    _check(lib.gdn_gated_norm_bwd(ref, _ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dgate), _ptr(dw),
+                                  _ptr(workspace), _bytes_of(workspace, "workspace", dev),
+                                  _stream_handle(dev, stream)))
+    return dx, dgate, dw

@@ -381,6 +381,132 @@ gdn_status gdn_decode(const gdn_problem* p, const void* q, const void* k, const 
                       const void* alpha, const void* beta, float* state, void* o, void* stream);
 
 /*
+ * ---- The linear-attention layer -------------------------------------------
+ *
+ * Linear attention with a fixed decay per head, the norm and rotation of its
+ * queries and keys, and the gated norm of its output.  Unlike the calls above,
+ * these take row tensors by a token stride: the elements from one token's rows to
+ * the next token's (0: dense), so that q, k, v and gates can be slices of a fused
+ * projection.  Batch rows lie T tokens apart, the [H, D] rows of a token are
+ * dense, and a stride covers them and is a multiple of 16 bytes.  Outputs are
+ * dense.  As above, errors are returned before any launch, nothing is allocated
+ * and the calls are asynchronous on `stream`.  B, H >= 0 and <= 65535, with
+ * B * H <= 2^24, T >= 0 and <= 2^30.
+ */
+
+typedef struct {
+    int64_t B, T, H, K, V;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t dtype;
+} gdn_la_problem;
+
+/*
+ * gdn_la_fwd -- per (b, h) stream, with gamma = exp(log_decay[h]):
+ *     S_t = gamma S_{t-1} + v_t k_t^T,    o_t = S_t q_t     (no scale on q)
+ *   q, k [B,T,H,K], v [B,T,H,V] in p->dtype, K and V of 16, 32, 64 or 128.
+ *   log_decay      float32 [H], <= 0 (0: nothing is forgotten; -inf: everything
+ *                  is), 4-byte aligned.  A constant of the layer: it gets no gradient.
+ *   initial_state  float32 [B,H,V,K] or NULL (= zeros).
+ *   o              [B,T,H,V]; bf16 results are rounded to nearest even.
+ *   final_state    float32 [B,H,V,K] or NULL; may be initial_state itself.
+ *   saved          NULL, or gdn_la_saved_bytes(p) bytes (which may be 0) that
+ *                  receive what gdn_la_bwd then need not compute again.
+ *   workspace      gdn_la_fwd_workspace_bytes(p) bytes.  Its first int is an error
+ *                  word: a bounded wait that gives up sets a bit there (nothing
+ *                  clears it; a caller that reads it clears it before the call).
+ * A value that is not finite reaches the outputs of its whole 128-token tile, and
+ * every later one.
+ */
+size_t gdn_la_fwd_workspace_bytes(const gdn_la_problem* p);
+size_t gdn_la_saved_bytes(const gdn_la_problem* p);
+gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, const void* v,
+                      const float* log_decay, const float* initial_state, void* o, float* final_state,
+                      void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_la_bwd -- gradients of sum(d_o * o) + sum(d_final_state * final_state):
+ *     dq_t = S_t^T d_o_t,  dS_t = gamma dS_{t+1} + d_o_t q_t^T,
+ *     dk_t = dS_t^T v_t,   dv_t = dS_t k_t,   d_initial_state = gamma dS_1.
+ *   saved            what gdn_la_fwd left for the same inputs, or NULL.
+ *   d_o              [B,T,H,V], dense.
+ *   d_final_state    float32 [B,H,V,K] or NULL (= zeros).
+ *   dq, dk, dv       dense, shapes of q, k, v.
+ *   d_initial_state  float32 [B,H,V,K] or NULL; may be d_final_state itself.
+ *   workspace        gdn_la_bwd_workspace_bytes(p) bytes, error word as above.
+ */
+size_t gdn_la_bwd_workspace_bytes(const gdn_la_problem* p);
+gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, const void* v,
+                      const float* log_decay, const float* initial_state, const void* saved, const void* d_o,
+                      const float* d_final_state, void* dq, void* dk, void* dv, float* d_initial_state,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_la_decode -- the same recurrence token by token on a state kept between
+ * calls (usually T = 1).  state float32 [B,H,V,K] is read and overwritten.  T calls
+ * of one token equal one call of T tokens bit for bit.
+ */
+gdn_status gdn_la_decode(const gdn_la_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, float* state, void* o, void* stream);
+
+/* Sizes of the q, k norm and rotation.  D: a multiple of 2 x 16 bytes (16 bf16 or 8
+ * float32 elements), 256 at most; R <= D, the rotated elements of a row, likewise a
+ * multiple (0: no rotation).  table_rows: rows of the cosine and sine tables. */
+typedef struct {
+    int64_t B, T, Hq, Hk, D, R, table_rows;
+    int64_t q_stride, k_stride;
+    float eps;
+    int32_t interleaved; /* pairs (2i, 2i+1) instead of (i, i + R/2) */
+    int32_t dtype;
+} gdn_rope_problem;
+
+/*
+ * gdn_qk_norm_rope_fwd -- every row x of q and k, with its weight w:
+ *     n = x w / sqrt(mean(x^2) + eps),
+ * then the first R elements rotated in pairs by the token's angles:
+ *     (n1, n2) -> (n1 c - n2 s, n2 c + n1 s).
+ *   q [B,T,Hq,D], k [B,T,Hk,D]; q_weight, k_weight [D]; all in p->dtype.
+ *   cos, sin   float32 [table_rows, R/2] (may be NULL when R = 0).
+ *   positions  int32 [B,T], the tokens' rows of the tables, or NULL: token t has
+ *              row t (then table_rows >= T).  A position outside the tables makes
+ *              its token's rows NaN.
+ *   q_out, k_out  dense, shapes of q and k.
+ */
+gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                void* q_out, void* k_out, void* stream);
+
+/*
+ * gdn_qk_norm_rope_bwd -- from the gradients dq_out, dk_out (dense) of its outputs,
+ * those of q, k (dense), q_weight and k_weight ([D], p->dtype; summed in float32
+ * in a fixed order, so equal calls give equal bits).
+ */
+size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p);
+gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                const void* dq_out, const void* dk_out, void* dq, void* dk, void* dq_weight,
+                                void* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sizes of the gated norm; D as in gdn_rope_problem. */
+typedef struct {
+    int64_t B, T, H, D;
+    int64_t x_stride, gate_stride;
+    float eps;
+    int32_t dtype;
+} gdn_gated_norm_problem;
+
+/*
+ * gdn_gated_norm_fwd -- y = x w silu(gate) / sqrt(mean(x^2) + eps) for every row of
+ * x, gate [B,T,H,D], weight [D]; y dense.
+ * gdn_gated_norm_bwd -- the gradients of x, gate (dense) and weight from dy (dense).
+ */
+gdn_status gdn_gated_norm_fwd(const gdn_gated_norm_problem* p, const void* x, const void* gate, const void* weight,
+                              void* y, void* stream);
+size_t gdn_gated_norm_bwd_workspace_bytes(const gdn_gated_norm_problem* p);
+gdn_status gdn_gated_norm_bwd(const gdn_gated_norm_problem* p, const void* x, const void* gate, const void* weight,
+                              const void* dy, void* dx, void* dgate, void* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * gdn_count_nonfinite -- adds to *count the number of elements of x[0 .. n-1]
  * that are NaN or +-inf: a device-side check of inputs or results (for example,
  * the outputs of gdn_fwd after suspect inputs).  It does not synchronise: the
