@@ -1674,7 +1674,8 @@ struct LaCall {
     size_t sums;   // floats of all segments' sums
 };
 
-gdn_status la_problem(const gdn_la_problem* p, LaCall* c) {
+// roles: the scans of the call (1 forward, 3 backward), which share the GPU.
+gdn_status la_problem(const gdn_la_problem* p, LaCall* c, int roles) {
     if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
     gdn_status st = check_layer_sizes(p->B, p->T, p->H, p->dtype);
     if (st != GDN_OK) return st;
@@ -1690,7 +1691,7 @@ gdn_status la_problem(const gdn_la_problem* p, LaCall* c) {
     c->d.K = (int)p->K;
     c->d.V = (int)p->V;
     c->d.wait_ns = g_wait_limit_ns;
-    gdn::la_segments(&c->d);
+    gdn::la_segments(&c->d, roles);
     c->tokens = p->B * p->T;
     c->state = (size_t)c->d.NS() * p->V * p->K;
     c->sums = c->state * (c->d.nseg - 1);
@@ -1712,7 +1713,7 @@ size_t carve_la(const LaCall& c, Carver& cv, LaBufs* b, bool bwd) {
 }
 size_t la_workspace(const gdn_la_problem* p, bool bwd) {
     LaCall c;
-    if (la_problem(p, &c) != GDN_OK) return 0;
+    if (la_problem(p, &c, bwd ? 3 : 1) != GDN_OK) return 0;
     Carver cv{nullptr};
     LaBufs b;
     return carve_la(c, cv, &b, bwd);
@@ -1741,9 +1742,11 @@ extern "C" {
 
 size_t gdn_la_fwd_workspace_bytes(const gdn_la_problem* p) { return la_workspace(p, false); }
 size_t gdn_la_bwd_workspace_bytes(const gdn_la_problem* p) { return la_workspace(p, true); }
+// The forward's sums serve the backward where both cut the sequences alike.
 size_t gdn_la_saved_bytes(const gdn_la_problem* p) {
-    LaCall c;
-    return la_problem(p, &c) == GDN_OK ? c.sums * sizeof(float) : 0;
+    LaCall c, b;
+    if (la_problem(p, &c, 1) != GDN_OK || la_problem(p, &b, 3) != GDN_OK) return 0;
+    return c.d.L == b.d.L ? c.sums * sizeof(float) : 0;
 }
 
 gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, const void* v, const float* log_decay,
@@ -1751,9 +1754,9 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
                       size_t workspace_bytes, void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c);
+    gdn_status st = la_problem(p, &c, 1);
     if (st != GDN_OK) return st;
-    const size_t need = la_workspace(p, false), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
+    const size_t nsaved = gdn_la_saved_bytes(p), need = la_workspace(p, false), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
     const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},
                         {k, row_span(c.tokens, c.sk, wk, p->dtype), "k"},
@@ -1761,7 +1764,7 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
                         {initial_state, nstate, "initial_state"}};
     const Span outs[] = {{o, (size_t)c.tokens * wv * es, "o"},
                          {final_state, nstate, "final_state"},
-                         {saved, c.sums * sizeof(float), "saved"},
+                         {saved, nsaved, "saved"},
                          {workspace, need, "workspace"}};
     if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 1u << 1 | 1u << 2, final_state, initial_state)) != GDN_OK)
         return st;
@@ -1776,7 +1779,7 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
     carve_la(c, cv, &b, false);
     c.d.err = b.err;
     c.d.log_decay = log_decay;
-    float* sums = saved ? (float*)saved : b.fwd;
+    float* sums = saved && nsaved ? (float*)saved : b.fwd;
     // with several segments the CTA that writes the final state is not the only one
     // that reads the initial state
     if (final_state && final_state == initial_state && c.d.nseg > 1) {
@@ -1795,16 +1798,16 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
                       void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c);
+    gdn_status st = la_problem(p, &c, 3);
     if (st != GDN_OK) return st;
-    const size_t need = la_workspace(p, true), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
+    const size_t nsaved = gdn_la_saved_bytes(p), need = la_workspace(p, true), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
     const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},
                         {k, row_span(c.tokens, c.sk, wk, p->dtype), "k"},
                         {v, row_span(c.tokens, c.sv, wv, p->dtype), "v"},
                         {d_o, (size_t)c.tokens * wv * es, "d_o"},
                         {initial_state, nstate, "initial_state"},
-                        {saved, c.sums * sizeof(float), "saved"},
+                        {saved, nsaved, "saved"},
                         {d_final_state, nstate, "d_final_state"}};
     const Span outs[] = {{dq, (size_t)c.tokens * wk * es, "dq"},
                          {dk, (size_t)c.tokens * wk * es, "dk"},
@@ -1820,6 +1823,7 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
     if ((st = check_word_ptr(log_decay, "log_decay")) != GDN_OK) return st;
     cudaStream_t cs = (cudaStream_t)stream;
     if (c.d.T == 0) return copy_state(d_initial_state, d_final_state, c.state, cs);
+    if (!nsaved) saved = nullptr;
     Carver cv{(char*)workspace};
     LaBufs b;
     carve_la(c, cv, &b, true);
@@ -1846,7 +1850,7 @@ gdn_status gdn_la_decode(const gdn_la_problem* p, const void* q, const void* k, 
                          const float* log_decay, float* state, void* o, void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c);
+    gdn_status st = la_problem(p, &c, 1);
     if (st != GDN_OK) return st;
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
     const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},

@@ -185,6 +185,8 @@ bool tmap_core8_rows(CUtensorMap* m, const void* ptr, int64_t rows, int cols, in
                      int box_groups);
 // [B, T, H, D] bf16 as 5D (8, T, D/8, H, B); box (8, 64, box_groups, 1, 1), no swizzle.
 bool tmap_core8_bthd(CUtensorMap* m, const void* ptr, int B, int T, int H, int D, int box_groups);
+// [B, T, H, D] bf16 with a token stride -> 4D TMA map (D, H, T, B), box 64 x 1 x 128 x 1.
+bool tmap_rows_bthd(CUtensorMap* m, const void* ptr, int B, int T, int H, int D, int64_t stride);
 bool tma_available();
 int sm_count();
 
@@ -322,7 +324,7 @@ struct LaDims {
     __host__ __device__ int64_t NS() const { return (int64_t)B * H; }
 };
 constexpr int kLaMaxSeg = 16;
-void la_segments(LaDims* d);
+void la_segments(LaDims* d, int roles);
 
 // One scan (see la.cu): out_r = sum of gamma^|r-s| (a_r . b_s) c_s, a and b of Db columns,
 // c and out of Dc; token strides in elements (out is dense).  M's element (c, b) is at
@@ -345,6 +347,9 @@ struct LaRoles {
 // The segments' sums into R (nseg > 1), then the outputs.
 cudaError_t launch_la_states(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
 cudaError_t launch_la_scan(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
+// The same on the tensor cores, bf16 only (la_tc.cu).
+cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st);
+cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st);
 cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const void* k, const void* v, int64_t sq,
                              int64_t sk, int64_t sv, float* state, void* o, cudaStream_t st);
 

@@ -342,12 +342,10 @@ cudaError_t launch_decode_t(const LaDims& d, const void* q, const void* k, const
 }  // namespace
 
 cudaError_t launch_la_states(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st) {
-    return ty == InType::BF16 ? launch_width<__nv_bfloat16, false>(d, roles, st)
-                              : launch_width<float, false>(d, roles, st);
+    return ty == InType::BF16 ? launch_la_states_tc(d, roles, st) : launch_width<float, false>(d, roles, st);
 }
 cudaError_t launch_la_scan(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st) {
-    return ty == InType::BF16 ? launch_width<__nv_bfloat16, true>(d, roles, st)
-                              : launch_width<float, true>(d, roles, st);
+    return ty == InType::BF16 ? launch_la_scan_tc(d, roles, st) : launch_width<float, true>(d, roles, st);
 }
 
 cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const void* k, const void* v, int64_t sq,
@@ -356,11 +354,12 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
                               : launch_decode_t<float>(d, q, k, v, sq, sk, sv, state, o, st);
 }
 
-// Segments: as many as it takes to give every SM a CTA, of whole 128-token tiles, and
-// at most kLaMaxSeg, since a segment reads every earlier segment's sum.
-void la_segments(LaDims* d) {
-    const int64_t tiles = (d->T + 127) / 128;
-    int64_t n = d->NS() > 0 ? sm_count() / d->NS() : 1;
+// Segments: as many as it takes to give every SM a CTA of the call's `roles` scans, of
+// whole 128-token tiles, and at most kLaMaxSeg, since a segment reads every earlier
+// segment's sum.
+void la_segments(LaDims* d, int roles) {
+    const int64_t tiles = (d->T + 127) / 128, streams = d->NS() * roles;
+    int64_t n = streams > 0 ? sm_count() / streams : 1;
     if (n > tiles) n = tiles;
     if (n > kLaMaxSeg) n = kLaMaxSeg;
     if (n < 1) n = 1;
