@@ -10,11 +10,18 @@
 // split into two bf16 terms (high part, and the rest), two products, so that the state
 // keeps 16 bits of every decayed value (2.7e-6 rms of the sum) instead of 8.
 //
-// One CTA per SM: two warpgroups carry the state (each half of the tokens of C' and
-// half of M's columns), one the rows of P and X (thread = token = tensor-memory lane),
-// one warp issues TMA, one the MMAs.  The hand-offs are mbarriers; every wait is
-// bounded.  Tensor memory: X, Y, U of 128 columns each and C' of 2 x 64.  Shared
-// memory: two stages of A, B, C and M; a tile's outputs are staged over its A.
+// One CTA per SM.  la_scan_kernel: two warpgroups carry the state (thread = row of M,
+// half of the columns each), two the rows of P and X (thread = token = tensor-memory
+// lane, half of the columns each), and each makes C' of 32 tokens; one warp issues TMA,
+// one the MMAs.  la_sums_kernel, the segments' sums, is the U part alone.  The hand-offs
+// are mbarriers; every wait is bounded.
+//
+// What bounds a tile is shared memory: an operand of an MMA is read at 128 bytes a
+// cycle, so A B^T and A M^T (both operands from there) take it whole while they run,
+// and the other products, the loads and stores and C' share the rest.  So P and C' are
+// operands in tensor memory, and most decay factors are multiplied up in registers
+// rather than read from tables.  Outputs stored from registers (32 bytes of a row per
+// lane) kept the load-store unit busy and cost more than staging them does.
 //
 // K or V below 128: TMA fills the missing columns with zeros, and the products run over
 // the columns that are there (N and K of each MMA follow Db and Dc).
@@ -31,8 +38,8 @@ using namespace tc;
 
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * 128 * 2;
-constexpr int kThreads = 448;  // 3 warpgroups, the TMA warp, the MMA warp
-constexpr int kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 576;  // 4 warpgroups, the TMA warp, the MMA warp
+constexpr int kTmaWarp = 16, kMmaWarp = 17;
 
 // Error bits of the workspace's first int.
 constexpr int kErrTma = 1, kErrMma = 2, kErrRows = 4, kErrState = 8, kErrDrain = 16;
@@ -41,362 +48,612 @@ struct LaMaps {
     CUtensorMap a[3], b[3], c[3], out[3];
 };
 
+// One CTA's part of the work: a role, a (stream, segment), and its tiles in the order
+// of the scan.
+struct Part {
+    const LaRole& ro;
+    int rl, nseg, slot, seg, rev, b, h, t_lo, t_hi, tiles;
+    int64_t stream;
+    float g;
+    __device__ Part(const LaDims& d, const LaRoles& roles, bool sums)
+        : ro(roles.r[blockIdx.y]), rl(blockIdx.y), nseg(sums ? d.nseg - 1 : d.nseg) {
+        stream = blockIdx.x / nseg;
+        slot = (int)(blockIdx.x % nseg);
+        rev = ro.rev;
+        seg = sums && rev ? slot + 1 : slot;  // the last segment's own sum feeds nobody
+        b = (int)(stream / d.H);
+        h = (int)(stream % d.H);
+        g = d.log_decay[h];
+        t_lo = seg * d.L;
+        t_hi = min(d.T, t_lo + d.L);
+        tiles = (t_hi - t_lo + kTile - 1) / kTile;
+    }
+    __device__ int t0(int it) const { return t_lo + (rev ? tiles - 1 - it : it) * kTile; }
+    __device__ int len(int it) const { return min(kTile, t_hi - t0(it)); }
+    __device__ int tail() const { return t_hi - t_lo - (tiles - 1) * kTile; }
+};
+
+__device__ __forceinline__ float power(float g, float e) { return e > 0.f ? expf(g * e) : 1.f; }
+
+// mbar_wait for a whole warp, one outcome for all its lanes.  The clock is read once in
+// 16 tries.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t ph, int* err, int code, uint32_t ns) {
+    bool ok = mbar_try_wait(bar, ph);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t limit = ns ? ns : kWaitLimitNs, t0 = globaltimer();
+        do {
+            for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, ph);
+        } while (!ok && globaltimer() - t0 <= limit);
+        if (!ok) atomicOr(err, code);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+    }
+    return true;
+}
+
+// The tile's rows c0 .. c0+15 of a product's operand as float pairs times a pair of
+// weights, rounded to bf16 (hi) and what that leaves, rounded (lo).
+__device__ __forceinline__ void split2(uint32_t v, uint64_t w, uint32_t& hi, uint32_t& lo) {
+    const uint64_t f = mul2(pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), w);
+    float x, y;
+    unpair(f, x, y);
+    hi = pack_bf16(x, y);
+    unpair(fma2(pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), pair(-1.f, -1.f), f), x, y);
+    lo = pack_bf16(x, y);
+}
+
+// C' of NT of the tile's tokens (from s0) for the 32 columns of C that are this warp's
+// lanes (from c0), as two bf16 terms in tensor memory columns s / 2 of t_hi, t_lo.
+// Blocks of 8 tokens x 8 columns are read transposed, which is the register layout of
+// the 16x128b store.
+template <int NT>
+__device__ __forceinline__ void put_updates(uint32_t sC, const float* upd, uint32_t t_hi, uint32_t t_lo, int c0, int s0,
+                                            int lane) {
+    // this lane's row in the four blocks of an ldmatrix: tokens (0-7, 0-7, 8-15, 8-15)
+    // of columns (0-7, 8-15, 0-7, 8-15)
+    const int row = (lane & 7) + ((lane >> 4) << 3), cb = (lane >> 3) & 1;
+    const uint32_t blk = sC + (uint32_t)(c0 >> 6) * (kTile * 128) + (uint32_t)(s0 + row) * 128;
+    const uint32_t ch = (uint32_t)((c0 & 63) >> 3) + cb;
+    const uint32_t from[2] = {blk + ((ch ^ (lane & 7)) << 4), blk + (((ch + 2) ^ (lane & 7)) << 4)};
+    upd += s0 + 2 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < NT; b += 16) {
+        const uint64_t w0 = *(const uint64_t*)(upd + b), w1 = *(const uint64_t*)(upd + b + 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 16 lanes at a time
+            uint32_t v[4], hi[4], lo[4];
+            ldmatrix_x4_trans(from[i] + b * 128, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2(v[j], j < 2 ? w0 : w1, hi[j], lo[j]);
+            const uint32_t to = ((uint32_t)(16 * i) << 16) + (s0 + b) / 2;
+            tmem_st_16x128b_x2(t_hi + to, hi);
+            tmem_st_16x128b_x2(t_lo + to, lo);
+        }
+    }
+    tmem_wait_st();
+}
+
+// The weights of C' for a whole tile, then for the sequence's last, shorter one.
+__device__ __forceinline__ void fill_weights(const Part& w, float* upd) {
+    for (int i = threadIdx.x; i < 2 * kTile; i += kThreads) {
+        const int s = i & (kTile - 1), n = i < kTile ? kTile : w.tail();
+        upd[i] = power(w.g, (float)max(w.rev ? s + 1 : n - 1 - s, 0));
+    }
+}
+
+// gamma^n M + U for NC columns of this thread's lane.
+template <int NC>
+__device__ __forceinline__ void add_update(float (&m)[NC], uint32_t t_u, float gn, int cols) {
+#pragma unroll
+    for (int i = 0; i < NC; i += 16) {
+        if (i < cols) {
+            uint32_t u[16];
+            tmem_ld16(t_u + i, u);
+            tmem_wait_ld(u);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+                unpair(fma2(pair(gn, gn), pair(m[i + j], m[i + j + 1]),
+                            pair(__uint_as_float(u[j]), __uint_as_float(u[j + 1]))),
+                       m[i + j], m[i + j + 1]);
+        }
+    }
+}
+
+// The first `cols` of NC elements of M's row to the caller's matrix.
+template <int NC>
+__device__ __forceinline__ void store_state(const float (&m)[NC], float* dst, int64_t step, int cols) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        if (i < cols) dst[i * step] = m[i];
+}
+
+// ------------------------------------------------------------------- the sums
+
+struct __align__(8) SumBars {
+    uint64_t full[3], free[3];
+    uint64_t cv[2];  // C' is in tensor memory (512 arrivals)
+    uint64_t u[2];   // U is complete
+    uint64_t drain;
+    uint32_t tmem;
+};
+constexpr int SS_STAGES = 3, SS_UPD = SS_STAGES * 2 * kTileBytes, SS_POW = SS_UPD + 2 * kTile * 4,
+              SS_BARS = SS_POW + 132 * 4, SS_SIZE = SS_BARS + (int)sizeof(SumBars);
+
+// One CTA: one (stream, segment) of one role; its sum to R.  Four warpgroups make C' of
+// 32 tokens each and hold 32 columns of M each; C' and U are double-buffered in tensor
+// memory, so that a tile's C' is made while the one before it is multiplied.
+__global__ void __launch_bounds__(kThreads, 1)
+la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    SumBars& bar = *reinterpret_cast<SumBars*>(sm + SS_BARS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Part w(d, roles, true);
+    const LaRole& ro = w.ro;
+    const int Db = ro.Db, Dc = ro.Dc, tiles = w.tiles;
+    float *upd = (float*)(sm + SS_UPD), *pw = (float*)(sm + SS_POW);
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    } else if (tid == kTmaWarp * 32) {
+        for (int i = 0; i < SS_STAGES; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bar.cv[i], 512), mbar_init(&bar.u[i], 1);
+        mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+    }
+    for (int e = tid; e <= kTile; e += kThreads) pw[e] = power(w.g, (float)e);
+    fill_weights(w, upd);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = bar.tmem;
+    auto t_cv = [&](int it) { return (uint32_t)(it & 1) * 128; };       // 64 columns each of hi, lo
+    auto t_u = [&](int it) { return 256 + (uint32_t)(it & 1) * 128; };
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
+            auto load = [&](int it) {
+                unsigned char* st = sm + (it % SS_STAGES) * 2 * kTileBytes;
+                uint64_t* f = &bar.full[it % SS_STAGES];
+                mbar_arrive_expect_tx(f, (uint32_t)((nb + nc) * (kTileBytes / 2)));
+                for (int i = 0; i < nb; ++i)
+                    tma_load_4d(st + i * (kTileBytes / 2), &maps.b[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
+                for (int i = 0; i < nc; ++i)
+                    tma_load_4d(st + kTileBytes + i * (kTileBytes / 2), &maps.c[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
+            };
+            int issued = 0;
+            for (; issued < tiles; ++issued) {
+                if (issued >= SS_STAGES && !mbar_wait(&bar.free[issued % SS_STAGES], (issued / SS_STAGES - 1) & 1,
+                                                      d.err, kErrTma, d.wait_ns))
+                    break;
+                load(issued);
+            }
+            for (int i = max(0, issued - SS_STAGES); i < issued; ++i)  // no copy outlives the CTA
+                mbar_wait(&bar.full[i % SS_STAGES], (i / SS_STAGES) & 1, d.err, kErrDrain);
+        }
+    } else if (warp == kMmaWarp) {
+        const uint32_t i_u = idesc_bf16(128, Db, false, true);
+        for (int it = 0; it < tiles; ++it) {
+            const uint64_t dB = desc_mnmaj(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes, 128, 0);
+            if (!warp_wait(&bar.cv[it & 1], (it >> 1) & 1, d.err, kErrMma, d.wait_ns)) break;
+            fence_after_sync();
+            const uint32_t c = tm + t_cv(it), u = tm + t_u(it);
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 16; ++s)
+                    mma_bf16_ts(u, c + 8 * s, desc_add(dB, (s & 7) * 2048), i_u, s > 0);
+                mma_commit(&bar.u[it & 1]);
+                mma_commit(&bar.free[it % SS_STAGES]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(&bar.drain);  // no MMA outlives the CTA
+        warp_wait(&bar.drain, 0, d.err, kErrDrain, 0);
+    } else {
+        const int c = tid & 127, part = warp >> 2, cols = Db - part * 32;
+        const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        float m[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[i] = 0.f;
+        auto make = [&](int it) {
+            if (!warp_wait(&bar.full[it % SS_STAGES], (it / SS_STAGES) & 1, d.err, kErrState, d.wait_ns)) return false;
+            put_updates<32>(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes + kTileBytes,
+                            upd + (w.len(it) < kTile ? kTile : 0), tl + t_cv(it), tl + t_cv(it) + 64, (warp & 3) * 32,
+                            part * 32, lane);
+            fence_before_sync();
+            mbar_arrive(&bar.cv[it & 1]);
+            return true;
+        };
+        bool ok = make(0);
+        for (int it = 0; it < tiles && ok; ++it) {
+            if (it + 1 < tiles && !(ok = make(it + 1))) break;
+            if (!(ok = warp_wait(&bar.u[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns))) break;
+            fence_after_sync();
+            add_update(m, tl + t_u(it) + part * 32, pw[w.len(it)], cols);
+            fence_before_sync();
+        }
+        if (ok && c < Dc)
+            store_state(m,
+                        const_cast<float*>(ro.R) + (w.stream * w.nseg + w.slot) * (int64_t)Db * Dc +
+                            (int64_t)c * ro.m_sc + part * 32 * ro.m_sb,
+                        ro.m_sb, cols);
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+}
+
+// ------------------------------------------------------------------- the scan
+
 // Tensor memory columns.
 constexpr uint32_t T_X = 0, T_Y = 128, T_U = 256, T_HI = 384, T_LO = 448;
 
 struct __align__(8) Bars {
     uint64_t full[2];   // TMA: the stage's tiles have landed
-    uint64_t cv;        // C' is in tensor memory (256 arrivals)
+    uint64_t free[2];   // the products have read the stage
+    uint64_t staged[2]; // the outputs lie over the stage's A (256 arrivals)
+    uint64_t cv;        // C' is in tensor memory (512 arrivals)
     uint64_t u;         // U is complete
     uint64_t s;         // M is in shared memory (256 arrivals)
     uint64_t k;         // the scores are complete
     uint64_t q;         // A M^T is complete (M's shared memory may be rewritten)
-    uint64_t p;         // P is in tensor memory and X rescaled (128 arrivals)
+    uint64_t r;         // the scores are read out of Y (256 arrivals)
+    uint64_t p;         // P is in tensor memory and X rescaled (256 arrivals)
     uint64_t o;         // the outputs are complete
-    uint64_t x;         // the outputs are read out of X (128 arrivals)
-    uint64_t free[2];   // the stage is used up, its outputs staged (128 arrivals; the sums: 1)
+    uint64_t x;         // the outputs are read out of X (256 arrivals)
     uint64_t drain;
     uint32_t tmem;
 };
 
-constexpr int S_M = 2 * 3 * kTileBytes, S_POW = S_M + kTileBytes, S_UPD = S_POW + 132 * 4,
-              S_BARS = S_UPD + 4 * kTile * 4, S_SIZE = S_BARS + (int)sizeof(Bars);
-static_assert(S_SIZE <= 232448, "shared memory of one CTA");
+// Behind the stages and M: gamma^0 .. gamma^128; a diagonal block's powers by 31 + row -
+// column (0 above it); the weights of C'.
+constexpr int S_M = 2 * 3 * kTileBytes, S_POW = S_M + kTileBytes, S_DIAG = S_POW + 132 * 4, S_UPD = S_DIAG + 64 * 4,
+              S_BARS = S_UPD + 2 * kTile * 4, S_SIZE = S_BARS + (int)sizeof(Bars);
+static_assert(S_SIZE <= 232448 && SS_SIZE <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ float power(float g, float e) { return e > 0.f ? expf(g * e) : 1.f; }
-
-// A wait whose outcome is the same for the whole warp.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t ph, int* err, int code, uint32_t ns) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, ph, err, code, ns));
+// P of a 32-column block off the diagonal: gamma^(distance) of the column nearest the
+// row is `near`; each pair of columns further on has gamma^2 of the last one's.  Every
+// exponent is >= 0.
+template <bool kRev>
+__device__ __forceinline__ void scale_block(const uint32_t (&y)[32], float near, float g1, uint32_t (&p)[16]) {
+    const uint64_t g2 = pair(g1 * g1, g1 * g1);
+    uint64_t w = kRev ? pair(near, near * g1) : pair(near * g1, near);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int j = kRev ? i : 15 - i;
+        float e, f;
+        unpair(mul2(pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), w), e, f);
+        p[j] = pack_bf16(e, f);
+        w = mul2(w, g2);
+    }
 }
 
-// C' of 64 of the tile's tokens (from s0) for this thread's lane c, as two bf16 terms
-// in tensor memory columns s / 2.
-__device__ __forceinline__ void put_updates(const unsigned char* sC, const float* upd, uint32_t tm, int c, int s0) {
-    const unsigned char* col = sC + (c >> 6) * (kTile * 128) + (c & 7) * 2;
-    const uint32_t ch = (c >> 3) & 7;
+// The state's warps: lane c of M, half of the columns.
+template <typename Make>
+__device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars& bar, unsigned char* sm, uint32_t tl,
+                                            Make&& make) {
+    const LaRole& ro = w.ro;
+    const float* sPow = (const float*)(sm + S_POW);
+    const int c = threadIdx.x & 127, half = (threadIdx.x >> 7) - 2, b0 = half * 64, cols = ro.Db - b0;
+    float m[64];
 #pragma unroll
-    for (int b = 0; b < 64; b += 32) {
-        uint32_t hi[16], lo[16];
+    for (int i = 0; i < 64; ++i) m[i] = 0.f;
+    const int64_t VK = (int64_t)ro.Db * ro.Dc;
+    auto add = [&](const float* src, float f) {
+        if (c >= ro.Dc) return;
+        src += (int64_t)c * ro.m_sc + b0 * ro.m_sb;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const int s = s0 + b + j;
-            const float4 w4 = *(const float4*)(upd + s);
-            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-            float f[4], r[4];
+        for (int i = 0; i < 64; i += 16) {
+            if (i < cols) {
+                float x[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint16_t v = *(const uint16_t*)(col + (s + e) * 128 + ((ch ^ ((s + e) & 7)) << 4));
-                f[e] = __uint_as_float((uint32_t)v << 16) * w[e];
-            }
+                for (int j = 0; j < 16; j += 4) {
+                    if (ro.m_sb == 1) {
+                        const float4 v = *(const float4*)(src + i + j);
+                        x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+                    } else {
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const uint32_t h = pack_bf16(f[e], f[e + 1]);
-                r[e] = f[e] - __uint_as_float(h << 16);
-                r[e + 1] = f[e + 1] - __uint_as_float(h & 0xffff0000u);
-                hi[(j + e) / 2] = h;
-                lo[(j + e) / 2] = pack_bf16(r[e], r[e + 1]);
+                        for (int e = 0; e < 4; ++e) x[j + e] = src[(i + j + e) * ro.m_sb];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) m[i + j] = fmaf(f, x[j], m[i + j]);
             }
         }
-        tmem_st16(tm + T_HI + (s0 + b) / 2, hi);
-        tmem_st16(tm + T_LO + (s0 + b) / 2, lo);
+    };
+    bool ok = make(0);
+    if (ro.m0) add(ro.m0 + w.stream * VK, power(w.g, (float)(w.rev ? d.T - w.t_hi : w.t_lo)));
+    const float* R = ro.R + w.stream * (d.nseg - 1) * VK;
+    if (!w.rev)
+        for (int i = 0; i < w.seg; ++i) add(R + i * VK, power(w.g, (float)(w.t_lo - (i + 1) * d.L)));
+    else
+        for (int i = d.nseg - 1; i > w.seg; --i) add(R + (i - 1) * VK, power(w.g, (float)(i * d.L - w.t_hi)));
+    auto put_state = [&] {  // M's bf16 copy, for A M^T
+#pragma unroll
+        for (int i = 0; i < 64; i += 16) {
+            if (i < cols) {
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = m[i + j];
+                tile_put16(sm + S_M, kTile, c, b0 + i, f);
+            }
+        }
+        fence_proxy_async();
+        mbar_arrive(&bar.s);
+    };
+    put_state();
+    for (int it = 0; it < w.tiles && ok; ++it) {
+        const uint32_t ph = it & 1;
+        if (!(ok = warp_wait(&bar.u, ph, d.err, kErrState, d.wait_ns))) break;
+        fence_after_sync();
+        add_update(m, tl + T_U + b0, sPow[w.len(it)], cols);
+        fence_before_sync();
+        if (it + 1 < w.tiles) {
+            if (!(ok = warp_wait(&bar.q, ph, d.err, kErrState, d.wait_ns))) break;
+            put_state();
+            ok = make(it + 1);
+        }
     }
-    tmem_wait_st();
+    if (ok && c < ro.Dc && ro.mT && w.seg == (w.rev ? 0 : d.nseg - 1))
+        store_state(m, ro.mT + w.stream * VK + (int64_t)c * ro.m_sc + b0 * ro.m_sb, ro.m_sb, cols);
 }
 
-// One CTA: role blockIdx.y, (stream, segment) blockIdx.x.  kOut: the outputs and, from
-// the last segment, the state that leaves; else the segments' sums.
-template <bool kOut>
+// The rows' warps: lane = token, half of the columns.
+template <typename Make>
+__device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& bar, unsigned char* sm, uint32_t tl,
+                                          Make&& make) {
+    const LaRole& ro = w.ro;
+    const float *sPow = (const float*)(sm + S_POW), *sDiag = (const float*)(sm + S_DIAG);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rev = w.rev;
+    const int r = threadIdx.x & 127, q = warp & 3, wg = warp >> 2;  // q: the 32-token block of this warp's rows
+    const int cw = ro.Dc > 16 ? ro.Dc / 2 : 16, x0 = wg * cw, xn = min(cw, ro.Dc - x0);  // columns of X
+    const float g1 = sPow[1];
+    if (!make(0)) return;
+    for (int it = 0; it < w.tiles; ++it) {
+        const uint32_t ph = it & 1;
+        const int n = w.len(it);
+        if (!warp_wait(&bar.k, ph, d.err, kErrRows, d.wait_ns)) return;
+        fence_after_sync();
+        // P = Y .* D: blocks of 32 columns below, on or above this warp's diagonal block.
+        // One warpgroup has blocks 0 and 3, the other 1 and 2, so that the causal half is
+        // shared evenly.
+        uint32_t p[2][16], y[2][32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tmem_ld32(tl + T_Y + (k ? 3 - wg : wg) * 32, y[k]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tmem_wait_ld(y[k]);
+        // P goes over the scores: only once both warpgroups have read theirs
+        fence_before_sync();
+        mbar_arrive(&bar.r);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int cb = k ? 3 - wg : wg;
+            if (cb == q) {
+                const float* f = sDiag + 31 + lane;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    float e0, e1;
+                    unpair(mul2(pair(__uint_as_float(y[k][j]), __uint_as_float(y[k][j + 1])), pair(f[-j], f[-j - 1])),
+                           e0, e1);
+                    p[k][j / 2] = pack_bf16(e0, e1);
+                }
+            } else if (rev ? cb < q : cb > q) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) p[k][j] = 0;
+            } else if (rev) {
+                scale_block<true>(y[k], sPow[cb * 32 - r], g1, p[k]);
+            } else {
+                scale_block<false>(y[k], sPow[r - cb * 32 - 31], g1, p[k]);
+            }
+        }
+        if (!warp_wait(&bar.r, ph, d.err, kErrRows, d.wait_ns)) return;
+        fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tmem_st16(tl + T_Y + (k ? 3 - wg : wg) * 16, p[k]);
+        if (!warp_wait(&bar.q, ph, d.err, kErrRows, d.wait_ns)) return;
+        fence_after_sync();
+        const float f = sPow[max(rev ? n - 1 - r : r + 1, 0)];
+        uint32_t x[4][16];  // this warpgroup's columns of X
+        auto read_x = [&] {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld16(tl + T_X + x0 + 16 * k, x[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_wait_ld(x[k]);
+        };
+        read_x();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (16 * k < xn) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[k][j] = __float_as_uint(__uint_as_float(x[k][j]) * f);
+                tmem_st16(tl + T_X + x0 + 16 * k, x[k]);
+            }
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&bar.p);
+        if (!warp_wait(&bar.o, ph, d.err, kErrRows, d.wait_ns)) return;
+        fence_after_sync();
+        read_x();
+        fence_before_sync();
+        mbar_arrive(&bar.x);
+        unsigned char* out = sm + (it & 1) * 3 * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (16 * k < xn) {
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[k][j]);
+                tile_put16(out, kTile, r, x0 + 16 * k, v);
+            }
+        fence_proxy_async();
+        mbar_arrive(&bar.staged[it & 1]);
+        // the next tile's C', once U no longer reads this one's: after the outputs, which
+        // must not wait for the next tile's load
+        if (it + 1 < w.tiles) {
+            if (!warp_wait(&bar.u, ph, d.err, kErrRows, d.wait_ns)) return;
+            fence_after_sync();
+            if (!make(it + 1)) return;
+        }
+    }
+}
+
+// One CTA: one (stream, segment) of one role: its outputs and, from the last segment,
+// the state that leaves.
 __global__ void __launch_bounds__(kThreads, 1)
-la_tile_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
+la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     extern __shared__ __align__(1024) unsigned char sm[];
     Bars& bar = *reinterpret_cast<Bars*>(sm + S_BARS);
-    float* sPow = reinterpret_cast<float*>(sm + S_POW);
+    float *sPow = reinterpret_cast<float*>(sm + S_POW), *sDiag = (float*)(sm + S_DIAG), *sUpd = (float*)(sm + S_UPD);
     unsigned char* sM = sm + S_M;
-    const int rl = blockIdx.y;
-    const LaRole& ro = roles.r[rl];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nseg = kOut ? d.nseg : d.nseg - 1;
-    const int64_t stream = blockIdx.x / nseg;
-    const int slot = (int)(blockIdx.x % nseg);
-    const int rev = ro.rev, seg = !kOut && rev ? slot + 1 : slot;
-    const int b = (int)(stream / d.H), h = (int)(stream % d.H);
-    const float g = d.log_decay[h];
-    const int t_lo = seg * d.L, t_hi = min(d.T, t_lo + d.L);
-    const int tiles = (t_hi - t_lo + kTile - 1) / kTile;
-    const int Db = ro.Db, Dc = ro.Dc;
-    auto tile_t0 = [&](int it) { return t_lo + (rev ? tiles - 1 - it : it) * kTile; };
+    const Part w(d, roles, false);
+    const LaRole& ro = w.ro;
+    const int Db = ro.Db, Dc = ro.Dc, tiles = w.tiles, rev = w.rev;
 
     if (warp == kMmaWarp) {
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
     } else if (tid == kTmaWarp * 32) {
-        mbar_init(&bar.full[0], 1);
-        mbar_init(&bar.full[1], 1);
-        mbar_init(&bar.cv, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.free[i], 1);
+            mbar_init(&bar.staged[i], 256);
+        }
+        mbar_init(&bar.cv, 512);
         mbar_init(&bar.u, 1);
         mbar_init(&bar.s, 256);
         mbar_init(&bar.k, 1);
         mbar_init(&bar.q, 1);
-        mbar_init(&bar.p, 128);
+        mbar_init(&bar.r, 256);
+        mbar_init(&bar.p, 256);
         mbar_init(&bar.o, 1);
-        mbar_init(&bar.x, 128);
-        mbar_init(&bar.free[0], kOut ? 128 : 1);
-        mbar_init(&bar.free[1], kOut ? 128 : 1);
+        mbar_init(&bar.x, 256);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
-    for (int e = tid; e <= kTile; e += kThreads) sPow[e] = power(g, (float)e);
+    for (int e = tid; e <= kTile; e += kThreads) sPow[e] = power(w.g, (float)e);
+    for (int i = tid; i < 63; i += kThreads) {
+        const int dist = rev ? 31 - i : i - 31;
+        sDiag[i] = dist >= 0 ? power(w.g, (float)dist) : 0.f;
+    }
+    fill_weights(w, sUpd);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = bar.tmem;
-    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the lanes
+    const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
             const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
-            const uint32_t bytes = (uint32_t)(((kOut ? 2 : 1) * nb + nc) * (kTileBytes / 2));
-            auto load = [&](int it) {
-                unsigned char* st = sm + (it & 1) * 3 * kTileBytes;
-                uint64_t* f = &bar.full[it & 1];
-                const int t0 = tile_t0(it);
-                mbar_arrive_expect_tx(f, bytes);
-                for (int i = 0; i < nb; ++i) {
-                    if (kOut) tma_load_4d(st + i * (kTileBytes / 2), &maps.a[rl], f, 64 * i, h, t0, b);
-                    tma_load_4d(st + kTileBytes + i * (kTileBytes / 2), &maps.b[rl], f, 64 * i, h, t0, b);
-                }
-                for (int i = 0; i < nc; ++i)
-                    tma_load_4d(st + 2 * kTileBytes + i * (kTileBytes / 2), &maps.c[rl], f, 64 * i, h, t0, b);
+            auto stage = [&](int it) { return sm + (it & 1) * 3 * kTileBytes; };
+            auto load = [&](int it, const CUtensorMap* map, int blocks, unsigned char* to) {
+                for (int i = 0; i < blocks; ++i)
+                    tma_load_4d(to + i * (kTileBytes / 2), map, &bar.full[it & 1], 64 * i, w.h, w.t0(it), w.b);
             };
-            int issued = 0, it = 0;
-            for (; issued < 2 && issued < tiles; ++issued) load(issued);
-            for (; it < tiles; ++it) {
-                if (!mbar_wait(&bar.free[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
-                if (kOut) {
-                    const unsigned char* st = sm + (it & 1) * 3 * kTileBytes;
-                    for (int i = 0; i < nc; ++i)
-                        tma_store_4d(&maps.out[rl], st + i * (kTileBytes / 2), 64 * i, h, tile_t0(it), b);
-                    bulk_commit();
-                    if (issued < tiles) bulk_wait_read0();
-                }
-                if (issued < tiles) load(issued++);
+            auto load_bc = [&](int it) {
+                mbar_arrive_expect_tx(&bar.full[it & 1], (uint32_t)((2 * nb + nc) * (kTileBytes / 2)));
+                load(it, &maps.b[w.rl], nb, stage(it) + kTileBytes);
+                load(it, &maps.c[w.rl], nc, stage(it) + 2 * kTileBytes);
+            };
+            int issued = 0;  // tiles whose loads are all issued
+            bool half = false;
+            for (; issued < 2 && issued < tiles; ++issued) {
+                load_bc(issued);
+                load(issued, &maps.a[w.rl], nb, stage(issued));
             }
-            for (int i = max(0, issued - 2); i < issued; ++i)  // no copy outlives the CTA
+            for (int it = 0; it < tiles; ++it) {
+                if (issued < tiles) {
+                    if (!mbar_wait(&bar.free[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
+                    load_bc(issued);
+                    half = true;
+                }
+                if (!mbar_wait(&bar.staged[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
+                for (int i = 0; i < nc; ++i)
+                    tma_store_4d(&maps.out[w.rl], stage(it) + i * (kTileBytes / 2), 64 * i, w.h, w.t0(it), w.b);
+                bulk_commit();
+                if (issued < tiles) {
+                    bulk_wait_read0();
+                    load(issued, &maps.a[w.rl], nb, stage(issued));
+                    half = false;
+                    ++issued;
+                }
+            }
+            // no copy outlives the CTA: a tile whose A was not asked for gets it now
+            if (half) load(issued, &maps.a[w.rl], nb, stage(issued)), ++issued;
+            for (int i = max(0, issued - 2); i < issued; ++i)
                 mbar_wait(&bar.full[i & 1], (i >> 1) & 1, d.err, kErrDrain);
             bulk_wait0();
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            const uint32_t i_k = idesc_bf16(128, 128, false, false), i_q = idesc_bf16(128, Dc, false, false),
-                           i_p = idesc_bf16(128, Dc, false, true), i_u = idesc_bf16(128, Db, false, true);
-            for (int it = 0; it < tiles; ++it) {
-                const uint32_t ph = it & 1;
-                const uint32_t sA = smem_u32(sm + (it & 1) * 3 * kTileBytes), sB = sA + kTileBytes,
-                               sC = sB + kTileBytes, sMm = smem_u32(sM);
-                if (!mbar_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrMma, d.wait_ns)) break;
-                if (kOut) {
-                    for (int s = 0; s < Db / 16; ++s)
-                        mma_bf16_ss(tm + T_Y, desc_kmaj(sA, 128, s), desc_kmaj(sB, 128, s), i_k, s > 0);
-                    mma_commit(&bar.k);
-                    if (!mbar_wait(&bar.s, ph, d.err, kErrMma, d.wait_ns)) break;
-                    if (it && !mbar_wait(&bar.x, ph ^ 1, d.err, kErrMma, d.wait_ns)) break;
-                    fence_after_sync();
-                    for (int s = 0; s < Db / 16; ++s)
-                        mma_bf16_ss(tm + T_X, desc_kmaj(sA, 128, s), desc_kmaj(sMm, 128, s), i_q, s > 0);
-                    mma_commit(&bar.q);
-                }
-                if (!mbar_wait(&bar.cv, ph, d.err, kErrMma, d.wait_ns)) break;
-                fence_after_sync();
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_bf16_ts(tm + T_U, tm + T_HI + 8 * s, desc_mnmaj(sB, 128, s), i_u, s > 0);
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_bf16_ts(tm + T_U, tm + T_LO + 8 * s, desc_mnmaj(sB, 128, s), i_u, 1);
-                mma_commit(&bar.u);
-                if (!kOut) mma_commit(&bar.free[it & 1]);
-                if (kOut) {
-                    if (!mbar_wait(&bar.p, ph, d.err, kErrMma, d.wait_ns)) break;
-                    fence_after_sync();
-                    for (int s = 0; s < kTile / 16; ++s)
-                        mma_bf16_ts(tm + T_X, tm + T_Y + 8 * s, desc_mnmaj(sC, 128, s), i_p, 1);
-                    mma_commit(&bar.o);
-                }
-            }
-            mma_commit(&bar.drain);  // no MMA outlives the CTA
-            mbar_wait(&bar.drain, 0, d.err, kErrDrain);
-        }
-    } else if (warp >= 4) {
-        // ------------------------------------------------ the state: lane c, half the columns
-        const int c = tid & 127, half = (warp >> 2) - 1, b0 = half * 64;
-        const uint32_t tl = tm + lane_base;
-        float m[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) m[i] = 0.f;
-        const int64_t VK = (int64_t)Db * Dc;
-        if (kOut) {
-            auto add = [&](const float* src, float w) {
-                if (c >= Dc) return;
-                src += (int64_t)c * ro.m_sc;
-#pragma unroll
-                for (int i = 0; i < 64; i += 4) {
-                    if (b0 + i >= Db) break;
-                    float4 f;
-                    if (ro.m_sb == 1) f = *(const float4*)(src + b0 + i);
-                    else
-                        f = make_float4(src[(b0 + i) * ro.m_sb], src[(b0 + i + 1) * ro.m_sb],
-                                        src[(b0 + i + 2) * ro.m_sb], src[(b0 + i + 3) * ro.m_sb]);
-                    m[i] = fmaf(w, f.x, m[i]), m[i + 1] = fmaf(w, f.y, m[i + 1]);
-                    m[i + 2] = fmaf(w, f.z, m[i + 2]), m[i + 3] = fmaf(w, f.w, m[i + 3]);
-                }
-            };
-            if (ro.m0) add(ro.m0 + stream * VK, power(g, (float)(rev ? d.T - t_hi : t_lo)));
-            const float* R = ro.R + stream * (d.nseg - 1) * VK;
-            if (!rev)
-                for (int i = 0; i < seg; ++i) add(R + i * VK, power(g, (float)(t_lo - (i + 1) * d.L)));
-            else
-                for (int i = d.nseg - 1; i > seg; --i) add(R + (i - 1) * VK, power(g, (float)(i * d.L - t_hi)));
-        }
-        auto put_state = [&] {  // M's bf16 copy, for A M^T
-#pragma unroll
-            for (int i = 0; i < 64; i += 16) {
-                if (b0 + i >= Db) break;
-                float f[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = m[i + j];
-                tile_put16(sM, kTile, c, b0 + i, f);
-            }
-            fence_proxy_async();
-            mbar_arrive(&bar.s);
-        };
-        if (kOut) put_state();
-        // this warp's copy of the update weights (the warps of a warpgroup's half share
-        // nothing, so that no warp waits for another outside the bounded waits)
-        float* upd = reinterpret_cast<float*>(sm + S_UPD) + (warp & 3) * kTile;
-        const int s0 = half * 64;
-        int n_have = -1;
-        bool ok = true;
-        for (int it = 0; it < tiles && ok; ++it) {
-            const uint32_t ph = it & 1;
-            const int n = min(kTile, t_hi - tile_t0(it));
-            if (n != n_have) {
-                __syncwarp();
-                for (int s = s0 + lane; s < s0 + 64; s += 32) upd[s] = sPow[max(rev ? min(s + 1, n) : n - 1 - s, 0)];
-                __syncwarp();
-                n_have = n;
-            }
-            if (!(ok = warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns))) break;
-            put_updates(sm + (it & 1) * 3 * kTileBytes + 2 * kTileBytes, upd, tl, c, s0);
-            fence_before_sync();
-            mbar_arrive(&bar.cv);
-            if (!(ok = warp_wait(&bar.u, ph, d.err, kErrState, d.wait_ns))) break;
-            fence_after_sync();
-            const float gn = sPow[n];
-#pragma unroll
-            for (int i = 0; i < 64; i += 32) {
-                if (b0 + i >= Db) break;
-                uint32_t u[32];
-                tmem_ld32(tl + T_U + b0 + i, u);
-                tmem_wait_ld(u);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) m[i + j] = fmaf(gn, m[i + j], __uint_as_float(u[j]));
-            }
-            fence_before_sync();
-            if (kOut && it + 1 < tiles) {
-                if (!(ok = warp_wait(&bar.q, ph, d.err, kErrState, d.wait_ns))) break;
-                put_state();
-            }
-        }
-        const bool last = kOut && ro.mT && seg == (rev ? 0 : d.nseg - 1);
-        if (ok && c < Dc && (!kOut || last)) {
-            float* dst = (kOut ? ro.mT + stream * VK : const_cast<float*>(ro.R) + (stream * nseg + slot) * VK) +
-                         (int64_t)c * ro.m_sc;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (b0 + i < Db) dst[(b0 + i) * ro.m_sb] = m[i];
-        }
-    } else if (kOut) {
-        // ------------------------------------------------ the rows: lane = token
-        const uint32_t tl = tm + lane_base;
-        const int r = tid;
-        float fine[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) fine[j] = sPow[rev ? j : 15 - j];
+        const uint32_t i_k = idesc_bf16(128, 128, false, false), i_q = idesc_bf16(128, Dc, false, false),
+                       i_p = idesc_bf16(128, Dc, false, true), i_u = idesc_bf16(128, Db, false, true);
+        const uint64_t dM = desc_kmaj(smem_u32(sM), 128, 0);
         for (int it = 0; it < tiles; ++it) {
             const uint32_t ph = it & 1;
-            const int n = min(kTile, t_hi - tile_t0(it));
-            if (!warp_wait(&bar.k, ph, d.err, kErrRows, d.wait_ns)) break;
-            fence_after_sync();
-            // P = Y .* D: 32 columns at a time, below, on or above this warp's diagonal
-            // block; within a block gamma^|r - s| is a power of the row's distance to its
-            // edge times one of the 16 (column) powers, both with exponents >= 0
-#pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                uint32_t y[32], p[16];
-                if (rev ? cb < warp : cb > warp) {
+            const uint32_t sA = smem_u32(sm) + (uint32_t)(it & 1) * 3 * kTileBytes;
+            const uint64_t dA = desc_kmaj(sA, 128, 0), dB = desc_add(dA, kTileBytes),
+                           dBt = desc_mnmaj(sA + kTileBytes, 128, 0), dCt = desc_add(dBt, kTileBytes);
+            if (!warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrMma, d.wait_ns)) break;
+            if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = 0;
-                } else {
-                    tmem_ld32(tl + T_Y + cb * 32, y);
-                    tmem_wait_ld(y);
-                    if (cb == warp) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int dist = rev ? j - lane : lane - j;
-                            y[j] = dist >= 0 ? __float_as_uint(__uint_as_float(y[j]) * sPow[max(dist, 0)]) : 0u;
-                        }
-                    } else {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int s = cb * 32 + hf * 16;
-                            const float far = sPow[rev ? s - r : r - s - 15];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                y[hf * 16 + j] =
-                                    __float_as_uint(__uint_as_float(y[hf * 16 + j]) * (far * fine[j]));
-                        }
+                for (int s = 0; s < 8; ++s)
+                    if (16 * s < Db) {
+                        const uint32_t at = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
+                        mma_bf16_ss(tm + T_Y, desc_add(dA, at), desc_add(dB, at), i_k, s > 0);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        p[j] = pack_bf16(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
-                }
-                tmem_st16(tl + T_Y + cb * 16, p);  // over scores already read
+                mma_commit(&bar.k);
             }
-            if (!warp_wait(&bar.q, ph, d.err, kErrRows, d.wait_ns)) break;
+            __syncwarp();
+            if (!warp_wait(&bar.s, ph, d.err, kErrMma, d.wait_ns)) break;
+            if (it && !warp_wait(&bar.x, ph ^ 1, d.err, kErrMma, d.wait_ns)) break;
             fence_after_sync();
-            const float w = sPow[max(rev ? n - 1 - r : r + 1, 0)];
-#pragma unroll 1
-            for (int cb = 0; cb < Dc; cb += 32) {
-                uint32_t x[32];
-                tmem_ld32(tl + T_X + cb, x);
-                tmem_wait_ld(x);
+            if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * w);
-                tmem_st32(tl + T_X + cb, x);
+                for (int s = 0; s < 8; ++s)
+                    if (16 * s < Db) {
+                        const uint32_t at = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
+                        mma_bf16_ss(tm + T_X, desc_add(dA, at), desc_add(dM, at), i_q, s > 0);
+                    }
+                mma_commit(&bar.q);
             }
-            tmem_wait_st();
-            fence_before_sync();
-            mbar_arrive(&bar.p);
-            if (!warp_wait(&bar.o, ph, d.err, kErrRows, d.wait_ns)) break;
+            __syncwarp();
+            if (!warp_wait(&bar.cv, ph, d.err, kErrMma, d.wait_ns)) break;
             fence_after_sync();
-            unsigned char* so = sm + (it & 1) * 3 * kTileBytes;
-#pragma unroll 1
-            for (int cb = 0; cb < Dc; cb += 32) {
-                uint32_t x[32];
-                tmem_ld32(tl + T_X + cb, x);
-                tmem_wait_ld(x);
+            if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 16) {
-                    float f[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[i + j]);
-                    tile_put16(so, kTile, r, cb + i, f);
-                }
+                for (int s = 0; s < 16; ++s)
+                    mma_bf16_ts(tm + T_U, tm + T_HI + 8 * s, desc_add(dBt, (s & 7) * 2048), i_u, s > 0);
+                mma_commit(&bar.u);
             }
-            fence_proxy_async();
-            fence_before_sync();
-            mbar_arrive(&bar.x);
-            mbar_arrive(&bar.free[it & 1]);
+            __syncwarp();
+            if (!warp_wait(&bar.p, ph, d.err, kErrMma, d.wait_ns)) break;
+            fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_bf16_ts(tm + T_X, tm + T_Y + 8 * s, desc_add(dCt, s * 2048), i_p, 1);
+                mma_commit(&bar.o);
+                mma_commit(&bar.free[it & 1]);
+            }
+            __syncwarp();
         }
+        if (elect_one()) mma_commit(&bar.drain);  // no MMA outlives the CTA
+        warp_wait(&bar.drain, 0, d.err, kErrDrain, 0);
+    } else {
+        // C' of this warpgroup's 32 tokens of tile it
+        auto make = [&](int it) {
+            if (!warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns)) return false;
+            put_updates<32>(smem_u32(sm) + (uint32_t)(it & 1) * 3 * kTileBytes + 2 * kTileBytes,
+                            sUpd + (w.len(it) < kTile ? kTile : 0), tl + T_HI, tl + T_LO, (warp & 3) * 32,
+                            (warp >> 2) * 32, lane);
+            fence_before_sync();
+            mbar_arrive(&bar.cv);
+            return true;
+        };
+        if (warp >= 8) state_warps(d, w, bar, sm, tl, make);
+        else row_warps(d, w, bar, sm, tl, make);
     }
     __syncwarp();
     fence_before_sync();
@@ -417,24 +674,23 @@ bool make_maps(const LaDims& d, const LaRoles& roles, bool out, LaMaps* m) {
     return true;
 }
 
-template <bool kOut>
-cudaError_t launch(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
-    LaMaps maps;
-    if (!make_maps(d, roles, kOut, &maps)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(la_tile_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SIZE);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(d.NS() * (kOut ? d.nseg : d.nseg - 1)), roles.n);
-    la_tile_kernel<kOut><<<grid, kThreads, S_SIZE, st>>>(d, roles, maps);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
-    return launch<false>(d, roles, st);
+    LaMaps maps;
+    if (!make_maps(d, roles, false, &maps)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(la_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SS_SIZE);
+    if (e != cudaSuccess) return e;
+    la_sums_kernel<<<dim3((unsigned)(d.NS() * (d.nseg - 1)), roles.n), kThreads, SS_SIZE, st>>>(d, roles, maps);
+    return cudaGetLastError();
 }
 cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
-    return launch<true>(d, roles, st);
+    LaMaps maps;
+    if (!make_maps(d, roles, true, &maps)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(la_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SIZE);
+    if (e != cudaSuccess) return e;
+    la_scan_kernel<<<dim3((unsigned)(d.NS() * d.nseg), roles.n), kThreads, S_SIZE, st>>>(d, roles, maps);
+    return cudaGetLastError();
 }
 
 }  // namespace gdn
