@@ -234,7 +234,7 @@ const char* const kKernelNames[gdn::KID_COUNT] = {
     "scan_bwd_tc", "grad_qk_tc", "grad_wy_tc", "decode_kernel", "prologue_fwd_kernel",
     "prologue_bwd_kernel", "varlen_offsets", "varlen_gather", "varlen_scatter", "scan_fwd_tc(split pass 1)",
     "scan_bwd_tc(split pass 1)", "scan_fwd_tc(transitions)", "split_combine", "count_nonfinite_kernel",
-    "la_states", "la_scan", "la_decode_kernel", "qk_norm_rope_fwd_kernel", "qk_norm_rope_bwd_kernel",
+    "la_states", "la_link_kernel", "la_scan", "la_decode_kernel", "qk_norm_rope_fwd_kernel", "qk_norm_rope_bwd_kernel",
     "gated_norm_fwd_kernel", "gated_norm_bwd_kernel", "weight_sum_kernel"};
 
 template <typename F>
@@ -1674,8 +1674,7 @@ struct LaCall {
     size_t sums;   // floats of all segments' sums
 };
 
-// roles: the scans of the call (1 forward, 3 backward), which share the GPU.
-gdn_status la_problem(const gdn_la_problem* p, LaCall* c, int roles) {
+gdn_status la_problem(const gdn_la_problem* p, LaCall* c, bool bwd) {
     if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
     gdn_status st = check_layer_sizes(p->B, p->T, p->H, p->dtype);
     if (st != GDN_OK) return st;
@@ -1691,7 +1690,7 @@ gdn_status la_problem(const gdn_la_problem* p, LaCall* c, int roles) {
     c->d.K = (int)p->K;
     c->d.V = (int)p->V;
     c->d.wait_ns = g_wait_limit_ns;
-    gdn::la_segments(&c->d, roles);
+    gdn::la_segments(&c->d, bwd);
     c->tokens = p->B * p->T;
     c->state = (size_t)c->d.NS() * p->V * p->K;
     c->sums = c->state * (c->d.nseg - 1);
@@ -1701,7 +1700,7 @@ gdn_status la_problem(const gdn_la_problem* p, LaCall* c, int roles) {
 struct LaBufs {
     int* err;
     float* copy;  // of a state that is read and overwritten by the same call
-    float* fwd;   // the segments' sums in the order of time
+    float* fwd;   // the segments' sums, then the states that enter them, in the order of time
     float* rev;   // and against it
 };
 size_t carve_la(const LaCall& c, Carver& cv, LaBufs* b, bool bwd) {
@@ -1713,7 +1712,7 @@ size_t carve_la(const LaCall& c, Carver& cv, LaBufs* b, bool bwd) {
 }
 size_t la_workspace(const gdn_la_problem* p, bool bwd) {
     LaCall c;
-    if (la_problem(p, &c, bwd ? 3 : 1) != GDN_OK) return 0;
+    if (la_problem(p, &c, bwd) != GDN_OK) return 0;
     Carver cv{nullptr};
     LaBufs b;
     return carve_la(c, cv, &b, bwd);
@@ -1730,8 +1729,10 @@ gdn_status copy_state(float* dst, const float* src, size_t n, cudaStream_t cs) {
 gdn_status run_la(const LaCall& c, gdn::InType ty, const gdn::LaRoles& sums, const gdn::LaRoles& outs,
                   cudaStream_t cs) {
     cudaError_t e = cudaSuccess;
-    if (c.d.nseg > 1 && sums.n)
+    if (c.d.nseg > 1 && sums.n) {
         e = timed(gdn::KID_LA_STATES, cs, [&] { return gdn::launch_la_states(c.d, ty, sums, cs); });
+        if (e == cudaSuccess) e = timed(gdn::KID_LA_LINK, cs, [&] { return gdn::launch_la_link(c.d, sums, cs); });
+    }
     if (e == cudaSuccess) e = timed(gdn::KID_LA_SCAN, cs, [&] { return gdn::launch_la_scan(c.d, ty, outs, cs); });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear-attention kernel");
 }
@@ -1745,7 +1746,7 @@ size_t gdn_la_bwd_workspace_bytes(const gdn_la_problem* p) { return la_workspace
 // The forward's sums serve the backward where both cut the sequences alike.
 size_t gdn_la_saved_bytes(const gdn_la_problem* p) {
     LaCall c, b;
-    if (la_problem(p, &c, 1) != GDN_OK || la_problem(p, &b, 3) != GDN_OK) return 0;
+    if (la_problem(p, &c, false) != GDN_OK || la_problem(p, &b, true) != GDN_OK) return 0;
     return c.d.L == b.d.L ? c.sums * sizeof(float) : 0;
 }
 
@@ -1754,7 +1755,7 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
                       size_t workspace_bytes, void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c, 1);
+    gdn_status st = la_problem(p, &c, false);
     if (st != GDN_OK) return st;
     const size_t nsaved = gdn_la_saved_bytes(p), need = la_workspace(p, false), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
@@ -1798,7 +1799,7 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
                       void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c, 3);
+    gdn_status st = la_problem(p, &c, true);
     if (st != GDN_OK) return st;
     const size_t nsaved = gdn_la_saved_bytes(p), need = la_workspace(p, true), es = elem_size(p->dtype), nstate = c.state * sizeof(float);
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
@@ -1837,8 +1838,8 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
     const int64_t so = wv;  // d_o is dense
     const float* fwd = saved ? (const float*)saved : b.fwd;
     gdn::LaRoles sums, outs3;
-    sums.r[sums.n++] = {nullptr, q, d_o, nullptr, 0, c.sq, so, K, V, nullptr, nullptr, b.rev, K, 1, 1};
-    if (!saved) sums.r[sums.n++] = {nullptr, k, v, nullptr, 0, c.sk, c.sv, K, V, nullptr, nullptr, b.fwd, K, 1, 0};
+    sums.r[sums.n++] = {nullptr, q, d_o, nullptr, 0, c.sq, so, K, V, d_final_state, nullptr, b.rev, K, 1, 1};
+    if (!saved) sums.r[sums.n++] = {nullptr, k, v, nullptr, 0, c.sk, c.sv, K, V, initial_state, nullptr, b.fwd, K, 1, 0};
     outs3.n = 3;
     outs3.r[0] = {d_o, v, k, dq, so, c.sv, c.sk, V, K, initial_state, nullptr, fwd, 1, K, 0};
     outs3.r[1] = {v, d_o, q, dk, c.sv, so, c.sq, V, K, d_final_state, nullptr, b.rev, 1, K, 1};
@@ -1850,7 +1851,7 @@ gdn_status gdn_la_decode(const gdn_la_problem* p, const void* q, const void* k, 
                          const float* log_decay, float* state, void* o, void* stream) {
     g_err[0] = 0;
     LaCall c;
-    gdn_status st = la_problem(p, &c, 1);
+    gdn_status st = la_problem(p, &c, false);
     if (st != GDN_OK) return st;
     const int64_t wk = p->H * p->K, wv = p->H * p->V;
     const Span ins[] = {{q, row_span(c.tokens, c.sq, wk, p->dtype), "q"},

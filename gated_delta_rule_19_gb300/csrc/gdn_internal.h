@@ -143,6 +143,7 @@ enum KernelId {
     KID_SPLIT_COMBINE,   // pieces_kernel, combine_fwd_kernel, combine_bwd_kernel
     KID_COUNT_NONFINITE, // count_nonfinite_kernel
     KID_LA_STATES,       // la_chunk_kernel, the segments' sums
+    KID_LA_LINK,         // la_link_kernel, the states that enter the segments
     KID_LA_SCAN,         // la_chunk_kernel, outputs or gradients
     KID_LA_DECODE,       // la_decode_kernel
     KID_NORM_ROPE_FWD,   // qk_norm_rope_fwd_kernel
@@ -323,13 +324,15 @@ struct LaDims {
     int* err = nullptr;      // the workspace's error word
     __host__ __device__ int64_t NS() const { return (int64_t)B * H; }
 };
-constexpr int kLaMaxSeg = 16;
-void la_segments(LaDims* d, int roles);
+void la_segments(LaDims* d, bool bwd);
 
 // One scan (see la.cu): out_r = sum of gamma^|r-s| (a_r . b_s) c_s, a and b of Db columns,
 // c and out of Dc; token strides in elements (out is dense).  M's element (c, b) is at
 // c * m_sc + b * m_sb of the caller's [V, K] matrices: m0 enters (or NULL), mT receives
-// the state that leaves (or NULL), R [stream][nseg - 1][V][K] holds the segments' sums.
+// the state that leaves (or NULL).  R [stream][nseg - 1][V][K] holds the segments' sums, of
+// the first nseg - 1 segments in the order of the scan, by position in time (against the
+// order of time segment i at i - 1); once linked, the state that enters segment i, at
+// i - 1, or against the order of time at i.
 struct LaRole {
     const void *a, *b, *c;
     void* out;
@@ -344,8 +347,27 @@ struct LaRoles {
     LaRole r[3];
     int n = 0;
 };
-// The segments' sums into R (nseg > 1), then the outputs.
+// Launches a kernel that may start while the one before it in the stream still runs: it
+// waits (griddepcontrol.wait) before it reads what that one writes.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                             const A&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// The segments' sums into R (nseg > 1), R linked, then the outputs.
 cudaError_t launch_la_states(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
+cudaError_t launch_la_link(const LaDims& d, const LaRoles& roles, cudaStream_t st);
 cudaError_t launch_la_scan(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st);
 // The same on the tensor cores, bf16 only (la_tc.cu).
 cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st);

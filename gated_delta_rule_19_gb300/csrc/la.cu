@@ -14,9 +14,8 @@
 // Every power of gamma has an exponent >= 0, so nothing overflows for g <= 0.
 //
 // Streams alone are too few to fill the GPU, so a sequence is cut into segments of L
-// tokens: a first pass sums c b^T over each segment (from M = 0), and a segment of the
-// second pass starts from the sum of the earlier segments' results, each decayed by its
-// distance, plus the decayed initial state.
+// tokens: a first pass sums c b^T over each segment (from M = 0), a second links the sums
+// to the states that enter the segments, and the third runs every segment from its own.
 
 #include <cuda_bf16.h>
 
@@ -26,11 +25,6 @@ namespace gdn {
 namespace {
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                       __uint_as_float(x.y & 0xffff0000u));
-}
 __device__ __forceinline__ void st1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -52,7 +46,7 @@ struct Smem {
 // One CTA: one (stream, segment), CS columns of c, one role.  256 threads as 16 x 16:
 // thread (ty, tx) has rows 4 ty .. 4 ty + 3 and columns 4 (tx) .. of each product, and
 // M's rows ty, ty + 16, ... in registers; a copy in shared memory feeds A M^T.
-template <typename T, int D, bool kOut>
+template <int D, bool kOut>
 __global__ void __launch_bounds__(256)
 la_chunk_kernel(LaDims d, LaRoles roles) {
     using L = Smem<D>;
@@ -79,28 +73,25 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
 #pragma unroll
         for (int j = 0; j < CT; ++j) m[i][j] = 0.f;
     if (kOut) {
-        auto add = [&](const float* src, float w) {
+        const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
+        const int64_t VK = (int64_t)ro.Db * ro.Dc;
+        const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
+                                 : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
+        if (src) {
 #pragma unroll
             for (int i = 0; i < BT; ++i)
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     const int bb = ty + 16 * i, cc = c0 + tx * CT + j;
-                    if (bb < ro.Db && cc < ro.Dc) m[i][j] = fmaf(w, src[cc * ro.m_sc + bb * ro.m_sb], m[i][j]);
+                    if (bb < ro.Db && cc < ro.Dc) m[i][j] = src[cc * ro.m_sc + bb * ro.m_sb];
                 }
-        };
-        const int64_t VK = (int64_t)ro.Db * ro.Dc;
-        if (ro.m0) add(ro.m0 + stream * VK, power(g, (float)(ro.rev ? d.T - t_hi : t_lo)));
-        const float* R = ro.R + stream * (d.nseg - 1) * VK;
-        if (!ro.rev)
-            for (int i = 0; i < seg; ++i) add(R + i * VK, power(g, (float)(t_lo - (i + 1) * d.L)));
-        else
-            for (int i = d.nseg - 1; i > seg; --i) add(R + (i - 1) * VK, power(g, (float)(i * d.L - t_hi)));
+        }
     }
 
-    const T* pa = (const T*)ro.a + (int64_t)b * d.T * ro.sa + (int64_t)h * ro.Db;
-    const T* pb = (const T*)ro.b + (int64_t)b * d.T * ro.sb + (int64_t)h * ro.Db;
-    const T* pc = (const T*)ro.c + (int64_t)b * d.T * ro.sc + (int64_t)h * ro.Dc + c0;
-    T* po = (T*)ro.out + ((int64_t)b * d.T * d.H + h) * ro.Dc + c0;
+    const float* pa = (const float*)ro.a + (int64_t)b * d.T * ro.sa + (int64_t)h * ro.Db;
+    const float* pb = (const float*)ro.b + (int64_t)b * d.T * ro.sb + (int64_t)h * ro.Db;
+    const float* pc = (const float*)ro.c + (int64_t)b * d.T * ro.sc + (int64_t)h * ro.Dc + c0;
+    float* po = (float*)ro.out + ((int64_t)b * d.T * d.H + h) * ro.Dc + c0;
     const int cw = min(L::CS, ro.Dc - c0);
     const int chunks = (t_hi - t_lo + kTok - 1) / kTok;
     for (int it = 0; it < chunks; ++it) {
@@ -210,7 +201,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
 #pragma unroll
                 for (int j = 0; j < CT; ++j)
                     if (r < n && tx * CT + j < cw)
-                        st1(po + (int64_t)(t0 + r) * d.H * ro.Dc + tx * CT + j, acc[i][j]);
+                        po[(int64_t)(t0 + r) * d.H * ro.Dc + tx * CT + j] = acc[i][j];
             }
         }
         // M <- gamma^n M + sum of gamma^(n-1-rho+rev) b c^T
@@ -249,25 +240,57 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     }
 }
 
-template <typename T, int D, bool kOut>
+template <int D, bool kOut>
 cudaError_t launch_chunk(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     using L = Smem<D>;
     const size_t smem = L::SIZE * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(la_chunk_kernel<T, D, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(la_chunk_kernel<D, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * (kOut ? d.nseg : d.nseg - 1)), D / L::CS, roles.n);
-    la_chunk_kernel<T, D, kOut><<<grid, 256, smem, st>>>(d, roles);
+    la_chunk_kernel<D, kOut><<<grid, 256, smem, st>>>(d, roles);
     return cudaGetLastError();
 }
 
-template <typename T, bool kOut>
+template <bool kOut>
 cudaError_t launch_width(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     switch (d.K > d.V ? d.K : d.V) {
-        case 16: return launch_chunk<T, 16, kOut>(d, roles, st);
-        case 32: return launch_chunk<T, 32, kOut>(d, roles, st);
-        case 64: return launch_chunk<T, 64, kOut>(d, roles, st);
-        default: return launch_chunk<T, 128, kOut>(d, roles, st);
+        case 16: return launch_chunk<16, kOut>(d, roles, st);
+        case 32: return launch_chunk<32, kOut>(d, roles, st);
+        case 64: return launch_chunk<64, kOut>(d, roles, st);
+        default: return launch_chunk<128, kOut>(d, roles, st);
+    }
+}
+
+// The segments' sums R become, in place, the states that enter the segments behind them
+// (in the order of the scan): S <- gamma^L S + R from the caller's state on.  A thread
+// has four elements of one stream's matrix; its loads do not wait for one another.
+__global__ void __launch_bounds__(256)
+la_link_kernel(LaDims d, LaRoles roles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const LaRole& ro = roles.r[blockIdx.y];
+    const int64_t VK = (int64_t)ro.Db * ro.Dc, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t stream = i / VK, e = i % VK;
+    if (stream >= d.NS()) return;
+    const float g = d.log_decay[stream % d.H];
+    const int n = d.nseg - 1;
+    const float step = power(g, (float)d.L), tail = power(g, (float)(d.T - n * d.L));
+    float* R = const_cast<float*>(ro.R) + stream * n * VK + e;
+    float4 s = ro.m0 ? *(const float4*)(ro.m0 + stream * VK + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        float4 r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < n) r[k] = *(const float4*)(R + (ro.rev ? n - 1 - k0 - k : k0 + k) * VK);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < n) {
+                const float w = ro.rev && k0 + k == 0 ? tail : step;
+                s = make_float4(fmaf(w, s.x, r[k].x), fmaf(w, s.y, r[k].y), fmaf(w, s.z, r[k].z),
+                                fmaf(w, s.w, r[k].w));
+                *(float4*)(R + (ro.rev ? n - 1 - k0 - k : k0 + k) * VK) = s;
+            }
     }
 }
 
@@ -342,10 +365,14 @@ cudaError_t launch_decode_t(const LaDims& d, const void* q, const void* k, const
 }  // namespace
 
 cudaError_t launch_la_states(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st) {
-    return ty == InType::BF16 ? launch_la_states_tc(d, roles, st) : launch_width<float, false>(d, roles, st);
+    return ty == InType::BF16 ? launch_la_states_tc(d, roles, st) : launch_width<false>(d, roles, st);
+}
+cudaError_t launch_la_link(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
+    const int64_t threads = d.NS() * d.K * d.V / 4;
+    return launch_dependent(la_link_kernel, dim3((unsigned)((threads + 255) / 256), roles.n), 256, 0, st, d, roles);
 }
 cudaError_t launch_la_scan(const LaDims& d, InType ty, const LaRoles& roles, cudaStream_t st) {
-    return ty == InType::BF16 ? launch_la_scan_tc(d, roles, st) : launch_width<float, true>(d, roles, st);
+    return ty == InType::BF16 ? launch_la_scan_tc(d, roles, st) : launch_width<true>(d, roles, st);
 }
 
 cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const void* k, const void* v, int64_t sq,
@@ -354,16 +381,49 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
                               : launch_decode_t<float>(d, q, k, v, sq, sk, sv, state, o, st);
 }
 
-// Segments: as many as it takes to give every SM a CTA of the call's `roles` scans, of
-// whole 128-token tiles, and at most kLaMaxSeg, since a segment reads every earlier
-// segment's sum.
-void la_segments(LaDims* d, int roles) {
-    const int64_t tiles = (d->T + 127) / 128, streams = d->NS() * roles;
-    int64_t n = streams > 0 ? sm_count() / streams : 1;
-    if (n > tiles) n = tiles;
-    if (n > kLaMaxSeg) n = kLaMaxSeg;
-    if (n < 1) n = 1;
-    const int64_t per = (tiles + n - 1) / n;
+// How a call cuts its sequences, in whole 128-token tiles: the cut with the least
+// estimated time, in units of a tile of the scan.  A CTA takes its tiles one after the
+// other behind a fixed part (launch, first loads, the state that enters); the CTAs go in
+// waves of one per SM; with several segments the sums (0.6 of a tile each) and the link
+// come first.  The backward's three scans want fewer segments than the forward's one;
+// but cut like the forward's it can take over the forward's sums (`saved`).
+namespace {
+constexpr double kScanFixed = 4, kSumFixed = 3, kSumTile = 0.6, kLinkFixed = 1.5;
+
+double cut_cost(int64_t streams, int64_t tiles, int64_t per, int scans, int sums) {
+    const int64_t nseg = (tiles + per - 1) / per, sms = sm_count();
+    auto waves = [&](int64_t ctas) { return (double)((ctas + sms - 1) / sms); };
+    double t = waves(streams * scans * nseg) * (per + kScanFixed);
+    if (nseg > 1) t += waves(streams * sums * (nseg - 1)) * (kSumTile * per + kSumFixed) + kLinkFixed;
+    return t;
+}
+
+// The best number of tiles a segment, and its cost.
+int64_t best_cut(int64_t streams, int64_t tiles, int scans, int sums, double* cost) {
+    int64_t best = tiles;
+    *cost = cut_cost(streams, tiles, tiles, scans, sums);
+    const int64_t most = streams * scans < sm_count() ? 2 * sm_count() / (streams * scans) : 1;
+    for (int64_t n = 2; n <= most && n <= tiles; ++n) {
+        const int64_t per = (tiles + n - 1) / n;
+        const double c = cut_cost(streams, tiles, per, scans, sums);
+        if (c < *cost) best = per, *cost = c;
+    }
+    return best;
+}
+}  // namespace
+
+void la_segments(LaDims* d, bool bwd) {
+    const int64_t tiles = (d->T + 127) / 128, streams = d->NS();
+    int64_t per = tiles;
+    if (streams > 0 && tiles > 1) {
+        double cf, cb;
+        per = best_cut(streams, tiles, 1, 1, &cf);
+        if (bwd) {
+            const double shared = cut_cost(streams, tiles, per, 3, 1);
+            const int64_t own = best_cut(streams, tiles, 3, 2, &cb);
+            if (cb < shared) per = own;
+        }
+    }
     d->L = (int)(per * 128);
     d->nseg = tiles ? (int)((tiles + per - 1) / per) : 1;
 }

@@ -191,6 +191,16 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     const LaRole& ro = w.ro;
     const int Db = ro.Db, Dc = ro.Dc, tiles = w.tiles;
     float *upd = (float*)(sm + SS_UPD), *pw = (float*)(sm + SS_POW);
+    const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
+    auto load = [&](int it) {
+        unsigned char* st = sm + (it % SS_STAGES) * 2 * kTileBytes;
+        uint64_t* f = &bar.full[it % SS_STAGES];
+        mbar_arrive_expect_tx(f, (uint32_t)((nb + nc) * (kTileBytes / 2)));
+        for (int i = 0; i < nb; ++i)
+            tma_load_4d(st + i * (kTileBytes / 2), &maps.b[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
+        for (int i = 0; i < nc; ++i)
+            tma_load_4d(st + kTileBytes + i * (kTileBytes / 2), &maps.c[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
+    };
     if (warp == kMmaWarp) {
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
@@ -199,7 +209,10 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         for (int i = 0; i < 2; ++i) mbar_init(&bar.cv[i], 512), mbar_init(&bar.u[i], 1);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
+        fence_proxy_async();
+        for (int i = 0; i < SS_STAGES && i < tiles; ++i) load(i);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = tid; e <= kTile; e += kThreads) pw[e] = power(w.g, (float)e);
     fill_weights(w, upd);
     fence_before_sync();
@@ -211,20 +224,9 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
-            auto load = [&](int it) {
-                unsigned char* st = sm + (it % SS_STAGES) * 2 * kTileBytes;
-                uint64_t* f = &bar.full[it % SS_STAGES];
-                mbar_arrive_expect_tx(f, (uint32_t)((nb + nc) * (kTileBytes / 2)));
-                for (int i = 0; i < nb; ++i)
-                    tma_load_4d(st + i * (kTileBytes / 2), &maps.b[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
-                for (int i = 0; i < nc; ++i)
-                    tma_load_4d(st + kTileBytes + i * (kTileBytes / 2), &maps.c[w.rl], f, 64 * i, w.h, w.t0(it), w.b);
-            };
-            int issued = 0;
+            int issued = min(SS_STAGES, tiles);
             for (; issued < tiles; ++issued) {
-                if (issued >= SS_STAGES && !mbar_wait(&bar.free[issued % SS_STAGES], (issued / SS_STAGES - 1) & 1,
-                                                      d.err, kErrTma, d.wait_ns))
+                if (!mbar_wait(&bar.free[issued % SS_STAGES], (issued / SS_STAGES - 1) & 1, d.err, kErrTma, d.wait_ns))
                     break;
                 load(issued);
             }
@@ -340,35 +342,26 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
 #pragma unroll
     for (int i = 0; i < 64; ++i) m[i] = 0.f;
     const int64_t VK = (int64_t)ro.Db * ro.Dc;
-    auto add = [&](const float* src, float f) {
-        if (c >= ro.Dc) return;
+    bool ok = make(0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the linked states
+    const bool first = w.seg == (w.rev ? d.nseg - 1 : 0);
+    const float* src = first ? (ro.m0 ? ro.m0 + w.stream * VK : nullptr)
+                             : ro.R + (w.stream * (d.nseg - 1) + (w.rev ? w.seg : w.seg - 1)) * VK;
+    if (src && c < ro.Dc) {
         src += (int64_t)c * ro.m_sc + b0 * ro.m_sb;
 #pragma unroll
-        for (int i = 0; i < 64; i += 16) {
+        for (int i = 0; i < 64; i += 4) {
             if (i < cols) {
-                float x[16];
+                if (ro.m_sb == 1) {
+                    const float4 v = *(const float4*)(src + i);
+                    m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    if (ro.m_sb == 1) {
-                        const float4 v = *(const float4*)(src + i + j);
-                        x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[j + e] = src[(i + j + e) * ro.m_sb];
-                    }
+                    for (int e = 0; e < 4; ++e) m[i + e] = src[(i + e) * ro.m_sb];
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) m[i + j] = fmaf(f, x[j], m[i + j]);
             }
         }
-    };
-    bool ok = make(0);
-    if (ro.m0) add(ro.m0 + w.stream * VK, power(w.g, (float)(w.rev ? d.T - w.t_hi : w.t_lo)));
-    const float* R = ro.R + w.stream * (d.nseg - 1) * VK;
-    if (!w.rev)
-        for (int i = 0; i < w.seg; ++i) add(R + i * VK, power(w.g, (float)(w.t_lo - (i + 1) * d.L)));
-    else
-        for (int i = d.nseg - 1; i > w.seg; --i) add(R + (i - 1) * VK, power(w.g, (float)(i * d.L - w.t_hi)));
+    }
     auto put_state = [&] {  // M's bf16 copy, for A M^T
 #pragma unroll
         for (int i = 0; i < 64; i += 16) {
@@ -510,6 +503,18 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     const Part w(d, roles, false);
     const LaRole& ro = w.ro;
     const int Db = ro.Db, Dc = ro.Dc, tiles = w.tiles, rev = w.rev;
+    const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
+    auto stage = [&](int it) { return sm + (it & 1) * 3 * kTileBytes; };
+    auto load = [&](int it, const CUtensorMap* map, int blocks, unsigned char* to) {
+        for (int i = 0; i < blocks; ++i)
+            tma_load_4d(to + i * (kTileBytes / 2), map, &bar.full[it & 1], 64 * i, w.h, w.t0(it), w.b);
+    };
+    auto load_a = [&](int it) { load(it, &maps.a[w.rl], nb, stage(it)); };
+    auto load_bc = [&](int it) {
+        mbar_arrive_expect_tx(&bar.full[it & 1], (uint32_t)((2 * nb + nc) * (kTileBytes / 2)));
+        load(it, &maps.b[w.rl], nb, stage(it) + kTileBytes);
+        load(it, &maps.c[w.rl], nc, stage(it) + 2 * kTileBytes);
+    };
 
     if (warp == kMmaWarp) {
         tmem_alloc(&bar.tmem, 512);
@@ -531,6 +536,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         mbar_init(&bar.x, 256);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
+        fence_proxy_async();
+        for (int i = 0; i < 2 && i < tiles; ++i) load_bc(i), load_a(i);
     }
     for (int e = tid; e <= kTile; e += kThreads) sPow[e] = power(w.g, (float)e);
     for (int i = tid; i < 63; i += kThreads) {
@@ -546,23 +553,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
-            auto stage = [&](int it) { return sm + (it & 1) * 3 * kTileBytes; };
-            auto load = [&](int it, const CUtensorMap* map, int blocks, unsigned char* to) {
-                for (int i = 0; i < blocks; ++i)
-                    tma_load_4d(to + i * (kTileBytes / 2), map, &bar.full[it & 1], 64 * i, w.h, w.t0(it), w.b);
-            };
-            auto load_bc = [&](int it) {
-                mbar_arrive_expect_tx(&bar.full[it & 1], (uint32_t)((2 * nb + nc) * (kTileBytes / 2)));
-                load(it, &maps.b[w.rl], nb, stage(it) + kTileBytes);
-                load(it, &maps.c[w.rl], nc, stage(it) + 2 * kTileBytes);
-            };
-            int issued = 0;  // tiles whose loads are all issued
+            int issued = min(2, tiles);  // tiles whose loads are all issued
             bool half = false;
-            for (; issued < 2 && issued < tiles; ++issued) {
-                load_bc(issued);
-                load(issued, &maps.a[w.rl], nb, stage(issued));
-            }
             for (int it = 0; it < tiles; ++it) {
                 if (issued < tiles) {
                     if (!mbar_wait(&bar.free[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
@@ -575,13 +567,13 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
                 bulk_commit();
                 if (issued < tiles) {
                     bulk_wait_read0();
-                    load(issued, &maps.a[w.rl], nb, stage(issued));
+                    load_a(issued);
                     half = false;
                     ++issued;
                 }
             }
             // no copy outlives the CTA: a tile whose A was not asked for gets it now
-            if (half) load(issued, &maps.a[w.rl], nb, stage(issued)), ++issued;
+            if (half) load_a(issued), ++issued;
             for (int i = max(0, issued - 2); i < issued; ++i)
                 mbar_wait(&bar.full[i & 1], (i >> 1) & 1, d.err, kErrDrain);
             bulk_wait0();
@@ -689,7 +681,9 @@ cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_
     if (!make_maps(d, roles, true, &maps)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(la_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SIZE);
     if (e != cudaSuccess) return e;
-    la_scan_kernel<<<dim3((unsigned)(d.NS() * d.nseg), roles.n), kThreads, S_SIZE, st>>>(d, roles, maps);
+    const dim3 grid((unsigned)(d.NS() * d.nseg), roles.n);
+    if (d.nseg > 1) return launch_dependent(la_scan_kernel, grid, kThreads, S_SIZE, st, d, roles, maps);
+    la_scan_kernel<<<grid, kThreads, S_SIZE, st>>>(d, roles, maps);
     return cudaGetLastError();
 }
 
