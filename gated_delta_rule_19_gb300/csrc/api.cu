@@ -1905,7 +1905,7 @@ gdn_status rope_problem(const gdn_rope_problem* p, gdn::RopeCall* c) {
     c->rows = (int)p->table_rows;
     c->eps = p->eps;
     c->interleaved = p->interleaved != 0;
-    c->blocks = gdn::rows_bwd_blocks(c->tokens * (p->Hq > p->Hk ? p->Hq : p->Hk));
+    c->blocks = gdn::rows_bwd_blocks(c->tokens * (p->Hq > p->Hk ? p->Hq : p->Hk), gdn::kRopeBwdPerSm);
     return GDN_OK;
 }
 
@@ -1936,7 +1936,7 @@ gdn_status gated_problem(const gdn_gated_norm_problem* p, gdn::GatedCall* c) {
     c->H = (int)p->H;
     c->D = (int)p->D;
     c->eps = p->eps;
-    c->blocks = gdn::rows_bwd_blocks(c->rows);
+    c->blocks = gdn::rows_bwd_blocks(c->rows, gdn::kGatedBwdPerSm);
     return GDN_OK;
 }
 

@@ -7,9 +7,7 @@
 //   y = xh w act
 //   dw = sum over rows of dy act xh,   dz = dy xh w (sg + act (1 - sg)),
 //   dx = r (t - xh mean(t xh)),  t = dy act w.
-// A group of lanes holds a row (rows.cuh: two neighbouring 16-byte pieces a lane) and
-// takes kRows rows at a time, all their loads in flight together.  Bound by reading
-// and writing the rows.
+// A group of lanes holds a row (rows.cuh: lane u has pieces u and u + D/(2 VEC)).
 
 #include "gdn_internal.h"
 #include "rows.cuh"
@@ -19,8 +17,6 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 256;
-
 struct GatedDims {
     int64_t rows;
     int H, D;
@@ -28,129 +24,156 @@ struct GatedDims {
     float eps;
 };
 
+// Stages of the ring, and blocks per SM: the backward's registers leave room for two.
+// (At 100 MB of rows: forward 2 stages in 4 blocks 25.8 us, 3 in 3 26.2; backward 2
+// stages 51.9, 3 53.8, 4 54.5.)
+constexpr int kStages = 2, kFwdPerSm = 4;
+using FwdRing = Ring<4, kStages>;
+using BwdRing = Ring<6, kStages>;
+
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kFwdPerSm)
 gated_norm_fwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ w,
                       T* __restrict__ y) {
-    constexpr int VEC = kVec<T>, kRows = 4;
-    const int c0 = (threadIdx.x % G) * 2 * VEC;
-    const bool live = c0 < d.D;
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G) * kRows;
-    uint4 xr[kRows][2], zr[kRows][2];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t row = first + i;
-        xr[i][0] = xr[i][1] = zr[i][0] = zr[i][1] = make_uint4(0, 0, 0, 0);
-        if (live && row < d.rows) {
-            const int64_t tok = row / d.H;
-            const int off = (int)(row - tok * d.H) * d.D + c0;
-            const T* xp = x + tok * d.x_stride + off;
-            const T* zp = z + tok * d.z_stride + off;
-            xr[i][0] = lds16(xp), xr[i][1] = lds16(xp + VEC);
-            zr[i][0] = lds16(zp), zr[i][1] = lds16(zp + VEC);
-        }
-    }
-    float wv[2][VEC];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) get(live ? ldg16(w + c0 + p * VEC) : make_uint4(0, 0, 0, 0), wv[p]);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        float xv[2][VEC], ss = 0.f;
+    constexpr int VEC = kVec<T>, S = kStages;
+    extern __shared__ __align__(16) unsigned char sm[];
+    const FwdRing ring(sm);
+    const float inv_d = 1.f / d.D;
+    const int c0 = (threadIdx.x % G) * VEC, half = d.D / 2;
+    const bool live = c0 < half;
+    const int64_t per = kThreads / G, step = (int64_t)gridDim.x * per, base = (int64_t)blockIdx.x * per;
+    const int64_t turns = (d.rows - base + step - 1) / step;
+    int64_t now = base + threadIdx.x / G, next = now;
+    Walk ahead(next, step, d.H);  // (token, head) of the row copied
+    auto issue = [&](int slot) {
+        const bool on = live && next < d.rows;
+        const int off = ahead.lo * d.D + c0;
+        const T* xp = x + ahead.hi * d.x_stride + off;
+        const T* zp = z + ahead.hi * d.z_stride + off;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            get(xr[i][p], xv[p]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(xv[p][j], xv[p][j], ss);
+            ring.copy(slot, p, xp + p * half, on);
+            ring.copy(slot, 2 + p, zp + p * half, on);
         }
-        const float r = rsqrtf(group_sum<G>(ss) / d.D + d.eps);
-        const int64_t row = first + i;
+        ring.commit();
+        ahead.move();
+        next += step;
+    };
+    uint64_t wv[2][VEC / 2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) get(live ? ldg16(w + c0 + p * half) : make_uint4(0, 0, 0, 0), wv[p]);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i);
+    // every lane of the block takes the same number of turns, so the row sums are whole
+    for (int slot = 0, fill = S - 1, left = (int)turns; left > 0; --left, slot = ring.after(slot), now += step) {
+        issue(fill);
+        fill = ring.after(fill);
+        ring.wait();
+        uint64_t xv[2][VEC / 2], ss = twice(0.f);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            float zv[VEC];
-            get(zr[i][p], zv);
+            get(ring.get(slot, p), xv[p]);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float act = __fdividef(zv[j], 1.f + expf(-zv[j]));
-                xv[p][j] = xv[p][j] * r * wv[p][j] * act;
-            }
-            if (live && row < d.rows) sts16(y + row * d.D + c0 + p * VEC, put(xv[p]));
+            for (int j = 0; j < VEC / 2; ++j) ss = fma2(xv[p][j], xv[p][j], ss);
+        }
+        const uint64_t r = twice(rsqrtf(fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps)));
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            uint64_t zv[VEC / 2];
+            get(ring.get(slot, 2 + p), zv);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j)
+                xv[p][j] = mul2(mul2(mul2(xv[p][j], r), wv[p][j]), mul2(zv[j], sigmoid2(zv[j])));
+            if (live && now < d.rows) sts16(y + now * d.D + c0 + p * half, put(xv[p]));
         }
     }
+    ring.wait_all();  // no copy outlives the block
 }
 
-// Persistent blocks; each leaves one row of column sums in part [gridDim.x][D].
+// Each block leaves one row of column sums in part [gridDim.x][D].
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kGatedBwdPerSm)
 gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ w,
                       const T* __restrict__ dy, T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ part) {
-    constexpr int VEC = kVec<T>, kRows = 2;
-    extern __shared__ float sm[];  // [8 warps][D]
-    const int c0 = (threadIdx.x % G) * 2 * VEC;
-    const bool live = c0 < d.D;
-    float wv[2][VEC], acc[2 * VEC];
+    constexpr int VEC = kVec<T>, S = kStages;
+    extern __shared__ __align__(16) unsigned char sm[];
+    const BwdRing ring(sm);
+    const float inv_d = 1.f / d.D;
+    const int c0 = (threadIdx.x % G) * VEC, half = d.D / 2;
+    const bool live = c0 < half;
+    uint64_t wv[2][VEC / 2], acc[VEC];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) get(live ? ldg16(w + c0 + p * VEC) : make_uint4(0, 0, 0, 0), wv[p]);
+    for (int p = 0; p < 2; ++p) get(live ? ldg16(w + c0 + p * half) : make_uint4(0, 0, 0, 0), wv[p]);
 #pragma unroll
-    for (int j = 0; j < 2 * VEC; ++j) acc[j] = 0.f;
-    const int64_t per = (kThreads / G) * kRows, step = (int64_t)gridDim.x * per;
-    for (int64_t base = (int64_t)blockIdx.x * per; base < d.rows; base += step) {
-        const int64_t first = base + (threadIdx.x / G) * kRows;
-        uint4 xr[kRows][2], zr[kRows][2], yr[kRows][2];
+    for (int j = 0; j < VEC; ++j) acc[j] = twice(0.f);
+    const int64_t per = kThreads / G, step = (int64_t)gridDim.x * per, base = (int64_t)blockIdx.x * per;
+    const int64_t turns = base < d.rows ? (d.rows - base + step - 1) / step : 0;
+    int64_t now = base + threadIdx.x / G, next = now;
+    Walk ahead(next, step, d.H);
+    auto issue = [&](int slot) {
+        const bool on = live && next < d.rows;
+        const int off = ahead.lo * d.D + c0;
+        const T* xp = x + ahead.hi * d.x_stride + off;
+        const T* zp = z + ahead.hi * d.z_stride + off;
+        const T* yp = dy + next * d.D + c0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t row = first + i;
+        for (int p = 0; p < 2; ++p) {
+            ring.copy(slot, p, xp + p * half, on);
+            ring.copy(slot, 2 + p, zp + p * half, on);
+            ring.copy(slot, 4 + p, yp + p * half, on);
+        }
+        ring.commit();
+        ahead.move();
+        next += step;
+    };
+    if (turns) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) xr[i][p] = zr[i][p] = yr[i][p] = make_uint4(0, 0, 0, 0);
-            if (live && row < d.rows) {
-                const int64_t tok = row / d.H;
-                const int off = (int)(row - tok * d.H) * d.D + c0;
+        for (int i = 0; i < S - 1; ++i) issue(i);
+    }
+    for (int slot = 0, fill = S - 1, left = (int)turns; left > 0; --left, slot = ring.after(slot), now += step) {
+        issue(fill);
+        fill = ring.after(fill);
+        ring.wait();
+        // with u = dy w, p = dy act x, sl = the slope of silu = sg (1 + z - act):
+        // t = u act, dz = r u x sl, dw += r p, t x = p w
+        uint64_t xv[2][VEC / 2], t[2][VEC / 2], gz[2][VEC / 2], pr[2][VEC / 2], ss = twice(0.f), tx = ss;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    xr[i][p] = lds16(x + tok * d.x_stride + off + p * VEC);
-                    zr[i][p] = lds16(z + tok * d.z_stride + off + p * VEC);
-                    yr[i][p] = lds16(dy + row * d.D + c0 + p * VEC);
-                }
+        for (int p = 0; p < 2; ++p) {
+            uint64_t zv[VEC / 2], yv[VEC / 2];
+            get(ring.get(slot, p), xv[p]);
+            get(ring.get(slot, 2 + p), zv);
+            get(ring.get(slot, 4 + p), yv);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                const uint64_t sg = sigmoid2(zv[j]), act = mul2(zv[j], sg), u = mul2(yv[j], wv[p][j]);
+                const uint64_t sl = mul2(sg, fma2(act, twice(-1.f), add2(zv[j], twice(1.f))));
+                gz[p][j] = mul2(mul2(u, xv[p][j]), sl);
+                t[p][j] = mul2(u, act);
+                pr[p][j] = mul2(mul2(yv[j], act), xv[p][j]);
+                ss = fma2(xv[p][j], xv[p][j], ss);
+                tx = fma2(pr[p][j], wv[p][j], tx);
             }
         }
+        const float r = rsqrtf(fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps));
+        // mean(t xh) = r mean(t x), times r of xh
+        const uint64_t m = twice(-group_sum<G>(sum2(tx)) * r * r * inv_d), r2 = twice(r);
+        const bool on = live && now < d.rows;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            float xv[2][VEC], t[2][VEC], gz[2][VEC], ss = 0.f, tx = 0.f;
+        for (int p = 0; p < 2; ++p) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float zv[VEC];
-                get(xr[i][p], xv[p]);
-                get(zr[i][p], zv);
-                get(yr[i][p], t[p]);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float sg = __fdividef(1.f, 1.f + expf(-zv[j])), act = zv[j] * sg;
-                    gz[p][j] = t[p][j] * wv[p][j] * xv[p][j] * (sg + act * (1.f - sg));
-                    t[p][j] *= act;
-                    ss = fmaf(xv[p][j], xv[p][j], ss);
-                    tx = fmaf(t[p][j] * wv[p][j], xv[p][j], tx);
-                }
+            for (int j = 0; j < VEC / 2; ++j) {
+                acc[p * (VEC / 2) + j] = fma2(pr[p][j], r2, acc[p * (VEC / 2) + j]);
+                gz[p][j] = mul2(gz[p][j], r2);
+                xv[p][j] = mul2(fma2(xv[p][j], m, t[p][j]), r2);
             }
-            ss = group_sum<G>(ss);
-            tx = group_sum<G>(tx);
-            const float r = rsqrtf(ss / d.D + d.eps);
-            const float m = tx * r * r / d.D;  // mean(t xh) = r mean(t x), times r of xh
-            const int64_t row = first + i;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    acc[p * VEC + j] = fmaf(t[p][j], xv[p][j] * r, acc[p * VEC + j]);
-                    gz[p][j] *= r;
-                    xv[p][j] = r * (t[p][j] * wv[p][j] - xv[p][j] * m);
-                }
-                if (live && row < d.rows) {
-                    sts16(dx + row * d.D + c0 + p * VEC, put(xv[p]));
-                    sts16(dz + row * d.D + c0 + p * VEC, put(gz[p]));
-                }
+            if (on) {
+                sts16(dx + now * d.D + c0 + p * half, put(xv[p]));
+                sts16(dz + now * d.D + c0 + p * half, put(gz[p]));
             }
         }
     }
-    block_columns<G, VEC, kThreads / 32>(acc, c0, c0 + VEC, live, d.D, sm, part + (int64_t)blockIdx.x * d.D);
+    ring.wait_all();  // the ring's memory serves the sums next
+    block_columns<G, VEC>(acc, c0, c0 + half, live, d.D, (float*)sm, part + (int64_t)blockIdx.x * d.D);
 }
 
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
@@ -163,6 +186,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 weight_sum_kernel(int blocks, int D, const float* __restrict__ part, T* __restrict__ dw0, T* __restrict__ dw1) {
     __shared__ float sm[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     const float* p = part + (int64_t)blockIdx.y * blocks * D;
     float s = 0.f;
@@ -181,10 +205,18 @@ template <typename T, int G>
 cudaError_t launch_g(const GatedCall& c, const GatedDims& d, bool bwd, cudaStream_t st) {
     const T *x = (const T*)c.x, *z = (const T*)c.z, *w = (const T*)c.w;
     if (!bwd) {
-        const int64_t per = (int64_t)(kThreads / G) * 4;
-        gated_norm_fwd_kernel<T, G><<<(unsigned)((d.rows + per - 1) / per), kThreads, 0, st>>>(d, x, z, w, (T*)c.y);
+        constexpr int smem = FwdRing::BYTES;
+        cudaError_t e = cudaFuncSetAttribute(gated_norm_fwd_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem);
+        if (e != cudaSuccess) return e;
+        gated_norm_fwd_kernel<T, G>
+            <<<(unsigned)blocks_for(d.rows, G, kFwdPerSm, sm_count()), kThreads, smem, st>>>(d, x, z, w, (T*)c.y);
     } else {
-        const size_t smem = (size_t)(kThreads / 32) * d.D * sizeof(float);
+        constexpr int smem = BwdRing::BYTES;
+        static_assert(smem >= (kThreads / 32) * 256 * 4, "the column sums fit the ring");
+        cudaError_t e = cudaFuncSetAttribute(gated_norm_bwd_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem);
+        if (e != cudaSuccess) return e;
         gated_norm_bwd_kernel<T, G>
             <<<c.blocks, kThreads, smem, st>>>(d, x, z, w, (const T*)c.dy, (T*)c.dx, (T*)c.dz, c.part);
     }
@@ -216,14 +248,15 @@ cudaError_t launch_weight_sum(int sides, int blocks, int D, InType ty, const flo
                               cudaStream_t st) {
     const dim3 grid((D + 31) / 32, sides);
     if (ty == InType::BF16)
-        weight_sum_kernel<<<grid, 256, 0, st>>>(blocks, D, part, (__nv_bfloat16*)dw0, (__nv_bfloat16*)dw1);
-    else weight_sum_kernel<<<grid, 256, 0, st>>>(blocks, D, part, (float*)dw0, (float*)dw1);
-    return cudaGetLastError();
+        return launch_dependent(weight_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, blocks, D, part,
+                                (__nv_bfloat16*)dw0, (__nv_bfloat16*)dw1);
+    return launch_dependent(weight_sum_kernel<float>, grid, 256, 0, st, blocks, D, part, (float*)dw0, (float*)dw1);
 }
 
-// Blocks of the backward kernels: a few per SM, never more than there is work for.
-int rows_bwd_blocks(int64_t rows) {
-    const int64_t cap = 4 * (int64_t)sm_count(), want = (rows + 63) / 64;
+// Blocks of the backward kernels: all that fit on the GPU at once, never more than there
+// is work for.
+int rows_bwd_blocks(int64_t rows, int per_sm) {
+    const int64_t cap = per_sm * (int64_t)sm_count(), want = (rows + 15) / 16;
     return (int)(want < 1 ? 1 : want < cap ? want : cap);
 }
 

@@ -410,6 +410,8 @@ cudaError_t launch_gated_norm(const GatedCall& c, InType ty, bool bwd, cudaStrea
 // dw of `sides` weights from their blocks' sums, in a fixed order.
 cudaError_t launch_weight_sum(int sides, int blocks, int D, InType ty, const float* part, void* dw0, void* dw1,
                               cudaStream_t st);
-int rows_bwd_blocks(int64_t rows);
+// Blocks of the two backward kernels (and rows of their partial sums).
+constexpr int kRopeBwdPerSm = 2, kGatedBwdPerSm = 2;
+int rows_bwd_blocks(int64_t rows, int per_sm);
 
 }  // namespace gdn

@@ -296,10 +296,65 @@ la_link_kernel(LaDims d, LaRoles roles) {
 
 // ------------------------------------------------------------ single tokens
 
+// N consecutive values (aligned to N elements) as floats, and N floats back.
+template <int N>
+__device__ __forceinline__ void ldn(const float* p, float (&f)[N]) {
+    if constexpr (N == 4) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+    } else if constexpr (N == 2) {
+        const float2 x = __ldcs(reinterpret_cast<const float2*>(p));
+        f[0] = x.x, f[1] = x.y;
+    } else {
+        f[0] = __ldcs(p);
+    }
+}
+template <int N>
+__device__ __forceinline__ void ldn(const __nv_bfloat16* p, float (&f)[N]) {
+    if constexpr (N == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        f[0] = __uint_as_float(x.x << 16), f[1] = __uint_as_float(x.x & 0xffff0000u);
+        f[2] = __uint_as_float(x.y << 16), f[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else if constexpr (N == 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        f[0] = __uint_as_float(x << 16), f[1] = __uint_as_float(x & 0xffff0000u);
+    } else {
+        f[0] = __bfloat162float(*p);
+    }
+}
+template <int N>
+__device__ __forceinline__ void stn(float* p, const float (&f)[N]) {
+    if constexpr (N == 4) __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    else if constexpr (N == 2) __stcs(reinterpret_cast<float2*>(p), make_float2(f[0], f[1]));
+    else __stcs(p, f[0]);
+}
+
 constexpr int kRows = 8;  // state rows of a warp
 
+// The sums over the warp of 8 values a lane; lane l receives that of row
+// (l / 16) * 4 + (l / 8 % 2) * 2 + l / 4 % 2: at each of the first three steps a lane
+// keeps half of its values and hands on the others, 9 exchanges instead of 40.
+__device__ __forceinline__ float sum_rows(const float (&v)[kRows], int lane) {
+    float a[4], b[2], c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+    }
+    const bool up = lane & 4;
+    c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
 // A warp holds kRows rows of one head's state in registers across the call's tokens,
-// lane l the K/32 columns from l K/32 on (K = 16: lanes 0-15, one column each).
+// lane l the K/32 columns from l K/32 on (K = 16: lanes 0-15, one column each).  Bound
+// by reading and writing the state once.
 template <typename T, int KPL>
 __global__ void __launch_bounds__(256)
 la_decode_kernel(LaDims d, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, int64_t sq,
@@ -311,44 +366,41 @@ la_decode_kernel(LaDims d, const T* __restrict__ q, const T* __restrict__ k, con
     const int v0 = (int)(unit % groups) * kRows, h = (int)(stream % d.H);
     const int64_t b = stream / d.H;
     const bool live = c0 < d.K;
-    const float gamma = expf(d.log_decay[h]);
     float* rows = state + (stream * d.V + v0) * d.K + c0;
     float S[kRows][KPL];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < kRows; ++r) {
+        if (live) ldn<KPL>(rows + r * d.K, S[r]);
+        else
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) S[r][i] = live ? rows[(int64_t)r * d.K + i] : 0.f;
+            for (int i = 0; i < KPL; ++i) S[r][i] = 0.f;
+    }
+    const float gamma = expf(d.log_decay[h]);
+    const int mine = (lane >> 4) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
     for (int t = 0; t < d.T; ++t) {
         const int64_t tok = b * d.T + t;
-        float kv[KPL], qv[KPL], red[kRows];
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) {
-            kv[i] = live ? (float)k[tok * sk + (int64_t)h * d.K + c0 + i] : 0.f;
-            qv[i] = live ? (float)q[tok * sq + (int64_t)h * d.K + c0 + i] : 0.f;
+        float kv[KPL] = {}, qv[KPL] = {}, vv[2][4], red[kRows];
+        if (live) {
+            ldn<KPL>(k + tok * sk + (int64_t)h * d.K + c0, kv);
+            ldn<KPL>(q + tok * sq + (int64_t)h * d.K + c0, qv);
         }
+        ldn<4>(v + tok * sv + (int64_t)h * d.V + v0, vv[0]);
+        ldn<4>(v + tok * sv + (int64_t)h * d.V + v0 + 4, vv[1]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const float vv = (float)v[tok * sv + (int64_t)h * d.V + v0 + r];
             red[r] = 0.f;
 #pragma unroll
             for (int i = 0; i < KPL; ++i) {
-                S[r][i] = fmaf(vv, kv[i], gamma * S[r][i]);
+                S[r][i] = fmaf(vv[r >> 2][r & 3], kv[i], gamma * S[r][i]);
                 red[r] = fmaf(S[r][i], qv[i], red[r]);
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) red[r] += __shfl_xor_sync(0xffffffffu, red[r], off);
         }
-        float mine = 0.f;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (lane == r) mine = red[r];
-        if (lane < kRows) st1(o + (tok * d.H + h) * d.V + v0 + lane, mine);
+        const float sum = sum_rows(red, lane);
+        if ((lane & 3) == 0) st1(o + (tok * d.H + h) * d.V + v0 + mine, sum);
     }
     if (live)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int i = 0; i < KPL; ++i) rows[(int64_t)r * d.K + i] = S[r][i];
+        for (int r = 0; r < kRows; ++r) stn<KPL>(rows + r * d.K, S[r]);
 }
 
 template <typename T>

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
+
 namespace gdn {
 namespace tc {
 
@@ -365,26 +367,6 @@ __device__ __forceinline__ uint64_t desc_kmaj(uint32_t base, int R, int s) {
 }
 __device__ __forceinline__ uint64_t desc_mnmaj(uint32_t base, int R, int s) {
     return sdesc(base + (uint32_t)s * 2048u, (uint32_t)R * 128u, 1024, SW_128B);
-}
-
-// Two float32 operations in one instruction (f32x2: the pair in a 64-bit register).
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 
 // True in one lane of a converged warp, the same one at every call.
