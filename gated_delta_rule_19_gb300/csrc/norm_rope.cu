@@ -69,10 +69,10 @@ __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, con
         const int p = p0 + k * (VEC / 4);
         if (!kInter) {
 #pragma unroll
-            for (int j = 0; j < VEC / 4; ++j) ring.copy(slot, p + j, f + 4 * j, true);
+            for (int j = 0; j < VEC / 4; ++j) ring.copy_shared(slot, p + j, f + 4 * j);
         } else if (VEC == 8) {
-            ring.copy(slot, p, f, true);
-            ring.copy(slot, p + VEC / 4 - 1, f + d.R / 4, true);
+            ring.copy_shared(slot, p, f);
+            ring.copy_shared(slot, p + VEC / 4 - 1, f + d.R / 4);
         } else {
             ring.copy8(slot, p, 0, f);
             ring.copy8(slot, p, 1, f + d.R / 4);
@@ -140,8 +140,11 @@ __device__ __forceinline__ Slot slot_of(const RopeDims& d, int u) {
     return s;
 }
 
-// Heads of an item, and stages of the ring: what two blocks of an SM hold.
-constexpr int kFwdHeads = 4, kFwdStages = 2, kBwdHeads = 2, kBwdStages = 2;
+// Heads of an item, and stages of the ring: what two blocks of an SM hold.  (B8 T4096,
+// 6 + 6 heads of 128, bf16: forward 3 heads 37.5 us, 4 39.8, 6 40.8; backward 2 heads
+// 56.5, 3 66.6.  The angles come through L1, as the blocks of a token's heads share
+// them: 41.6 and 61.3 us past it.)
+constexpr int kFwdHeads = 3, kFwdStages = 2, kBwdHeads = 2, kBwdStages = 2;
 template <typename T>
 using FwdRing = Ring<2 * kFwdHeads + kVec<T> / 2, kFwdStages>;
 template <typename T>

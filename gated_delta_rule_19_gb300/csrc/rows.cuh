@@ -83,6 +83,10 @@ struct Ring {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(slot, piece)), "l"(src), "r"(on ? 16 : 0)
                      : "memory");
     }
+    // through L1, for what the block's other groups read too
+    __device__ __forceinline__ void copy_shared(int slot, int piece, const void* src) const {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at(slot, piece)), "l"(src) : "memory");
+    }
     // 8 bytes at a time, to the piece's half `half`
     __device__ __forceinline__ void copy8(int slot, int piece, int half, const void* src) const {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at(slot, piece) + 8 * half), "l"(src) : "memory");
