@@ -1690,7 +1690,7 @@ gdn_status la_problem(const gdn_la_problem* p, LaCall* c, bool bwd) {
     c->d.K = (int)p->K;
     c->d.V = (int)p->V;
     c->d.wait_ns = g_wait_limit_ns;
-    gdn::la_segments(&c->d, bwd);
+    gdn::la_segments(&c->d, elem_type(p->dtype), bwd);
     c->tokens = p->B * p->T;
     c->state = (size_t)c->d.NS() * p->V * p->K;
     c->sums = c->state * (c->d.nseg - 1);

@@ -324,7 +324,7 @@ struct LaDims {
     int* err = nullptr;      // the workspace's error word
     __host__ __device__ int64_t NS() const { return (int64_t)B * H; }
 };
-void la_segments(LaDims* d, bool bwd);
+void la_segments(LaDims* d, InType ty, bool bwd);
 
 // One scan (see la.cu): out_r = sum of gamma^|r-s| (a_r . b_s) c_s, a and b of Db columns,
 // c and out of Dc; token strides in elements (out is dense).  M's element (c, b) is at

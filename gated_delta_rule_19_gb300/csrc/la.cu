@@ -19,12 +19,12 @@
 
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void st1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -33,26 +33,32 @@ __device__ __forceinline__ float power(float g, float e) { return e > 0.f ? expf
 
 constexpr int kTok = 64;  // tokens of a chunk
 
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
 // Shared memory of the chunk kernel, in floats: rows of D (or 64) padded by four so
-// that the float4 reads of neighbouring rows fall into different banks.
+// that the float4 reads of neighbouring rows fall into different banks; two buffers of
+// A, B, C, so that a chunk is loaded while the one before it is worked on.
 template <int D>
 struct Smem {
     static constexpr int CS = D < 64 ? D : 64;  // columns of c that one CTA carries
     static constexpr int RA = D + 4, RC = CS + 4, RP = kTok + 4;
-    static constexpr int A = 0, B = A + kTok * RA, C = B + kTok * RA, M = C + kTok * RC, P = M + D * RC,
-                         W = P + kTok * RP, SIZE = W + kTok + 8;
+    static constexpr int A = 0, B = A + kTok * RA, C = B + kTok * RA, BUF = C + kTok * RC;
+    static constexpr int M = 2 * BUF, P = M + D * RC, W = P + kTok * RP, SIZE = W + kTok + 8;
 };
+static_assert(Smem<128>::SIZE * 4 <= 232448, "shared memory of one CTA");
 
 // One CTA: one (stream, segment), CS columns of c, one role.  256 threads as 16 x 16:
-// thread (ty, tx) has rows 4 ty .. 4 ty + 3 and columns 4 (tx) .. of each product, and
-// M's rows ty, ty + 16, ... in registers; a copy in shared memory feeds A M^T.
+// thread (ty, tx) has rows 4 ty .. 4 ty + 3 and CS / 16 columns of each product, and in
+// registers M's rows (b) BV ty .. of every 16 BV; a copy in shared memory feeds A M^T.
+// The products run on pairs of columns (f32x2), which leaves issue slots for the reads.
 template <int D, bool kOut>
 __global__ void __launch_bounds__(256)
 la_chunk_kernel(LaDims d, LaRoles roles) {
     using L = Smem<D>;
-    constexpr int CT = L::CS / 16, BT = D / 16;  // columns of c, rows of b per thread
+    constexpr int CT = L::CS / 16, CP = (CT + 1) / 2;  // columns of c per thread, pairs of them
+    constexpr int BV = D < 64 ? D / 16 : 4, BG = D / (16 * BV);  // rows of b per thread: BG groups of BV
     extern __shared__ __align__(16) float sm[];
-    float *sA = sm + L::A, *sB = sm + L::B, *sC = sm + L::C, *sM = sm + L::M, *sP = sm + L::P, *sW = sm + L::W;
+    float *sM = sm + L::M, *sP = sm + L::P, *sW = sm + L::W;
     const LaRole& ro = roles.r[blockIdx.z];
     const int c0 = blockIdx.y * L::CS;
     if (c0 >= ro.Dc) return;
@@ -64,163 +70,211 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     const int b = (int)(stream / d.H), h = (int)(stream % d.H);
     const float g = d.log_decay[h];
     const int t_lo = seg * d.L, t_hi = min(d.T, t_lo + d.L);
+    const int chunks = (t_hi - t_lo + kTok - 1) / kTok;
     for (int e = tid; e <= kTok; e += 256) sW[e] = power(g, (float)e);
-
-    // The state that enters: M[c][b] of the caller's [V, K] matrices by strides.
-    float m[BT][CT];
-#pragma unroll
-    for (int i = 0; i < BT; ++i)
-#pragma unroll
-        for (int j = 0; j < CT; ++j) m[i][j] = 0.f;
-    if (kOut) {
-        const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
-        const int64_t VK = (int64_t)ro.Db * ro.Dc;
-        const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
-                                 : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
-        if (src) {
-#pragma unroll
-            for (int i = 0; i < BT; ++i)
-#pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    const int bb = ty + 16 * i, cc = c0 + tx * CT + j;
-                    if (bb < ro.Db && cc < ro.Dc) m[i][j] = src[cc * ro.m_sc + bb * ro.m_sb];
-                }
-        }
-    }
 
     const float* pa = (const float*)ro.a + (int64_t)b * d.T * ro.sa + (int64_t)h * ro.Db;
     const float* pb = (const float*)ro.b + (int64_t)b * d.T * ro.sb + (int64_t)h * ro.Db;
     const float* pc = (const float*)ro.c + (int64_t)b * d.T * ro.sc + (int64_t)h * ro.Dc + c0;
     float* po = (float*)ro.out + ((int64_t)b * d.T * d.H + h) * ro.Dc + c0;
     const int cw = min(L::CS, ro.Dc - c0);
-    const int chunks = (t_hi - t_lo + kTok - 1) / kTok;
-    for (int it = 0; it < chunks; ++it) {
-        const int t0 = t_lo + (ro.rev ? chunks - 1 - it : it) * kTok, n = min(kTok, t_hi - t0);
-        __syncthreads();
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = tid; i < kTok * (D / 4); i += 256) {
-            const int r = i / (D / 4), x = (i % (D / 4)) * 4;
-            const bool in = r < n && x < ro.Db;
-            if (kOut) *(float4*)(sA + r * L::RA + x) = in ? ld4(pa + (int64_t)(t0 + r) * ro.sa + x) : zero;
-            *(float4*)(sB + r * L::RA + x) = in ? ld4(pb + (int64_t)(t0 + r) * ro.sb + x) : zero;
-        }
-        for (int i = tid; i < kTok * (L::CS / 4); i += 256) {
-            const int r = i / (L::CS / 4), x = (i % (L::CS / 4)) * 4;
-            *(float4*)(sC + r * L::RC + x) = r < n && x < cw ? ld4(pc + (int64_t)(t0 + r) * ro.sc + x) : zero;
-        }
-        if (kOut) {
-#pragma unroll
-            for (int i = 0; i < BT; ++i)
-#pragma unroll
-                for (int j = 0; j < CT; ++j) sM[(ty + 16 * i) * L::RC + tx * CT + j] = m[i][j];
-        }
-        __syncthreads();
+    auto chunk_t0 = [&](int it) { return t_lo + (ro.rev ? chunks - 1 - it : it) * kTok; };
+    // rows past the sequence and columns past the tensors' are zeros
+    auto load = [&](int it) {
+        const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
+        float* buf = sm + (it & 1) * L::BUF;
+        auto rows = [&](float* to, int stride, const float* from, int64_t step, int width, int cols) {
+            for (int i = tid; i < kTok * (width / 4); i += 256) {
+                const int r = i / (width / 4), x = (i % (width / 4)) * 4;
+                const bool in = r < n && x < cols;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(to + r * stride + x)),
+                             "l"(in ? from + (int64_t)(t0 + r) * step + x : from), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+        };
+        if (kOut) rows(buf + L::A, L::RA, pa, ro.sa, D, ro.Db);
+        rows(buf + L::B, L::RA, pb, ro.sb, D, ro.Db);
+        rows(buf + L::C, L::RC, pc, ro.sc, L::CS, cw);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(0);
 
-        float acc[4][CT];
+    // The state that enters: M[c][b] of the caller's [V, K] matrices by strides.
+    auto row_b = [&](int gi, int i) { return gi * 16 * BV + ty * BV + i; };
+    uint64_t m[BG][BV][CP];
+#pragma unroll
+    for (int gi = 0; gi < BG; ++gi)
+#pragma unroll
+        for (int i = 0; i < BV; ++i)
+#pragma unroll
+            for (int j = 0; j < CP; ++j) m[gi][i][j] = twice(0.f);
+    // f(row of b, column of c, value) over this thread's part of M
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int gi = 0; gi < BG; ++gi)
+#pragma unroll
+            for (int i = 0; i < BV; ++i)
+#pragma unroll
+                for (int j = 0; j < CT; j += 2) {
+                    float x, y;
+                    unpair(m[gi][i][j / 2], x, y);
+                    const int bb = row_b(gi, i), cc = c0 + tx * CT + j;
+                    if (bb < ro.Db && cc < ro.Dc) f(bb, cc, x);
+                    if (CT > 1 && bb < ro.Db && cc + 1 < ro.Dc) f(bb, cc + 1, y);
+                    m[gi][i][j / 2] = pair(x, y);
+                }
+    };
+    if (kOut) {
+        const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
+        const int64_t VK = (int64_t)ro.Db * ro.Dc;
+        const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
+                                 : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
+        if (src) each([&](int bb, int cc, float& x) { x = src[cc * ro.m_sc + bb * ro.m_sb]; });
+    }
+
+    // this thread's CT columns of a row of C or M, as pairs
+    auto cols_of = [&](const float* row, uint64_t (&v)[CP]) {
+        if constexpr (CT == 4) {
+            const float4 x = lds4(row + tx * 4);
+            v[0] = pair(x.x, x.y), v[1] = pair(x.z, x.w);
+        } else if constexpr (CT == 2) {
+            const float2 x = *(const float2*)(row + tx * 2);
+            v[0] = pair(x.x, x.y);
+        } else {
+            v[0] = pair(row[tx], 0.f);
+        }
+    };
+    for (int it = 0; it < chunks; ++it) {
+        const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
+        const float *sA = sm + (it & 1) * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (kOut) {
-            // scores: rows 4 ty + i, columns tx + 16 j
-            float p[4][4] = {};
+#pragma unroll
+            for (int gi = 0; gi < BG; ++gi)
+#pragma unroll
+                for (int i = 0; i < BV; ++i)
+#pragma unroll
+                    for (int j = 0; j < CT; j += 2) {
+                        float x, y;
+                        unpair(m[gi][i][j / 2], x, y);
+                        float* to = sM + row_b(gi, i) * L::RC + tx * CT + j;
+                        to[0] = x;
+                        if (CT > 1) to[1] = y;
+                    }
+        }
+        __syncthreads();  // this chunk is there, the other buffer and P are free
+        if (it + 1 < chunks) load(it + 1);
+
+        uint64_t acc[4][CP];
+        if (kOut) {
+            // scores: rows 4 ty + i, columns tx + 16 j; pairs of the sum's terms
+            uint64_t p[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[i][j] = twice(0.f);
 #pragma unroll 4
             for (int x = 0; x < D; x += 4) {
-                float4 av[4], bv[4];
+                float4 av[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) av[i] = *(const float4*)(sA + (4 * ty + i) * L::RA + x);
+                for (int i = 0; i < 4; ++i) av[i] = lds4(sA + (4 * ty + i) * L::RA + x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bv[j] = *(const float4*)(sB + (tx + 16 * j) * L::RA + x);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 bv = lds4(sB + (tx + 16 * j) * L::RA + x);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[i][j] = fmaf(av[i].x, bv[j].x, p[i][j]);
-                        p[i][j] = fmaf(av[i].y, bv[j].y, p[i][j]);
-                        p[i][j] = fmaf(av[i].z, bv[j].z, p[i][j]);
-                        p[i][j] = fmaf(av[i].w, bv[j].w, p[i][j]);
+                    for (int i = 0; i < 4; ++i) {
+                        p[i][j] = fma2(pair(av[i].x, av[i].y), pair(bv.x, bv.y), p[i][j]);
+                        p[i][j] = fma2(pair(av[i].z, av[i].w), pair(bv.z, bv.w), p[i][j]);
                     }
+                }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = 4 * ty + i, s = tx + 16 * j, dist = ro.rev ? s - r : r - s;
-                    sP[r * L::RP + s] = dist >= 0 ? p[i][j] * sW[dist] : 0.f;
+                    sP[r * L::RP + s] = dist >= 0 ? sum2(p[i][j]) * sW[dist] : 0.f;
                 }
-            // A M^T from the state that entered the chunk
+            // rows times a matrix of CS columns: acc += X[4 ty + i][x] R[x][columns]
+            auto product = [&](const float* X, int rx, const float* R, int len) {
+#pragma unroll 2
+                for (int x = 0; x < len; x += 4) {
+                    float av[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = lds4(X + (4 * ty + i) * rx + x);
+                        av[i][0] = f.x, av[i][1] = f.y, av[i][2] = f.z, av[i][3] = f.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint64_t v[CP];
+                        cols_of(R + (x + e) * L::RC, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < CP; ++j) acc[i][j] = fma2(twice(av[i][e]), v[j], acc[i][j]);
+                    }
+                }
+            };
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < CT; ++j) acc[i][j] = 0.f;
-#pragma unroll 2
-            for (int x = 0; x < D; x += 4) {
-                float av[4][4], mv[4][CT];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = *(const float4*)(sA + (4 * ty + i) * L::RA + x);
-                    av[i][0] = f.x, av[i][1] = f.y, av[i][2] = f.z, av[i][3] = f.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) mv[e][j] = sM[(x + e) * L::RC + tx * CT + j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int j = 0; j < CT; ++j) acc[i][j] = fmaf(av[i][e], mv[e][j], acc[i][j]);
-            }
+                for (int j = 0; j < CP; ++j) acc[i][j] = twice(0.f);
+            product(sA, L::RA, sM, D);  // A M^T, the state that entered the chunk
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 4 * ty + i, e = ro.rev ? n - 1 - r : r + 1;
-                const float w = sW[max(e, 0)];
+                const uint64_t w = twice(sW[max(e, 0)]);
 #pragma unroll
-                for (int j = 0; j < CT; ++j) acc[i][j] *= w;
+                for (int j = 0; j < CP; ++j) acc[i][j] = mul2(acc[i][j], w);
             }
             __syncthreads();
-#pragma unroll 2
-            for (int s = 0; s < kTok; s += 4) {
-                float pv[4][4], cv[4][CT];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = *(const float4*)(sP + (4 * ty + i) * L::RP + s);
-                    pv[i][0] = f.x, pv[i][1] = f.y, pv[i][2] = f.z, pv[i][3] = f.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) cv[e][j] = sC[(s + e) * L::RC + tx * CT + j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int j = 0; j < CT; ++j) acc[i][j] = fmaf(pv[i][e], cv[e][j], acc[i][j]);
-            }
+            product(sP, L::RP, sC, kTok);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 4 * ty + i;
+                float* to = po + (int64_t)(t0 + r) * d.H * ro.Dc + tx * CT;
+                float f[2 * CP];
 #pragma unroll
-                for (int j = 0; j < CT; ++j)
-                    if (r < n && tx * CT + j < cw)
-                        po[(int64_t)(t0 + r) * d.H * ro.Dc + tx * CT + j] = acc[i][j];
+                for (int j = 0; j < CP; ++j) unpair(acc[i][j], f[2 * j], f[2 * j + 1]);
+                if (r < n && tx * CT < cw) {
+                    if constexpr (CT == 4) *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
+                    else if constexpr (CT == 2) *(float2*)to = make_float2(f[0], f[1]);
+                    else to[0] = f[0];
+                }
             }
         }
         // M <- gamma^n M + sum of gamma^(n-1-rho+rev) b c^T
-        const float gn = sW[n];
+        const uint64_t gn = twice(sW[n]);
 #pragma unroll
-        for (int i = 0; i < BT; ++i)
+        for (int gi = 0; gi < BG; ++gi)
 #pragma unroll
-            for (int j = 0; j < CT; ++j) m[i][j] *= gn;
-#pragma unroll 2
+            for (int i = 0; i < BV; ++i)
+#pragma unroll
+                for (int j = 0; j < CP; ++j) m[gi][i][j] = mul2(m[gi][i][j], gn);
+#pragma unroll 4
         for (int s = 0; s < n; ++s) {
-            const float w = sW[ro.rev ? s + 1 : n - 1 - s];
-            float cv[CT];
+            const uint64_t w = twice(sW[ro.rev ? s + 1 : n - 1 - s]);
+            uint64_t v[CP];
+            cols_of(sC + s * L::RC, v);
 #pragma unroll
-            for (int j = 0; j < CT; ++j) cv[j] = w * sC[s * L::RC + tx * CT + j];
+            for (int j = 0; j < CP; ++j) v[j] = mul2(v[j], w);
 #pragma unroll
-            for (int i = 0; i < BT; ++i) {
-                const float bv = sB[s * L::RA + ty + 16 * i];
+            for (int gi = 0; gi < BG; ++gi) {
+                float bv[BV];
+                const float* row = sB + s * L::RA + row_b(gi, 0);
+                if constexpr (BV == 4) {
+                    const float4 x = lds4(row);
+                    bv[0] = x.x, bv[1] = x.y, bv[2] = x.z, bv[3] = x.w;
+                } else {
 #pragma unroll
-                for (int j = 0; j < CT; ++j) m[i][j] = fmaf(bv, cv[j], m[i][j]);
+                    for (int i = 0; i < BV; ++i) bv[i] = row[i];
+                }
+#pragma unroll
+                for (int i = 0; i < BV; ++i)
+#pragma unroll
+                    for (int j = 0; j < CP; ++j) m[gi][i][j] = fma2(twice(bv[i]), v[j], m[gi][i][j]);
             }
         }
     }
@@ -230,13 +284,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     if (!kOut || last) {
         const int64_t VK = (int64_t)ro.Db * ro.Dc;
         float* dst = kOut ? ro.mT + stream * VK : const_cast<float*>(ro.R) + (stream * nseg + slot) * VK;
-#pragma unroll
-        for (int i = 0; i < BT; ++i)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                const int bb = ty + 16 * i, cc = c0 + tx * CT + j;
-                if (bb < ro.Db && cc < ro.Dc) dst[cc * ro.m_sc + bb * ro.m_sb] = m[i][j];
-            }
+        each([&](int bb, int cc, float& x) { dst[cc * ro.m_sc + bb * ro.m_sb] = x; });
     }
 }
 
@@ -436,44 +484,57 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
 // How a call cuts its sequences, in whole 128-token tiles: the cut with the least
 // estimated time, in units of a tile of the scan.  A CTA takes its tiles one after the
 // other behind a fixed part (launch, first loads, the state that enters); the CTAs go in
-// waves of one per SM; with several segments the sums (0.6 of a tile each) and the link
-// come first.  The backward's three scans want fewer segments than the forward's one;
-// but cut like the forward's it can take over the forward's sums (`saved`).
+// waves of as many as the GPU holds; with several segments the sums and the link come
+// first.  On the tensor cores a tile takes 2.4 us alone, the fixed parts 11 us (scan)
+// and 2 us each (sums, link), a tile of the sums 0.9 us; on CUDA cores a tile takes 15
+// us and more, which leaves little to the fixed parts.  The backward's three scans want
+// fewer segments than the forward's one; but cut like the forward's it can take over the
+// forward's sums (`saved`).
 namespace {
-constexpr double kScanFixed = 4, kSumFixed = 3, kSumTile = 0.6, kLinkFixed = 1.5;
+struct CutModel {
+    double scan_fixed, sum_fixed, sum_tile, link;
+    int64_t slots;   // CTAs that run at once
+    int64_t slices;  // CTAs per (stream, segment, role)
+};
 
-double cut_cost(int64_t streams, int64_t tiles, int64_t per, int scans, int sums) {
-    const int64_t nseg = (tiles + per - 1) / per, sms = sm_count();
-    auto waves = [&](int64_t ctas) { return (double)((ctas + sms - 1) / sms); };
-    double t = waves(streams * scans * nseg) * (per + kScanFixed);
-    if (nseg > 1) t += waves(streams * sums * (nseg - 1)) * (kSumTile * per + kSumFixed) + kLinkFixed;
+CutModel cut_model(const LaDims& d, InType ty) {
+    if (ty == InType::BF16) return {4.5, 1.0, 0.4, 1.0, sm_count(), 1};
+    const int D = d.K > d.V ? d.K : d.V;
+    return {0.3, 0.2, 0.4, 0.2, (int64_t)sm_count() * (D > 32 ? 1 : 2), D > 64 ? 2 : 1};
+}
+
+double cut_cost(const CutModel& m, int64_t streams, int64_t tiles, int64_t per, int scans, int sums) {
+    const int64_t nseg = (tiles + per - 1) / per;
+    auto waves = [&](int64_t ctas) { return (double)((ctas * m.slices + m.slots - 1) / m.slots); };
+    double t = waves(streams * scans * nseg) * (per + m.scan_fixed);
+    if (nseg > 1) t += waves(streams * sums * (nseg - 1)) * (m.sum_tile * per + m.sum_fixed) + m.link;
     return t;
 }
 
 // The best number of tiles a segment, and its cost.
-int64_t best_cut(int64_t streams, int64_t tiles, int scans, int sums, double* cost) {
+int64_t best_cut(const CutModel& m, int64_t streams, int64_t tiles, int scans, int sums, double* cost) {
     int64_t best = tiles;
-    *cost = cut_cost(streams, tiles, tiles, scans, sums);
-    const int64_t most = streams * scans < sm_count() ? 2 * sm_count() / (streams * scans) : 1;
-    for (int64_t n = 2; n <= most && n <= tiles; ++n) {
+    *cost = cut_cost(m, streams, tiles, tiles, scans, sums);
+    for (int64_t n = 2; n <= tiles && streams * scans * (n - 1) < 2 * m.slots; ++n) {
         const int64_t per = (tiles + n - 1) / n;
-        const double c = cut_cost(streams, tiles, per, scans, sums);
+        const double c = cut_cost(m, streams, tiles, per, scans, sums);
         if (c < *cost) best = per, *cost = c;
     }
     return best;
 }
 }  // namespace
 
-void la_segments(LaDims* d, bool bwd) {
+void la_segments(LaDims* d, InType ty, bool bwd) {
     const int64_t tiles = (d->T + 127) / 128, streams = d->NS();
     int64_t per = tiles;
     if (streams > 0 && tiles > 1) {
-        double cf, cb;
-        per = best_cut(streams, tiles, 1, 1, &cf);
+        const CutModel m = cut_model(*d, ty);
+        double cost;
+        per = best_cut(m, streams, tiles, 1, 1, &cost);
         if (bwd) {
-            const double shared = cut_cost(streams, tiles, per, 3, 1);
-            const int64_t own = best_cut(streams, tiles, 3, 2, &cb);
-            if (cb < shared) per = own;
+            const double shared = cut_cost(m, streams, tiles, per, 3, 1);
+            const int64_t own = best_cut(m, streams, tiles, 3, 2, &cost);
+            if (cost < shared) per = own;
         }
     }
     d->L = (int)(per * 128);
