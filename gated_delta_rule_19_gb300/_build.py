@@ -1,4 +1,5 @@
-"""Builds libgdn.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs)."""
+"""Builds libgdn.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs), and _layer.so,
+the C++ binding of the linear-attention layer's calls, with g++ against torch's headers."""
 from __future__ import annotations
 
 import glob
@@ -12,6 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING = os.path.join(PKG, "_layer.so")
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,10 +44,49 @@ def is_stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
+def _binding_is_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "gdn.h")))
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile the C++ binding against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    dirs = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for d in dirs for f in ("-isystem" if d != INCLUDE else "-I", d)), BINDING_SRC, "-o", tmp, "-L" + lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every csrc/*.cu to an object file (in parallel) and link libgdn.so."""
-    if not force and not is_stale():
-        return LIB
+    """Compile every csrc/*.cu to an object file (in parallel) and link libgdn.so; compile
+    the binding beside them."""
+    with ThreadPoolExecutor(1) as ex:
+        binding = ex.submit(build_binding, verbose) if force or _binding_is_stale() else None
+        if force or is_stale():
+            _build_lib(verbose, extra_flags)
+        if binding is not None:
+            binding.result()
+    return LIB
+
+
+def _build_lib(verbose: bool, extra_flags) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
     objs = [os.path.join(BUILD_DIR, os.path.basename(s)[:-3] + ".o") for s in srcs]

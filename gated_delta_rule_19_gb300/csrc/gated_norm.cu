@@ -206,16 +206,16 @@ cudaError_t launch_g(const GatedCall& c, const GatedDims& d, bool bwd, cudaStrea
     const T *x = (const T*)c.x, *z = (const T*)c.z, *w = (const T*)c.w;
     if (!bwd) {
         constexpr int smem = FwdRing::BYTES;
-        cudaError_t e = cudaFuncSetAttribute(gated_norm_fwd_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+        static std::atomic<uint64_t> done{0};
+        cudaError_t e = allow_smem(gated_norm_fwd_kernel<T, G>, smem, done);
         if (e != cudaSuccess) return e;
         gated_norm_fwd_kernel<T, G>
             <<<(unsigned)blocks_for(d.rows, G, kFwdPerSm, sm_count()), kThreads, smem, st>>>(d, x, z, w, (T*)c.y);
     } else {
         constexpr int smem = BwdRing::BYTES;
         static_assert(smem >= (kThreads / 32) * 256 * 4, "the column sums fit the ring");
-        cudaError_t e = cudaFuncSetAttribute(gated_norm_bwd_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+        static std::atomic<uint64_t> done{0};
+        cudaError_t e = allow_smem(gated_norm_bwd_kernel<T, G>, smem, done);
         if (e != cudaSuccess) return e;
         gated_norm_bwd_kernel<T, G>
             <<<c.blocks, kThreads, smem, st>>>(d, x, z, w, (const T*)c.dy, (T*)c.dx, (T*)c.dz, c.part);

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gdn {
 
 // Problem dimensions as the kernels see them.  NC = ceil(T / C) chunks per
@@ -348,6 +350,20 @@ struct LaRoles {
     LaRole r[3];
     int n = 0;
 };
+// Lets a kernel have more than 48 KB of dynamic shared memory, once per device (`done`:
+// a static of the caller, one bit per device).
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Launches a kernel that may start while the one before it in the stream still runs: it
 // waits (griddepcontrol.wait) before it reads what that one writes.
 template <typename... P, typename... A>

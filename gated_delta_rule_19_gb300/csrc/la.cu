@@ -292,8 +292,8 @@ template <int D, bool kOut>
 cudaError_t launch_chunk(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     using L = Smem<D>;
     const size_t smem = L::SIZE * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(la_chunk_kernel<D, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(la_chunk_kernel<D, kOut>, (int)smem, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * (kOut ? d.nseg : d.nseg - 1)), D / L::CS, roles.n);
     la_chunk_kernel<D, kOut><<<grid, 256, smem, st>>>(d, roles);
@@ -528,14 +528,26 @@ void la_segments(LaDims* d, InType ty, bool bwd) {
     const int64_t tiles = (d->T + 127) / 128, streams = d->NS();
     int64_t per = tiles;
     if (streams > 0 && tiles > 1) {
-        const CutModel m = cut_model(*d, ty);
-        double cost;
-        per = best_cut(m, streams, tiles, 1, 1, &cost);
-        if (bwd) {
-            const double shared = cut_cost(m, streams, tiles, per, 3, 1);
-            const int64_t own = best_cut(m, streams, tiles, 3, 2, &cost);
-            if (cost < shared) per = own;
+        // the search takes up to 30 us, so a thread keeps its last results by size
+        struct Found {
+            int64_t streams, tiles, per;
+            int width, ty, bwd;
+        };
+        static thread_local Found kept[16] = {};
+        const int width = d->K > d->V ? d->K : d->V;
+        Found& f = kept[(streams * 31 + tiles * 7 + width / 16 + (int)ty * 2 + bwd) % 16];
+        if (f.streams != streams || f.tiles != tiles || f.width != width || f.ty != (int)ty || f.bwd != bwd) {
+            const CutModel m = cut_model(*d, ty);
+            double cost;
+            per = best_cut(m, streams, tiles, 1, 1, &cost);
+            if (bwd) {
+                const double shared = cut_cost(m, streams, tiles, per, 3, 1);
+                const int64_t own = best_cut(m, streams, tiles, 3, 2, &cost);
+                if (cost < shared) per = own;
+            }
+            f = {streams, tiles, per, width, (int)ty, (int)bwd};
         }
+        per = f.per;
     }
     d->L = (int)(per * 128);
     d->nseg = tiles ? (int)((tiles + per - 1) / per) : 1;

@@ -672,7 +672,8 @@ bool make_maps(const LaDims& d, const LaRoles& roles, bool out, LaMaps* m) {
 cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     LaMaps maps;
     if (!make_maps(d, roles, false, &maps)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(la_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SS_SIZE);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(la_sums_kernel, SS_SIZE, done);
     if (e != cudaSuccess) return e;
     la_sums_kernel<<<dim3((unsigned)(d.NS() * (d.nseg - 1)), roles.n), kThreads, SS_SIZE, st>>>(d, roles, maps);
     return cudaGetLastError();
@@ -680,7 +681,8 @@ cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStrea
 cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     LaMaps maps;
     if (!make_maps(d, roles, true, &maps)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(la_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SIZE);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(la_scan_kernel, S_SIZE, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * d.nseg), roles.n);
     if (d.nseg > 1) return launch_dependent(la_scan_kernel, grid, kThreads, S_SIZE, st, d, roles, maps);

@@ -324,7 +324,8 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
     if (!bwd) {
         auto kern = qk_norm_rope_fwd_kernel<T, G, kInter>;
         constexpr int smem = FwdRing<T>::BYTES;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> done{0};
+        cudaError_t e = allow_smem(kern, smem, done);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)blocks_for(d.tokens * (q.blocks + k.blocks), G, 2, sm_count()), kThreads, smem, st>>>(d, q, k,
                                                                                                               tab);
@@ -332,7 +333,8 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
         auto kern = qk_norm_rope_bwd_kernel<T, G, kInter>;
         constexpr int smem = BwdRing<T>::BYTES;
         static_assert(smem >= (kThreads / 32) * 256 * 4, "the column sums fit the ring");
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> done{0};
+        cudaError_t e = allow_smem(kern, smem, done);
         if (e != cudaSuccess) return e;
         kern<<<blocks, kThreads, smem, st>>>(d, q, k, tab, part);
     }

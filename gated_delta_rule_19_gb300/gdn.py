@@ -10,7 +10,6 @@ missing, importing or calling raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -883,152 +882,30 @@ def gdn_fwd_noalloc(q, k, v, alpha, beta, initial_state, o, final_state=None, *,
 # ---- The linear-attention layer: linear attention with a decay per head, the norm and
 # rotation of its q and k rows, the gated norm of its output (see include/gdn.h).
 
-# These calls are short (a decode step's kernel takes a few microseconds), so the
-# binding passes addresses as plain integers and keeps problem structures and buffer
-# sizes by shape.
+# Their marshalling is in C++ (csrc/layer_binding.cpp): a decode step's kernel takes a few
+# microseconds, which the checks in Python would multiply.
 
-def _rows(t, name, shape, dtype, device):
-    """Checks a [B, T, H, D] tensor whose tokens lie a fixed stride apart (a slice of a
-    fused projection, say) and returns that stride in elements (0: dense)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {device}")
-    if t.is_contiguous() or t.numel() == 0:
-        return 0
-    B, T, H, D = shape
-    sb, st, sh, sd = t.stride()
-    token = st if T > 1 else sb
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 1 and sb != T * st) or (B * T > 1 and token < H * D):
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be dense in its last two dimensions and its tokens a fixed "
-                                            f"stride apart, got strides {t.stride()}")
-    return token if B * T > 1 else 0
+_layer = None
 
 
-def _dense(t, name, shape, dtype, device):
-    """As :func:`_rows` for a tensor of any shape that has to be dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be contiguous")
-    return t
+def _binding():
+    """The C++ binding, on the library at LIB_PATH (raises if it has not been built)."""
+    global _layer
+    if _layer is None:
+        load_library()
+        path = os.path.join(_PKG, "_layer.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _layer as module
+
+        module.load(LIB_PATH, GdnError)
+        _layer = module
+    return _layer
 
 
-def _required(t, name, shape, dtype, device):
-    if t is None:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} is required")
-    return _dense(t, name, shape, dtype, device)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-# the current stream's handle without a Stream object (2 us less on the launch path)
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _raw_stream(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-class _Plan:
-    """A problem structure with the buffer sizes that follow from it."""
-
-    def __init__(self, problem, **sizes):
-        lib = load_library()
-        self.problem = problem
-        self.ref = ctypes.byref(problem)
-        for name, fn in sizes.items():
-            setattr(self, name, int(getattr(lib, fn)(self.ref)))
-
-
-@functools.lru_cache(maxsize=1024)
-def _la_plan(*fields):
-    return _Plan(gdn_la_problem(*fields), fwd="gdn_la_fwd_workspace_bytes", saved="gdn_la_saved_bytes",
-                 bwd="gdn_la_bwd_workspace_bytes")
-
-
-@functools.lru_cache(maxsize=1024)
-def _rope_plan(*fields):
-    return _Plan(gdn_rope_problem(*fields), bwd="gdn_qk_norm_rope_bwd_workspace_bytes")
-
-
-@functools.lru_cache(maxsize=1024)
-def _gated_plan(*fields):
-    return _Plan(gdn_gated_norm_problem(*fields), bwd="gdn_gated_norm_bwd_workspace_bytes")
-
-
-def _cuda_device(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise GdnError(GDN_ERR_INVALID_ARG, "inputs must be CUDA tensors")
-    if t.dim() != 4:
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected four dimensions")
-    return t.device
-
-
-def _la_inputs(q, k, v, log_decay):
-    dev, dt = _cuda_device(q, "q"), q.dtype
-    _cuda_device(v, "v")
-    code = _dtype_code(dt)
-    qshape = q.shape
-    B, T, H, K = qshape
-    V = v.shape[3]
-    vshape = (B, T, H, V)
-    plan = _la_plan(B, T, H, K, V, _rows(q, "q", qshape, dt, dev), _rows(k, "k", qshape, dt, dev),
-                    _rows(v, "v", vshape, dt, dev), code)
-    _required(log_decay, "log_decay", (H,), torch.float32, dev)
-    return plan, dev, dt, vshape, (B, H, V, K)
-
-
-def _scratch(nbytes, dev):
-    return torch.empty(nbytes if nbytes else 1, dtype=torch.uint8, device=dev)
-
-
-def _buffer(t, name, dev):
-    """Address and bytes of a caller's buffer."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
-        raise GdnError(GDN_ERR_INVALID_ARG, f"{name} must be a contiguous tensor on {dev}")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _workspace(t, nbytes, dev):
-    """A workspace tensor with its address and bytes: the caller's, or a new one."""
-    if t is not None:
-        return (t, *_buffer(t, "workspace", dev))
-    t = _scratch(nbytes, dev)
-    return t, t.data_ptr(), nbytes
-
-
-def _out(t, name, shape, dtype, dev):
-    """An output to fill: the caller's, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _dense(t, name, shape, dtype, dev)
-
-
-def _out_state(t, name, shape, dev):
-    if t is True:
-        return torch.empty(shape, dtype=torch.float32, device=dev)
-    if t is False or t is None:
-        return None
-    return _dense(t, name, shape, torch.float32, dev)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def gdn_la_fwd(q, k, v, log_decay, initial_state=None, *, o=None, final_state=True, saved=False, workspace=None,
@@ -1044,22 +921,8 @@ def gdn_la_fwd(q, k, v, log_decay, initial_state=None, *, o=None, final_state=Tr
     True to allocate and return what :func:`gdn_la_bwd` then need not compute again,
     or a buffer of at least gdn_la_saved_bytes() bytes.
     Returns ``(o, final_state or None, saved or None)``."""
-    plan, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
-    if initial_state is not None:
-        _dense(initial_state, "initial_state", sshape, torch.float32, dev)
-    o = _out(o, "o", oshape, dt, dev)
-    final_state = _out_state(final_state, "final_state", sshape, dev)
-    if saved is True:
-        saved = _scratch(plan.saved, dev)
-    elif saved is False:
-        saved = None
-    elif saved is not None and _buffer(saved, "saved", dev)[1] < plan.saved:
-        raise GdnError(GDN_ERR_INVALID_ARG, "saved buffer is smaller than gdn_la_saved_bytes()")
-    workspace, ws, ws_bytes = _workspace(workspace, plan.fwd, dev)
-    _check(_lib.gdn_la_fwd(plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                           _at(initial_state), o.data_ptr(), _at(final_state), _at(saved), ws, ws_bytes,
-                           _raw_stream(dev, stream)))
-    return o, final_state, saved
+    return (_layer or _binding()).la_fwd(q, k, v, log_decay, initial_state, o, final_state, saved, workspace,
+                                         _raw(stream))
 
 
 def gdn_la_bwd(q, k, v, log_decay, initial_state, d_o, d_final_state=None, *, saved=None, grads=None,
@@ -1067,58 +930,15 @@ def gdn_la_bwd(q, k, v, log_decay, initial_state, d_o, d_final_state=None, *, sa
     """Gradients of ``sum(d_o * o) + sum(d_final_state * final_state)`` of
     :func:`gdn_la_fwd` (``gdn_la_bwd``); ``saved`` is what the forward returned for
     the same inputs, or None.  Returns ``(dq, dk, dv, d_initial_state or None)``."""
-    plan, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
-    if initial_state is not None:
-        _dense(initial_state, "initial_state", sshape, torch.float32, dev)
-    _required(d_o, "d_o", oshape, dt, dev)
-    if d_final_state is not None:
-        _dense(d_final_state, "d_final_state", sshape, torch.float32, dev)
     dq, dk, dv = grads if grads is not None else (None, None, None)
-    dq, dk = _out(dq, "dq", q.shape, dt, dev), _out(dk, "dk", q.shape, dt, dev)
-    dv = _out(dv, "dv", oshape, dt, dev)
-    d_initial_state = _out_state(d_initial_state, "d_initial_state", sshape, dev)
-    if saved is not None and _buffer(saved, "saved", dev)[1] < plan.saved:
-        raise GdnError(GDN_ERR_INVALID_ARG, "saved buffer is smaller than gdn_la_saved_bytes()")
-    workspace, ws, ws_bytes = _workspace(workspace, plan.bwd, dev)
-    _check(_lib.gdn_la_bwd(plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                           _at(initial_state), _at(saved), d_o.data_ptr(), _at(d_final_state), dq.data_ptr(),
-                           dk.data_ptr(), dv.data_ptr(), _at(d_initial_state), ws, ws_bytes, _raw_stream(dev, stream)))
-    return dq, dk, dv, d_initial_state
+    return (_layer or _binding()).la_bwd(q, k, v, log_decay, initial_state, d_o, d_final_state, saved, dq, dk, dv,
+                                         d_initial_state, workspace, _raw(stream))
 
 
 def gdn_la_decode(q, k, v, log_decay, state, *, o=None, stream=None):
     """The same recurrence token by token (``gdn_la_decode``, usually T = 1):
     ``state`` [B,H,V,K] float32 is updated in place.  Returns ``(o, state)``."""
-    plan, dev, dt, oshape, sshape = _la_inputs(q, k, v, log_decay)
-    o = _out(o, "o", oshape, dt, dev)
-    _required(state, "state", sshape, torch.float32, dev)
-    _check(_lib.gdn_la_decode(plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                              state.data_ptr(), o.data_ptr(), _raw_stream(dev, stream)))
-    return o, state
-
-
-def _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-    dev, dt = _cuda_device(q, "q"), q.dtype
-    _cuda_device(k, "k")
-    code = _dtype_code(dt)
-    qshape = q.shape
-    B, T, Hq, D = qshape
-    kshape = (B, T, k.shape[2], D)
-    R = rows = 0
-    if cos is not None or sin is not None:
-        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-            raise GdnError(GDN_ERR_INVALID_ARG, "cos must be a [table_rows, R/2] tensor")
-        rows, pairs = cos.shape
-        R = 2 * pairs
-        _dense(cos, "cos", (rows, pairs), torch.float32, dev)
-        _required(sin, "sin", (rows, pairs), torch.float32, dev)
-    _required(q_weight, "q_weight", (D,), dt, dev)
-    _required(k_weight, "k_weight", (D,), dt, dev)
-    if positions is not None:
-        _dense(positions, "positions", (B, T), torch.int32, dev)
-    plan = _rope_plan(B, T, Hq, kshape[2], D, R, rows, _rows(q, "q", qshape, dt, dev),
-                      _rows(k, "k", kshape, dt, dev), float(eps), 1 if interleaved else 0, code)
-    return plan, dev, dt, kshape
+    return (_layer or _binding()).la_decode(q, k, v, log_decay, state, o, _raw(stream))
 
 
 def gdn_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos=None, sin=None, positions=None, *, eps: float = 1e-6,
@@ -1129,64 +949,28 @@ def gdn_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos=None, sin=None, positions
     (None: no rotation); positions int32 [B,T], rows of the tables (None: 0 .. T-1).
     Pairs are (i, i + R/2), or (2i, 2i+1) with ``interleaved``.  A position outside the
     tables makes its token's rows NaN.  Returns ``(q_out, k_out)``, dense."""
-    plan, dev, dt, kshape = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    q_out = _out(q_out, "q_out", q.shape, dt, dev)
-    k_out = _out(k_out, "k_out", kshape, dt, dev)
-    _check(_lib.gdn_qk_norm_rope_fwd(plan.ref, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-                                     _at(cos), _at(sin), _at(positions), q_out.data_ptr(), k_out.data_ptr(),
-                                     _raw_stream(dev, stream)))
-    return q_out, k_out
+    return (_layer or _binding()).rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
+                                           k_out, _raw(stream))
 
 
 def gdn_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, *, eps: float = 1e-6,
                          interleaved: bool = False, grads=None, workspace=None, stream=None):
     """Backward of :func:`gdn_qk_norm_rope_fwd` (``gdn_qk_norm_rope_bwd``) from the
     gradients of its outputs.  Returns ``(dq, dk, dq_weight, dk_weight)``."""
-    plan, dev, dt, kshape = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    _required(dq_out, "dq_out", q.shape, dt, dev)
-    _required(dk_out, "dk_out", kshape, dt, dev)
     dq, dk, dwq, dwk = grads if grads is not None else (None,) * 4
-    dq, dk = _out(dq, "dq", q.shape, dt, dev), _out(dk, "dk", kshape, dt, dev)
-    dwq, dwk = _out(dwq, "dq_weight", q_weight.shape, dt, dev), _out(dwk, "dk_weight", k_weight.shape, dt, dev)
-    workspace, ws, ws_bytes = _workspace(workspace, plan.bwd, dev)
-    _check(_lib.gdn_qk_norm_rope_bwd(plan.ref, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-                                     _at(cos), _at(sin), _at(positions), dq_out.data_ptr(), dk_out.data_ptr(),
-                                     dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), ws, ws_bytes,
-                                     _raw_stream(dev, stream)))
-    return dq, dk, dwq, dwk
-
-
-def _gated_inputs(x, gate, weight, eps):
-    dev, dt = _cuda_device(x, "x"), x.dtype
-    code = _dtype_code(dt)
-    shape = x.shape
-    B, T, H, D = shape
-    _required(weight, "weight", (D,), dt, dev)
-    return _gated_plan(B, T, H, D, _rows(x, "x", shape, dt, dev), _rows(gate, "gate", shape, dt, dev), float(eps),
-                       code), dev, dt
+    return (_layer or _binding()).rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps,
+                                           interleaved, dq, dk, dwq, dwk, workspace, _raw(stream))
 
 
 def gdn_gated_norm_fwd(x, gate, weight, *, eps: float = 1e-6, y=None, stream=None):
     """``y = x weight silu(gate) / sqrt(mean(x^2) + eps)`` for every row of x, gate
     [B,T,H,D] (tokens may lie a fixed stride apart), weight [D]
     (``gdn_gated_norm_fwd``).  Returns ``y``, dense."""
-    plan, dev, dt = _gated_inputs(x, gate, weight, eps)
-    y = _out(y, "y", x.shape, dt, dev)
-    _check(_lib.gdn_gated_norm_fwd(plan.ref, x.data_ptr(), gate.data_ptr(), weight.data_ptr(), y.data_ptr(),
-                                   _raw_stream(dev, stream)))
-    return y
+    return (_layer or _binding()).gated_fwd(x, gate, weight, eps, y, _raw(stream))
 
 
 def gdn_gated_norm_bwd(x, gate, weight, dy, *, eps: float = 1e-6, grads=None, workspace=None, stream=None):
     """Backward of :func:`gdn_gated_norm_fwd` (``gdn_gated_norm_bwd``).
     Returns ``(dx, dgate, dweight)``."""
-    plan, dev, dt = _gated_inputs(x, gate, weight, eps)
-    _required(dy, "dy", x.shape, dt, dev)
     dx, dgate, dw = grads if grads is not None else (None,) * 3
-    dx, dgate = _out(dx, "dx", x.shape, dt, dev), _out(dgate, "dgate", x.shape, dt, dev)
-    dw = _out(dw, "dweight", weight.shape, dt, dev)
-    workspace, ws, ws_bytes = _workspace(workspace, plan.bwd, dev)
-    _check(_lib.gdn_gated_norm_bwd(plan.ref, x.data_ptr(), gate.data_ptr(), weight.data_ptr(), dy.data_ptr(),
-                                   dx.data_ptr(), dgate.data_ptr(), dw.data_ptr(), ws, ws_bytes,
-                                   _raw_stream(dev, stream)))
-    return dx, dgate, dw
+    return (_layer or _binding()).gated_bwd(x, gate, weight, dy, eps, dx, dgate, dw, workspace, _raw(stream))
