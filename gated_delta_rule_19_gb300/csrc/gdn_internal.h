@@ -317,7 +317,7 @@ cudaError_t launch_grad_wy_tc(const Dims& d, const void* k, const void* v, const
 // ---- the linear-attention layer (la.cu, norm_rope.cu, gated_norm.cu) ----
 
 // Linear attention with a decay per head: a sequence is cut into nseg segments of L
-// tokens (a multiple of 128), the last one shorter.
+// tokens (whole tiles), the last one shorter.
 struct LaDims {
     int B, T, H, K, V;
     int L, nseg;

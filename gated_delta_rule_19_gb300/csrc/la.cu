@@ -36,23 +36,24 @@ constexpr int kTok = 64;  // tokens of a chunk
 __device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // Shared memory of the chunk kernel, in floats: rows of D (or 64) padded by four so
-// that the float4 reads of neighbouring rows fall into different banks; two buffers of
-// A, B, C, so that a chunk is loaded while the one before it is worked on.
+// that the float4 reads of neighbouring rows fall into different banks.  Up to D = 64
+// two CTAs share an SM and hide each other's loads and reads; at 128 one has it alone and
+// two buffers of A, B, C, so that a chunk is loaded while the one before it is worked on.
 template <int D>
 struct Smem {
     static constexpr int CS = D < 64 ? D : 64;  // columns of c that one CTA carries
     static constexpr int RA = D + 4, RC = CS + 4, RP = kTok + 4;
     static constexpr int A = 0, B = A + kTok * RA, C = B + kTok * RA, BUF = C + kTok * RC;
-    static constexpr int M = 2 * BUF, P = M + D * RC, W = P + kTok * RP, SIZE = W + kTok + 8;
+    static constexpr int NBUF = D > 64 ? 2 : 1, M = NBUF * BUF, P = M + D * RC, W = P + kTok * RP, SIZE = W + kTok + 8;
 };
-static_assert(Smem<128>::SIZE * 4 <= 232448, "shared memory of one CTA");
+static_assert(Smem<128>::SIZE * 4 <= 232448 && Smem<64>::SIZE * 8 <= 231424, "shared memory");
 
 // One CTA: one (stream, segment), CS columns of c, one role.  256 threads as 16 x 16:
 // thread (ty, tx) has rows 4 ty .. 4 ty + 3 and CS / 16 columns of each product, and in
 // registers M's rows (b) BV ty .. of every 16 BV; a copy in shared memory feeds A M^T.
 // The products run on pairs of columns (f32x2), which leaves issue slots for the reads.
 template <int D, bool kOut>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, D > 64 ? 1 : 2)
 la_chunk_kernel(LaDims d, LaRoles roles) {
     using L = Smem<D>;
     constexpr int CT = L::CS / 16, CP = (CT + 1) / 2;  // columns of c per thread, pairs of them
@@ -82,7 +83,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     // rows past the sequence and columns past the tensors' are zeros
     auto load = [&](int it) {
         const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
-        float* buf = sm + (it & 1) * L::BUF;
+        float* buf = sm + it % L::NBUF * L::BUF;
         auto rows = [&](float* to, int stride, const float* from, int64_t step, int width, int cols) {
             for (int i = tid; i < kTok * (width / 4); i += 256) {
                 const int r = i / (width / 4), x = (i % (width / 4)) * 4;
@@ -147,7 +148,11 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     };
     for (int it = 0; it < chunks; ++it) {
         const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
-        const float *sA = sm + (it & 1) * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
+        const float *sA = sm + it % L::NBUF * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
+        if (L::NBUF == 1 && it) {
+            __syncthreads();  // the chunk before is done with the buffer
+            load(it);
+        }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (kOut) {
 #pragma unroll
@@ -164,7 +169,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
                     }
         }
         __syncthreads();  // this chunk is there, the other buffer and P are free
-        if (it + 1 < chunks) load(it + 1);
+        if (L::NBUF == 2 && it + 1 < chunks) load(it + 1);
 
         uint64_t acc[4][CP];
         if (kOut) {
@@ -481,26 +486,28 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
                               : launch_decode_t<float>(d, q, k, v, sq, sk, sv, state, o, st);
 }
 
-// How a call cuts its sequences, in whole 128-token tiles: the cut with the least
-// estimated time, in units of a tile of the scan.  A CTA takes its tiles one after the
-// other behind a fixed part (launch, first loads, the state that enters); the CTAs go in
-// waves of as many as the GPU holds; with several segments the sums and the link come
-// first.  On the tensor cores a tile takes 2.4 us alone, the fixed parts 11 us (scan)
-// and 2 us each (sums, link), a tile of the sums 0.9 us; on CUDA cores a tile takes 15
-// us and more, which leaves little to the fixed parts.  The backward's three scans want
-// fewer segments than the forward's one; but cut like the forward's it can take over the
-// forward's sums (`saved`).
+// How a call cuts its sequences, in whole tiles (128 tokens on the tensor cores, a chunk
+// of 64 on CUDA cores): the cut with the least estimated time, in units of a tile of the
+// scan.  A CTA takes its tiles one after the other behind a fixed part (launch, first
+// loads, the state that enters); the CTAs go in waves of as many as the GPU holds; with
+// several segments the sums and the link come first.  On the tensor cores a tile takes
+// 2.4 us alone, the fixed parts 11 us (scan) and 2 us each (sums, link), a tile of the
+// sums 0.9 us; on CUDA cores a chunk of K = V = 64 takes 9 us and the fixed parts less.
+// The backward's three scans want fewer segments than the forward's one; but cut like
+// the forward's it can take over the forward's sums (`saved`).
 namespace {
+// in tiles, but for the counts
 struct CutModel {
     double scan_fixed, sum_fixed, sum_tile, link;
+    int64_t tile;    // tokens
     int64_t slots;   // CTAs that run at once
     int64_t slices;  // CTAs per (stream, segment, role)
 };
 
 CutModel cut_model(const LaDims& d, InType ty) {
-    if (ty == InType::BF16) return {4.5, 1.0, 0.4, 1.0, sm_count(), 1};
+    if (ty == InType::BF16) return {4.5, 1.0, 0.4, 1.0, 128, sm_count(), 1};
     const int D = d.K > d.V ? d.K : d.V;
-    return {0.3, 0.2, 0.4, 0.2, (int64_t)sm_count() * (D > 32 ? 1 : 2), D > 64 ? 2 : 1};
+    return {0.6, 0.4, 0.4, 0.4, kTok, (int64_t)sm_count() * (D > 64 ? 1 : 2), D > 64 ? 2 : 1};
 }
 
 double cut_cost(const CutModel& m, int64_t streams, int64_t tiles, int64_t per, int scans, int sums) {
@@ -525,7 +532,8 @@ int64_t best_cut(const CutModel& m, int64_t streams, int64_t tiles, int scans, i
 }  // namespace
 
 void la_segments(LaDims* d, InType ty, bool bwd) {
-    const int64_t tiles = (d->T + 127) / 128, streams = d->NS();
+    const CutModel m = cut_model(*d, ty);
+    const int64_t tiles = (d->T + m.tile - 1) / m.tile, streams = d->NS();
     int64_t per = tiles;
     if (streams > 0 && tiles > 1) {
         // the search takes up to 30 us, so a thread keeps its last results by size
@@ -537,7 +545,6 @@ void la_segments(LaDims* d, InType ty, bool bwd) {
         const int width = d->K > d->V ? d->K : d->V;
         Found& f = kept[(streams * 31 + tiles * 7 + width / 16 + (int)ty * 2 + bwd) % 16];
         if (f.streams != streams || f.tiles != tiles || f.width != width || f.ty != (int)ty || f.bwd != bwd) {
-            const CutModel m = cut_model(*d, ty);
             double cost;
             per = best_cut(m, streams, tiles, 1, 1, &cost);
             if (bwd) {
@@ -549,7 +556,7 @@ void la_segments(LaDims* d, InType ty, bool bwd) {
         }
         per = f.per;
     }
-    d->L = (int)(per * 128);
+    d->L = (int)(per * m.tile);
     d->nseg = tiles ? (int)((tiles + per - 1) / per) : 1;
 }
 
