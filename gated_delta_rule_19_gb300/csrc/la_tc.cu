@@ -3,12 +3,14 @@
 //
 // Per tile, with A, B, C [128 tokens, 128] in shared memory and M [c, b] the state
 // that enters:
-//   scores Y = A B^T,   P = Y .* D (bf16, written over Y in tensor memory)
+//   scores Y = A B^T,   P = Y .* D (bf16, in tensor memory)
 //   X = A M^T,  X <- diag(gamma^(rho + 1 - rev)) X,  X += P C    -> the tile's outputs
 //   U = C'^T B,  M <- gamma^n M + U,   C' = C's rows times gamma^(n - 1 - rho + rev).
 // M is kept in float32 in registers; the product A M^T reads it rounded to bf16.  C' is
-// split into two bf16 terms (high part, and the rest), two products, so that the state
-// keeps 16 bits of every decayed value (2.7e-6 rms of the sum) instead of 8.
+// split into bf16 terms (the high part, then what is left), one product each: two where
+// M only feeds outputs (16 bits of every decayed value, 2.5e-6 rms of the sum; one would
+// add as much error to the outputs as M's own rounding), three in the sums and where M is
+// returned (24 bits: the state is then as exact as float32 sums are).
 //
 // One CTA per SM.  la_scan_kernel: two warpgroups carry the state (thread = row of M,
 // half of the columns each), two the rows of P and X (thread = token = tensor-memory
@@ -91,24 +93,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t ph, int* err, 
     return true;
 }
 
-// The tile's rows c0 .. c0+15 of a product's operand as float pairs times a pair of
-// weights, rounded to bf16 (hi) and what that leaves, rounded (lo).
-__device__ __forceinline__ void split2(uint32_t v, uint64_t w, uint32_t& hi, uint32_t& lo) {
-    const uint64_t f = mul2(pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), w);
+// A pair of bf16 values times a pair of weights, rounded to bf16; `left` is what that
+// leaves of the products.
+__device__ __forceinline__ uint32_t split_off(uint64_t f, uint64_t& left) {
     float x, y;
     unpair(f, x, y);
-    hi = pack_bf16(x, y);
-    unpair(fma2(pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), pair(-1.f, -1.f), f), x, y);
-    lo = pack_bf16(x, y);
+    const uint32_t h = pack_bf16(x, y);
+    left = fma2(bf16_pair(h), twice(-1.f), f);
+    return h;
 }
 
 // C' of NT of the tile's tokens (from s0) for the 32 columns of C that are this warp's
-// lanes (from c0), as two bf16 terms in tensor memory columns s / 2 of t_hi, t_lo.
-// Blocks of 8 tokens x 8 columns are read transposed, which is the register layout of
-// the 16x128b store.
+// lanes (from c0), as `terms` (2 or 3) bf16 terms in tensor memory, 64 columns apart from
+// t_c on, token s in column s / 2.  Blocks of 8 tokens x 8 columns are read transposed,
+// which is the register layout of the 16x128b store.
 template <int NT>
-__device__ __forceinline__ void put_updates(uint32_t sC, const float* upd, uint32_t t_hi, uint32_t t_lo, int c0, int s0,
-                                            int lane) {
+__device__ __forceinline__ void put_updates(uint32_t sC, const float* upd, uint32_t t_c, int c0, int s0, int lane,
+                                            int terms) {
     // this lane's row in the four blocks of an ldmatrix: tokens (0-7, 0-7, 8-15, 8-15)
     // of columns (0-7, 8-15, 0-7, 8-15)
     const int row = (lane & 7) + ((lane >> 4) << 3), cb = (lane >> 3) & 1;
@@ -121,13 +122,21 @@ __device__ __forceinline__ void put_updates(uint32_t sC, const float* upd, uint3
         const uint64_t w0 = *(const uint64_t*)(upd + b), w1 = *(const uint64_t*)(upd + b + 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // 16 lanes at a time
-            uint32_t v[4], hi[4], lo[4];
+            uint32_t v[4], h[4];
+            uint64_t f[4];
             ldmatrix_x4_trans(from[i] + b * 128, v);
+            uint32_t to = t_c + ((uint32_t)(16 * i) << 16) + (s0 + b) / 2;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split2(v[j], j < 2 ? w0 : w1, hi[j], lo[j]);
-            const uint32_t to = ((uint32_t)(16 * i) << 16) + (s0 + b) / 2;
-            tmem_st_16x128b_x2(t_hi + to, hi);
-            tmem_st_16x128b_x2(t_lo + to, lo);
+            for (int j = 0; j < 4; ++j) h[j] = split_off(mul2(bf16_pair(v[j]), j < 2 ? w0 : w1), f[j]);
+            tmem_st_16x128b_x2(to, h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = split_off(f[j], f[j]);
+            tmem_st_16x128b_x2(to + 64, h);
+            if (terms == 3) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = split_off(f[j], f[j]);
+                tmem_st_16x128b_x2(to + 128, h);
+            }
         }
     }
     tmem_wait_st();
@@ -173,7 +182,8 @@ __device__ __forceinline__ void store_state(const float (&m)[NC], float* dst, in
 struct __align__(8) SumBars {
     uint64_t full[3], free[3];
     uint64_t cv[2];  // C' is in tensor memory (512 arrivals)
-    uint64_t u[2];   // U is complete
+    uint64_t u;      // U is complete
+    uint64_t a;      // U is read (512 arrivals)
     uint64_t drain;
     uint32_t tmem;
 };
@@ -181,8 +191,8 @@ constexpr int SS_STAGES = 3, SS_UPD = SS_STAGES * 2 * kTileBytes, SS_POW = SS_UP
               SS_BARS = SS_POW + 132 * 4, SS_SIZE = SS_BARS + (int)sizeof(SumBars);
 
 // One CTA: one (stream, segment) of one role; its sum to R.  Four warpgroups make C' of
-// 32 tokens each and hold 32 columns of M each; C' and U are double-buffered in tensor
-// memory, so that a tile's C' is made while the one before it is multiplied.
+// 32 tokens each and hold 32 columns of M each; C' is double-buffered in tensor memory,
+// so that a tile's is made while the one before it is multiplied.
 __global__ void __launch_bounds__(kThreads, 1)
 la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -207,7 +217,10 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         tmem_relinquish();
     } else if (tid == kTmaWarp * 32) {
         for (int i = 0; i < SS_STAGES; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bar.cv[i], 512), mbar_init(&bar.u[i], 1);
+        mbar_init(&bar.cv[0], 512);
+        mbar_init(&bar.cv[1], 512);
+        mbar_init(&bar.u, 1);
+        mbar_init(&bar.a, 512);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
         fence_proxy_async();
@@ -220,8 +233,8 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = bar.tmem;
-    auto t_cv = [&](int it) { return (uint32_t)(it & 1) * 128; };       // 64 columns each of hi, lo
-    auto t_u = [&](int it) { return 256 + (uint32_t)(it & 1) * 128; };
+    constexpr uint32_t t_u = 384;
+    auto t_c = [&](int it) { return (uint32_t)(it & 1) * 192; };  // three terms of 64 columns
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
@@ -239,13 +252,14 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         for (int it = 0; it < tiles; ++it) {
             const uint64_t dB = desc_mnmaj(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes, 128, 0);
             if (!warp_wait(&bar.cv[it & 1], (it >> 1) & 1, d.err, kErrMma, d.wait_ns)) break;
+            if (it && !warp_wait(&bar.a, (it & 1) ^ 1, d.err, kErrMma, d.wait_ns)) break;
             fence_after_sync();
-            const uint32_t c = tm + t_cv(it), u = tm + t_u(it);
+            const uint32_t c = tm + t_c(it);
             if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < 16; ++s)
-                    mma_bf16_ts(u, c + 8 * s, desc_add(dB, (s & 7) * 2048), i_u, s > 0);
-                mma_commit(&bar.u[it & 1]);
+                for (int s = 0; s < 24; ++s)
+                    mma_bf16_ts(tm + t_u, c + 8 * s, desc_add(dB, (s & 7) * 2048), i_u, s > 0);
+                mma_commit(&bar.u);
                 mma_commit(&bar.free[it % SS_STAGES]);
             }
             __syncwarp();
@@ -261,8 +275,7 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         auto make = [&](int it) {
             if (!warp_wait(&bar.full[it % SS_STAGES], (it / SS_STAGES) & 1, d.err, kErrState, d.wait_ns)) return false;
             put_updates<32>(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes + kTileBytes,
-                            upd + (w.len(it) < kTile ? kTile : 0), tl + t_cv(it), tl + t_cv(it) + 64, (warp & 3) * 32,
-                            part * 32, lane);
+                            upd + (w.len(it) < kTile ? kTile : 0), tl + t_c(it), (warp & 3) * 32, part * 32, lane, 3);
             fence_before_sync();
             mbar_arrive(&bar.cv[it & 1]);
             return true;
@@ -270,10 +283,11 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         bool ok = make(0);
         for (int it = 0; it < tiles && ok; ++it) {
             if (it + 1 < tiles && !(ok = make(it + 1))) break;
-            if (!(ok = warp_wait(&bar.u[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns))) break;
+            if (!(ok = warp_wait(&bar.u, it & 1, d.err, kErrState, d.wait_ns))) break;
             fence_after_sync();
-            add_update(m, tl + t_u(it) + part * 32, pw[w.len(it)], cols);
+            add_update(m, tl + t_u + part * 32, pw[w.len(it)], cols);
             fence_before_sync();
+            mbar_arrive(&bar.a);
         }
         if (ok && c < Dc)
             store_state(m,
@@ -289,8 +303,8 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
 
 // ------------------------------------------------------------------- the scan
 
-// Tensor memory columns.
-constexpr uint32_t T_X = 0, T_Y = 128, T_U = 256, T_HI = 384, T_LO = 448;
+// Tensor memory columns: X; the scores, and after they are read U; P; C' (three terms).
+constexpr uint32_t T_X = 0, T_Y = 128, T_U = 128, T_P = 256, T_C = 320;
 
 struct __align__(8) Bars {
     uint64_t full[2];   // TMA: the stage's tiles have landed
@@ -301,7 +315,8 @@ struct __align__(8) Bars {
     uint64_t s;         // M is in shared memory (256 arrivals)
     uint64_t k;         // the scores are complete
     uint64_t q;         // A M^T is complete (M's shared memory may be rewritten)
-    uint64_t r;         // the scores are read out of Y (256 arrivals)
+    uint64_t r;         // the scores are read (256 arrivals)
+    uint64_t a;         // U is read (256 arrivals)
     uint64_t p;         // P is in tensor memory and X rescaled (256 arrivals)
     uint64_t o;         // the outputs are complete
     uint64_t x;         // the outputs are read out of X (256 arrivals)
@@ -383,6 +398,7 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
         fence_after_sync();
         add_update(m, tl + T_U + b0, sPow[w.len(it)], cols);
         fence_before_sync();
+        mbar_arrive(&bar.a);
         if (it + 1 < w.tiles) {
             if (!(ok = warp_wait(&bar.q, ph, d.err, kErrState, d.wait_ns))) break;
             put_state();
@@ -417,7 +433,6 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
         for (int k = 0; k < 2; ++k) tmem_ld32(tl + T_Y + (k ? 3 - wg : wg) * 32, y[k]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) tmem_wait_ld(y[k]);
-        // P goes over the scores: only once both warpgroups have read theirs
         fence_before_sync();
         mbar_arrive(&bar.r);
 #pragma unroll
@@ -441,10 +456,9 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
                 scale_block<false>(y[k], sPow[r - cb * 32 - 31], g1, p[k]);
             }
         }
-        if (!warp_wait(&bar.r, ph, d.err, kErrRows, d.wait_ns)) return;
-        fence_after_sync();
+        // the P before it is used up: its outputs have been read
 #pragma unroll
-        for (int k = 0; k < 2; ++k) tmem_st16(tl + T_Y + (k ? 3 - wg : wg) * 16, p[k]);
+        for (int k = 0; k < 2; ++k) tmem_st16(tl + T_P + (k ? 3 - wg : wg) * 16, p[k]);
         if (!warp_wait(&bar.q, ph, d.err, kErrRows, d.wait_ns)) return;
         fence_after_sync();
         const float f = sPow[max(rev ? n - 1 - r : r + 1, 0)];
@@ -504,6 +518,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     const Part w(d, roles, false);
     const LaRole& ro = w.ro;
     const int Db = ro.Db, Dc = ro.Dc, tiles = w.tiles, rev = w.rev;
+    const bool last = w.seg == (rev ? 0 : d.nseg - 1);
+    const int terms = last && ro.mT ? 3 : 2;
     const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
     auto stage = [&](int it) { return sm + (it & 1) * 3 * kTileBytes; };
     auto load = [&](int it, const CUtensorMap* map, int blocks, unsigned char* to) {
@@ -532,6 +548,7 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         mbar_init(&bar.k, 1);
         mbar_init(&bar.q, 1);
         mbar_init(&bar.r, 256);
+        mbar_init(&bar.a, 256);
         mbar_init(&bar.p, 256);
         mbar_init(&bar.o, 1);
         mbar_init(&bar.x, 256);
@@ -589,6 +606,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             const uint64_t dA = desc_kmaj(sA, 128, 0), dB = desc_add(dA, kTileBytes),
                            dBt = desc_mnmaj(sA + kTileBytes, 128, 0), dCt = desc_add(dBt, kTileBytes);
             if (!warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrMma, d.wait_ns)) break;
+            if (it && !warp_wait(&bar.a, ph ^ 1, d.err, kErrMma, d.wait_ns)) break;
+            fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
@@ -613,11 +632,13 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             }
             __syncwarp();
             if (!warp_wait(&bar.cv, ph, d.err, kErrMma, d.wait_ns)) break;
+            if (!warp_wait(&bar.r, ph, d.err, kErrMma, d.wait_ns)) break;
             fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < 16; ++s)
-                    mma_bf16_ts(tm + T_U, tm + T_HI + 8 * s, desc_add(dBt, (s & 7) * 2048), i_u, s > 0);
+                for (int s = 0; s < 24; ++s)
+                    if (s < 8 * terms)
+                        mma_bf16_ts(tm + T_U, tm + T_C + 8 * s, desc_add(dBt, (s & 7) * 2048), i_u, s > 0);
                 mma_commit(&bar.u);
             }
             __syncwarp();
@@ -626,7 +647,7 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_bf16_ts(tm + T_X, tm + T_Y + 8 * s, desc_add(dCt, s * 2048), i_p, 1);
+                    mma_bf16_ts(tm + T_X, tm + T_P + 8 * s, desc_add(dCt, s * 2048), i_p, 1);
                 mma_commit(&bar.o);
                 mma_commit(&bar.free[it & 1]);
             }
@@ -639,8 +660,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         auto make = [&](int it) {
             if (!warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns)) return false;
             put_updates<32>(smem_u32(sm) + (uint32_t)(it & 1) * 3 * kTileBytes + 2 * kTileBytes,
-                            sUpd + (w.len(it) < kTile ? kTile : 0), tl + T_HI, tl + T_LO, (warp & 3) * 32,
-                            (warp >> 2) * 32, lane);
+                            sUpd + (w.len(it) < kTile ? kTile : 0), tl + T_C, (warp & 3) * 32, (warp >> 2) * 32, lane,
+                            terms);
             fence_before_sync();
             mbar_arrive(&bar.cv);
             return true;
