@@ -1842,8 +1842,8 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
     if (!saved) sums.r[sums.n++] = {nullptr, k, v, nullptr, 0, c.sk, c.sv, K, V, initial_state, nullptr, b.fwd, K, 1, 0};
     outs3.n = 3;
     outs3.r[0] = {d_o, v, k, dq, so, c.sv, c.sk, V, K, initial_state, nullptr, fwd, 1, K, 0};
-    outs3.r[1] = {v, d_o, q, dk, c.sv, so, c.sq, V, K, d_final_state, nullptr, b.rev, 1, K, 1};
-    outs3.r[2] = {k, q, d_o, dv, c.sk, c.sq, so, K, V, d_final_state, d_initial_state, b.rev, K, 1, 1};
+    outs3.r[1] = {v, d_o, q, dk, c.sv, so, c.sq, V, K, d_final_state, d_initial_state, b.rev, 1, K, 1};
+    outs3.r[2] = {k, q, d_o, dv, c.sk, c.sq, so, K, V, d_final_state, nullptr, b.rev, K, 1, 1};
     return run_la(c, elem_type(p->dtype), sums, outs3, cs);
 }
 

@@ -331,8 +331,7 @@ void la_segments(LaDims* d, InType ty, bool bwd);
 // One scan (see la.cu): out_r = sum of gamma^|r-s| (a_r . b_s) c_s, a and b of Db columns,
 // c and out of Dc; token strides in elements (out is dense).  M's element (c, b) is at
 // c * m_sc + b * m_sb of the caller's [V, K] matrices: m0 enters (or NULL), mT receives
-// the state that leaves (or NULL; given only where
-// M is the caller's matrix itself, m_sb = 1).  R [stream][nseg - 1][V][K] holds the segments' sums, of
+// the state that leaves (or NULL).  R [stream][nseg - 1][V][K] holds the segments' sums, of
 // the first nseg - 1 segments in the order of the scan, by position in time (against the
 // order of time segment i at i - 1); once linked, the state that enters segment i, at
 // i - 1, or against the order of time at i.

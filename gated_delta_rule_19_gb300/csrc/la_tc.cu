@@ -168,13 +168,21 @@ __device__ __forceinline__ void add_update(float (&m)[NC], uint32_t t_u, float g
     }
 }
 
-// The first `cols` of NC elements of M's row to a matrix with rows like M's (16-byte
-// stores: a lane's row is its own, and single ones took 8 us for a state).
+// The first `cols` of NC elements of M's row to the caller's matrix: 16 bytes at a time
+// where the row lies there as a row (single stores took 8 us for a state), else one by
+// one, with the lanes' elements side by side.
 template <int NC>
-__device__ __forceinline__ void store_state(const float (&m)[NC], float* dst, int cols) {
+__device__ __forceinline__ void store_state(const float (&m)[NC], float* dst, int step, int cols) {
 #pragma unroll
     for (int i = 0; i < NC; i += 4)
-        if (i < cols) *(float4*)(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        if (i < cols) {
+            if (step == 1) {
+                *(float4*)(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[(i + e) * step] = m[i + e];
+            }
+        }
 }
 
 // ------------------------------------------------------------------- the sums
@@ -293,7 +301,7 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             store_state(m,
                         const_cast<float*>(ro.R) + (w.stream * w.nseg + w.slot) * (int64_t)Db * Dc +
                             (int64_t)c * Db + part * 32,
-                        cols);
+                        1, cols);
     }
     __syncwarp();
     fence_before_sync();
@@ -406,7 +414,7 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
         }
     }
     if (ok && c < ro.Dc && ro.mT && w.seg == (w.rev ? 0 : d.nseg - 1))
-        store_state(m, ro.mT + w.stream * VK + (int64_t)c * ro.Db + b0, cols);
+        store_state(m, ro.mT + w.stream * VK + (int64_t)c * ro.m_sc + b0 * ro.m_sb, ro.m_sb, cols);
 }
 
 // The rows' warps: lane = token, half of the columns.
