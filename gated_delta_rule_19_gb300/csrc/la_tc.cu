@@ -277,12 +277,14 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     } else {
         const int c = tid & 127, part = warp >> 2, cols = Db - part * 32;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
+        const bool live = (warp & 3) * 32 < Dc;  // this warp's lanes have columns of C
         float m[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) m[i] = 0.f;
         auto make = [&](int it) {
             if (!warp_wait(&bar.full[it % SS_STAGES], (it / SS_STAGES) & 1, d.err, kErrState, d.wait_ns)) return false;
-            put_updates<32>(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes + kTileBytes,
+            if (live)
+                put_updates<32>(smem_u32(sm) + (uint32_t)(it % SS_STAGES) * 2 * kTileBytes + kTileBytes,
                             upd + (w.len(it) < kTile ? kTile : 0), tl + t_c(it), (warp & 3) * 32, part * 32, lane, 3);
             fence_before_sync();
             mbar_arrive(&bar.cv[it & 1]);
@@ -293,7 +295,7 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             if (it + 1 < tiles && !(ok = make(it + 1))) break;
             if (!(ok = warp_wait(&bar.u, it & 1, d.err, kErrState, d.wait_ns))) break;
             fence_after_sync();
-            add_update(m, tl + t_u + part * 32, pw[w.len(it)], cols);
+            add_update(m, tl + t_u + part * 32, pw[w.len(it)], live ? cols : 0);
             fence_before_sync();
             mbar_arrive(&bar.a);
         }
@@ -361,7 +363,8 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
                                             Make&& make) {
     const LaRole& ro = w.ro;
     const float* sPow = (const float*)(sm + S_POW);
-    const int c = threadIdx.x & 127, half = (threadIdx.x >> 7) - 2, b0 = half * 64, cols = ro.Db - b0;
+    const int c = threadIdx.x & 127, half = (threadIdx.x >> 7) - 2, b0 = half * 64;
+    const int cols = (c & ~31) < ro.Dc ? ro.Db - b0 : 0;  // none where the warp has no row of M
     float m[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) m[i] = 0.f;
@@ -667,7 +670,8 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         // C' of this warpgroup's 32 tokens of tile it
         auto make = [&](int it) {
             if (!warp_wait(&bar.full[it & 1], (it >> 1) & 1, d.err, kErrState, d.wait_ns)) return false;
-            put_updates<32>(smem_u32(sm) + (uint32_t)(it & 1) * 3 * kTileBytes + 2 * kTileBytes,
+            if ((warp & 3) * 32 < Dc)  // else this warp's lanes have no columns of C
+                put_updates<32>(smem_u32(sm) + (uint32_t)(it & 1) * 3 * kTileBytes + 2 * kTileBytes,
                             sUpd + (w.len(it) < kTile ? kTile : 0), tl + T_C, (warp & 3) * 32, (warp >> 2) * 32, lane,
                             terms);
             fence_before_sync();
