@@ -179,24 +179,26 @@ gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict_
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// dw[c] = sum over the blocks' rows of part, in a fixed order: a warp takes 32
-// columns' rows w, w + 8, ..., the warps' sums are added in order.  blockIdx.y picks
-// the side (part and dw of the queries, then of the keys).
+// dw[c] = sum over the blocks' rows of part, in a fixed order: a warp takes 32 columns'
+// rows w, w + 32, ..., the warps' sums are added in order.  blockIdx.y picks the side
+// (part and dw of the queries, then of the keys).  Bound by latency: 32 warps a block, so
+// that a thread's few loads are in flight together (8 warps took 9 us for 304 rows).
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 weight_sum_kernel(int blocks, int D, const float* __restrict__ part, T* __restrict__ dw0, T* __restrict__ dw1) {
-    __shared__ float sm[8][32];
+    __shared__ float sm[32][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     const float* p = part + (int64_t)blockIdx.y * blocks * D;
     float s = 0.f;
     if (c < D)
-#pragma unroll 8
-        for (int b = w; b < blocks; b += 8) s += p[(int64_t)b * D + c];
-    sm[w][threadIdx.x & 31] = s;
+#pragma unroll 10
+        for (int b = w; b < blocks; b += 32) s += p[(int64_t)b * D + c];
+    sm[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < D) {
-        for (int i = 1; i < 8; ++i) s += sm[i][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) s += sm[i][lane];
         store1((blockIdx.y ? dw1 : dw0) + c, s);
     }
 }
@@ -248,9 +250,9 @@ cudaError_t launch_weight_sum(int sides, int blocks, int D, InType ty, const flo
                               cudaStream_t st) {
     const dim3 grid((D + 31) / 32, sides);
     if (ty == InType::BF16)
-        return launch_dependent(weight_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, blocks, D, part,
+        return launch_dependent(weight_sum_kernel<__nv_bfloat16>, grid, 1024, 0, st, blocks, D, part,
                                 (__nv_bfloat16*)dw0, (__nv_bfloat16*)dw1);
-    return launch_dependent(weight_sum_kernel<float>, grid, 256, 0, st, blocks, D, part, (float*)dw0, (float*)dw1);
+    return launch_dependent(weight_sum_kernel<float>, grid, 1024, 0, st, blocks, D, part, (float*)dw0, (float*)dw1);
 }
 
 // Blocks of the backward kernels: all that fit on the GPU at once, never more than there
