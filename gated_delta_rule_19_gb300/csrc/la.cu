@@ -349,122 +349,116 @@ la_link_kernel(LaDims d, LaRoles roles) {
 
 // ------------------------------------------------------------ single tokens
 
-// N consecutive values (aligned to N elements) as floats, and N floats back.
-template <int N>
-__device__ __forceinline__ void ldn(const float* p, float (&f)[N]) {
-    if constexpr (N == 4) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
-    } else if constexpr (N == 2) {
-        const float2 x = __ldcs(reinterpret_cast<const float2*>(p));
-        f[0] = x.x, f[1] = x.y;
-    } else {
-        f[0] = __ldcs(p);
-    }
+// Four consecutive values (aligned to four elements) as floats.
+__device__ __forceinline__ void ld4(const float* p, float (&f)[4]) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
 }
-template <int N>
-__device__ __forceinline__ void ldn(const __nv_bfloat16* p, float (&f)[N]) {
-    if constexpr (N == 4) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        f[0] = __uint_as_float(x.x << 16), f[1] = __uint_as_float(x.x & 0xffff0000u);
-        f[2] = __uint_as_float(x.y << 16), f[3] = __uint_as_float(x.y & 0xffff0000u);
-    } else if constexpr (N == 2) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
-        f[0] = __uint_as_float(x << 16), f[1] = __uint_as_float(x & 0xffff0000u);
-    } else {
-        f[0] = __bfloat162float(*p);
-    }
+__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float (&f)[4]) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(x.x << 16), f[1] = __uint_as_float(x.x & 0xffff0000u);
+    f[2] = __uint_as_float(x.y << 16), f[3] = __uint_as_float(x.y & 0xffff0000u);
 }
-template <int N>
-__device__ __forceinline__ void stn(float* p, const float (&f)[N]) {
-    if constexpr (N == 4) __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    else if constexpr (N == 2) __stcs(reinterpret_cast<float2*>(p), make_float2(f[0], f[1]));
-    else __stcs(p, f[0]);
-}
+__device__ __forceinline__ float ld1(const float* p) { return *p; }
+__device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-constexpr int kRows = 8;  // state rows of a warp
-
-// The sums over the warp of 8 values a lane; lane l receives that of row
-// (l / 16) * 4 + (l / 8 % 2) * 2 + l / 4 % 2: at each of the first three steps a lane
-// keeps half of its values and hands on the others, 9 exchanges instead of 40.
-__device__ __forceinline__ float sum_rows(const float (&v)[kRows], int lane) {
-    float a[4], b[2], c;
+// Sums over each group of L lanes of R values a lane.  While a lane has several values
+// it keeps half of them at each step and hands on the others (R = 8, L = 32: 9 exchanges
+// instead of 40).  Leaves the sums of rows `first` .. `first` + kept - 1 in v[0 .. kept-1],
+// in the lanes where `writes`.
+template <int R, int L>
+struct RowSums {
+    static constexpr int kept = R > L ? R / L : 1;
+    int first = 0;
+    bool writes = true;
+    __device__ __forceinline__ RowSums(float (&v)[R], int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool up = lane & 16;
-        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
-    }
+        for (int off = L / 2, n = R; off > 0; off >>= 1) {
+            const bool up = lane & off;
+            if (n > 1) {
+                n >>= 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool up = lane & 8;
-        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+                for (int i = 0; i < n; ++i)
+                    v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], off);
+                first += up ? n : 0;
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+                writes = writes && !up;
+            }
+        }
     }
-    const bool up = lane & 4;
-    c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
-    c += __shfl_xor_sync(0xffffffffu, c, 2);
-    return c + __shfl_xor_sync(0xffffffffu, c, 1);
-}
+};
 
-// A warp holds kRows rows of one head's state in registers across the call's tokens,
-// lane l the K/32 columns from l K/32 on (K = 16: lanes 0-15, one column each).  Bound
-// by reading and writing the state once.
-template <typename T, int KPL>
+// A warp holds R * 32 / L rows of one head's state in registers across the call's tokens:
+// L = K / 4 lanes a row, four columns each, so that a load takes whole 128-byte lines
+// for any K.  Bound by reading and writing the state once.
+template <typename T, int L, int R>
 __global__ void __launch_bounds__(256)
 la_decode_kernel(LaDims d, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, int64_t sq,
                  int64_t sk, int64_t sv, float* __restrict__ state, T* __restrict__ o) {
-    const int lane = threadIdx.x & 31, groups = d.V / kRows, c0 = lane * KPL;
+    constexpr int K = 4 * L, W = 32 / L;  // rows of one load
+    const int lane = threadIdx.x & 31, groups = d.V / (R * W), c0 = lane % L * 4;
     const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (unit >= d.NS() * groups) return;
     const int64_t stream = unit / groups;
-    const int v0 = (int)(unit % groups) * kRows, h = (int)(stream % d.H);
+    const int v0 = (int)(unit % groups) * R * W + lane / L, h = (int)(stream % d.H);  // row of load r: v0 + r W
     const int64_t b = stream / d.H;
-    const bool live = c0 < d.K;
-    float* rows = state + (stream * d.V + v0) * d.K + c0;
-    float S[kRows][KPL];
+    float* rows = state + (stream * d.V + v0) * K + c0;
+    float S[R][4];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        if (live) ldn<KPL>(rows + r * d.K, S[r]);
-        else
-#pragma unroll
-            for (int i = 0; i < KPL; ++i) S[r][i] = 0.f;
+    for (int r = 0; r < R; ++r) {
+        const float4 x = __ldcs((const float4*)(rows + r * W * K));
+        S[r][0] = x.x, S[r][1] = x.y, S[r][2] = x.z, S[r][3] = x.w;
     }
     const float gamma = expf(d.log_decay[h]);
-    const int mine = (lane >> 4) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
     for (int t = 0; t < d.T; ++t) {
         const int64_t tok = b * d.T + t;
-        float kv[KPL] = {}, qv[KPL] = {}, vv[2][4], red[kRows];
-        if (live) {
-            ldn<KPL>(k + tok * sk + (int64_t)h * d.K + c0, kv);
-            ldn<KPL>(q + tok * sq + (int64_t)h * d.K + c0, qv);
-        }
-        ldn<4>(v + tok * sv + (int64_t)h * d.V + v0, vv[0]);
-        ldn<4>(v + tok * sv + (int64_t)h * d.V + v0 + 4, vv[1]);
+        float kv[4], qv[4], red[R];
+        ld4(k + tok * sk + (int64_t)h * K + c0, kv);
+        ld4(q + tok * sq + (int64_t)h * K + c0, qv);
+        const T* vp = v + tok * sv + (int64_t)h * d.V + v0;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < R; ++r) {
+            const float vr = ld1(vp + r * W);
             red[r] = 0.f;
 #pragma unroll
-            for (int i = 0; i < KPL; ++i) {
-                S[r][i] = fmaf(vv[r >> 2][r & 3], kv[i], gamma * S[r][i]);
+            for (int i = 0; i < 4; ++i) {
+                S[r][i] = fmaf(vr, kv[i], gamma * S[r][i]);
                 red[r] = fmaf(S[r][i], qv[i], red[r]);
             }
         }
-        const float sum = sum_rows(red, lane);
-        if ((lane & 3) == 0) st1(o + (tok * d.H + h) * d.V + v0 + mine, sum);
-    }
-    if (live)
+        const RowSums<R, L> sum(red, lane);
+        if (sum.writes) {
+            T* op = o + (tok * d.H + h) * d.V + v0 + sum.first * W;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) stn<KPL>(rows + r * d.K, S[r]);
+            for (int i = 0; i < sum.kept; ++i) st1(op + i * W, red[i]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        __stcs((float4*)(rows + r * W * K), make_float4(S[r][0], S[r][1], S[r][2], S[r][3]));
 }
 
+template <typename T, int L, int R>
+cudaError_t launch_decode_k(const LaDims& d, const void* q, const void* k, const void* v, int64_t sq, int64_t sk,
+                            int64_t sv, float* state, void* o, cudaStream_t st) {
+    const int64_t units = d.NS() * (d.V / (R * 32 / L));
+    la_decode_kernel<T, L, R><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(d, (const T*)q, (const T*)k, (const T*)v, sq,
+                                                                          sk, sv, state, (T*)o);
+    return cudaGetLastError();
+}
+
+// Eight loads a lane, or as many as the head's V rows give one warp.
 template <typename T>
 cudaError_t launch_decode_t(const LaDims& d, const void* q, const void* k, const void* v, int64_t sq, int64_t sk,
                             int64_t sv, float* state, void* o, cudaStream_t st) {
-    const unsigned grid = (unsigned)((d.NS() * (d.V / kRows) + 7) / 8);
-    const T *qp = (const T*)q, *kp = (const T*)k, *vp = (const T*)v;
-    if (d.K <= 32) la_decode_kernel<T, 1><<<grid, 256, 0, st>>>(d, qp, kp, vp, sq, sk, sv, state, (T*)o);
-    else if (d.K == 64) la_decode_kernel<T, 2><<<grid, 256, 0, st>>>(d, qp, kp, vp, sq, sk, sv, state, (T*)o);
-    else la_decode_kernel<T, 4><<<grid, 256, 0, st>>>(d, qp, kp, vp, sq, sk, sv, state, (T*)o);
-    return cudaGetLastError();
+    if (d.K == 128) return launch_decode_k<T, 32, 8>(d, q, k, v, sq, sk, sv, state, o, st);
+    if (d.K == 64) return launch_decode_k<T, 16, 8>(d, q, k, v, sq, sk, sv, state, o, st);
+    if (d.K == 32 && d.V >= 32) return launch_decode_k<T, 8, 8>(d, q, k, v, sq, sk, sv, state, o, st);
+    if (d.K == 32) return launch_decode_k<T, 8, 4>(d, q, k, v, sq, sk, sv, state, o, st);
+    if (d.V >= 64) return launch_decode_k<T, 4, 8>(d, q, k, v, sq, sk, sv, state, o, st);
+    if (d.V == 32) return launch_decode_k<T, 4, 4>(d, q, k, v, sq, sk, sv, state, o, st);
+    return launch_decode_k<T, 4, 2>(d, q, k, v, sq, sk, sv, state, o, st);
 }
 
 }  // namespace
