@@ -144,9 +144,9 @@ enum KernelId {
     KID_SPLIT_TRANS,     // scan_fwd_tc, transitions only (backward with saved)
     KID_SPLIT_COMBINE,   // pieces_kernel, combine_fwd_kernel, combine_bwd_kernel
     KID_COUNT_NONFINITE, // count_nonfinite_kernel
-    KID_LA_STATES,       // la_chunk_kernel, the segments' sums
+    KID_LA_STATES,       // la_sums_kernel, la_chunk_kernel: the segments' sums
     KID_LA_LINK,         // la_link_kernel, the states that enter the segments
-    KID_LA_SCAN,         // la_chunk_kernel, outputs or gradients
+    KID_LA_SCAN,         // la_scan_kernel, la_chunk_kernel: outputs or gradients
     KID_LA_DECODE,       // la_decode_kernel
     KID_NORM_ROPE_FWD,   // qk_norm_rope_fwd_kernel
     KID_NORM_ROPE_BWD,   // qk_norm_rope_bwd_kernel

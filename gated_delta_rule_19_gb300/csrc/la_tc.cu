@@ -43,6 +43,10 @@ constexpr int kTileBytes = kTile * 128 * 2;
 constexpr int kThreads = 576;  // 4 warpgroups, the TMA warp, the MMA warp
 constexpr int kTmaWarp = 16, kMmaWarp = 17;
 
+// Up to this many tiles a segment the scan moves its states in whole lines (see
+// la_scan_kernel).
+constexpr int kLinesMax = 8;
+
 // Error bits of the workspace's first int.
 constexpr int kErrTma = 1, kErrMma = 2, kErrRows = 4, kErrState = 8, kErrDrain = 16;
 
@@ -185,6 +189,57 @@ __device__ __forceinline__ void store_state(const float (&m)[NC], float* dst, in
         }
 }
 
+// A warp's 32 rows of a state (lane = row, NC columns each) from and to a matrix with
+// rows `ld` apart, of which `rows` rows and `cols` columns are there.  Whole 128-byte lines
+// go through 4 KB of the warp's own shared memory `sx`, its 16-byte pieces swizzled by
+// the row; lanes that read their own rows took 3.6 us for a state, each way.
+template <int NC>
+__device__ __forceinline__ void load_rows(float (&m)[NC], const float* src, int ld, int rows, int cols, float* sx,
+                                          int lane) {
+#pragma unroll
+    for (int p = 0; p < NC / 32; ++p) {
+        float4 t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), x = 32 * p + (lane & 7) * 4;
+            t[i] = r < rows && x < cols ? *(const float4*)(src + (int64_t)r * ld + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            *(float4*)(sx + r * 32 + ((lane ^ r) & 7) * 4) = t[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 f = *(const float4*)(sx + lane * 32 + ((j ^ lane) & 7) * 4);
+            float* to = m + 32 * p + 4 * j;
+            to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w;
+        }
+    }
+}
+template <int NC>
+__device__ __forceinline__ void store_rows(const float (&m)[NC], float* dst, int ld, int rows, int cols, float* sx,
+                                           int lane) {
+#pragma unroll
+    for (int p = 0; p < NC / 32; ++p) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float* from = m + 32 * p + 4 * j;
+            *(float4*)(sx + lane * 32 + ((j ^ lane) & 7) * 4) = make_float4(from[0], from[1], from[2], from[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), x = 32 * p + (lane & 7) * 4;
+            if (r < rows && x < cols)
+                *(float4*)(dst + (int64_t)r * ld + x) = *(const float4*)(sx + r * 32 + ((lane ^ r) & 7) * 4);
+        }
+    }
+}
+
 // ------------------------------------------------------------------- the sums
 
 struct __align__(8) SumBars {
@@ -275,7 +330,7 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         if (elect_one()) mma_commit(&bar.drain);  // no MMA outlives the CTA
         warp_wait(&bar.drain, 0, d.err, kErrDrain, 0);
     } else {
-        const int c = tid & 127, part = warp >> 2, cols = Db - part * 32;
+        const int part = warp >> 2, cols = Db - part * 32;
         const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);
         const bool live = (warp & 3) * 32 < Dc;  // this warp's lanes have columns of C
         float m[32];
@@ -299,11 +354,12 @@ la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             fence_before_sync();
             mbar_arrive(&bar.a);
         }
-        if (ok && c < Dc)
-            store_state(m,
-                        const_cast<float*>(ro.R) + (w.stream * w.nseg + w.slot) * (int64_t)Db * Dc +
-                            (int64_t)c * Db + part * 32,
-                        1, cols);
+        // every product is done with the stages: they serve the rows' way out
+        if (ok && live)
+            store_rows(m,
+                       const_cast<float*>(ro.R) + (w.stream * w.nseg + w.slot) * (int64_t)Db * Dc +
+                           (int64_t)(warp & 3) * 32 * Db + part * 32,
+                       Db, Dc - (warp & 3) * 32, cols, (float*)(sm + warp * 4096), lane);
     }
     __syncwarp();
     fence_before_sync();
@@ -357,14 +413,17 @@ __device__ __forceinline__ void scale_block(const uint32_t (&y)[32], float near,
     }
 }
 
-// The state's warps: lane c of M, half of the columns.
-template <typename Make>
+// The state's warps: lane c of M, half of the columns.  M's bf16 copy of a warp's rows
+// and columns is 4 KB in one piece, which its whole lines go through before and after.
+template <bool kLines, typename Make>
 __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars& bar, unsigned char* sm, uint32_t tl,
                                             Make&& make) {
     const LaRole& ro = w.ro;
     const float* sPow = (const float*)(sm + S_POW);
     const int c = threadIdx.x & 127, half = (threadIdx.x >> 7) - 2, b0 = half * 64;
     const int cols = (c & ~31) < ro.Dc ? ro.Db - b0 : 0;  // none where the warp has no row of M
+    const int lane = threadIdx.x & 31;
+    float* near = (float*)(sm + S_M) + ((threadIdx.x >> 5) - 8) * 1024;
     float m[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) m[i] = 0.f;
@@ -374,7 +433,9 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
     const bool first = w.seg == (w.rev ? d.nseg - 1 : 0);
     const float* src = first ? (ro.m0 ? ro.m0 + w.stream * VK : nullptr)
                              : ro.R + (w.stream * (d.nseg - 1) + (w.rev ? w.seg : w.seg - 1)) * VK;
-    if (src && c < ro.Dc) {
+    if (kLines && src && ro.m_sb == 1) {
+        load_rows(m, src + (int64_t)(c - lane) * ro.m_sc + b0, ro.m_sc, ro.Dc - (c - lane), cols, near, lane);
+    } else if (src && c < ro.Dc) {
         src += (int64_t)c * ro.m_sc + b0 * ro.m_sb;
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
@@ -416,8 +477,12 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
             ok = make(it + 1);
         }
     }
-    if (ok && c < ro.Dc && ro.mT && w.seg == (w.rev ? 0 : d.nseg - 1))
-        store_state(m, ro.mT + w.stream * VK + (int64_t)c * ro.m_sc + b0 * ro.m_sb, ro.m_sb, cols);
+    if (!ok || !ro.mT || w.seg != (w.rev ? 0 : d.nseg - 1)) return;
+    float* dst = ro.mT + w.stream * VK;
+    if (kLines && ro.m_sb == 1)
+        store_rows(m, dst + (int64_t)(c - lane) * ro.m_sc + b0, ro.m_sc, ro.Dc - (c - lane), cols, near, lane);
+    else if (c < ro.Dc)
+        store_state(m, dst + (int64_t)c * ro.m_sc + b0 * ro.m_sb, ro.m_sb, cols);
 }
 
 // The rows' warps: lane = token, half of the columns.
@@ -518,7 +583,12 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
 }
 
 // One CTA: one (stream, segment) of one role: its outputs and, from the last segment,
-// the state that leaves.
+// the state that leaves.  kLines: states that lie there as M does move in whole lines,
+// which saves 4.5 us a call (forward at K = V = 128: T128 H16 14.3 -> 9.9 us, B64 T1024
+// H2, 8 tiles a segment, 40.6 -> 36.7), but the compiler's loop over the tiles is then
+// 5 to 10% slower (T32768 H16, 29 tiles, 145 -> 152 us; B32 T4096 H6 K = V = 64 171 ->
+// 193), so it is for segments of few tiles.
+template <bool kLines>
 __global__ void __launch_bounds__(kThreads, 1)
 la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -678,7 +748,7 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
             mbar_arrive(&bar.cv);
             return true;
         };
-        if (warp >= 8) state_warps(d, w, bar, sm, tl, make);
+        if (warp >= 8) state_warps<kLines>(d, w, bar, sm, tl, make);
         else row_warps(d, w, bar, sm, tl, make);
     }
     __syncwarp();
@@ -700,6 +770,17 @@ bool make_maps(const LaDims& d, const LaRoles& roles, bool out, LaMaps* m) {
     return true;
 }
 
+template <bool kLines>
+cudaError_t launch_scan(const LaDims& d, const LaRoles& roles, const LaMaps& maps, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(la_scan_kernel<kLines>, S_SIZE, done);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(d.NS() * d.nseg), roles.n);
+    if (d.nseg > 1) return launch_dependent(la_scan_kernel<kLines>, grid, kThreads, S_SIZE, st, d, roles, maps);
+    la_scan_kernel<kLines><<<grid, kThreads, S_SIZE, st>>>(d, roles, maps);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
@@ -714,13 +795,7 @@ cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStrea
 cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     LaMaps maps;
     if (!make_maps(d, roles, true, &maps)) return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(la_scan_kernel, S_SIZE, done);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(d.NS() * d.nseg), roles.n);
-    if (d.nseg > 1) return launch_dependent(la_scan_kernel, grid, kThreads, S_SIZE, st, d, roles, maps);
-    la_scan_kernel<<<grid, kThreads, S_SIZE, st>>>(d, roles, maps);
-    return cudaGetLastError();
+    return d.L <= kLinesMax * kTile ? launch_scan<true>(d, roles, maps, st) : launch_scan<false>(d, roles, maps, st);
 }
 
 }  // namespace gdn
