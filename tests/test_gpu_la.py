@@ -88,6 +88,8 @@ CASES = [
     (1, 2049, 2, 16, 64, "f32", "none", False, False),
     (7, 200, 23, 32, 32, "bf16", "slopes", False, True),  # more streams than SMs
     (5, 150, 40, 16, 16, "f32", "slopes", False, True),
+    (1, 1100, 160, 128, 16, "bf16", "slopes", False, True),  # nine tiles a segment
+    (1, 1100, 160, 16, 128, "bf16", "slow", True, True),
 ]
 
 
