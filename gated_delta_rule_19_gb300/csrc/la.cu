@@ -1,4 +1,4 @@
-// la.cu -- linear attention with a fixed decay per head, on CUDA cores in 32 bits:
+// la.cu -- linear attention with a fixed decay per head: float32 inputs, and the step:
 //   S_t = gamma S_{t-1} + v_t k_t^T,   o_t = S_t q_t,   gamma = e^g, g <= 0, S [V, K],
 // chunked for prompts and training, and the recurrent step for single tokens.
 //
@@ -33,37 +33,79 @@ __device__ __forceinline__ float power(float g, float e) { return e > 0.f ? expf
 
 constexpr int kTok = 64;  // tokens of a chunk
 
-__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// A float32 product on the tensor cores: each factor is split into two tf32 numbers, its
+// rounding to 11 bits and the rest (which the product reads 11 bits of), and
+// x y = hi hi + (hi lo + lo hi); what is left out, lo lo, is 2^-22 of a product and of
+// either sign.  The hardware's sums round towards zero, so the small products have sums
+// of their own, and no sum runs over more than one chunk: what is carried from chunk to
+// chunk is added in float32.
+struct Sum {
+    float hi[4], lo[4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hi[i] = lo[i] = 0.f;
+    }
+    __device__ __forceinline__ float get(int i) const { return hi[i] + lo[i]; }
+};
+template <int N>
+struct Split {
+    uint32_t hi[N], lo[N];
+    __device__ __forceinline__ void set(int i, float x) {
+        hi[i] = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+        lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
+    }
+};
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// d[j] += a b[j]; the products of one sum are kept apart, each waits for the one before
+template <int N>
+__device__ __forceinline__ void mma8(Sum (&d)[N], const Split<4>& a, const Split<2> (&b)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma8(d[j].lo, a.lo, b[j].hi);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma8(d[j].hi, a.hi, b[j].hi);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma8(d[j].lo, a.hi, b[j].lo);
+}
 
-// Shared memory of the chunk kernel, in floats: rows of D (or 64) padded by four so
-// that the float4 reads of neighbouring rows fall into different banks.  Up to D = 64
-// two CTAs share an SM and hide each other's loads and reads; at 128 one has it alone and
-// two buffers of A, B, C, so that a chunk is loaded while the one before it is worked on.
+// Shared memory of the chunk kernel, in floats.  With rows 4 (mod 32) words apart, the
+// fragments read along a row (8 rows, 4 columns) and those read across rows 2 t, 2 t + 1
+// (the sum over tokens may take them in any order) fall into 32 banks; P and M's copy
+// have rows 8 apart for theirs.  Up to D = 64 two CTAs share an SM and hide each other's
+// loads; at 128 one has it alone and two buffers of A, B, C, so that a chunk is loaded
+// while the one before it is worked on.
 template <int D>
 struct Smem {
     static constexpr int CS = D < 64 ? D : 64;  // columns of c that one CTA carries
-    static constexpr int RA = D + 4, RC = CS + 4, RP = kTok + 4;
+    static constexpr int RA = D + 4, RC = CS + 4, RM = CS + 8, RP = kTok + 8;
     static constexpr int A = 0, B = A + kTok * RA, C = B + kTok * RA, BUF = C + kTok * RC;
-    static constexpr int NBUF = D > 64 ? 2 : 1, M = NBUF * BUF, P = M + D * RC, W = P + kTok * RP, SIZE = W + kTok + 8;
+    static constexpr int NBUF = D > 64 ? 2 : 1, M = NBUF * BUF, P = M + D * RM, W = P + kTok * RP, SIZE = W + kTok + 8;
 };
 static_assert(Smem<128>::SIZE * 4 <= 232448 && Smem<64>::SIZE * 8 <= 231424, "shared memory");
 
-// One CTA: one (stream, segment), CS columns of c, one role.  256 threads as 16 x 16:
-// thread (ty, tx) has rows 4 ty .. 4 ty + 3 and CS / 16 columns of each product, and in
-// registers M's rows (b) BV ty .. of every 16 BV; a copy in shared memory feeds A M^T.
-// The products run on pairs of columns (f32x2), which leaves issue slots for the reads.
+// One CTA: one (stream, segment), CS columns of c, one role.  Eight warps: for the scores
+// and the outputs 4 groups of 16 rows by 2 halves of the columns, for M RG groups of
+// rows (b) by CG of columns; a warp's part of M stays in its registers, and a copy in
+// shared memory feeds A M^T.  Warps w and w + 4, which share a scheduler, have row groups
+// w and 3 - w, so that what the causal mask leaves out is shared evenly.
 template <int D, bool kOut>
 __global__ void __launch_bounds__(256, D > 64 ? 1 : 2)
 la_chunk_kernel(LaDims d, LaRoles roles) {
     using L = Smem<D>;
-    constexpr int CT = L::CS / 16, CP = (CT + 1) / 2;  // columns of c per thread, pairs of them
-    constexpr int BV = D < 64 ? D / 16 : 4, BG = D / (16 * BV);  // rows of b per thread: BG groups of BV
+    constexpr int RG = D < 64 ? D / 16 : 4, MT = D / 16 / RG;                  // M: groups of rows, tiles in each
+    constexpr int CG = 8 / RG < L::CS / 8 ? 8 / RG : L::CS / 8, NM = L::CS / 8 / CG;  // and of columns
+    constexpr int NO = L::CS / 16;                                             // column tiles of the outputs
     extern __shared__ __align__(16) float sm[];
     float *sM = sm + L::M, *sP = sm + L::P, *sW = sm + L::W;
     const LaRole& ro = roles.r[blockIdx.z];
     const int c0 = blockIdx.y * L::CS;
     if (c0 >= ro.Dc) return;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const int nseg = kOut ? d.nseg : d.nseg - 1;  // the last segment's own sum feeds nobody
     const int64_t stream = blockIdx.x / nseg;
     const int slot = (int)(blockIdx.x % nseg);
@@ -101,51 +143,34 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     };
     load(0);
 
-    // The state that enters: M[c][b] of the caller's [V, K] matrices by strides.
-    auto row_b = [&](int gi, int i) { return gi * 16 * BV + ty * BV + i; };
-    uint64_t m[BG][BV][CP];
+    // M[c][b] of the caller's [V, K] matrices by strides: this warp's tiles of 16 rows (b)
+    // by 8 columns (c).  A lane has rows gq and gq + 8, columns 2 tq and 2 tq + 1 of a tile.
+    const int mg = warp / CG, mc = warp % CG;
+    const bool carries = RG * CG == 8 || warp < RG * CG;
+    float m[MT][NM][4];
+    auto row_b = [&](int x) { return (x * RG + mg) * 16 + gq; };
+    auto col_c = [&](int j) { return (mc * NM + j) * 8 + 2 * tq; };
+    auto each = [&](auto&& f) {  // f(row, column within the CTA's, element)
 #pragma unroll
-    for (int gi = 0; gi < BG; ++gi)
+        for (int x = 0; x < MT; ++x)
 #pragma unroll
-        for (int i = 0; i < BV; ++i)
+            for (int j = 0; j < NM; ++j)
 #pragma unroll
-            for (int j = 0; j < CP; ++j) m[gi][i][j] = twice(0.f);
-    // f(row of b, column of c, value) over this thread's part of M
-    auto each = [&](auto&& f) {
-#pragma unroll
-        for (int gi = 0; gi < BG; ++gi)
-#pragma unroll
-            for (int i = 0; i < BV; ++i)
-#pragma unroll
-                for (int j = 0; j < CT; j += 2) {
-                    float x, y;
-                    unpair(m[gi][i][j / 2], x, y);
-                    const int bb = row_b(gi, i), cc = c0 + tx * CT + j;
-                    if (bb < ro.Db && cc < ro.Dc) f(bb, cc, x);
-                    if (CT > 1 && bb < ro.Db && cc + 1 < ro.Dc) f(bb, cc + 1, y);
-                    m[gi][i][j / 2] = pair(x, y);
-                }
+                for (int e = 0; e < 4; ++e) f(row_b(x) + 8 * (e >> 1), col_c(j) + (e & 1), m[x][j][e]);
     };
-    if (kOut) {
+    each([](int, int, float& x) { x = 0.f; });
+    if (kOut && carries) {
         const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
         const int64_t VK = (int64_t)ro.Db * ro.Dc;
         const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
                                  : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
-        if (src) each([&](int bb, int cc, float& x) { x = src[cc * ro.m_sc + bb * ro.m_sb]; });
+        if (src)
+            each([&](int bb, int cc, float& x) {
+                if (bb < ro.Db && cc < cw) x = src[(c0 + cc) * ro.m_sc + bb * ro.m_sb];
+            });
     }
 
-    // this thread's CT columns of a row of C or M, as pairs
-    auto cols_of = [&](const float* row, uint64_t (&v)[CP]) {
-        if constexpr (CT == 4) {
-            const float4 x = lds4(row + tx * 4);
-            v[0] = pair(x.x, x.y), v[1] = pair(x.z, x.w);
-        } else if constexpr (CT == 2) {
-            const float2 x = *(const float2*)(row + tx * 2);
-            v[0] = pair(x.x, x.y);
-        } else {
-            v[0] = pair(row[tx], 0.f);
-        }
-    };
+    const int r0 = (warp < 4 ? warp : 7 - warp) * 16, half = warp >> 2;  // rows and half of the columns
     for (int it = 0; it < chunks; ++it) {
         const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
         const float *sA = sm + it % L::NBUF * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
@@ -154,142 +179,147 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             load(it);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (kOut) {
+        if (kOut && carries) {
 #pragma unroll
-            for (int gi = 0; gi < BG; ++gi)
+            for (int x = 0; x < MT; ++x)
 #pragma unroll
-                for (int i = 0; i < BV; ++i)
+                for (int j = 0; j < NM; ++j)
 #pragma unroll
-                    for (int j = 0; j < CT; j += 2) {
-                        float x, y;
-                        unpair(m[gi][i][j / 2], x, y);
-                        float* to = sM + row_b(gi, i) * L::RC + tx * CT + j;
-                        to[0] = x;
-                        if (CT > 1) to[1] = y;
-                    }
+                    for (int e = 0; e < 4; e += 2)
+                        *(float2*)(sM + (row_b(x) + 4 * e) * L::RM + col_c(j)) = make_float2(m[x][j][e], m[x][j][e + 1]);
         }
         __syncthreads();  // this chunk is there, the other buffer and P are free
         if (L::NBUF == 2 && it + 1 < chunks) load(it + 1);
 
-        uint64_t acc[4][CP];
         if (kOut) {
-            // scores: rows 4 ty + i, columns tx + 16 j; pairs of the sum's terms
-            uint64_t p[4][4];
+            auto rows_a = [&](int k, Split<4>& a) {  // A's fragment: rows r0 .. r0 + 15, columns k .. k + 7
+                const float* at = sA + (r0 + gq) * L::RA + k + tq;
+                a.set(0, at[0]), a.set(1, at[8 * L::RA]), a.set(2, at[4]), a.set(3, at[8 * L::RA + 4]);
+            };
+            {  // scores, where the mask leaves some of this warp's
+                Sum y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[i][j] = twice(0.f);
+                for (int j = 0; j < 4; ++j) y[j].zero();
+                if (ro.rev ? half * 32 + 31 >= r0 : half * 32 <= r0 + 15) {
 #pragma unroll 4
-            for (int x = 0; x < D; x += 4) {
-                float4 av[4];
+                    for (int k = 0; k < D; k += 8) {
+                        Split<4> a;
+                        Split<2> f[4];
+                        rows_a(k, a);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) av[i] = lds4(sA + (4 * ty + i) * L::RA + x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 bv = lds4(sB + (tx + 16 * j) * L::RA + x);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[i][j] = fma2(pair(av[i].x, av[i].y), pair(bv.x, bv.y), p[i][j]);
-                        p[i][j] = fma2(pair(av[i].z, av[i].w), pair(bv.z, bv.w), p[i][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float* at = sB + (half * 32 + j * 8 + gq) * L::RA + k + tq;
+                            f[j].set(0, at[0]), f[j].set(1, at[4]);
+                        }
+                        mma8(y, a, f);
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const int r = r0 + gq + 4 * e, s = half * 32 + j * 8 + 2 * tq, dist = ro.rev ? s - r : r - s;
+                        const int next = ro.rev ? dist + 1 : dist - 1;
+                        *(float2*)(sP + r * L::RP + s) =
+                            make_float2(dist >= 0 ? y[j].get(e) * sW[dist] : 0.f,
+                                        next >= 0 ? y[j].get(e + 1) * sW[next] : 0.f);
+                    }
+            }
+            Sum o[NO];
+#pragma unroll
+            for (int j = 0; j < NO; ++j) o[j].zero();
+            const int cb = half * (L::CS / 2) + gq;
+            // A M^T, the state that entered the chunk
+#pragma unroll 4
+            for (int k = 0; k < D; k += 8) {
+                Split<4> a;
+                Split<2> f[NO];
+                rows_a(k, a);
+#pragma unroll
+                for (int j = 0; j < NO; ++j) {
+                    const float* at = sM + (k + tq) * L::RM + cb + j * 8;
+                    f[j].set(0, at[0]), f[j].set(1, at[4 * L::RM]);
+                }
+                mma8(o, a, f);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; e += 2) {
+                const int r = r0 + gq + 4 * e;
+                const float w = sW[max(ro.rev ? n - 1 - r : r + 1, 0)];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 4 * ty + i, s = tx + 16 * j, dist = ro.rev ? s - r : r - s;
-                    sP[r * L::RP + s] = dist >= 0 ? sum2(p[i][j]) * sW[dist] : 0.f;
-                }
-            // rows times a matrix of CS columns: acc += X[4 ty + i][x] R[x][columns]
-            auto product = [&](const float* X, int rx, const float* R, int len) {
-#pragma unroll 2
-                for (int x = 0; x < len; x += 4) {
-                    float av[4][4];
+                for (int j = 0; j < NO; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = lds4(X + (4 * ty + i) * rx + x);
-                        av[i][0] = f.x, av[i][1] = f.y, av[i][2] = f.z, av[i][3] = f.w;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint64_t v[CP];
-                        cols_of(R + (x + e) * L::RC, v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < CP; ++j) acc[i][j] = fma2(twice(av[i][e]), v[j], acc[i][j]);
-                    }
-                }
-            };
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < CP; ++j) acc[i][j] = twice(0.f);
-            product(sA, L::RA, sM, D);  // A M^T, the state that entered the chunk
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * ty + i, e = ro.rev ? n - 1 - r : r + 1;
-                const uint64_t w = twice(sW[max(e, 0)]);
-#pragma unroll
-                for (int j = 0; j < CP; ++j) acc[i][j] = mul2(acc[i][j], w);
+                    for (int i = e; i < e + 2; ++i) o[j].hi[i] *= w, o[j].lo[i] *= w;
             }
             __syncthreads();
-            product(sP, L::RP, sC, kTok);
+            const int s_lo = ro.rev ? r0 : 0, s_hi = ro.rev ? kTok : r0 + 16;
+#pragma unroll 2
+            for (int s = s_lo; s < s_hi; s += 8) {
+                const float2 x = *(const float2*)(sP + (r0 + gq) * L::RP + s + 2 * tq),
+                             z = *(const float2*)(sP + (r0 + gq + 8) * L::RP + s + 2 * tq);
+                Split<4> a;
+                Split<2> f[NO];
+                a.set(0, x.x), a.set(1, z.x), a.set(2, x.y), a.set(3, z.y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * ty + i;
-                float* to = po + (int64_t)(t0 + r) * d.H * ro.Dc + tx * CT;
-                float f[2 * CP];
-#pragma unroll
-                for (int j = 0; j < CP; ++j) unpair(acc[i][j], f[2 * j], f[2 * j + 1]);
-                if (r < n && tx * CT < cw) {
-                    if constexpr (CT == 4) *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
-                    else if constexpr (CT == 2) *(float2*)to = make_float2(f[0], f[1]);
-                    else to[0] = f[0];
+                for (int j = 0; j < NO; ++j) {
+                    const float* at = sC + (s + 2 * tq) * L::RC + cb + j * 8;
+                    f[j].set(0, at[0]), f[j].set(1, at[L::RC]);
                 }
+                mma8(o, a, f);
             }
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int r = r0 + gq + 4 * e, c = half * (L::CS / 2) + j * 8 + 2 * tq;
+                    if (r < n && c < cw)
+                        *(float2*)(po + (int64_t)(t0 + r) * d.H * ro.Dc + c) = make_float2(o[j].get(e), o[j].get(e + 1));
+                }
         }
         // M <- gamma^n M + sum of gamma^(n-1-rho+rev) b c^T
-        const uint64_t gn = twice(sW[n]);
+        if (carries) {
+            Sum u[MT][NM];
 #pragma unroll
-        for (int gi = 0; gi < BG; ++gi)
+            for (int x = 0; x < MT; ++x)
 #pragma unroll
-            for (int i = 0; i < BV; ++i)
+                for (int j = 0; j < NM; ++j) u[x][j].zero();
+#pragma unroll 2
+            for (int s = 0; s < n; s += 8) {
+                const int s0 = s + 2 * tq;
+                const float w0 = sW[ro.rev ? s0 + 1 : max(n - 1 - s0, 0)], w1 = sW[ro.rev ? s0 + 2 : max(n - 2 - s0, 0)];
+                Split<4> a[MT];
 #pragma unroll
-                for (int j = 0; j < CP; ++j) m[gi][i][j] = mul2(m[gi][i][j], gn);
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-            const uint64_t w = twice(sW[ro.rev ? s + 1 : n - 1 - s]);
-            uint64_t v[CP];
-            cols_of(sC + s * L::RC, v);
+                for (int x = 0; x < MT; ++x) {
+                    const float* at = sB + s0 * L::RA + row_b(x);
+                    a[x].set(0, at[0]), a[x].set(1, at[8]), a[x].set(2, at[L::RA]), a[x].set(3, at[L::RA + 8]);
+                }
+                Split<2> f[NM];
 #pragma unroll
-            for (int j = 0; j < CP; ++j) v[j] = mul2(v[j], w);
-#pragma unroll
-            for (int gi = 0; gi < BG; ++gi) {
-                float bv[BV];
-                const float* row = sB + s * L::RA + row_b(gi, 0);
-                if constexpr (BV == 4) {
-                    const float4 x = lds4(row);
-                    bv[0] = x.x, bv[1] = x.y, bv[2] = x.z, bv[3] = x.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < BV; ++i) bv[i] = row[i];
+                for (int j = 0; j < NM; ++j) {
+                    const float* at = sC + s0 * L::RC + (mc * NM + j) * 8 + gq;
+                    f[j].set(0, at[0] * w0), f[j].set(1, at[L::RC] * w1);
                 }
 #pragma unroll
-                for (int i = 0; i < BV; ++i)
-#pragma unroll
-                    for (int j = 0; j < CP; ++j) m[gi][i][j] = fma2(twice(bv[i]), v[j], m[gi][i][j]);
+                for (int x = 0; x < MT; ++x) mma8(u[x], a[x], f);
             }
+            const float gn = sW[n];
+#pragma unroll
+            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                for (int j = 0; j < NM; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[x][j][e] = fmaf(m[x][j][e], gn, u[x][j].get(e));
         }
     }
 
     // What leaves: a segment's own sum, or the state behind the last one.
     const bool last = kOut && ro.mT && seg == (ro.rev ? 0 : d.nseg - 1);
-    if (!kOut || last) {
+    if (carries && (!kOut || last)) {
         const int64_t VK = (int64_t)ro.Db * ro.Dc;
         float* dst = kOut ? ro.mT + stream * VK : const_cast<float*>(ro.R) + (stream * nseg + slot) * VK;
-        each([&](int bb, int cc, float& x) { dst[cc * ro.m_sc + bb * ro.m_sb] = x; });
+        each([&](int bb, int cc, float& x) {
+            if (bb < ro.Db && cc < cw) dst[(c0 + cc) * ro.m_sc + bb * ro.m_sb] = x;
+        });
     }
 }
 
