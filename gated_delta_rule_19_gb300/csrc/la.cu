@@ -84,6 +84,7 @@ struct Smem {
     static constexpr int CS = D < 64 ? D : 64;  // columns of c that one CTA carries
     static constexpr int RA = D + 4, RC = CS + 4, RM = CS + 8, RP = kTok + 8;
     static constexpr int A = 0, B = A + kTok * RA, C = B + kTok * RA, BUF = C + kTok * RC;
+    static constexpr int THREADS = D > 64 ? 512 : 256, COLS = THREADS / 128;  // groups of columns
     static constexpr int NBUF = D > 64 ? 2 : 1, M = NBUF * BUF, P = M + D * RM, W = P + kTok * RP, SIZE = W + kTok + 8;
 };
 static_assert(Smem<128>::SIZE * 4 <= 232448 && Smem<64>::SIZE * 8 <= 231424, "shared memory");
@@ -94,12 +95,13 @@ static_assert(Smem<128>::SIZE * 4 <= 232448 && Smem<64>::SIZE * 8 <= 231424, "sh
 // shared memory feeds A M^T.  Warps w and w + 4, which share a scheduler, have row groups
 // w and 3 - w, so that what the causal mask leaves out is shared evenly.
 template <int D, bool kOut>
-__global__ void __launch_bounds__(256, D > 64 ? 1 : 2)
+__global__ void __launch_bounds__(Smem<D>::THREADS, D > 64 ? 1 : 2)
 la_chunk_kernel(LaDims d, LaRoles roles) {
     using L = Smem<D>;
     constexpr int RG = D < 64 ? D / 16 : 4, MT = D / 16 / RG;                  // M: groups of rows, tiles in each
-    constexpr int CG = 8 / RG < L::CS / 8 ? 8 / RG : L::CS / 8, NM = L::CS / 8 / CG;  // and of columns
-    constexpr int NO = L::CS / 16;                                             // column tiles of the outputs
+    constexpr int WARPS = L::THREADS / 32, CM = L::CS / 8;
+    constexpr int CG = WARPS / RG < CM ? WARPS / RG : CM, NM = CM / CG;        // and of columns
+    constexpr int NO = CM / L::COLS, NY = kTok / 8 / L::COLS;                  // column tiles of outputs, scores
     extern __shared__ __align__(16) float sm[];
     float *sM = sm + L::M, *sP = sm + L::P, *sW = sm + L::W;
     const LaRole& ro = roles.r[blockIdx.z];
@@ -114,7 +116,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     const float g = d.log_decay[h];
     const int t_lo = seg * d.L, t_hi = min(d.T, t_lo + d.L);
     const int chunks = (t_hi - t_lo + kTok - 1) / kTok;
-    for (int e = tid; e <= kTok; e += 256) sW[e] = power(g, (float)e);
+    for (int e = tid; e <= kTok; e += L::THREADS) sW[e] = power(g, (float)e);
 
     const float* pa = (const float*)ro.a + (int64_t)b * d.T * ro.sa + (int64_t)h * ro.Db;
     const float* pb = (const float*)ro.b + (int64_t)b * d.T * ro.sb + (int64_t)h * ro.Db;
@@ -127,7 +129,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
         const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
         float* buf = sm + it % L::NBUF * L::BUF;
         auto rows = [&](float* to, int stride, const float* from, int64_t step, int width, int cols) {
-            for (int i = tid; i < kTok * (width / 4); i += 256) {
+            for (int i = tid; i < kTok * (width / 4); i += L::THREADS) {
                 const int r = i / (width / 4), x = (i % (width / 4)) * 4;
                 const bool in = r < n && x < cols;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -146,7 +148,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     // M[c][b] of the caller's [V, K] matrices by strides: this warp's tiles of 16 rows (b)
     // by 8 columns (c).  A lane has rows gq and gq + 8, columns 2 tq and 2 tq + 1 of a tile.
     const int mg = warp / CG, mc = warp % CG;
-    const bool carries = RG * CG == 8 || warp < RG * CG;
+    const bool carries = RG * CG == WARPS || warp < RG * CG;
     float m[MT][NM][4];
     auto row_b = [&](int x) { return (x * RG + mg) * 16 + gq; };
     auto col_c = [&](int j) { return (mc * NM + j) * 8 + 2 * tq; };
@@ -170,7 +172,8 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             });
     }
 
-    const int r0 = (warp < 4 ? warp : 7 - warp) * 16, half = warp >> 2;  // rows and half of the columns
+    const int part = warp >> 2, r0 = (part & 1 ? 3 - (warp & 3) : warp & 3) * 16;  // group of columns, first row
+    const int y0 = part * NY * 8, o0 = part * NO * 8;                             // first columns
     for (int it = 0; it < chunks; ++it) {
         const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
         const float *sA = sm + it % L::NBUF * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
@@ -197,28 +200,28 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
                 a.set(0, at[0]), a.set(1, at[8 * L::RA]), a.set(2, at[4]), a.set(3, at[8 * L::RA + 4]);
             };
             {  // scores, where the mask leaves some of this warp's
-                Sum y[4];
+                Sum y[NY];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j].zero();
-                if (ro.rev ? half * 32 + 31 >= r0 : half * 32 <= r0 + 15) {
+                for (int j = 0; j < NY; ++j) y[j].zero();
+                if (ro.rev ? y0 + NY * 8 > r0 : y0 <= r0 + 15) {
 #pragma unroll 4
                     for (int k = 0; k < D; k += 8) {
                         Split<4> a;
-                        Split<2> f[4];
+                        Split<2> f[NY];
                         rows_a(k, a);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float* at = sB + (half * 32 + j * 8 + gq) * L::RA + k + tq;
+                        for (int j = 0; j < NY; ++j) {
+                            const float* at = sB + (y0 + j * 8 + gq) * L::RA + k + tq;
                             f[j].set(0, at[0]), f[j].set(1, at[4]);
                         }
                         mma8(y, a, f);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < NY; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
-                        const int r = r0 + gq + 4 * e, s = half * 32 + j * 8 + 2 * tq, dist = ro.rev ? s - r : r - s;
+                        const int r = r0 + gq + 4 * e, s = y0 + j * 8 + 2 * tq, dist = ro.rev ? s - r : r - s;
                         const int next = ro.rev ? dist + 1 : dist - 1;
                         *(float2*)(sP + r * L::RP + s) =
                             make_float2(dist >= 0 ? y[j].get(e) * sW[dist] : 0.f,
@@ -228,7 +231,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             Sum o[NO];
 #pragma unroll
             for (int j = 0; j < NO; ++j) o[j].zero();
-            const int cb = half * (L::CS / 2) + gq;
+            const int cb = o0 + gq;
             // A M^T, the state that entered the chunk
 #pragma unroll 4
             for (int k = 0; k < D; k += 8) {
@@ -271,7 +274,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             for (int j = 0; j < NO; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
-                    const int r = r0 + gq + 4 * e, c = half * (L::CS / 2) + j * 8 + 2 * tq;
+                    const int r = r0 + gq + 4 * e, c = o0 + j * 8 + 2 * tq;
                     if (r < n && c < cw)
                         *(float2*)(po + (int64_t)(t0 + r) * d.H * ro.Dc + c) = make_float2(o[j].get(e), o[j].get(e + 1));
                 }
@@ -331,7 +334,7 @@ cudaError_t launch_chunk(const LaDims& d, const LaRoles& roles, cudaStream_t st)
     cudaError_t e = allow_smem(la_chunk_kernel<D, kOut>, (int)smem, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * (kOut ? d.nseg : d.nseg - 1)), D / L::CS, roles.n);
-    la_chunk_kernel<D, kOut><<<grid, 256, smem, st>>>(d, roles);
+    la_chunk_kernel<D, kOut><<<grid, L::THREADS, smem, st>>>(d, roles);
     return cudaGetLastError();
 }
 
