@@ -35,10 +35,16 @@ constexpr int kTok = 64;  // tokens of a chunk
 
 // A float32 product on the tensor cores: each factor is split into two tf32 numbers, its
 // rounding to 11 bits and the rest (which the product reads 11 bits of), and
-// x y = hi hi + (hi lo + lo hi); what is left out, lo lo, is 2^-22 of a product and of
-// either sign.  The hardware's sums round towards zero, so the small products have sums
-// of their own, and no sum runs over more than one chunk: what is carried from chunk to
-// chunk is added in float32.
+// x y = hi hi + (hi lo + lo hi); what is left out, lo lo, is below 2^-22 of a product and
+// of either sign.  (Cutting instead of rounding saves 5% of the time, but leaves a lo lo
+// of one sign.)  The small products have sums of their own, and no sum on the tensor
+// cores runs over more than one chunk: what is carried from chunk to chunk is added in
+// float32.  Results are within 5e-7 of the value (relative L2, T up to 4096), as
+// sums in float32 are.
+//
+// These warp-level products run at 512 a cycle and SM, which three tf32 products for one
+// make 170; float32 arithmetic has 128, of which its operands' reads from shared memory
+// left about half (B4 T2048 H6 K = V = 128 forward 197 us, now 144).
 struct Sum {
     float hi[4], lo[4];
     __device__ __forceinline__ void zero() {
@@ -93,7 +99,9 @@ static_assert(Smem<128>::SIZE * 4 <= 232448 && Smem<64>::SIZE * 8 <= 231424, "sh
 // and the outputs 4 groups of 16 rows by 2 halves of the columns, for M RG groups of
 // rows (b) by CG of columns; a warp's part of M stays in its registers, and a copy in
 // shared memory feeds A M^T.  Warps w and w + 4, which share a scheduler, have row groups
-// w and 3 - w, so that what the causal mask leaves out is shared evenly.
+// w and 3 - w, so that what the causal mask leaves out is shared evenly.  (At 128 columns
+// sixteen warps of half the columns each: 1 to 7% less time.)  Bound by the warps' issue
+// and the tensor pipe together: 61 and 54% of their rates where two CTAs share an SM.
 template <int D, bool kOut>
 __global__ void __launch_bounds__(Smem<D>::THREADS, D > 64 ? 1 : 2)
 la_chunk_kernel(LaDims d, LaRoles roles) {
@@ -204,7 +212,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
 #pragma unroll
                 for (int j = 0; j < NY; ++j) y[j].zero();
                 if (ro.rev ? y0 + NY * 8 > r0 : y0 <= r0 + 15) {
-#pragma unroll 4
+#pragma unroll 8
                     for (int k = 0; k < D; k += 8) {
                         Split<4> a;
                         Split<2> f[NY];
@@ -233,7 +241,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             for (int j = 0; j < NO; ++j) o[j].zero();
             const int cb = o0 + gq;
             // A M^T, the state that entered the chunk
-#pragma unroll 4
+#pragma unroll 8
             for (int k = 0; k < D; k += 8) {
                 Split<4> a;
                 Split<2> f[NO];
@@ -256,7 +264,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             }
             __syncthreads();
             const int s_lo = ro.rev ? r0 : 0, s_hi = ro.rev ? kTok : r0 + 16;
-#pragma unroll 2
+#pragma unroll 4
             for (int s = s_lo; s < s_hi; s += 8) {
                 const float2 x = *(const float2*)(sP + (r0 + gq) * L::RP + s + 2 * tq),
                              z = *(const float2*)(sP + (r0 + gq + 8) * L::RP + s + 2 * tq);
@@ -286,7 +294,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
             for (int x = 0; x < MT; ++x)
 #pragma unroll
                 for (int j = 0; j < NM; ++j) u[x][j].zero();
-#pragma unroll 2
+#pragma unroll 4
             for (int s = 0; s < n; s += 8) {
                 const int s0 = s + 2 * tq;
                 const float w0 = sW[ro.rev ? s0 + 1 : max(n - 1 - s0, 0)], w1 = sW[ro.rev ? s0 + 2 : max(n - 2 - s0, 0)];
@@ -513,13 +521,14 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
                               : launch_decode_t<float>(d, q, k, v, sq, sk, sv, state, o, st);
 }
 
-// How a call cuts its sequences, in whole tiles (128 tokens on the tensor cores, a chunk
-// of 64 on CUDA cores): the cut with the least estimated time, in units of a tile of the
+// How a call cuts its sequences, in whole tiles (128 tokens of bf16, a chunk of 64 of
+// float32): the cut with the least estimated time, in units of a tile of the
 // scan.  A CTA takes its tiles one after the other behind a fixed part (launch, first
 // loads, the state that enters); the CTAs go in waves of as many as the GPU holds; with
-// several segments the sums and the link come first.  On the tensor cores a tile takes
-// 2.4 us alone, the fixed parts 11 us (scan) and 2 us each (sums, link), a tile of the
-// sums 0.9 us; on CUDA cores a chunk of K = V = 64 takes 9 us and the fixed parts less.
+// several segments the sums and the link come first.  In bf16 a tile takes 2.4 us
+// alone, the fixed parts 11 us (scan) and 2 us each (sums, link), a tile of the sums
+// 0.9 us; in float32 a chunk of K = V = 64 takes 6 us and the fixed parts about as much
+// together.
 // The backward's three scans want fewer segments than the forward's one; but cut like
 // the forward's it can take over the forward's sums (`saved`).
 namespace {
