@@ -374,7 +374,6 @@ constexpr uint32_t T_X = 0, T_Y = 128, T_U = 128, T_P = 256, T_C = 320;
 
 struct __align__(8) Bars {
     uint64_t full[2];   // TMA: the stage's tiles have landed
-    uint64_t free[2];   // the products have read the stage
     uint64_t staged[2]; // the outputs lie over the stage's A (256 arrivals)
     uint64_t cv;        // C' is in tensor memory (512 arrivals)
     uint64_t u;         // U is complete
@@ -603,15 +602,16 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     const int terms = last && ro.mT ? 3 : 2;
     const int nb = Db > 64 ? 2 : 1, nc = Dc > 64 ? 2 : 1;
     auto stage = [&](int it) { return sm + (it & 1) * 3 * kTileBytes; };
-    auto load = [&](int it, const CUtensorMap* map, int blocks, unsigned char* to) {
-        for (int i = 0; i < blocks; ++i)
-            tma_load_4d(to + i * (kTileBytes / 2), map, &bar.full[it & 1], 64 * i, w.h, w.t0(it), w.b);
-    };
-    auto load_a = [&](int it) { load(it, &maps.a[w.rl], nb, stage(it)); };
-    auto load_bc = [&](int it) {
-        mbar_arrive_expect_tx(&bar.full[it & 1], (uint32_t)((2 * nb + nc) * (kTileBytes / 2)));
-        load(it, &maps.b[w.rl], nb, stage(it) + kTileBytes);
-        load(it, &maps.c[w.rl], nc, stage(it) + 2 * kTileBytes);
+    auto load = [&](int it) {
+        uint64_t* full = &bar.full[it & 1];
+        mbar_arrive_expect_tx(full, (uint32_t)((2 * nb + nc) * (kTileBytes / 2)));
+        auto put = [&](const CUtensorMap* map, int blocks, unsigned char* to) {
+            for (int i = 0; i < blocks; ++i)
+                tma_load_4d(to + i * (kTileBytes / 2), map, full, 64 * i, w.h, w.t0(it), w.b);
+        };
+        put(&maps.b[w.rl], nb, stage(it) + kTileBytes);
+        put(&maps.c[w.rl], nc, stage(it) + 2 * kTileBytes);
+        put(&maps.a[w.rl], nb, stage(it));
     };
 
     if (warp == kMmaWarp) {
@@ -620,7 +620,6 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
     } else if (tid == kTmaWarp * 32) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.free[i], 1);
             mbar_init(&bar.staged[i], 256);
         }
         mbar_init(&bar.cv, 512);
@@ -636,7 +635,7 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
         fence_proxy_async();
-        for (int i = 0; i < 2 && i < tiles; ++i) load_bc(i), load_a(i);
+        for (int i = 0; i < 2 && i < tiles; ++i) load(i);
     }
     for (int e = tid; e <= kTile; e += kThreads) sPow[e] = power(w.g, (float)e);
     for (int i = tid; i < 63; i += kThreads) {
@@ -652,27 +651,21 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            int issued = min(2, tiles);  // tiles whose loads are all issued
-            bool half = false;
+            // The next load waits for the outputs and their store's reads: sooner, it took
+            // shared memory from the tile under work (B, C after the products, A after the
+            // store: backward of B8 T4096 H6 108 instead of 104 us; A after A M^T, 117).
+            int issued = min(2, tiles);
             for (int it = 0; it < tiles; ++it) {
-                if (issued < tiles) {
-                    if (!mbar_wait(&bar.free[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
-                    load_bc(issued);
-                    half = true;
-                }
                 if (!mbar_wait(&bar.staged[it & 1], (it >> 1) & 1, d.err, kErrTma, d.wait_ns)) break;
                 for (int i = 0; i < nc; ++i)
                     tma_store_4d(&maps.out[w.rl], stage(it) + i * (kTileBytes / 2), 64 * i, w.h, w.t0(it), w.b);
                 bulk_commit();
                 if (issued < tiles) {
                     bulk_wait_read0();
-                    load_a(issued);
-                    half = false;
-                    ++issued;
+                    load(issued++);
                 }
             }
-            // no copy outlives the CTA: a tile whose A was not asked for gets it now
-            if (half) load_a(issued), ++issued;
+            // no copy outlives the CTA
             for (int i = max(0, issued - 2); i < issued; ++i)
                 mbar_wait(&bar.full[i & 1], (i >> 1) & 1, d.err, kErrDrain);
             bulk_wait0();
@@ -730,7 +723,6 @@ la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
                 for (int s = 0; s < 8; ++s)
                     mma_bf16_ts(tm + T_X, tm + T_P + 8 * s, desc_add(dCt, s * 2048), i_p, 1);
                 mma_commit(&bar.o);
-                mma_commit(&bar.free[it & 1]);
             }
             __syncwarp();
         }
