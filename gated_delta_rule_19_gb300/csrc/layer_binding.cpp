@@ -8,8 +8,10 @@
 
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -85,8 +87,11 @@ struct Like {
         else if (type == at::kBFloat16) code = GDN_BF16;
         else fail(GDN_ERR_UNSUPPORTED, "dtype %s (use float32 or bfloat16)", c10::toString(type));
     }
+    // at::empty's own steps without its dispatch: a call makes four to six tensors.
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType t) const {
-        return at::empty(shape, at::TensorOptions().device(device).dtype(t));
+        const c10::cuda::CUDAGuard guard(device);
+        return at::Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                                    c10::DispatchKeySet(c10::DispatchKey::CUDA), t, std::nullopt));
     }
 };
 
