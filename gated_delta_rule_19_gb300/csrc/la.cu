@@ -112,6 +112,7 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
     constexpr int NO = CM / L::COLS, NY = kTok / 8 / L::COLS;                  // column tiles of outputs, scores
     extern __shared__ __align__(16) float sm[];
     float *sM = sm + L::M, *sP = sm + L::P, *sW = sm + L::W;
+    await_previous();
     const LaRole& ro = roles.r[blockIdx.z];
     const int c0 = blockIdx.y * L::CS;
     if (c0 >= ro.Dc) return;
@@ -342,8 +343,7 @@ cudaError_t launch_chunk(const LaDims& d, const LaRoles& roles, cudaStream_t st)
     cudaError_t e = allow_smem(la_chunk_kernel<D, kOut>, (int)smem, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * (kOut ? d.nseg : d.nseg - 1)), D / L::CS, roles.n);
-    la_chunk_kernel<D, kOut><<<grid, L::THREADS, smem, st>>>(d, roles);
-    return cudaGetLastError();
+    return launch_dependent(la_chunk_kernel<D, kOut>, grid, L::THREADS, smem, st, d, roles);
 }
 
 template <bool kOut>
@@ -362,7 +362,7 @@ cudaError_t launch_width(const LaDims& d, const LaRoles& roles, cudaStream_t st)
 __global__ void __launch_bounds__(256)
 la_link_kernel(LaDims d, LaRoles roles) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    await_previous();
     const LaRole& ro = roles.r[blockIdx.y];
     const int64_t VK = (int64_t)ro.Db * ro.Dc, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     const int64_t stream = i / VK, e = i % VK;
@@ -437,6 +437,7 @@ template <typename T, int L, int R>
 __global__ void __launch_bounds__(256)
 la_decode_kernel(LaDims d, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, int64_t sq,
                  int64_t sk, int64_t sv, float* __restrict__ state, T* __restrict__ o) {
+    await_previous();
     constexpr int K = 4 * L, W = 32 / L;  // rows of one load
     const int lane = threadIdx.x & 31, groups = d.V / (R * W), c0 = lane % L * 4;
     const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -484,9 +485,8 @@ template <typename T, int L, int R>
 cudaError_t launch_decode_k(const LaDims& d, const void* q, const void* k, const void* v, int64_t sq, int64_t sk,
                             int64_t sv, float* state, void* o, cudaStream_t st) {
     const int64_t units = d.NS() * (d.V / (R * 32 / L));
-    la_decode_kernel<T, L, R><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(d, (const T*)q, (const T*)k, (const T*)v, sq,
-                                                                          sk, sv, state, (T*)o);
-    return cudaGetLastError();
+    return launch_dependent(la_decode_kernel<T, L, R>, dim3((unsigned)((units + 7) / 8)), 256, 0, st, d, (const T*)q,
+                            (const T*)k, (const T*)v, sq, sk, sv, state, (T*)o);
 }
 
 // Eight loads a lane, or as many as the head's V rows give one warp.

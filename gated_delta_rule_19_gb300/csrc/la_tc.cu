@@ -258,6 +258,7 @@ constexpr int SS_STAGES = 3, SS_UPD = SS_STAGES * 2 * kTileBytes, SS_POW = SS_UP
 // so that a tile's is made while the one before it is multiplied.
 __global__ void __launch_bounds__(kThreads, 1)
 la_sums_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
+    await_previous();
     extern __shared__ __align__(1024) unsigned char sm[];
     SumBars& bar = *reinterpret_cast<SumBars*>(sm + SS_BARS);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -428,7 +429,7 @@ __device__ __forceinline__ void state_warps(const LaDims& d, const Part& w, Bars
     for (int i = 0; i < 64; ++i) m[i] = 0.f;
     const int64_t VK = (int64_t)ro.Db * ro.Dc;
     bool ok = make(0);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the linked states
+    await_previous();  // the linked states
     const bool first = w.seg == (w.rev ? d.nseg - 1 : 0);
     const float* src = first ? (ro.m0 ? ro.m0 + w.stream * VK : nullptr)
                              : ro.R + (w.stream * (d.nseg - 1) + (w.rev ? w.seg : w.seg - 1)) * VK;
@@ -590,6 +591,7 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
 template <bool kLines>
 __global__ void __launch_bounds__(kThreads, 1)
 la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
+    if (d.nseg == 1) await_previous();  // else the sums did; the linked states are waited for below
     extern __shared__ __align__(1024) unsigned char sm[];
     Bars& bar = *reinterpret_cast<Bars*>(sm + S_BARS);
     float *sPow = reinterpret_cast<float*>(sm + S_POW), *sDiag = (float*)(sm + S_DIAG), *sUpd = (float*)(sm + S_UPD);
@@ -768,9 +770,7 @@ cudaError_t launch_scan(const LaDims& d, const LaRoles& roles, const LaMaps& map
     cudaError_t e = allow_smem(la_scan_kernel<kLines>, S_SIZE, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(d.NS() * d.nseg), roles.n);
-    if (d.nseg > 1) return launch_dependent(la_scan_kernel<kLines>, grid, kThreads, S_SIZE, st, d, roles, maps);
-    la_scan_kernel<kLines><<<grid, kThreads, S_SIZE, st>>>(d, roles, maps);
-    return cudaGetLastError();
+    return launch_dependent(la_scan_kernel<kLines>, grid, kThreads, S_SIZE, st, d, roles, maps);
 }
 
 }  // namespace
@@ -781,8 +781,8 @@ cudaError_t launch_la_states_tc(const LaDims& d, const LaRoles& roles, cudaStrea
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(la_sums_kernel, SS_SIZE, done);
     if (e != cudaSuccess) return e;
-    la_sums_kernel<<<dim3((unsigned)(d.NS() * (d.nseg - 1)), roles.n), kThreads, SS_SIZE, st>>>(d, roles, maps);
-    return cudaGetLastError();
+    return launch_dependent(la_sums_kernel, dim3((unsigned)(d.NS() * (d.nseg - 1)), roles.n), kThreads, SS_SIZE, st, d,
+                            roles, maps);
 }
 cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_t st) {
     LaMaps maps;

@@ -154,6 +154,7 @@ template <typename T, int G, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_norm_rope_fwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab) {
     constexpr int VEC = kVec<T>, NH = kFwdHeads, S = kFwdStages;
+    await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     const FwdRing<T> ring(sm);
     const float inv_d = 1.f / d.D;
@@ -232,6 +233,7 @@ template <typename T, int G, bool kInter>
 __global__ void __launch_bounds__(kThreads, kRopeBwdPerSm)
 qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __restrict__ part) {
     constexpr int VEC = kVec<T>, NH = kBwdHeads, S = kBwdStages;
+    await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     const BwdRing<T> ring(sm);
     const float inv_d = 1.f / d.D;
@@ -327,8 +329,8 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
         static std::atomic<uint64_t> done{0};
         cudaError_t e = allow_smem(kern, smem, done);
         if (e != cudaSuccess) return e;
-        kern<<<(unsigned)blocks_for(d.tokens * (q.blocks + k.blocks), G, 2, sm_count()), kThreads, smem, st>>>(d, q, k,
-                                                                                                              tab);
+        return launch_dependent(kern, dim3((unsigned)blocks_for(d.tokens * (q.blocks + k.blocks), G, 2, sm_count())),
+                                kThreads, smem, st, d, q, k, tab);
     } else {
         auto kern = qk_norm_rope_bwd_kernel<T, G, kInter>;
         constexpr int smem = BwdRing<T>::BYTES;
@@ -336,9 +338,8 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
         static std::atomic<uint64_t> done{0};
         cudaError_t e = allow_smem(kern, smem, done);
         if (e != cudaSuccess) return e;
-        kern<<<blocks, kThreads, smem, st>>>(d, q, k, tab, part);
+        return launch_dependent(kern, dim3((unsigned)blocks), kThreads, smem, st, d, q, k, tab, part);
     }
-    return cudaGetLastError();
 }
 
 template <typename T, int G>

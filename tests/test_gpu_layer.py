@@ -127,3 +127,47 @@ def test_wait_limit_ends_the_kernels(example):
         got = run()
         torch.cuda.synchronize()
         assert word() == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [1, 50, 400])
+def test_calls_behind_one_another(dtype, T):
+    """A chain of calls, each on the one before's outputs and over what an earlier one
+    still reads, gives the bits of the same chain with a wait after every call."""
+    B, H, D = 2, 6, 64
+    g = torch.Generator(device="cuda").manual_seed(T)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, k0, gate, w = n(B, T, H, D), n(B, T, H, D), n(B, T, H, D), 1 + 0.1 * n(D)
+    a = torch.randn(T, D // 2, generator=g, device="cuda")
+    cos, sin, ld = a.cos(), a.sin(), torch.full((H,), -0.05, device="cuda")
+    state0 = torch.randn(B, H, D, D, generator=g, device="cuda")
+
+    def chain(wait):
+        q, state, bufs = x.clone(), state0.clone(), (torch.empty_like(x), torch.empty_like(x), torch.empty_like(x))
+        qn, kn, y = bufs
+        out = []
+        for _ in range(30):
+            gdn.gdn_qk_norm_rope_fwd(q, k0, w, w, cos, sin, q_out=qn, k_out=kn)
+            wait()
+            if T == 1:
+                o, _ = gdn.gdn_la_decode(qn, kn, q, ld, state)
+            else:
+                o, _, saved = gdn.gdn_la_fwd(qn, kn, q, ld, state, final_state=state, saved=True)
+            wait()
+            gdn.gdn_gated_norm_fwd(o, gate, w, y=y)
+            wait()
+            dx, dz, dw = gdn.gdn_gated_norm_bwd(o, gate, w, y)
+            wait()
+            dq, dk, dv, ds = gdn.gdn_la_bwd(qn, kn, q, ld, state, dx, state)
+            wait()
+            gdn.gdn_qk_norm_rope_bwd(q, k0, w, w, cos, sin, None, dq, dk, grads=None)
+            wait()
+            q.copy_(y)
+            wait()
+        return q, state, dx, dz, dw, dq, dk, dv, ds
+
+    apart = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        together = chain(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(apart, together))
