@@ -504,37 +504,35 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
         // P = Y .* D: blocks of 32 columns below, on or above this warp's diagonal block.
         // One warpgroup has blocks 0 and 3, the other 1 and 2, so that the causal half is
         // shared evenly.
-        uint32_t p[2][16], y[2][32];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) tmem_ld32(tl + T_Y + (k ? 3 - wg : wg) * 32, y[k]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) tmem_wait_ld(y[k]);
-        fence_before_sync();
-        mbar_arrive(&bar.r);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+            uint32_t y[32];
+            tmem_ld32(tl + T_Y + (k ? 3 - wg : wg) * 32, y);
+            tmem_wait_ld(y);
+            if (k) {
+                fence_before_sync();
+                mbar_arrive(&bar.r);
+            }
             const int cb = k ? 3 - wg : wg;
+            uint32_t p[16];
             if (cb == q) {
                 const float* f = sDiag + 31 + lane;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     float e0, e1;
-                    unpair(mul2(pair(__uint_as_float(y[k][j]), __uint_as_float(y[k][j + 1])), pair(f[-j], f[-j - 1])),
-                           e0, e1);
-                    p[k][j / 2] = pack_bf16(e0, e1);
+                    unpair(mul2(pair(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), pair(f[-j], f[-j - 1])), e0, e1);
+                    p[j / 2] = pack_bf16(e0, e1);
                 }
             } else if (rev ? cb < q : cb > q) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) p[k][j] = 0;
+                for (int j = 0; j < 16; ++j) p[j] = 0;
             } else if (rev) {
-                scale_block<true>(y[k], sPow[cb * 32 - r], g1, p[k]);
+                scale_block<true>(y, sPow[cb * 32 - r], g1, p);
             } else {
-                scale_block<false>(y[k], sPow[r - cb * 32 - 31], g1, p[k]);
+                scale_block<false>(y, sPow[r - cb * 32 - 31], g1, p);
             }
+            tmem_st16(tl + T_P + cb * 16, p);  // the P before it is used up: its outputs have been read
         }
-        // the P before it is used up: its outputs have been read
-#pragma unroll
-        for (int k = 0; k < 2; ++k) tmem_st16(tl + T_P + (k ? 3 - wg : wg) * 16, p[k]);
         if (!warp_wait(&bar.q, ph, d.err, kErrRows, d.wait_ns)) return;
         fence_after_sync();
         const float f = sPow[max(rev ? n - 1 - r : r + 1, 0)];
