@@ -583,9 +583,9 @@ __device__ __forceinline__ void row_warps(const LaDims& d, const Part& w, Bars& 
 // One CTA: one (stream, segment) of one role: its outputs and, from the last segment,
 // the state that leaves.  kLines: states that lie there as M does move in whole lines,
 // which saves 4.5 us a call (forward at K = V = 128: T128 H16 14.3 -> 9.9 us, B64 T1024
-// H2, 8 tiles a segment, 41.6 -> 37.1), but the loop over many tiles is then up to 10%
-// slower (B32 T4096 H6 K = V = 64, 32 tiles a segment, forward 160 -> 175 us, backward 341
-// -> 378), so it is for segments of few tiles.
+// H2, 8 tiles a segment, 41.6 -> 37.1), but the compiler's loop over many tiles is then up
+// to 16% slower (32 tiles a segment: B32 T4096 H6 K = V = 64 forward 156 -> 177 us, B8
+// T4096 H6 K = V = 128 backward 104 -> 121), so it is for segments of few tiles.
 template <bool kLines>
 __global__ void __launch_bounds__(kThreads, 1)
 la_scan_kernel(LaDims d, LaRoles roles, const __grid_constant__ LaMaps maps) {
