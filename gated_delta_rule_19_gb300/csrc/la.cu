@@ -44,7 +44,7 @@ constexpr int kTok = 64;  // tokens of a chunk
 //
 // These warp-level products run at 512 a cycle and SM, which three tf32 products for one
 // make 170; float32 arithmetic has 128, of which its operands' reads from shared memory
-// left about half (B4 T2048 H6 K = V = 128 forward 197 us, now 144).
+// left about half (B4 T2048 H6 K = V = 128 forward 197 us, now 146).
 struct Sum {
     float hi[4], lo[4];
     __device__ __forceinline__ void zero() {
