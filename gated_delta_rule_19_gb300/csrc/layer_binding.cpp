@@ -162,12 +162,22 @@ struct Buffer {
     void* at() const { return t.data_ptr(); }
 };
 
-void* stream_of(PyObject* o, const Like& like) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device.index()).stream();
-    void* s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw PythonError{};
-    return s;
-}
+// The call's stream: the given one, or the current one.  What the call makes belongs to it:
+// a workspace that goes back to the current stream would be handed out again while the
+// given one still has to run.
+struct OnStream {
+    void* raw;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    OnStream(PyObject* o, const Like& like) {
+        const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(like.device.index());
+        raw = now.stream();
+        if (o == Py_None) return;
+        raw = PyLong_AsVoidPtr(o);
+        if (!raw && PyErr_Occurred()) throw PythonError{};
+        if (raw != now.stream())
+            guard.emplace(c10::cuda::getStreamFromExternal((cudaStream_t)raw, like.device.index()));
+    }
+};
 
 void done(gdn_status st) {
     if (st != GDN_OK) throw Error{(int)st, api.gdn_last_error()};
@@ -241,6 +251,7 @@ struct La {
 PyObject* la_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 10, [&] {
         La c(a);
+        const OnStream stream(a[9], c.like);
         const at::DimVector state{c.B, c.H, c.V, c.K};
         const void* s0 = input(a[4], "initial_state", state, at::kFloat, c.like, true);
         const at::Tensor o = output(a[5], "o", {c.B, c.T, c.H, c.V}, c.like.type, c.like);
@@ -255,7 +266,7 @@ PyObject* la_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Buffer ws(a[8], "workspace", a[8] == Py_None ? api.gdn_la_fwd_workspace_bytes(&c.p) : 0, c.like);
         done(api.gdn_la_fwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.log_decay, (const float*)s0,
                             o.data_ptr(), data(sT), saved ? saved->data_ptr() : nullptr, ws.at(), ws.bytes,
-                            stream_of(a[9], c.like)));
+                            stream.raw));
         return results(o, sT, saved);
     });
 }
@@ -265,6 +276,7 @@ PyObject* la_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* la_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 14, [&] {
         La c(a);
+        const OnStream stream(a[13], c.like);
         const at::DimVector state{c.B, c.H, c.V, c.K}, vs{c.B, c.T, c.H, c.V};
         const void* s0 = input(a[4], "initial_state", state, at::kFloat, c.like, true);
         const void* d_o = input(a[5], "d_o", vs, c.like.type, c.like);
@@ -282,7 +294,7 @@ PyObject* la_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Buffer ws(a[12], "workspace", a[12] == Py_None ? api.gdn_la_bwd_workspace_bytes(&c.p) : 0, c.like);
         done(api.gdn_la_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.log_decay, (const float*)s0, saved,
                             d_o, (const float*)dS, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), data(ds0), ws.at(),
-                            ws.bytes, stream_of(a[13], c.like)));
+                            ws.bytes, stream.raw));
         return results(dq, dk, dv, ds0);
     });
 }
@@ -291,11 +303,12 @@ PyObject* la_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* la_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 7, [&] {
         La c(a);
+        const OnStream stream(a[6], c.like);
         const at::Tensor& state = *tensor(a[4], "state");
         dense(state, "state", {c.B, c.H, c.V, c.K}, at::kFloat, c.like);
         const at::Tensor o = output(a[5], "o", {c.B, c.T, c.H, c.V}, c.like.type, c.like);
         done(api.gdn_la_decode(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.log_decay,
-                               state.data_ptr<float>(), o.data_ptr(), stream_of(a[6], c.like)));
+                               state.data_ptr<float>(), o.data_ptr(), stream.raw));
         return results(o, state);
     });
 }
@@ -338,10 +351,11 @@ struct Rope {
 PyObject* rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 12, [&] {
         Rope c(a, a[7], a[8]);
+        const OnStream stream(a[11], c.like);
         const at::Tensor qo = output(a[9], "q_out", c.q.sizes(), c.like.type, c.like),
                          ko = output(a[10], "k_out", c.ks, c.like.type, c.like);
         done(api.gdn_qk_norm_rope_fwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions,
-                                      qo.data_ptr(), ko.data_ptr(), stream_of(a[11], c.like)));
+                                      qo.data_ptr(), ko.data_ptr(), stream.raw));
         return results(qo, ko);
     });
 }
@@ -351,6 +365,7 @@ PyObject* rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 17, [&] {
         Rope c(a, a[9], a[10]);
+        const OnStream stream(a[16], c.like);
         const at::DimVector ws{c.p.D};
         const void *dqo = input(a[7], "dq_out", c.q.sizes(), c.like.type, c.like),
                    *dko = input(a[8], "dk_out", c.ks, c.like.type, c.like);
@@ -362,7 +377,7 @@ PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                        c.like);
         done(api.gdn_qk_norm_rope_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions, dqo,
                                       dko, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), b.at(),
-                                      b.bytes, stream_of(a[16], c.like)));
+                                      b.bytes, stream.raw));
         return results(dq, dk, dwq, dwk);
     });
 }
@@ -386,9 +401,10 @@ struct Gated {
 PyObject* gated_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 6, [&] {
         Gated c(a, a[3]);
+        const OnStream stream(a[5], c.like);
         const at::Tensor y = output(a[4], "y", c.x.sizes(), c.like.type, c.like);
         done(api.gdn_gated_norm_fwd(&c.p, c.x.data_ptr(), c.gate.data_ptr(), c.weight, y.data_ptr(),
-                                    stream_of(a[5], c.like)));
+                                    stream.raw));
         return wrap(y);
     });
 }
@@ -397,13 +413,14 @@ PyObject* gated_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* gated_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 10, [&] {
         Gated c(a, a[4]);
+        const OnStream stream(a[9], c.like);
         const void* dy = input(a[3], "dy", c.x.sizes(), c.like.type, c.like);
         const at::Tensor dx = output(a[5], "dx", c.x.sizes(), c.like.type, c.like),
                          dz = output(a[6], "dgate", c.x.sizes(), c.like.type, c.like),
                          dw = output(a[7], "dweight", {c.p.D}, c.like.type, c.like);
         const Buffer b(a[8], "workspace", a[8] == Py_None ? api.gdn_gated_norm_bwd_workspace_bytes(&c.p) : 0, c.like);
         done(api.gdn_gated_norm_bwd(&c.p, c.x.data_ptr(), c.gate.data_ptr(), c.weight, dy, dx.data_ptr(),
-                                    dz.data_ptr(), dw.data_ptr(), b.at(), b.bytes, stream_of(a[9], c.like)));
+                                    dz.data_ptr(), dw.data_ptr(), b.at(), b.bytes, stream.raw));
         return results(dx, dz, dw);
     });
 }

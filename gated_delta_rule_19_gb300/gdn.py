@@ -919,7 +919,8 @@ def gdn_la_fwd(q, k, v, log_decay, initial_state=None, *, o=None, final_state=Tr
     initial_state float32 [B,H,V,K] or None.  ``final_state``: True (allocate), a
     float32 tensor to fill (may be initial_state itself), or False/None.  ``saved``:
     True to allocate and return what :func:`gdn_la_bwd` then need not compute again,
-    or a buffer of at least gdn_la_saved_bytes() bytes.
+    or a buffer of at least gdn_la_saved_bytes() bytes.  ``stream``: a torch stream
+    instead of the current one; what this call and the ones below make belongs to it.
     Returns ``(o, final_state or None, saved or None)``."""
     return (_layer or _binding()).la_fwd(q, k, v, log_decay, initial_state, o, final_state, saved, workspace,
                                          _raw(stream))

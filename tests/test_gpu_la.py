@@ -286,3 +286,22 @@ def test_refusals():
     # the context is as it was
     gdn.gdn_la_fwd(q, k, v, ld, s0)
     torch.cuda.synchronize()
+
+
+def test_new_tensors_belong_to_the_given_stream():
+    """Memory that a call makes is the given stream's, so that what it gives back (its
+    workspace) is not handed to the current stream while the given one still runs."""
+    q, k, v, ld, s0, d_o, dS = _inputs(1, 2500, 2, 128, 128, "bf16", "slow", 15)
+    ref = gdn.gdn_la_fwd(q, k, v, ld, s0)[:2] + gdn.gdn_la_bwd(q, k, v, ld, s0, d_o, dS)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = {s["stream"]: s["active_size"] for s in torch.cuda.memory_snapshot()}
+    got = gdn.gdn_la_fwd(q, k, v, ld, s0, stream=side)[:2] + gdn.gdn_la_bwd(q, k, v, ld, s0, d_o, dS, stream=side)
+    torch.cuda.synchronize()
+    assert side.cuda_stream not in held
+    mine = [s for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream]
+    for t in got:
+        assert any(s["address"] <= t.data_ptr() < s["address"] + s["total_size"] for s in mine)
+    # more than the outputs: the workspaces came and went here too
+    assert sum(s["total_size"] for s in mine) > sum(t.numel() * t.element_size() for t in got)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
