@@ -144,22 +144,31 @@ std::optional<at::Tensor> state_output(PyObject* o, const char* name, at::IntArr
     return output(o == Py_True ? Py_None : o, name, shape, at::kFloat, like);
 }
 
-// A caller's buffer of bytes, or (None) a new one of `need`.
-struct Buffer {
-    at::Tensor t;
+// A caller's buffer of bytes.
+const at::Tensor& bytes_of(const at::Tensor& t, const char* name, const Like& like) {
+    if (t.device() != like.device || !t.is_contiguous())
+        invalid(std::string(name) + " must be a contiguous tensor on " + like.device.str());
+    return t;
+}
+
+// The workspace: the caller's, or (None) memory of `need()` bytes for the time of the call.
+struct Workspace {
+    c10::DataPtr own;
+    void* at;
     size_t bytes;
-    Buffer(PyObject* o, const char* name, size_t need, const Like& like) {
-        if (const at::Tensor* given = tensor(o, name, true)) {
-            if (given->device() != like.device || !given->is_contiguous())
-                invalid(std::string(name) + " must be a contiguous tensor on " + like.device.str());
-            t = *given;
+    template <typename Need>
+    Workspace(PyObject* o, const Like& like, Need&& need) {
+        if (const at::Tensor* given = tensor(o, "workspace", true)) {
+            const at::Tensor& t = bytes_of(*given, "workspace", like);
+            at = t.data_ptr();
             bytes = (size_t)t.numel() * t.element_size();
         } else {
-            t = like.empty({(int64_t)(need ? need : 1)}, at::kByte);
-            bytes = need;
+            bytes = need();
+            const c10::cuda::CUDAGuard guard(like.device);
+            if (bytes) own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+            at = own.get();
         }
     }
-    void* at() const { return t.data_ptr(); }
 };
 
 // The call's stream: the given one, or the current one.  What the call makes belongs to it:
@@ -259,13 +268,13 @@ PyObject* la_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         std::optional<at::Tensor> saved;
         if (a[7] != Py_None && a[7] != Py_False) {
             const size_t need = api.gdn_la_saved_bytes(&c.p);
-            const Buffer b(a[7] == Py_True ? Py_None : a[7], "saved", need, c.like);
-            if (b.bytes < need) invalid("saved buffer is smaller than gdn_la_saved_bytes()");
-            saved = b.t;
+            if (a[7] == Py_True) saved = c.like.empty({(int64_t)need}, at::kByte);
+            else saved = bytes_of(*tensor(a[7], "saved"), "saved", c.like);
+            if ((size_t)saved->nbytes() < need) invalid("saved buffer is smaller than gdn_la_saved_bytes()");
         }
-        const Buffer ws(a[8], "workspace", a[8] == Py_None ? api.gdn_la_fwd_workspace_bytes(&c.p) : 0, c.like);
+        const Workspace ws(a[8], c.like, [&] { return api.gdn_la_fwd_workspace_bytes(&c.p); });
         done(api.gdn_la_fwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.log_decay, (const float*)s0,
-                            o.data_ptr(), data(sT), saved ? saved->data_ptr() : nullptr, ws.at(), ws.bytes,
+                            o.data_ptr(), data(sT), saved ? saved->data_ptr() : nullptr, ws.at, ws.bytes,
                             stream.raw));
         return results(o, sT, saved);
     });
@@ -283,17 +292,18 @@ PyObject* la_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* dS = input(a[6], "d_final_state", state, at::kFloat, c.like, true);
         const void* saved = nullptr;
         if (a[7] != Py_None) {
-            const Buffer b(a[7], "saved", 0, c.like);
-            if (b.bytes < api.gdn_la_saved_bytes(&c.p)) invalid("saved buffer is smaller than gdn_la_saved_bytes()");
-            saved = b.at();
+            const at::Tensor& b = bytes_of(*tensor(a[7], "saved"), "saved", c.like);
+            if ((size_t)b.nbytes() < api.gdn_la_saved_bytes(&c.p))
+                invalid("saved buffer is smaller than gdn_la_saved_bytes()");
+            saved = b.data_ptr();
         }
         const at::Tensor dq = output(a[8], "dq", c.q.sizes(), c.like.type, c.like),
                          dk = output(a[9], "dk", c.q.sizes(), c.like.type, c.like),
                          dv = output(a[10], "dv", vs, c.like.type, c.like);
         const auto ds0 = state_output(a[11], "d_initial_state", state, c.like);
-        const Buffer ws(a[12], "workspace", a[12] == Py_None ? api.gdn_la_bwd_workspace_bytes(&c.p) : 0, c.like);
+        const Workspace ws(a[12], c.like, [&] { return api.gdn_la_bwd_workspace_bytes(&c.p); });
         done(api.gdn_la_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.log_decay, (const float*)s0, saved,
-                            d_o, (const float*)dS, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), data(ds0), ws.at(),
+                            d_o, (const float*)dS, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), data(ds0), ws.at,
                             ws.bytes, stream.raw));
         return results(dq, dk, dv, ds0);
     });
@@ -366,18 +376,17 @@ PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return call(n, 17, [&] {
         Rope c(a, a[9], a[10]);
         const OnStream stream(a[16], c.like);
-        const at::DimVector ws{c.p.D};
+        const at::DimVector width{c.p.D};
         const void *dqo = input(a[7], "dq_out", c.q.sizes(), c.like.type, c.like),
                    *dko = input(a[8], "dk_out", c.ks, c.like.type, c.like);
         const at::Tensor dq = output(a[11], "dq", c.q.sizes(), c.like.type, c.like),
                          dk = output(a[12], "dk", c.ks, c.like.type, c.like),
-                         dwq = output(a[13], "dq_weight", ws, c.like.type, c.like),
-                         dwk = output(a[14], "dk_weight", ws, c.like.type, c.like);
-        const Buffer b(a[15], "workspace", a[15] == Py_None ? api.gdn_qk_norm_rope_bwd_workspace_bytes(&c.p) : 0,
-                       c.like);
+                         dwq = output(a[13], "dq_weight", width, c.like.type, c.like),
+                         dwk = output(a[14], "dk_weight", width, c.like.type, c.like);
+        const Workspace ws(a[15], c.like, [&] { return api.gdn_qk_norm_rope_bwd_workspace_bytes(&c.p); });
         done(api.gdn_qk_norm_rope_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions, dqo,
-                                      dko, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), b.at(),
-                                      b.bytes, stream.raw));
+                                      dko, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), ws.at,
+                                      ws.bytes, stream.raw));
         return results(dq, dk, dwq, dwk);
     });
 }
@@ -418,9 +427,9 @@ PyObject* gated_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor dx = output(a[5], "dx", c.x.sizes(), c.like.type, c.like),
                          dz = output(a[6], "dgate", c.x.sizes(), c.like.type, c.like),
                          dw = output(a[7], "dweight", {c.p.D}, c.like.type, c.like);
-        const Buffer b(a[8], "workspace", a[8] == Py_None ? api.gdn_gated_norm_bwd_workspace_bytes(&c.p) : 0, c.like);
+        const Workspace ws(a[8], c.like, [&] { return api.gdn_gated_norm_bwd_workspace_bytes(&c.p); });
         done(api.gdn_gated_norm_bwd(&c.p, c.x.data_ptr(), c.gate.data_ptr(), c.weight, dy, dx.data_ptr(),
-                                    dz.data_ptr(), dw.data_ptr(), b.at(), b.bytes, stream.raw));
+                                    dz.data_ptr(), dw.data_ptr(), ws.at, ws.bytes, stream.raw));
         return results(dx, dz, dw);
     });
 }
