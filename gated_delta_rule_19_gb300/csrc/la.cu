@@ -527,7 +527,7 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
 // loads, the state that enters); the CTAs go in waves of as many as the GPU holds; with
 // several segments the sums and the link come first.  In bf16 a tile takes 2.4 us
 // alone, the fixed parts 11 us (scan) and 2 us each (sums, link), a tile of the sums
-// 0.9 us; in float32 a chunk of K = V = 64 takes 6 us and the fixed parts about as much
+// 1.2 us (at 0.9 B6 T1000 H12 was cut, 34.9 us; whole it takes 30.0); in float32 a chunk of K = V = 64 takes 6 us and the fixed parts about as much
 // together.
 // The backward's three scans want fewer segments than the forward's one; but cut like
 // the forward's it can take over the forward's sums (`saved`).
@@ -541,7 +541,7 @@ struct CutModel {
 };
 
 CutModel cut_model(const LaDims& d, InType ty) {
-    if (ty == InType::BF16) return {4.5, 1.0, 0.4, 1.0, 128, sm_count(), 1};
+    if (ty == InType::BF16) return {4.5, 1.0, 0.5, 1.0, 128, sm_count(), 1};
     const int D = d.K > d.V ? d.K : d.V;
     return {0.6, 0.4, 0.4, 0.4, kTok, (int64_t)sm_count() * (D > 64 ? 1 : 2), D > 64 ? 2 : 1};
 }
