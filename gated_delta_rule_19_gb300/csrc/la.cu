@@ -522,13 +522,13 @@ cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const vo
 }
 
 // How a call cuts its sequences, in whole tiles (128 tokens of bf16, a chunk of 64 of
-// float32): the cut with the least estimated time, in units of a tile of the
-// scan.  A CTA takes its tiles one after the other behind a fixed part (launch, first
-// loads, the state that enters); the CTAs go in waves of as many as the GPU holds; with
-// several segments the sums and the link come first.  In bf16 a tile takes 2.4 us
-// alone, the fixed parts 11 us (scan) and 2 us each (sums, link), a tile of the sums
-// 1.2 us (at 0.9 B6 T1000 H12 was cut, 34.9 us; whole it takes 30.0); in float32 a chunk of K = V = 64 takes 6 us and the fixed parts about as much
-// together.
+// float32): the cut with the least estimated time, in units of a tile of the scan.  A CTA
+// takes its tiles one after the other behind a fixed part (launch, first loads, the state
+// that enters); the CTAs go in waves of as many as the GPU holds; with several segments
+// the sums and the link come first.  In bf16 a tile takes 2.4 us alone, the fixed parts 11
+// us (scan) and 2 us each (sums, link), a tile of the sums 1.2 us (with 0.9 B6 T1000 H12
+// was cut and took 34.9 us, whole it takes 30.0); in float32 a chunk of K = V = 64 takes
+// 6 us and the fixed parts about as much together.
 // The backward's three scans want fewer segments than the forward's one; but cut like
 // the forward's it can take over the forward's sums (`saved`).
 namespace {
