@@ -156,10 +156,12 @@ gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict_
                 tx = fma2(pr[p][j], wv[p][j], tx);
             }
         }
-        const float r = rsqrtf(fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps));
+        const bool on = live && now < d.rows;
+        const float ms = fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps);
+        // 0 where there is no row: its zeros times 1 / sqrt(eps) are NaN for eps = 0
+        const float r = on ? rsqrtf(ms) : 0.f;
         // mean(t xh) = r mean(t x), times r of xh
         const uint64_t m = twice(-group_sum<G>(sum2(tx)) * r * r * inv_d), r2 = twice(r);
-        const bool on = live && now < d.rows;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
 #pragma unroll
