@@ -296,7 +296,9 @@ qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __r
                         pa[j] = mul2(ta[j], a[j]), pb[j] = mul2(tb[j], b[j]);
                         tx = fma2(pa[j], wa[j], fma2(pb[j], wb[j], tx));
                     }
-                    const float r = rsqrtf(fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps));
+                    const float ms = fmaf(group_sum<G>(sum2(ss)), inv_d, d.eps);
+                    // 0 where there is no row: its zeros times 1 / sqrt(eps) are NaN for eps = 0
+                    const float r = i < n ? rsqrtf(ms) : 0.f;
                     // mean(t xh) = r mean(t x), times r of xh
                     const uint64_t m = twice(-group_sum<G>(sum2(tx)) * r * r * inv_d), r2 = twice(r);
 #pragma unroll

@@ -53,3 +53,21 @@ def test_gated_norm_without_eps(B, T, H, D, dtype):
     _close("y", y, layer.gated_norm_fwd(_np(x), _np(z), _np(w), 0.0))
     for name, t, r in zip(("dx", "dgate", "dw"), grads, layer.gated_norm_bwd(_np(x), _np(z), _np(w), 0.0, _np(dy))):
         _close(name, t, r)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,R", [(1, 1, 1, 1, 128, 128), (2, 5, 3, 1, 96, 32), (1, 37, 5, 2, 256, 0),
+                                           (3, 500, 7, 3, 128, 64)])
+def test_norm_rope_without_eps(B, T, Hq, Hk, D, R, dtype):
+    """As above for the q, k norm: also the second head of an item of an odd count."""
+    n = _normal(B * T + D, dtype)
+    q, k, dq, dk, wq, wk = n(B, T, Hq, D), n(B, T, Hk, D), n(B, T, Hq, D), n(B, T, Hk, D), 1 + 0.2 * n(D), 1 + 0.2 * n(D)
+    a = torch.linspace(-3, 3, T * (R // 2), device="cuda").view(T, R // 2)
+    cos, sin = (a.cos(), a.sin()) if R else (None, None)
+    c, s = (np.broadcast_to(_np(t), (B, T, R // 2)) for t in (a.cos(), a.sin()))
+    grads = gdn.gdn_qk_norm_rope_bwd(q, k, wq, wk, cos, sin, None, dq, dk, eps=0.0)
+    torch.cuda.synchronize()
+    for x, w, dy, dx, dw in ((q, wq, dq, grads[0], grads[2]), (k, wk, dk, grads[1], grads[3])):
+        rx, rw = layer.norm_rope_bwd(_np(x), _np(w), c, s, 0.0, False, _np(dy))
+        _close("dx", dx, rx)
+        _close("dw", dw, rw)
