@@ -136,7 +136,8 @@ gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict_
         issue(fill);
         fill = ring.after(fill);
         ring.wait();
-        // with u = dy w, p = dy act x, sl = the slope of silu = sg (1 + z - act):
+        // with u = dy w, p = dy act x, sl = the slope of silu = sg + act (1 - sg), which is
+        // 1 for any large gate (as sg (1 + z - act) the sum 1 + z is wrong from 2^24 on):
         // t = u act, dz = r u x sl, dw += r p, t x = p w
         uint64_t xv[2][VEC / 2], t[2][VEC / 2], gz[2][VEC / 2], pr[2][VEC / 2], ss = twice(0.f), tx = ss;
 #pragma unroll
@@ -148,7 +149,7 @@ gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict_
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) {
                 const uint64_t sg = sigmoid2(zv[j]), act = mul2(zv[j], sg), u = mul2(yv[j], wv[p][j]);
-                const uint64_t sl = mul2(sg, fma2(act, twice(-1.f), add2(zv[j], twice(1.f))));
+                const uint64_t sl = fma2(act, fma2(sg, twice(-1.f), twice(1.f)), sg);
                 gz[p][j] = mul2(mul2(u, xv[p][j]), sl);
                 t[p][j] = mul2(u, act);
                 pr[p][j] = mul2(mul2(yv[j], act), xv[p][j]);

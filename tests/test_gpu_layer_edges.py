@@ -71,3 +71,19 @@ def test_norm_rope_without_eps(B, T, Hq, Hk, D, R, dtype):
         rx, rw = layer.norm_rope_bwd(_np(x), _np(w), c, s, 0.0, False, _np(dy))
         _close("dx", dx, rx)
         _close("dw", dw, rw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_norm_gates_past_2_24(dtype):
+    """The slope of silu is 1 for a large gate of any size, and 0 for a large negative one."""
+    gates = [3e3, 2.0 ** 22 + 2 ** 20, 2.0 ** 24 + 2, 2.0 ** 24 + 2 ** 18, 2.0 ** 26, 1e8, 1e30, -1e8, -1e30]
+    n = _normal(1, dtype)
+    shape = (1, len(gates), 1, 64)
+    z = torch.tensor(gates, device="cuda").view(1, -1, 1, 1).expand(shape).to(DT[dtype]).contiguous()
+    x, dy, w = n(*shape), n(*shape), 1 + 0.2 * n(64)
+    _, dz, _ = gdn.gdn_gated_norm_bwd(x, z, w, dy)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore"):
+        ref = layer.gated_norm_bwd(_np(x), _np(z), _np(w), 1e-6, _np(dy))[1]
+    for t, gate in enumerate(gates):
+        _close(f"dgate of {gate}", dz[:, t], ref[:, t])
