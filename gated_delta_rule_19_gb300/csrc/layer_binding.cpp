@@ -10,6 +10,8 @@
 
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -87,9 +89,9 @@ struct Like {
         else if (type == at::kBFloat16) code = GDN_BF16;
         else fail(GDN_ERR_UNSUPPORTED, "dtype %s (use float32 or bfloat16)", c10::toString(type));
     }
-    // at::empty's own steps without its dispatch: a call makes four to six tensors.
+    // at::empty's own steps without its dispatch: a call makes four to six tensors.  Under an
+    // OnStream, whose device and stream they belong to.
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType t) const {
-        const c10::cuda::CUDAGuard guard(device);
         return at::Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
                                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), t, std::nullopt));
     }
@@ -164,21 +166,22 @@ struct Workspace {
             bytes = (size_t)t.numel() * t.element_size();
         } else {
             bytes = need();
-            const c10::cuda::CUDAGuard guard(like.device);
             if (bytes) own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
             at = own.get();
         }
     }
 };
 
-// The call's stream: the given one, or the current one.  What the call makes belongs to it:
-// a workspace that goes back to the current stream would be handed out again while the
-// given one still has to run.
+// The call's device, which is the tensors' (the library launches on the current one), and
+// its stream: the given one, or that device's current one.  What the call makes belongs to
+// them: a workspace that goes back to the current stream would be handed out again while
+// the given one still has to run.
 struct OnStream {
+    c10::DeviceGuard device;
     void* raw;
     std::optional<c10::cuda::CUDAStreamGuard> guard;
-    OnStream(PyObject* o, const Like& like) {
-        const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(like.device.index());
+    OnStream(PyObject* o, const Like& like) : device(like.device) {
+        const c10::cuda::CUDAStream now(c10::impl::VirtualGuardImpl(like.device.type()).getStream(like.device));
         raw = now.stream();
         if (o == Py_None) return;
         raw = PyLong_AsVoidPtr(o);
