@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -235,8 +236,8 @@ PyObject* call(Py_ssize_t given, Py_ssize_t want, F&& body) {
             Py_DECREF(x);
         }
     } catch (const PythonError&) {
-    } catch (const std::exception& e) {  // an allocation that failed, say
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception&) {  // torch's own: an allocation that failed is its OutOfMemoryError
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

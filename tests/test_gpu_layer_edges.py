@@ -87,3 +87,22 @@ def test_gated_norm_gates_past_2_24(dtype):
         ref = layer.gated_norm_bwd(_np(x), _np(z), _np(w), 1e-6, _np(dy))[1]
     for t, gate in enumerate(gates):
         _close(f"dgate of {gate}", dz[:, t], ref[:, t])
+
+
+def test_memory_that_runs_out_is_torchs_error():
+    """An allocation that fails raises what torch's own do, and leaves calls usable."""
+    q = torch.randn(1, 32768, 16, 128, device="cuda").bfloat16()  # outputs of 128 MB
+    ld = torch.zeros(16, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-6)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            gdn.gdn_la_fwd(q, q, q, ld)
+        with pytest.raises(torch.OutOfMemoryError):
+            gdn.gdn_gated_norm_fwd(q, q, q[0, 0, 0])
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    o, _, _ = gdn.gdn_la_fwd(q, q, q, ld)
+    torch.cuda.synchronize()
+    assert o.shape == q.shape
