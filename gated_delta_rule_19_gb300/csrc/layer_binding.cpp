@@ -203,8 +203,17 @@ PyObject* wrap(const std::optional<at::Tensor>& t) {
     if (t) return THPVariable_Wrap(*t);
     Py_RETURN_NONE;
 }
+// What the call wrote counts as changed, so that autograd sees a saved state that was
+// overwritten (tensors of inference mode have no count).
+void changed(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void changed(const std::optional<at::Tensor>& t) {
+    if (t) changed(*t);
+}
 template <typename... T>
 PyObject* results(const T&... t) {
+    (changed(t), ...);
     PyObject* r = PyTuple_New(sizeof...(T));
     Py_ssize_t i = 0;
     (PyTuple_SET_ITEM(r, i++, wrap(t)), ...);
@@ -418,6 +427,7 @@ PyObject* gated_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor y = output(a[4], "y", c.x.sizes(), c.like.type, c.like);
         done(api.gdn_gated_norm_fwd(&c.p, c.x.data_ptr(), c.gate.data_ptr(), c.weight, y.data_ptr(),
                                     stream.raw));
+        changed(y);
         return wrap(y);
     });
 }

@@ -106,3 +106,31 @@ def test_memory_that_runs_out_is_torchs_error():
     o, _, _ = gdn.gdn_la_fwd(q, q, q, ld)
     torch.cuda.synchronize()
     assert o.shape == q.shape
+
+
+def test_autograd_sees_a_state_that_was_overwritten():
+    B, T, H, K, V = 2, 3, 3, 32, 16
+    n = _normal(3, "f32")
+    q, v, state, ld, w = n(B, T, H, K), n(B, T, H, V), n(B, H, V, K), torch.zeros(H, device="cuda"), n(K)
+    for call in (lambda s: gdn.gdn_la_decode(q, q, v, ld, s), lambda s: gdn.gdn_la_fwd(q, q, v, ld, s, final_state=s),
+                 lambda s: gdn.gdn_la_bwd(q, q, v, ld, None, v, s, d_initial_state=s)):
+        x = state.clone().requires_grad_()
+        s = x * 2
+        loss = (s * s).sum()  # saves s
+        with torch.no_grad():
+            call(s)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    y, out = n(B, T, H, V), n(B, T, H, K)
+    before = y._version, out._version
+    gdn.gdn_la_fwd(q, q, v, ld, o=y)
+    gdn.gdn_gated_norm_fwd(q, q, w, y=out)
+    assert y._version > before[0] and out._version > before[1] and q._version == v._version == 0
+    with torch.inference_mode():
+        kept = state.clone()
+    gdn.gdn_la_decode(q, q, v, ld, kept)  # a state of inference mode has no version
+    before = state._version
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_la_decode(q, q, v, None, state)
+    assert state._version == before  # nothing was written
+    torch.cuda.synchronize()
