@@ -19,6 +19,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "gdn_internal.h"
 
@@ -39,8 +41,14 @@ constexpr int kTok = 64;  // tokens of a chunk
 // of either sign.  (Cutting instead of rounding saves 5% of the time, but leaves a lo lo
 // of one sign.)  The small products have sums of their own, and no sum on the tensor
 // cores runs over more than one chunk: what is carried from chunk to chunk is added in
-// float32.  Results are within 5e-7 of the value (relative L2, T up to 4096), as
-// sums in float32 are.
+// float32.  Results are within 5.5e-7 of the value (relative L2, T up to 4096), about twice
+// as far as the same sums in float32.
+//
+// The rounding takes a number within 2^-12 of the largest one to infinity, and what is left
+// of an infinity is a NaN, so no such number comes out finite.  kSafe's hi stops at the
+// largest tf32 number, but in every split it takes 14 to 32% more time (B8 T2048 H8 K = V = 64
+// forward 127 -> 149 us, B4 T2048 H6 K = V = 128 backward 298 -> 394).  So a CTA looks at its
+// results, and does its work again that way if one is not finite (127 -> 129, 298 -> 300).
 //
 // These warp-level products run at 512 a cycle and SM, which three tf32 products for one
 // make 170; float32 arithmetic has 128, of which its operands' reads from shared memory
@@ -53,11 +61,14 @@ struct Sum {
     }
     __device__ __forceinline__ float get(int i) const { return hi[i] + lo[i]; }
 };
-template <int N>
+template <int N, bool kSafe>
 struct Split {
     uint32_t hi[N], lo[N];
     __device__ __forceinline__ void set(int i, float x) {
-        hi[i] = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+        if constexpr (kSafe)
+            asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(x));
+        else
+            hi[i] = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
         lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
     }
 };
@@ -69,8 +80,8 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], cons
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // d[j] += a b[j]; the products of one sum are kept apart, each waits for the one before
-template <int N>
-__device__ __forceinline__ void mma8(Sum (&d)[N], const Split<4>& a, const Split<2> (&b)[N]) {
+template <int N, bool kSafe>
+__device__ __forceinline__ void mma8(Sum (&d)[N], const Split<4, kSafe>& a, const Split<2, kSafe> (&b)[N]) {
 #pragma unroll
     for (int j = 0; j < N; ++j) mma8(d[j].lo, a.lo, b[j].hi);
 #pragma unroll
@@ -152,7 +163,6 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
         rows(buf + L::C, L::RC, pc, ro.sc, L::CS, cw);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load(0);
 
     // M[c][b] of the caller's [V, K] matrices by strides: this warp's tiles of 16 rows (b)
     // by 8 columns (c).  A lane has rows gq and gq + 8, columns 2 tq and 2 tq + 1 of a tile.
@@ -169,164 +179,178 @@ la_chunk_kernel(LaDims d, LaRoles roles) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f(row_b(x) + 8 * (e >> 1), col_c(j) + (e & 1), m[x][j][e]);
     };
-    each([](int, int, float& x) { x = 0.f; });
-    if (kOut && carries) {
-        const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
-        const int64_t VK = (int64_t)ro.Db * ro.Dc;
-        const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
-                                 : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
-        if (src)
-            each([&](int bb, int cc, float& x) {
-                if (bb < ro.Db && cc < cw) x = src[(c0 + cc) * ro.m_sc + bb * ro.m_sb];
-            });
-    }
-
+    const bool last = kOut && ro.mT && seg == (ro.rev ? 0 : d.nseg - 1);
+    const bool leaves = carries && (!kOut || last);  // M does: a segment's own sum, or the last state
     const int part = warp >> 2, r0 = (part & 1 ? 3 - (warp & 3) : warp & 3) * 16;  // group of columns, first row
     const int y0 = part * NY * 8, o0 = part * NO * 8;                             // first columns
-    for (int it = 0; it < chunks; ++it) {
-        const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
-        const float *sA = sm + it % L::NBUF * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
-        if (L::NBUF == 1 && it) {
-            __syncthreads();  // the chunk before is done with the buffer
-            load(it);
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // All chunks.  Returns 0, or a NaN if some result is not finite.
+    auto pass = [&](auto safe) {
+        using SplitA = Split<4, decltype(safe)::value>;
+        using SplitB = Split<2, decltype(safe)::value>;
+        float bad = 0.f;
+        load(0);
+        each([](int, int, float& x) { x = 0.f; });
         if (kOut && carries) {
-#pragma unroll
-            for (int x = 0; x < MT; ++x)
-#pragma unroll
-                for (int j = 0; j < NM; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2)
-                        *(float2*)(sM + (row_b(x) + 4 * e) * L::RM + col_c(j)) = make_float2(m[x][j][e], m[x][j][e + 1]);
+            const bool first = seg == (ro.rev ? d.nseg - 1 : 0);
+            const int64_t VK = (int64_t)ro.Db * ro.Dc;
+            const float* src = first ? (ro.m0 ? ro.m0 + stream * VK : nullptr)
+                                     : ro.R + (stream * (d.nseg - 1) + (ro.rev ? seg : seg - 1)) * VK;
+            if (src)
+                each([&](int bb, int cc, float& x) {
+                    if (bb < ro.Db && cc < cw) x = src[(c0 + cc) * ro.m_sc + bb * ro.m_sb];
+                });
         }
-        __syncthreads();  // this chunk is there, the other buffer and P are free
-        if (L::NBUF == 2 && it + 1 < chunks) load(it + 1);
 
-        if (kOut) {
-            auto rows_a = [&](int k, Split<4>& a) {  // A's fragment: rows r0 .. r0 + 15, columns k .. k + 7
-                const float* at = sA + (r0 + gq) * L::RA + k + tq;
-                a.set(0, at[0]), a.set(1, at[8 * L::RA]), a.set(2, at[4]), a.set(3, at[8 * L::RA + 4]);
-            };
-            {  // scores, where the mask leaves some of this warp's
-                Sum y[NY];
+        for (int it = 0; it < chunks; ++it) {
+            const int t0 = chunk_t0(it), n = min(kTok, t_hi - t0);
+            const float *sA = sm + it % L::NBUF * L::BUF + L::A, *sB = sA + L::B, *sC = sA + L::C;
+            if (L::NBUF == 1 && it) {
+                __syncthreads();  // the chunk before is done with the buffer
+                load(it);
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if (kOut && carries) {
 #pragma unroll
-                for (int j = 0; j < NY; ++j) y[j].zero();
-                if (ro.rev ? y0 + NY * 8 > r0 : y0 <= r0 + 15) {
+                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                    for (int j = 0; j < NM; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            *(float2*)(sM + (row_b(x) + 4 * e) * L::RM + col_c(j)) =
+                                make_float2(m[x][j][e], m[x][j][e + 1]);
+            }
+            __syncthreads();  // this chunk is there, the other buffer and P are free
+            if (L::NBUF == 2 && it + 1 < chunks) load(it + 1);
+
+            if (kOut) {
+                auto rows_a = [&](int k, SplitA& a) {  // A's fragment: rows r0 .. r0 + 15, columns k .. k + 7
+                    const float* at = sA + (r0 + gq) * L::RA + k + tq;
+                    a.set(0, at[0]), a.set(1, at[8 * L::RA]), a.set(2, at[4]), a.set(3, at[8 * L::RA + 4]);
+                };
+                {  // scores, where the mask leaves some of this warp's
+                    Sum y[NY];
+#pragma unroll
+                    for (int j = 0; j < NY; ++j) y[j].zero();
+                    if (ro.rev ? y0 + NY * 8 > r0 : y0 <= r0 + 15) {
 #pragma unroll 8
-                    for (int k = 0; k < D; k += 8) {
-                        Split<4> a;
-                        Split<2> f[NY];
-                        rows_a(k, a);
+                        for (int k = 0; k < D; k += 8) {
+                            SplitA a;
+                            SplitB f[NY];
+                            rows_a(k, a);
 #pragma unroll
-                        for (int j = 0; j < NY; ++j) {
-                            const float* at = sB + (y0 + j * 8 + gq) * L::RA + k + tq;
-                            f[j].set(0, at[0]), f[j].set(1, at[4]);
+                            for (int j = 0; j < NY; ++j) {
+                                const float* at = sB + (y0 + j * 8 + gq) * L::RA + k + tq;
+                                f[j].set(0, at[0]), f[j].set(1, at[4]);
+                            }
+                            mma8(y, a, f);
                         }
-                        mma8(y, a, f);
                     }
+#pragma unroll
+                    for (int j = 0; j < NY; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const int r = r0 + gq + 4 * e, s = y0 + j * 8 + 2 * tq, dist = ro.rev ? s - r : r - s;
+                            const int next = ro.rev ? dist + 1 : dist - 1;
+                            *(float2*)(sP + r * L::RP + s) =
+                                make_float2(dist >= 0 ? y[j].get(e) * sW[dist] : 0.f,
+                                            next >= 0 ? y[j].get(e + 1) * sW[next] : 0.f);
+                        }
                 }
+                Sum o[NO];
 #pragma unroll
-                for (int j = 0; j < NY; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const int r = r0 + gq + 4 * e, s = y0 + j * 8 + 2 * tq, dist = ro.rev ? s - r : r - s;
-                        const int next = ro.rev ? dist + 1 : dist - 1;
-                        *(float2*)(sP + r * L::RP + s) =
-                            make_float2(dist >= 0 ? y[j].get(e) * sW[dist] : 0.f,
-                                        next >= 0 ? y[j].get(e + 1) * sW[next] : 0.f);
-                    }
-            }
-            Sum o[NO];
-#pragma unroll
-            for (int j = 0; j < NO; ++j) o[j].zero();
-            const int cb = o0 + gq;
-            // A M^T, the state that entered the chunk
+                for (int j = 0; j < NO; ++j) o[j].zero();
+                const int cb = o0 + gq;
+                // A M^T, the state that entered the chunk
 #pragma unroll 8
-            for (int k = 0; k < D; k += 8) {
-                Split<4> a;
-                Split<2> f[NO];
-                rows_a(k, a);
+                for (int k = 0; k < D; k += 8) {
+                    SplitA a;
+                    SplitB f[NO];
+                    rows_a(k, a);
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    const float* at = sM + (k + tq) * L::RM + cb + j * 8;
-                    f[j].set(0, at[0]), f[j].set(1, at[4 * L::RM]);
+                    for (int j = 0; j < NO; ++j) {
+                        const float* at = sM + (k + tq) * L::RM + cb + j * 8;
+                        f[j].set(0, at[0]), f[j].set(1, at[4 * L::RM]);
+                    }
+                    mma8(o, a, f);
                 }
-                mma8(o, a, f);
-            }
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const int r = r0 + gq + 4 * e;
-                const float w = sW[max(ro.rev ? n - 1 - r : r + 1, 0)];
+                for (int e = 0; e < 4; e += 2) {
+                    const int r = r0 + gq + 4 * e;
+                    const float w = sW[max(ro.rev ? n - 1 - r : r + 1, 0)];
+#pragma unroll
+                    for (int j = 0; j < NO; ++j)
+#pragma unroll
+                        for (int i = e; i < e + 2; ++i) o[j].hi[i] *= w, o[j].lo[i] *= w;
+                }
+                __syncthreads();
+                const int s_lo = ro.rev ? r0 : 0, s_hi = ro.rev ? kTok : r0 + 16;
+#pragma unroll 4
+                for (int s = s_lo; s < s_hi; s += 8) {
+                    const float2 x = *(const float2*)(sP + (r0 + gq) * L::RP + s + 2 * tq),
+                                 z = *(const float2*)(sP + (r0 + gq + 8) * L::RP + s + 2 * tq);
+                    SplitA a;
+                    SplitB f[NO];
+                    a.set(0, x.x), a.set(1, z.x), a.set(2, x.y), a.set(3, z.y);
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) {
+                        const float* at = sC + (s + 2 * tq) * L::RC + cb + j * 8;
+                        f[j].set(0, at[0]), f[j].set(1, at[L::RC]);
+                    }
+                    mma8(o, a, f);
+                }
 #pragma unroll
                 for (int j = 0; j < NO; ++j)
 #pragma unroll
-                    for (int i = e; i < e + 2; ++i) o[j].hi[i] *= w, o[j].lo[i] *= w;
+                    for (int e = 0; e < 4; e += 2) {
+                        const int r = r0 + gq + 4 * e, c = o0 + j * 8 + 2 * tq;
+                        const float2 y = make_float2(o[j].get(e), o[j].get(e + 1));
+                        bad = fmaf(y.x, 0.f, fmaf(y.y, 0.f, bad));
+                        if (r < n && c < cw) *(float2*)(po + (int64_t)(t0 + r) * d.H * ro.Dc + c) = y;
+                    }
             }
-            __syncthreads();
-            const int s_lo = ro.rev ? r0 : 0, s_hi = ro.rev ? kTok : r0 + 16;
+            // M <- gamma^n M + sum of gamma^(n-1-rho+rev) b c^T
+            if (carries) {
+                Sum u[MT][NM];
+#pragma unroll
+                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                    for (int j = 0; j < NM; ++j) u[x][j].zero();
 #pragma unroll 4
-            for (int s = s_lo; s < s_hi; s += 8) {
-                const float2 x = *(const float2*)(sP + (r0 + gq) * L::RP + s + 2 * tq),
-                             z = *(const float2*)(sP + (r0 + gq + 8) * L::RP + s + 2 * tq);
-                Split<4> a;
-                Split<2> f[NO];
-                a.set(0, x.x), a.set(1, z.x), a.set(2, x.y), a.set(3, z.y);
+                for (int s = 0; s < n; s += 8) {
+                    const int s0 = s + 2 * tq;
+                    const float w0 = sW[ro.rev ? s0 + 1 : max(n - 1 - s0, 0)],
+                                w1 = sW[ro.rev ? s0 + 2 : max(n - 2 - s0, 0)];
+                    SplitA a[MT];
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    const float* at = sC + (s + 2 * tq) * L::RC + cb + j * 8;
-                    f[j].set(0, at[0]), f[j].set(1, at[L::RC]);
+                    for (int x = 0; x < MT; ++x) {
+                        const float* at = sB + s0 * L::RA + row_b(x);
+                        a[x].set(0, at[0]), a[x].set(1, at[8]), a[x].set(2, at[L::RA]), a[x].set(3, at[L::RA + 8]);
+                    }
+                    SplitB f[NM];
+#pragma unroll
+                    for (int j = 0; j < NM; ++j) {
+                        const float* at = sC + s0 * L::RC + (mc * NM + j) * 8 + gq;
+                        f[j].set(0, at[0] * w0), f[j].set(1, at[L::RC] * w1);
+                    }
+#pragma unroll
+                    for (int x = 0; x < MT; ++x) mma8(u[x], a[x], f);
                 }
-                mma8(o, a, f);
+                const float gn = sW[n];
+#pragma unroll
+                for (int x = 0; x < MT; ++x)
+#pragma unroll
+                    for (int j = 0; j < NM; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[x][j][e] = fmaf(m[x][j][e], gn, u[x][j].get(e));
             }
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const int r = r0 + gq + 4 * e, c = o0 + j * 8 + 2 * tq;
-                    if (r < n && c < cw)
-                        *(float2*)(po + (int64_t)(t0 + r) * d.H * ro.Dc + c) = make_float2(o[j].get(e), o[j].get(e + 1));
-                }
         }
-        // M <- gamma^n M + sum of gamma^(n-1-rho+rev) b c^T
-        if (carries) {
-            Sum u[MT][NM];
-#pragma unroll
-            for (int x = 0; x < MT; ++x)
-#pragma unroll
-                for (int j = 0; j < NM; ++j) u[x][j].zero();
-#pragma unroll 4
-            for (int s = 0; s < n; s += 8) {
-                const int s0 = s + 2 * tq;
-                const float w0 = sW[ro.rev ? s0 + 1 : max(n - 1 - s0, 0)], w1 = sW[ro.rev ? s0 + 2 : max(n - 2 - s0, 0)];
-                Split<4> a[MT];
-#pragma unroll
-                for (int x = 0; x < MT; ++x) {
-                    const float* at = sB + s0 * L::RA + row_b(x);
-                    a[x].set(0, at[0]), a[x].set(1, at[8]), a[x].set(2, at[L::RA]), a[x].set(3, at[L::RA + 8]);
-                }
-                Split<2> f[NM];
-#pragma unroll
-                for (int j = 0; j < NM; ++j) {
-                    const float* at = sC + s0 * L::RC + (mc * NM + j) * 8 + gq;
-                    f[j].set(0, at[0] * w0), f[j].set(1, at[L::RC] * w1);
-                }
-#pragma unroll
-                for (int x = 0; x < MT; ++x) mma8(u[x], a[x], f);
-            }
-            const float gn = sW[n];
-#pragma unroll
-            for (int x = 0; x < MT; ++x)
-#pragma unroll
-                for (int j = 0; j < NM; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m[x][j][e] = fmaf(m[x][j][e], gn, u[x][j].get(e));
-        }
-    }
 
-    // What leaves: a segment's own sum, or the state behind the last one.
-    const bool last = kOut && ro.mT && seg == (ro.rev ? 0 : d.nseg - 1);
-    if (carries && (!kOut || last)) {
+        if (leaves) each([&](int, int, float& x) { bad = fmaf(x, 0.f, bad); });
+        return bad;
+    };
+    if (__syncthreads_or(pass(std::false_type()) != 0.f)) pass(std::true_type());
+
+    if (leaves) {
         const int64_t VK = (int64_t)ro.Db * ro.Dc;
         float* dst = kOut ? ro.mT + stream * VK : const_cast<float*>(ro.R) + (stream * nseg + slot) * VK;
         each([&](int bb, int cc, float& x) {

@@ -134,3 +134,54 @@ def test_autograd_sees_a_state_that_was_overwritten():
         gdn.gdn_la_decode(q, q, v, None, state)
     assert state._version == before  # nothing was written
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,H,K,V", [(150, 2, 16, 16), (1000, 2, 64, 64), (150, 160, 128, 128), (1000, 2, 128, 32)])
+def test_float32_values_next_to_the_largest(T, H, K, V):
+    """Inputs and states up to the largest float32 give finite results where the definition
+    does; with one segment and with several."""
+    n = _normal(K + T, "f32")
+    q, k, v, d_o = n(1, T, H, K) * 1e-6, n(1, T, H, K) * 1e-3, n(1, T, H, V), n(1, T, H, V) * 1e-3
+    ld = torch.full((H,), -0.05, device="cuda")
+    most = torch.finfo(torch.float32).max
+    v[0, 70, 0, 3], v[0, 71, 1, 5] = most, -3.4025e38
+    k[0, 140, 1, 0], v[0, 140, 1, 2] = 1.0, most  # the state's element itself next to the largest
+    s0 = torch.zeros(1, H, V, K, device="cuda")
+    s0[0, 0, 1, 2] = most
+    o, final, saved = gdn.gdn_la_fwd(q, k, v, ld, s0, saved=True)
+    grads = gdn.gdn_la_bwd(q, k, v, ld, s0, d_o, saved=saved)
+    torch.cuda.synchronize()
+    args = [_np(t[:, :, :2]) for t in (q, k, v)] + [_np(ld[:2]), _np(s0[:, :2])]
+    ro, rs, _ = layer.la_fwd(*args)
+    ref = layer.la_bwd(*args, _np(d_o[:, :, :2]))
+    for name, t, r in zip(("o", "dq", "dk", "dv"), (o, *grads[:3]), (ro, *ref[:3])):
+        _close(name, t[:, :, :2], r)
+    _close("final_state", final[:, :2], rs)
+    _close("d_initial_state", grads[3][:, :2], ref[3])
+
+
+@pytest.mark.parametrize("D", [32, 128])
+def test_float32_values_that_are_not_finite_stay_in_their_stream(D):
+    """A NaN or an infinity reaches its own stream from its 64-token chunk on, no other stream
+    and no earlier chunk, and an infinite result stays one; and its gradients likewise."""
+    n = _normal(5, "f32")
+    B, T, H = 2, 700, 3
+    q, k, v, d_o = n(B, T, H, D), n(B, T, H, D), n(B, T, H, D), n(B, T, H, D)
+    ld = torch.full((H,), -0.01, device="cuda")
+    o, final, _ = gdn.gdn_la_fwd(q, k, v, ld)
+    grads = gdn.gdn_la_bwd(q, k, v, ld, None, d_o)
+    bad = v.clone()
+    bad[1, 300, 2, 5] = float("nan")
+    bad[0, 400, 1, 7] = float("inf")
+    o2, final2, _ = gdn.gdn_la_fwd(q, k, bad, ld)
+    grads2 = gdn.gdn_la_bwd(q, k, bad, ld, None, d_o)
+    torch.cuda.synchronize()
+    for a, b in [(o, o2)] + list(zip(grads[:3], grads2[:3])):
+        same = (a == b).all(-1)
+        assert same[0, :, 0].all() and same[0, :, 2].all() and same[1, :, :2].all()
+    assert torch.equal(o[1, :256, 2], o2[1, :256, 2]) and torch.equal(o[0, :384, 1], o2[0, :384, 1])
+    assert o2[1, 300:, 2, 5].isnan().all() and final2[1, 2, 5].isnan().all()
+    assert not o2[0, 400:, 1, 7].isfinite().any() and torch.equal(final[0, 0], final2[0, 0])
+    # the state's row is v k^T: infinities of k's signs
+    assert torch.equal(final2[0, 1, 7], float("inf") * k[0, 400, 1])
+    assert torch.equal(grads[1][1, 320:, 2], grads2[1][1, 320:, 2])
