@@ -16,6 +16,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from gated_delta_rule_19_gb300 import gdn  # noqa: E402
@@ -28,6 +29,7 @@ class NormRope(torch.autograd.Function):
         return gdn.gdn_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         grads = gdn.gdn_qk_norm_rope_bwd(*ctx.saved_tensors, dq.contiguous(), dk.contiguous())
         return (*grads, None, None, None)
@@ -41,6 +43,7 @@ class LinearAttention(torch.autograd.Function):
         return o, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_final):
         *inputs, saved = ctx.saved_tensors
         dq, dk, dv, d_state = gdn.gdn_la_bwd(*inputs, d_o.contiguous(), d_final.contiguous(), saved=saved)
@@ -54,6 +57,7 @@ class GatedNorm(torch.autograd.Function):
         return gdn.gdn_gated_norm_fwd(x, gate, weight)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return gdn.gdn_gated_norm_bwd(*ctx.saved_tensors, dy.contiguous())
 

@@ -185,3 +185,23 @@ def test_float32_values_that_are_not_finite_stay_in_their_stream(D):
     # the state's row is v k^T: infinities of k's signs
     assert torch.equal(final2[0, 1, 7], float("inf") * k[0, 400, 1])
     assert torch.equal(grads[1][1, 320:, 2], grads2[1][1, 320:, 2])
+
+
+def test_example_refuses_second_derivatives():
+    """The operators have first derivatives; a second one through the example's functions is
+    an error, not a gradient that takes the first for a constant."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "linear_attention_layer.py")
+    spec = importlib.util.spec_from_file_location("linear_attention_layer_edges", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    n = _normal(9, "f32")
+    x, w, ld, s0 = n(1, 4, 2, 32).requires_grad_(), n(32), torch.zeros(2, device="cuda"), n(1, 2, 32, 32)
+    for y in (ex.GatedNorm.apply(x, x, w), ex.NormRope.apply(x, x, w, w, None, None, None)[0],
+              ex.LinearAttention.apply(x, x, x, ld, s0)[0]):
+        (d,) = torch.autograd.grad((y * y).sum() + (x ** 3).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="differentiate twice"):
+            d.sum().backward()
