@@ -16,6 +16,7 @@ LIB = os.path.join(PKG, "libgdn.so")
 BINDING = os.path.join(PKG, "_layer.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
+BINDING_FOR = os.path.join(BUILD_DIR, "layer_built_for.txt")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -44,10 +45,25 @@ def is_stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
+def _built_for() -> str:
+    """What the binding is compiled against besides its sources."""
+    from importlib import metadata
+
+    try:
+        torch = metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        torch = None
+    return f"torch {torch}, Python {sys.version}, {PKG}"
+
+
 def _binding_is_stale() -> bool:
-    if not os.path.exists(BINDING):
+    try:
+        with open(BINDING_FOR) as f:
+            if f.read() != _built_for():
+                return True
+        t = os.path.getmtime(BINDING)
+    except OSError:
         return True
-    t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "gdn.h")))
 
 
@@ -71,6 +87,9 @@ def build_binding(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_built_for())
     return BINDING
 
 

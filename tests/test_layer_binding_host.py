@@ -1,5 +1,5 @@
 """Host-side tests of the linear-attention layer's C++ binding (no GPU needed): the
-device its calls run on."""
+device its calls run on, and when it is built."""
 import os
 import subprocess
 import sys
@@ -113,3 +113,29 @@ def test_calls_run_on_their_tensors_device(built, tmp_path):
                    check=True)
     r = subprocess.run([sys.executable, "-c", RUN, str(lib)], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stdout + r.stderr
+
+
+def test_binding_of_another_torch_or_python_is_rebuilt(built, monkeypatch):
+    """Sources that are older do not make a binding current: it belongs to the torch and
+    the Python that it was compiled against."""
+    from importlib import metadata
+
+    from gated_delta_rule_19_gb300 import _build
+
+    made = []
+    monkeypatch.setattr(_build, "build_binding", lambda verbose=False: made.append(1))
+    monkeypatch.setattr(_build, "is_stale", lambda: False)
+    _build.build()
+    assert not made  # as it is, it is current
+    version = metadata.version
+    with monkeypatch.context() as m:
+        m.setattr(metadata, "version", lambda name: "99.0" if name == "torch" else version(name))
+        _build.build()
+        assert len(made) == 1
+    with monkeypatch.context() as m:
+        m.setattr(sys, "version", "3.99.0 (another)")
+        _build.build()
+        assert len(made) == 2
+    monkeypatch.setattr(_build, "BINDING_FOR", _build.BINDING_FOR + ".gone")
+    _build.build()
+    assert len(made) == 3
