@@ -6,6 +6,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -67,19 +68,43 @@ def _binding_is_stale() -> bool:
     return any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "gdn.h")))
 
 
-def build_binding(verbose: bool = False) -> str:
-    """Compile the C++ binding against the installed torch."""
+def _binding_dirs() -> list[str]:
+    """The folders of torch's, Python's and CUDA's headers; FileNotFoundError if some, or
+    torch's CUDA library, are not installed."""
     import sysconfig
 
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        raise FileNotFoundError(f"no torch: {e}") from e
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    for header in ("ATen/EmptyTensor.h", "Python.h", "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in dirs):
+            raise FileNotFoundError(f"{header} is not in any of {dirs}")
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "lib", "libc10_cuda.so")):
+        raise FileNotFoundError("torch is installed without CUDA")
+    return dirs
+
+
+def build_binding(verbose: bool = False) -> str | None:
+    """Compile the C++ binding against the installed torch.  Without its headers the library
+    is all that can be built, and serves every caller of the C ABI: a warning, and no binding
+    (gdn.py's calls of the layer then raise)."""
+    try:
+        dirs = _binding_dirs()
+    except FileNotFoundError as e:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # it is of other sources or another torch
+        warnings.warn(f"the linear-attention layer's Python binding is not built: {e}", stacklevel=2)
+        return None
     import torch
-    from torch.utils import cpp_extension
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    dirs = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f for d in dirs for f in ("-isystem" if d != INCLUDE else "-I", d)), BINDING_SRC, "-o", tmp, "-L" + lib,
+           "-I", INCLUDE, *(f for d in dirs for f in ("-isystem", d)), BINDING_SRC, "-o", tmp, "-L" + lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

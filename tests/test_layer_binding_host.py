@@ -139,3 +139,26 @@ def test_binding_of_another_torch_or_python_is_rebuilt(built, monkeypatch):
     monkeypatch.setattr(_build, "BINDING_FOR", _build.BINDING_FOR + ".gone")
     _build.build()
     assert len(made) == 3
+
+
+def test_library_builds_without_the_bindings_headers(built, monkeypatch, tmp_path):
+    """A caller of the C ABI needs neither torch's nor Python's C++ headers; the layer's calls
+    through gdn.py say what is missing."""
+    import sysconfig
+
+    from gated_delta_rule_19_gb300 import _build, gdn
+
+    old = tmp_path / "_layer.so"
+    old.write_bytes(b"of another torch")
+    monkeypatch.setattr(_build, "BINDING", str(old))
+    monkeypatch.setattr(_build, "BINDING_FOR", str(tmp_path / "none.txt"))
+    monkeypatch.setattr(_build, "is_stale", lambda: False)
+    paths = dict(sysconfig.get_paths(), include=str(tmp_path))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda *a, **k: paths)
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert _build.build() == _build.LIB
+    assert not old.exists()
+    monkeypatch.setattr(gdn, "_PKG", str(tmp_path))
+    monkeypatch.setattr(gdn, "_layer", None)
+    with pytest.raises(RuntimeError, match="_layer.so is missing"):
+        gdn.gdn_la_decode(None, None, None, None, None)
