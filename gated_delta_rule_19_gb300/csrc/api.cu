@@ -1633,14 +1633,19 @@ gdn_status check_layer_sizes(int64_t B, int64_t T, int64_t H, int32_t dtype) {
     return GDN_OK;
 }
 
-// The token stride of [B, T, H, D] rows (0: dense): checked and filled in.
-gdn_status row_stride(const char* name, int64_t stride, int64_t H, int64_t D, int32_t dtype, int64_t* out) {
+// The token stride of [B, T, H, D] rows (0: dense): checked and filled in.  The rows of all
+// tokens span at most 2^58 elements, so that sizes in bytes stay within 64 bits.
+gdn_status row_stride(const char* name, int64_t stride, int64_t tokens, int64_t H, int64_t D, int32_t dtype,
+                      int64_t* out) {
     *out = stride ? stride : H * D;
     if (*out < H * D || *out > (int64_t)1 << 40)
         return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld does not cover a token's %lld elements", name,
                     (long long)stride, (long long)(H * D));
     if (*out * elem_size(dtype) % 16 != 0)
         return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld is not a multiple of 16 bytes", name, (long long)stride);
+    if (tokens > 0 && *out > ((int64_t)1 << 58) / tokens)
+        return fail(GDN_ERR_UNSUPPORTED, "%s_stride=%lld: %lld tokens span more than 2^58 elements", name,
+                    (long long)stride, (long long)tokens);
     return GDN_OK;
 }
 
@@ -1681,9 +1686,9 @@ gdn_status la_problem(const gdn_la_problem* p, LaCall* c, bool bwd) {
     if (!supported_dim(p->K) || !supported_dim(p->V))
         return fail(GDN_ERR_UNSUPPORTED, "K=%lld V=%lld: each must be 16, 32, 64 or 128", (long long)p->K,
                     (long long)p->V);
-    if ((st = row_stride("q", p->q_stride, p->H, p->K, p->dtype, &c->sq)) != GDN_OK) return st;
-    if ((st = row_stride("k", p->k_stride, p->H, p->K, p->dtype, &c->sk)) != GDN_OK) return st;
-    if ((st = row_stride("v", p->v_stride, p->H, p->V, p->dtype, &c->sv)) != GDN_OK) return st;
+    if ((st = row_stride("q", p->q_stride, p->B * p->T, p->H, p->K, p->dtype, &c->sq)) != GDN_OK) return st;
+    if ((st = row_stride("k", p->k_stride, p->B * p->T, p->H, p->K, p->dtype, &c->sk)) != GDN_OK) return st;
+    if ((st = row_stride("v", p->v_stride, p->B * p->T, p->H, p->V, p->dtype, &c->sv)) != GDN_OK) return st;
     c->d.B = (int)p->B;
     c->d.T = (int)p->T;
     c->d.H = (int)p->H;
@@ -1894,8 +1899,8 @@ gdn_status rope_problem(const gdn_rope_problem* p, gdn::RopeCall* c) {
     if (!(p->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps=%g is negative", (double)p->eps);
     if (p->B * p->T > ((int64_t)1 << 33) / (p->Hq + p->Hk > 0 ? p->Hq + p->Hk : 1))
         return fail(GDN_ERR_UNSUPPORTED, "B*T*(Hq+Hk) exceeds 2^33");
-    if ((st = row_stride("q", p->q_stride, p->Hq, p->D, p->dtype, &c->q_stride)) != GDN_OK) return st;
-    if ((st = row_stride("k", p->k_stride, p->Hk, p->D, p->dtype, &c->k_stride)) != GDN_OK) return st;
+    if ((st = row_stride("q", p->q_stride, p->B * p->T, p->Hq, p->D, p->dtype, &c->q_stride)) != GDN_OK) return st;
+    if ((st = row_stride("k", p->k_stride, p->B * p->T, p->Hk, p->D, p->dtype, &c->k_stride)) != GDN_OK) return st;
     c->tokens = p->B * p->T;
     c->T = (int)p->T;
     c->Hq = (int)p->Hq;
@@ -1930,8 +1935,8 @@ gdn_status gated_problem(const gdn_gated_norm_problem* p, gdn::GatedCall* c) {
     if (!(p->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps=%g is negative", (double)p->eps);
     if (p->B * p->T > ((int64_t)1 << 33) / (p->H > 0 ? p->H : 1))
         return fail(GDN_ERR_UNSUPPORTED, "B*T*H exceeds 2^33");
-    if ((st = row_stride("x", p->x_stride, p->H, p->D, p->dtype, &c->x_stride)) != GDN_OK) return st;
-    if ((st = row_stride("gate", p->gate_stride, p->H, p->D, p->dtype, &c->z_stride)) != GDN_OK) return st;
+    if ((st = row_stride("x", p->x_stride, p->B * p->T, p->H, p->D, p->dtype, &c->x_stride)) != GDN_OK) return st;
+    if ((st = row_stride("gate", p->gate_stride, p->B * p->T, p->H, p->D, p->dtype, &c->z_stride)) != GDN_OK) return st;
     c->rows = p->B * p->T * p->H;
     c->H = (int)p->H;
     c->D = (int)p->D;
