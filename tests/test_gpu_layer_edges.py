@@ -205,3 +205,45 @@ def test_example_refuses_second_derivatives():
         (d,) = torch.autograd.grad((y * y).sum() + (x ** 3).sum(), x, create_graph=True)
         with pytest.raises(RuntimeError, match="differentiate twice"):
             d.sum().backward()
+
+
+def _bf16(x):
+    """Rounded to bf16 (float64 in and out)."""
+    return torch.from_numpy(np.ascontiguousarray(x)).float().bfloat16().double().numpy()
+
+
+@pytest.mark.parametrize("B,T,H,K,V,dtype", [
+    (1, 100, 200, 128, 128, "bf16"), (1, 1500, 2, 128, 128, "bf16"), (2, 700, 3, 64, 32, "bf16"),
+    (1, 1500, 160, 16, 16, "bf16"), (1, 100, 200, 128, 128, "f32"), (1, 1500, 2, 128, 128, "f32"), (2, 700, 3, 64, 32, "f32"),
+])
+def test_returned_states_and_float32_results_are_as_exact_as_float32_sums(B, T, H, K, V, dtype):
+    """Decays of 100 to 4000 tokens, one segment and several.  Tolerance 1.5e-6: bf16 inputs'
+    states are sums of 24-bit products in float32, 24 partial sums a tile, each cut to 24
+    bits: 24 * 2^-24 = 1.4e-6 if all went one way.  float32 products are exact to 2 * 2^-23
+    and their sums of 8 tokens or columns at a time go the same way.  With decayed rows of 16
+    bits (two bf16 numbers) a state is about 2.5e-6 off, which this tells apart."""
+    n = _normal(T + K, "f32")
+    cast = lambda t: t.to(DT[dtype])  # noqa: E731
+    q, k, v, d_o = cast(n(B, T, H, K) * K ** -0.5), cast(n(B, T, H, K)), cast(n(B, T, H, V)), cast(n(B, T, H, V))
+    h = torch.arange(1, H + 1, device="cuda", dtype=torch.float32)
+    ld = torch.log1p(-torch.exp2(-7 - 5 * h / H))
+    s0, dS = n(B, H, V, K) * 0.5, n(B, H, V, K) * 0.1
+    o, final, saved = gdn.gdn_la_fwd(q, k, v, ld, s0, saved=True)
+    grads = gdn.gdn_la_bwd(q, k, v, ld, s0, d_o, dS, saved=saved)
+    torch.cuda.synchronize()
+    at = sorted({0, H // 2, H - 1})
+    rows = lambda t: t[:1, :, at]  # noqa: E731
+    args = [_np(rows(t)) for t in (q, k, v)] + [_np(ld[at]), _np(s0[:1, at])]
+    ro, rs, _ = layer.la_fwd(*args)
+    ref = layer.la_bwd(*args, _np(rows(d_o)), _np(dS[:1, at]))
+    _close("final_state", final[:1, at], rs, 1.5e-6)
+    _close("d_initial_state", grads[3][:1, at], ref[3], 1.5e-6)
+    if dtype == "f32":
+        for name, t, r in zip(("o", "dq", "dk", "dv"), (o, *grads[:3]), (ro, *ref[:3])):
+            _close(name, rows(t), r, 1.5e-6)
+    else:  # the state that decayed rows of 16 bits would give
+        fade = np.exp(args[3][None, None, :, None] * (T - 1 - np.arange(T))[None, :, None, None])
+        c = args[2] * fade
+        short = np.einsum("bthv,bthk->bhvk", _bf16(c) + _bf16(c - _bf16(c)) - c, args[1])
+        with pytest.raises(AssertionError):
+            _close("final_state", final[:1, at], rs + short, 1.5e-6)
