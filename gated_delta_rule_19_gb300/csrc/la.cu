@@ -41,7 +41,7 @@ constexpr int kTok = 64;  // tokens of a chunk
 // of either sign.  (Cutting instead of rounding saves 5% of the time, but leaves a lo lo
 // of one sign.)  The small products have sums of their own, and no sum on the tensor
 // cores runs over more than one chunk: what is carried from chunk to chunk is added in
-// float32.  Results are within 5.5e-7 of the value (relative L2, T up to 4096), about twice
+// float32.  Results are within 5.5e-7 of the value (relative L2, T up to 4096), up to twice
 // as far as the same sums in float32.
 //
 // The rounding takes a number within 2^-12 of the largest one to infinity, and what is left
@@ -52,7 +52,7 @@ constexpr int kTok = 64;  // tokens of a chunk
 //
 // These warp-level products run at 512 a cycle and SM, which three tf32 products for one
 // make 170; float32 arithmetic has 128, of which its operands' reads from shared memory
-// left about half (B4 T2048 H6 K = V = 128 forward 197 us, now 146).
+// left about half (B4 T2048 H6 K = V = 128 forward 197 us, now 147).
 struct Sum {
     float hi[4], lo[4];
     __device__ __forceinline__ void zero() {

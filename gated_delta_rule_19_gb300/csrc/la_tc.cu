@@ -6,7 +6,10 @@
 //   scores Y = A B^T,   P = Y .* D (bf16, in tensor memory)
 //   X = A M^T,  X <- diag(gamma^(rho + 1 - rev)) X,  X += P C    -> the tile's outputs
 //   U = C'^T B,  M <- gamma^n M + U,   C' = C's rows times gamma^(n - 1 - rho + rev).
-// M is kept in float32 in registers; the product A M^T reads it rounded to bf16.  C' is
+// M is kept in float32 in registers; the products A M^T and P C read M and P rounded to
+// bf16, an error of the size of the outputs' own rounding (2.35e-3 relative L2 in all, the
+// outputs' rounding alone 1.66e-3): a second term of each would double two of the four
+// products, and tensor memory and shared memory have no room for it.  C' is
 // split into bf16 terms (the high part, then what is left), one product each: two where
 // M only feeds outputs (16 bits of every decayed value, 2.5e-6 rms of the sum; one would
 // add as much error to the outputs as M's own rounding), three in the sums and where M is
@@ -18,11 +21,12 @@
 // one the MMAs.  la_sums_kernel, the segments' sums, is the U part alone.  The hand-offs
 // are mbarriers; every wait is bounded.
 //
-// What bounds a tile is shared memory: an operand of an MMA is read at 128 bytes a
-// cycle, so A B^T and A M^T (both operands from there) take it whole while they run,
-// and the other products, the loads and stores and C' share the rest.  So P and C' are
-// operands in tensor memory, and most decay factors are multiplied up in registers
-// rather than read from tables.  Outputs stored from registers (32 bytes of a row per
+// What bounds a tile is its chain of hand-offs (scores, P, outputs; C', U, M), through a
+// shared memory that is busy most of it: of 6400 cycles a tile of the backward takes (B8
+// T4096 H6 K = V = 128), operands of MMAs read it for 1880 and the warps use it for 1660, and
+// the copies in and out need another 1000; tensor pipe 47%, issue 41%, DRAM 52%, L2 30% of
+// their rates.  An operand is read at 128 bytes a cycle, so P and C' are operands in tensor
+// memory, and most decay factors are multiplied up in registers rather than read from tables.  Outputs stored from registers (32 bytes of a row per
 // lane) kept the load-store unit busy and cost more than staging them does.
 //
 // K or V below 128: TMA fills the missing columns with zeros, and the products run over

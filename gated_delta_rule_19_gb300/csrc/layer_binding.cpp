@@ -1,7 +1,8 @@
 // layer_binding.cpp -- the Python binding of the linear-attention layer's calls
 // (include/gdn.h) on torch tensors: the same checks, allocations and errors as gdn.py's,
 // in C++.  A decode step's kernel takes a few microseconds; marshalling one call in
-// Python took 13 us on the benchmark's host, here it takes 3.3 (the launch is 2.5 of them).
+// Python took 13 us on the benchmark's host, here it takes 3.4 (the launch is 2.5 of them;
+// 4.2 with a program's own Python between the calls).
 //
 // The functions take positional arguments only; gdn.py has their signatures and
 // documentation.  An argument that may be left out is None.

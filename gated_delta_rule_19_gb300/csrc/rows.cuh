@@ -52,8 +52,9 @@ __device__ __forceinline__ uint4 put(const uint64_t (&f)[4]) {
 }
 
 // 1 / (1 + e^-z) by the PTX approximations ex2.approx.ftz (relative error about 2^-22)
-// and rcp.approx.ftz (1 ulp): within 1e-6 of the value for |z| up to 10, its own
-// limits 0 and 1 beyond.
+// and rcp.approx.ftz (1 ulp), for float32 gates too: with the rounding of z log2(e), half an
+// ulp of up to 128, the relative error is below 1e-6 for z >= -10 and grows to 5e-6 at
+// z = -87, where the value is 1e-38; below that it is 0.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
     const float l = -1.4426950408889634f;
     float x, y;

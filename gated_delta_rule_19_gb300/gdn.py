@@ -920,8 +920,12 @@ def gdn_la_fwd(q, k, v, log_decay, initial_state=None, *, o=None, final_state=Tr
     float32 tensor to fill (may be initial_state itself), or False/None.  ``saved``:
     True to allocate and return what :func:`gdn_la_bwd` then need not compute again,
     or a buffer of at least gdn_la_saved_bytes() bytes.  ``stream``: a torch stream
-    instead of the current one; what this call and the ones below make belongs to it.
-    Returns ``(o, final_state or None, saved or None)``."""
+    instead of the current one; what this call and the ones below make belongs to it, unlike
+    the calls above, whose new tensors belong to the current stream.  ``workspace``: as
+    there, and a caller that passes one with its first int32 cleared can see there, after
+    the call has run, whether a kernel's bounded wait gave up (not 0: the outputs are not
+    valid).  Calls run on their tensors' device, and what they write counts as changed for
+    autograd.  Returns ``(o, final_state or None, saved or None)``."""
     return (_layer or _binding()).la_fwd(q, k, v, log_decay, initial_state, o, final_state, saved, workspace,
                                          _raw(stream))
 
@@ -949,7 +953,9 @@ def gdn_qk_norm_rope_fwd(q, k, q_weight, k_weight, cos=None, sin=None, positions
     a fixed stride apart); q_weight, k_weight [D]; cos, sin float32 [table_rows, R/2]
     (None: no rotation); positions int32 [B,T], rows of the tables (None: 0 .. T-1).
     Pairs are (i, i + R/2), or (2i, 2i+1) with ``interleaved``.  A position outside the
-    tables makes its token's rows NaN.  Returns ``(q_out, k_out)``, dense."""
+    tables makes its token's rotated elements NaN (the first R of each row), and in
+    :func:`gdn_qk_norm_rope_bwd` its whole gradient rows.  Returns ``(q_out, k_out)``,
+    dense."""
     return (_layer or _binding()).rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
                                            k_out, _raw(stream))
 

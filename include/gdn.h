@@ -388,8 +388,8 @@ gdn_status gdn_decode(const gdn_problem* p, const void* q, const void* k, const 
  * these take row tensors by a token stride: the elements from one token's rows to
  * the next token's (0: dense), so that q, k, v and gates can be slices of a fused
  * projection.  Batch rows lie T tokens apart, the [H, D] rows of a token are
- * dense, and a stride covers them and is a multiple of 16 bytes.  Outputs are
- * dense.  As above, errors are returned before any launch, nothing is allocated
+ * dense, and a stride covers them and is a multiple of 16 bytes; all tokens span at
+ * most 2^58 elements.  Outputs are dense.  As above, errors are returned before any launch, nothing is allocated
  * and the calls are asynchronous on `stream`.  B, H >= 0 and <= 65535, with
  * B * H <= 2^24, T >= 0 and <= 2^30.
  */
@@ -414,8 +414,9 @@ typedef struct {
  *   workspace      gdn_la_fwd_workspace_bytes(p) bytes.  Its first int is an error
  *                  word: a bounded wait that gives up sets a bit there (nothing
  *                  clears it; a caller that reads it clears it before the call).
- * A value that is not finite reaches the outputs of its whole 128-token tile, and
- * every later one.
+ * A value that is not finite reaches the outputs of its whole tile (128 tokens of
+ * bf16, 64 of float32), and every later one; in bf16 an infinity may come out as NaN,
+ * and a state past bf16's largest number feeds the outputs as an infinity.
  */
 size_t gdn_la_fwd_workspace_bytes(const gdn_la_problem* p);
 size_t gdn_la_saved_bytes(const gdn_la_problem* p);
@@ -468,7 +469,8 @@ typedef struct {
  *   cos, sin   float32 [table_rows, R/2] (may be NULL when R = 0).
  *   positions  int32 [B,T], the tokens' rows of the tables, or NULL: token t has
  *              row t (then table_rows >= T).  A position outside the tables makes
- *              its token's rows NaN.
+ *              its token's rotated elements NaN, the first R of each row; the others
+ *              do not depend on it (nor does anything where R = 0).
  *   q_out, k_out  dense, shapes of q and k.
  */
 gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
@@ -478,7 +480,8 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
 /*
  * gdn_qk_norm_rope_bwd -- from the gradients dq_out, dk_out (dense) of its outputs,
  * those of q, k (dense), q_weight and k_weight ([D], p->dtype; summed in float32
- * in a fixed order, so equal calls give equal bits).
+ * in a fixed order, so equal calls give equal bits).  A position outside the tables
+ * makes its token's whole gradient rows NaN, and elements of the weights' gradients.
  */
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p);
 gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
