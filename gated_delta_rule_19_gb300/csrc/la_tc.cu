@@ -22,12 +22,13 @@
 // are mbarriers; every wait is bounded.
 //
 // What bounds a tile is its chain of hand-offs (scores, P, outputs; C', U, M), through a
-// shared memory that is busy most of it: of 6400 cycles a tile of the backward takes (B8
-// T4096 H6 K = V = 128), operands of MMAs read it for 1880 and the warps use it for 1660, and
-// the copies in and out need another 1000; tensor pipe 47%, issue 41%, DRAM 52%, L2 30% of
+// shared memory that is busy most of it: of the 6400 cycles that a tile of the backward takes
+// (B8 T4096 H6 K = V = 128), operands of MMAs read it for 1880 and the warps use it for 1660,
+// and the copies in and out need another 1000; tensor pipe 47%, issue 41%, DRAM 52%, L2 30% of
 // their rates.  An operand is read at 128 bytes a cycle, so P and C' are operands in tensor
-// memory, and most decay factors are multiplied up in registers rather than read from tables.  Outputs stored from registers (32 bytes of a row per
-// lane) kept the load-store unit busy and cost more than staging them does.
+// memory, and most decay factors are multiplied up in registers rather than read from
+// tables.  Outputs stored from registers (32 bytes of a row per lane) kept the load-store
+// unit busy and cost more than staging them does.
 //
 // K or V below 128: TMA fills the missing columns with zeros, and the products run over
 // the columns that are there (N and K of each MMA follow Db and Dc).

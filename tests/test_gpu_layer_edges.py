@@ -169,6 +169,9 @@ def test_float32_values_next_to_the_largest(T, H, K, V):
         _close(name, t[:, :, :2], r)
     _close("final_state", final[:, :2], rs)
     _close("d_initial_state", grads[3][:, :2], ref[3])
+    gdn.gdn_la_fwd(q, k, v, ld, s0, final_state=s0)  # a state that is overwritten is read first
+    torch.cuda.synchronize()
+    assert torch.equal(s0, final)
 
 
 @pytest.mark.parametrize("D", [32, 128])
@@ -225,7 +228,8 @@ def _bf16(x):
 
 @pytest.mark.parametrize("B,T,H,K,V,dtype", [
     (1, 100, 200, 128, 128, "bf16"), (1, 1500, 2, 128, 128, "bf16"), (2, 700, 3, 64, 32, "bf16"),
-    (1, 1500, 160, 16, 16, "bf16"), (1, 100, 200, 128, 128, "f32"), (1, 1500, 2, 128, 128, "f32"), (2, 700, 3, 64, 32, "f32"),
+    (1, 1500, 160, 16, 16, "bf16"), (1, 100, 200, 128, 128, "f32"), (1, 1500, 2, 128, 128, "f32"),
+    (2, 700, 3, 64, 32, "f32"),
 ])
 def test_returned_states_and_float32_results_are_as_exact_as_float32_sums(B, T, H, K, V, dtype):
     """Decays of 100 to 4000 tokens, one segment and several.  Tolerance 1.5e-6: bf16 inputs'
