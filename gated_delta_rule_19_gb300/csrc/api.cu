@@ -9,7 +9,9 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <algorithm>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include "gdn.h"
@@ -235,7 +237,9 @@ const char* const kKernelNames[gdn::KID_COUNT] = {
     "prologue_bwd_kernel", "varlen_offsets", "varlen_gather", "varlen_scatter", "scan_fwd_tc(split pass 1)",
     "scan_bwd_tc(split pass 1)", "scan_fwd_tc(transitions)", "split_combine", "count_nonfinite_kernel",
     "la_states", "la_link_kernel", "la_scan", "la_decode_kernel", "qk_norm_rope_fwd_kernel", "qk_norm_rope_bwd_kernel",
-    "gated_norm_fwd_kernel", "gated_norm_bwd_kernel", "weight_sum_kernel"};
+    "gated_norm_fwd_kernel", "gated_norm_bwd_kernel", "weight_sum_kernel", "qk_norm_rope_fwd_kernel(axes)",
+    "qk_norm_rope_bwd_kernel(axes)", "add_norm_fwd_kernel", "add_norm_fwd_kernel(8 bits)", "add_norm_bwd_kernel",
+    "grad_sum_kernel", "grad_norm_kernel", "grad_scale_kernel", "state_store_kernel", "state_load_kernel"};
 
 template <typename F>
 cudaError_t timed(int kid, cudaStream_t st, F&& launch) {
@@ -1949,11 +1953,9 @@ gdn_status gated_problem(const gdn_gated_norm_problem* p, gdn::GatedCall* c) {
 
 extern "C" {
 
-gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
-                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
-                                void* q_out, void* k_out, void* stream) {
-    g_err[0] = 0;
-    gdn::RopeCall c{};
+static gdn_status rope_fwd(const gdn_rope_problem* p, gdn::RopeCall& c, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                           const int32_t* positions, void* q_out, void* k_out, void* stream) {
     gdn_status st = rope_problem(p, &c);
     if (st != GDN_OK) return st;
     const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
@@ -1971,9 +1973,19 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
     c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
     c.qo = q_out, c.ko = k_out;
     cudaStream_t cs = (cudaStream_t)stream;
-    cudaError_t e = timed(gdn::KID_NORM_ROPE_FWD, cs,
-                          [&] { return gdn::launch_qk_norm_rope(c, elem_type(p->dtype), false, cs); });
+    const gdn::InType ty = elem_type(p->dtype);
+    cudaError_t e = timed(c.axes ? gdn::KID_NORM_AXES_FWD : gdn::KID_NORM_ROPE_FWD, cs, [&] {
+        return c.axes ? gdn::launch_qk_norm_rope_axes(c, ty, false, cs) : gdn::launch_qk_norm_rope(c, ty, false, cs);
+    });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "q, k norm and rotation kernel");
+}
+
+gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                void* q_out, void* k_out, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    return rope_fwd(p, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream);
 }
 
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p) {
@@ -1981,12 +1993,10 @@ size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p) {
     return rope_problem(p, &c) == GDN_OK ? (size_t)2 * c.blocks * c.D * sizeof(float) : 0;
 }
 
-gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
-                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
-                                const void* dq_out, const void* dk_out, void* dq, void* dk, void* dq_weight,
-                                void* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
-    g_err[0] = 0;
-    gdn::RopeCall c{};
+static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                           const int32_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                           void* dq_weight, void* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
     gdn_status st = rope_problem(p, &c);
     if (st != GDN_OK) return st;
     const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
@@ -2014,11 +2024,23 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
     c.qo = dq, c.ko = dk, c.dqo = dq_out, c.dko = dk_out, c.part = (float*)workspace;
     cudaStream_t cs = (cudaStream_t)stream;
     const gdn::InType ty = elem_type(p->dtype);
-    cudaError_t e = timed(gdn::KID_NORM_ROPE_BWD, cs, [&] { return gdn::launch_qk_norm_rope(c, ty, true, cs); });
+    cudaError_t e = timed(c.axes ? gdn::KID_NORM_AXES_BWD : gdn::KID_NORM_ROPE_BWD, cs, [&] {
+        return c.axes ? gdn::launch_qk_norm_rope_axes(c, ty, true, cs) : gdn::launch_qk_norm_rope(c, ty, true, cs);
+    });
     if (e == cudaSuccess)
         e = timed(gdn::KID_WEIGHT_SUM, cs,
                   [&] { return gdn::launch_weight_sum(2, c.blocks, c.D, ty, c.part, dq_weight, dk_weight, cs); });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "q, k norm and rotation gradient kernel");
+}
+
+gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                                const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                const void* dq_out, const void* dk_out, void* dq, void* dk, void* dq_weight,
+                                void* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    return rope_bwd(p, c, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk, dq_weight, dk_weight,
+                    workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_gated_norm_fwd(const gdn_gated_norm_problem* p, const void* x, const void* gate, const void* weight,
@@ -2074,6 +2096,320 @@ gdn_status gdn_gated_norm_bwd(const gdn_gated_norm_problem* p, const void* x, co
         e = timed(gdn::KID_WEIGHT_SUM, cs,
                   [&] { return gdn::launch_weight_sum(1, c.blocks, c.D, ty, c.part, dweight, dweight, cs); });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gated norm gradient kernel");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// What surrounds the layer in its block: the rotation by several positions, the residual's
+// addition with the norm, the gradients' norm and clipping, the cache of states.
+
+namespace {
+
+// The axes' part of a call: which axis turns each pair.
+gdn_status axes_map(const gdn_rope_axes_problem* p, const int32_t* positions, gdn::RopeCall* c) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    const int64_t pairs = p->rope.R / 2;
+    if (p->axes < 1 || p->axes > 4) return fail(GDN_ERR_UNSUPPORTED, "axes=%d: must be 1 to 4", (int)p->axes);
+    if (p->rope.R < 0 || p->rope.R > 256)
+        return fail(GDN_ERR_UNSUPPORTED, "R=%lld: must be 0 to 256", (long long)p->rope.R);
+    int64_t sum = 0;
+    for (int a = 0; a < p->axes; ++a) {
+        if (p->sections[a] < 0 || p->sections[a] > pairs)
+            return fail(GDN_ERR_INVALID_ARG, "sections[%d]=%d: must be 0 to R/2=%lld", a, (int)p->sections[a],
+                        (long long)pairs);
+        sum += p->sections[a];
+    }
+    if (sum != pairs)
+        return fail(GDN_ERR_INVALID_ARG, "sections sum to %lld, expected R/2=%lld", (long long)sum, (long long)pairs);
+    int counts[4] = {0, 0, 0, 0};
+    for (int i = 0, block = 0, end = p->sections[0]; i < pairs; ++i) {
+        int a;
+        if (p->alternating) {
+            a = i % p->axes;
+            if (i / p->axes >= p->sections[a]) a = 0;
+        } else {
+            while (i >= end) end += p->sections[++block];
+            a = block;
+        }
+        ++counts[a];
+        c->map.w[i >> 5] |= (uint64_t)a << (2 * (i & 31));
+    }
+    for (int a = 0; a < p->axes; ++a)
+        if (counts[a] != p->sections[a])
+            return fail(GDN_ERR_INVALID_ARG, "sections[%d]=%d: %d of the alternating pairs fall to this axis", a,
+                        (int)p->sections[a], counts[a]);
+    if (pairs && p->rope.B > 0 && p->rope.T > 0) {
+        if (!positions) return fail(GDN_ERR_INVALID_ARG, "positions is NULL");
+        if ((uintptr_t)positions % 4 != 0) return fail(GDN_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+    }
+    c->axes = p->axes;
+    return GDN_OK;
+}
+
+gdn_status add_norm_problem(const gdn_add_norm_problem* p, gdn::AddNormCall* c) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    for (int32_t t : {p->dtype, p->stream_dtype})
+        if (t != GDN_F32 && t != GDN_BF16)
+            return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_F32 or GDN_BF16", (int)t);
+    if (p->stream_dtype != p->dtype && p->stream_dtype != GDN_F32)
+        return fail(GDN_ERR_UNSUPPORTED, "a bf16 residual stream with float32 x");
+    if (p->rows < 0) return fail(GDN_ERR_INVALID_ARG, "negative size (rows=%lld)", (long long)p->rows);
+    if (p->rows > (int64_t)1 << 33) return fail(GDN_ERR_UNSUPPORTED, "rows=%lld exceeds 2^33", (long long)p->rows);
+    const int64_t step = 16 / (int64_t)elem_size(p->dtype);
+    if (p->D < 1 || p->D > gdn::kAddNormMost || p->D % step != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "D=%lld: must be a multiple of %lld, at most %d", (long long)p->D,
+                    (long long)step, gdn::kAddNormMost);
+    if (!(p->eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps=%g is negative", (double)p->eps);
+    gdn_status st = row_stride("x", p->x_stride, p->rows, 1, p->D, p->dtype, &c->x_stride);
+    if (st == GDN_OK) st = row_stride("stream", p->stream_stride, p->rows, 1, p->D, p->stream_dtype, &c->r_stride);
+    c->rows = p->rows;
+    c->D = (int)p->D;
+    c->eps = p->eps;
+    return st;
+}
+
+gdn_status add_norm(const gdn_add_norm_problem* p, gdn::AddNormKind kind, int32_t group, const void* x,
+                    const void* residual, const void* weight, void* h, void* y, float* scales, void* stream) {
+    g_err[0] = 0;
+    gdn::AddNormCall c{};
+    gdn_status st = add_norm_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const bool quant = kind == gdn::AddNormKind::QUANT;
+    if (quant && group != 0 && ((group != 32 && group != 64 && group != 128) || p->D % group != 0))
+        return fail(GDN_ERR_UNSUPPORTED, "group=%d: must be 0, 32, 64 or 128 and divide D=%lld", (int)group,
+                    (long long)p->D);
+    if (!residual && h) return fail(GDN_ERR_INVALID_ARG, "h is given without a residual: it would be x");
+    if (!residual && p->stream_dtype != p->dtype)
+        return fail(GDN_ERR_INVALID_ARG, "stream_dtype differs from dtype without a residual");
+    const size_t es = elem_size(p->dtype), er = elem_size(p->stream_dtype), n = (size_t)p->rows * p->D;
+    const Span ins[] = {{x, row_span(p->rows, c.x_stride, p->D, p->dtype), "x"},
+                        {residual, row_span(p->rows, c.r_stride, p->D, p->stream_dtype), "residual"},
+                        {weight, p->D * es, "weight"}};
+    const Span outs[] = {{y, n * (quant ? 1 : es), "y"},
+                         {h, n * er, "h"},
+                         {scales, quant ? (size_t)p->rows * (group ? p->D / group : 1) * sizeof(float) : 0, "scales"}};
+    if (h && h == residual && p->rows > 1 && c.r_stride != p->D)
+        return fail(GDN_ERR_INVALID_ARG, "h is the residual, which is not dense");
+    if ((st = check_spans(ins, 3, 1u << 1, outs, 3, 1u << 1, h, residual)) != GDN_OK) return st;
+    if (p->rows == 0) return GDN_OK;
+    c.x = x, c.res = residual, c.w = weight, c.h = h, c.y = y, c.scales = scales, c.group = group;
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = timed(quant ? gdn::KID_ADD_NORM_QUANT : gdn::KID_ADD_NORM_FWD, cs, [&] {
+        return gdn::launch_add_norm(c, elem_type(p->dtype), elem_type(p->stream_dtype), kind, cs);
+    });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "residual norm kernel");
+}
+
+size_t add_norm_part(const gdn::AddNormCall& c) { return (size_t)c.blocks * c.D * sizeof(float); }
+
+// The tensors of a gradient call; with `write` their outputs too, which must lie apart.
+gdn_status check_grads(const gdn_grad* g, int64_t count, bool write, const Span* others, int nothers) {
+    if (count < 0) return fail(GDN_ERR_INVALID_ARG, "negative count %lld", (long long)count);
+    if (count > (int64_t)1 << 20) return fail(GDN_ERR_UNSUPPORTED, "count=%lld exceeds 2^20", (long long)count);
+    if (count && !g) return fail(GDN_ERR_INVALID_ARG, "grads is NULL");
+    int64_t tiles = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const long long at = i;
+        if (g[i].n < 0) return fail(GDN_ERR_INVALID_ARG, "grads[%lld]: negative length", at);
+        if (g[i].n > (int64_t)1 << 43) return fail(GDN_ERR_UNSUPPORTED, "grads[%lld]: more than 2^43 elements", at);
+        if (g[i].dtype != GDN_F32 && g[i].dtype != GDN_BF16)
+            return fail(GDN_ERR_UNSUPPORTED, "grads[%lld]: dtype %d is not GDN_F32 or GDN_BF16", at, (int)g[i].dtype);
+        if (write && g[i].out_dtype != GDN_F32 && g[i].out_dtype != GDN_BF16)
+            return fail(GDN_ERR_UNSUPPORTED, "grads[%lld]: out_dtype %d is not GDN_F32 or GDN_BF16", at,
+                        (int)g[i].out_dtype);
+        tiles += gdn::grad_tiles(g[i].n);
+        if (tiles > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "the gradients have more than 2^43 elements");
+        if (g[i].n == 0) continue;
+        if (!g[i].grad || (write && !g[i].out)) return fail(GDN_ERR_INVALID_ARG, "grads[%lld]: NULL pointer", at);
+        if ((uintptr_t)g[i].grad % elem_size(g[i].dtype) || (write && (uintptr_t)g[i].out % elem_size(g[i].out_dtype)))
+            return fail(GDN_ERR_INVALID_ARG, "grads[%lld]: not aligned to its elements", at);
+        if (write && g[i].out == g[i].grad && g[i].out_dtype != g[i].dtype)
+            return fail(GDN_ERR_INVALID_ARG, "grads[%lld]: its own output in another type", at);
+    }
+    // every span of memory by its address: none that is written reaches into another one
+    struct Reach {
+        uintptr_t from, to;
+        bool out;
+    };
+    try {
+        std::vector<Reach> r;
+        r.reserve(2 * (size_t)count + nothers);
+        auto add = [&](const void* p, size_t bytes, bool out) {
+            if (p && bytes) r.push_back({(uintptr_t)p, (uintptr_t)p + bytes, out});
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const bool own = write && g[i].out == g[i].grad;
+            add(g[i].grad, (size_t)g[i].n * elem_size(g[i].dtype), own);
+            if (write && !own) add(g[i].out, (size_t)g[i].n * elem_size(g[i].out_dtype), true);
+        }
+        for (int i = 0; i < nothers; ++i) add(others[i].p, others[i].n, true);
+        std::sort(r.begin(), r.end(), [](const Reach& a, const Reach& b) { return a.from < b.from; });
+        uintptr_t any = 0, out = 0;
+        for (const Reach& x : r) {
+            if (x.from < out || (x.out && x.from < any))
+                return fail(GDN_ERR_INVALID_ARG, "an output overlaps a gradient or another output at %p", (void*)x.from);
+            any = std::max(any, x.to);
+            if (x.out) out = std::max(out, x.to);
+        }
+    } catch (const std::bad_alloc&) {
+        return fail(GDN_ERR_UNSUPPORTED, "out of host memory for %lld gradients", (long long)count);
+    }
+    return GDN_OK;
+}
+
+gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, float* norm, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    if (clip && !(max_norm >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "max_norm=%g is negative", (double)max_norm);
+    gdn_status st;
+    if ((!clip || norm) && (st = check_word_ptr(norm, "norm")) != GDN_OK) return st;
+    const size_t need = gdn_grad_workspace_bytes(count < 0 ? 0 : count);
+    const Span others[] = {{norm, sizeof(float), "norm"}, {workspace, need, "workspace"}};
+    if ((st = check_grads(g, count, clip, others, 2)) != GDN_OK || (st = check_ptr(others[1], true)) != GDN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    cudaStream_t cs = (cudaStream_t)stream;
+    double* part = (double*)workspace;
+    int parts = 0;
+    cudaError_t e = timed(gdn::KID_GRAD_SUM, cs, [&] { return gdn::launch_grad_sums(g, count, part, &parts, cs); });
+    if (e == cudaSuccess && clip)
+        e = timed(gdn::KID_GRAD_SCALE, cs,
+                  [&] { return gdn::launch_grad_scale(g, count, part, parts, max_norm, norm, cs); });
+    else if (e == cudaSuccess)
+        e = timed(gdn::KID_GRAD_NORM, cs, [&] { return gdn::launch_grad_norm(part, parts, norm, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gradient norm kernel");
+}
+
+gdn_status state_cache(const gdn_state_cache_problem* p, bool load, const void* states, const int32_t* slot,
+                       const void* cache, const float* scales, void* stream) {
+    g_err[0] = 0;
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
+    gdn_status st = check_layer_sizes(p->B, 1, p->H, GDN_F32);
+    if (st != GDN_OK) return st;
+    if (!supported_dim(p->K) || !supported_dim(p->V))
+        return fail(GDN_ERR_UNSUPPORTED, "K=%lld V=%lld: each must be 16, 32, 64 or 128", (long long)p->K,
+                    (long long)p->V);
+    if (p->slots < 0 || p->slots > INT32_MAX)
+        return fail(p->slots < 0 ? GDN_ERR_INVALID_ARG : GDN_ERR_UNSUPPORTED, "slots=%lld", (long long)p->slots);
+    const size_t rows = (size_t)p->H * p->V, es = sizeof(float);
+    const Span own = {states, (size_t)p->B * rows * p->K * es, "states"};
+    const Span kept[] = {{cache, (size_t)p->slots * rows * p->K, "cache"}, {scales, (size_t)p->slots * rows * es, "scales"}};
+    const Span at = {slot, (size_t)p->B * 4, "slot"};
+    const Span ins[] = {load ? kept[0] : own, kept[1]}, outs[] = {load ? own : kept[0], kept[1]};
+    st = load ? check_spans(ins, 2, 0, outs, 1, 0, nullptr, nullptr) : check_spans(ins, 1, 0, outs, 2, 0, nullptr, nullptr);
+    if (st != GDN_OK || own.n == 0) return st;
+    if ((st = check_word_ptr(slot, "slot")) != GDN_OK) return st;
+    if ((st = check_overlaps(&at, 1, outs, load ? 1 : 2, nullptr, nullptr)) != GDN_OK) return st;
+    const gdn::StateCall c{(int)p->B, (int)p->K, (int64_t)rows, p->slots, slot, (const float*)states, (float*)states,
+                           (void*)cache, (float*)scales};
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = timed(load ? gdn::KID_STATE_LOAD : gdn::KID_STATE_STORE, cs,
+                          [&] { return gdn::launch_state_cache(c, load, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "state cache kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
+                                     const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                     const int32_t* positions, void* q_out, void* k_out, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    const gdn_status st = axes_map(p, positions, &c);
+    return st == GDN_OK ? rope_fwd(&p->rope, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream) : st;
+}
+
+gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
+                                     const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                     const int32_t* positions, const void* dq_out, const void* dk_out, void* dq,
+                                     void* dk, void* dq_weight, void* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    gdn::RopeCall c{};
+    const gdn_status st = axes_map(p, positions, &c);
+    return st == GDN_OK ? rope_bwd(&p->rope, c, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk,
+                                   dq_weight, dk_weight, workspace, workspace_bytes, stream)
+                        : st;
+}
+
+gdn_status gdn_add_norm_fwd(const gdn_add_norm_problem* p, const void* x, const void* residual, const void* weight,
+                            void* h, void* y, void* stream) {
+    return add_norm(p, gdn::AddNormKind::FWD, 0, x, residual, weight, h, y, nullptr, stream);
+}
+
+gdn_status gdn_add_norm_quant(const gdn_add_norm_problem* p, int32_t group, const void* x, const void* residual,
+                              const void* weight, void* h, void* y8, float* scales, void* stream) {
+    return add_norm(p, gdn::AddNormKind::QUANT, group, x, residual, weight, h, y8, scales, stream);
+}
+
+size_t gdn_add_norm_bwd_workspace_bytes(const gdn_add_norm_problem* p) {
+    gdn::AddNormCall c{};
+    if (add_norm_problem(p, &c) != GDN_OK) return 0;
+    c.blocks = gdn::add_norm_bwd_blocks(c.rows, c.D, (int)elem_size(p->stream_dtype));
+    return add_norm_part(c);
+}
+
+gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const void* weight, const void* dy,
+                            const void* dh, void* dx, void* d_residual, void* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    gdn::AddNormCall c{};
+    gdn_status st = add_norm_problem(p, &c);
+    if (st != GDN_OK) return st;
+    const bool apart = p->dtype != p->stream_dtype;
+    const size_t es = elem_size(p->dtype), er = elem_size(p->stream_dtype), n = (size_t)p->rows * p->D;
+    c.blocks = gdn::add_norm_bwd_blocks(c.rows, c.D, (int)er);
+    const size_t need = add_norm_part(c);
+    if (!apart && d_residual)
+        return fail(GDN_ERR_INVALID_ARG, "d_residual is given where the types agree: dx is both gradients");
+    const Span ins[] = {{h, row_span(p->rows, c.r_stride, p->D, p->stream_dtype), "h"},
+                        {weight, p->D * es, "weight"},
+                        {dy, n * es, "dy"},
+                        {dh, n * er, "dh"}};
+    const Span outs[] = {{dx, n * es, "dx"},
+                         {d_residual, apart ? n * er : 0, "d_residual"},
+                         {dweight, p->D * es, "dweight"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    c.h_in = h, c.w = weight, c.dy = dy, c.dh = dh, c.dx = dx, c.dr = d_residual, c.part = (float*)workspace;
+    cudaStream_t cs = (cudaStream_t)stream;
+    const gdn::InType ty = elem_type(p->dtype);
+    cudaError_t e = timed(gdn::KID_ADD_NORM_BWD, cs, [&] {
+        return gdn::launch_add_norm(c, ty, elem_type(p->stream_dtype), gdn::AddNormKind::BWD, cs);
+    });
+    if (e == cudaSuccess)
+        e = timed(gdn::KID_WEIGHT_SUM, cs,
+                  [&] { return gdn::launch_weight_sum(1, c.blocks, c.D, ty, c.part, dweight, dweight, cs); });
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "residual norm gradient kernel");
+}
+
+size_t gdn_grad_workspace_bytes(int64_t count) {
+    return count < 0 || count > (int64_t)1 << 20 ? 0 : gdn::grad_parts(count) * sizeof(double);
+}
+
+gdn_status gdn_grad_norm(const gdn_grad* g, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    return grads(g, count, false, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_clip_grads(const gdn_grad* g, int64_t count, float max_norm, float* norm, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    return grads(g, count, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_state_store(const gdn_state_cache_problem* p, const float* states, const int32_t* slot, void* cache,
+                           float* scales, void* stream) {
+    return state_cache(p, false, states, slot, cache, scales, stream);
+}
+
+gdn_status gdn_state_load(const gdn_state_cache_problem* p, const void* cache, const float* scales,
+                          const int32_t* slot, float* states, void* stream) {
+    return state_cache(p, true, states, slot, cache, scales, stream);
 }
 
 }  // extern "C"

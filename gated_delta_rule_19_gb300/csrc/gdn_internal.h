@@ -10,6 +10,8 @@
 
 #include <atomic>
 
+#include "gdn.h"
+
 namespace gdn {
 
 // Problem dimensions as the kernels see them.  NC = ceil(T / C) chunks per
@@ -153,6 +155,16 @@ enum KernelId {
     KID_GATED_NORM_FWD,  // gated_norm_fwd_kernel
     KID_GATED_NORM_BWD,  // gated_norm_bwd_kernel
     KID_WEIGHT_SUM,      // weight_sum_kernel
+    KID_NORM_AXES_FWD,   // qk_norm_rope_fwd_kernel, several positions
+    KID_NORM_AXES_BWD,   // qk_norm_rope_bwd_kernel, several positions
+    KID_ADD_NORM_FWD,    // add_norm_fwd_kernel
+    KID_ADD_NORM_QUANT,  // add_norm_fwd_kernel, 8-bit output
+    KID_ADD_NORM_BWD,    // add_norm_bwd_kernel
+    KID_GRAD_SUM,        // grad_sum_kernel
+    KID_GRAD_NORM,       // grad_norm_kernel
+    KID_GRAD_SCALE,      // grad_scale_kernel
+    KID_STATE_STORE,     // state_store_kernel
+    KID_STATE_LOAD,      // state_load_kernel
     KID_COUNT
 };
 
@@ -397,6 +409,11 @@ cudaError_t launch_la_scan_tc(const LaDims& d, const LaRoles& roles, cudaStream_
 cudaError_t launch_la_decode(const LaDims& d, InType ty, const void* q, const void* k, const void* v, int64_t sq,
                              int64_t sk, int64_t sv, float* state, void* o, cudaStream_t st);
 
+// The axis of each of R / 2 pairs (128 at most), two bits a pair.
+struct AxesMap {
+    uint64_t w[4];
+};
+
 // RMS norm and rotation of q and k rows; backward: qo, ko are dq, dk, dqo, dko the
 // gradients of the outputs, part [2][blocks][D] the blocks' sums for the weights.
 struct RopeCall {
@@ -412,8 +429,11 @@ struct RopeCall {
     const void *dqo = nullptr, *dko = nullptr;
     float* part = nullptr;
     int blocks = 0;
+    int axes = 0;  // launch_qk_norm_rope_axes: pos is [axes][tokens]
+    AxesMap map = {};
 };
 cudaError_t launch_qk_norm_rope(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
+cudaError_t launch_qk_norm_rope_axes(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
 
 // RMS norm of x times silu(z); backward: part [blocks][D].
 struct GatedCall {
@@ -435,5 +455,52 @@ cudaError_t launch_weight_sum(int sides, int blocks, int D, InType ty, const flo
 // Blocks of the two backward kernels (and rows of their partial sums).
 constexpr int kRopeBwdPerSm = 2, kGatedBwdPerSm = 2;
 int rows_bwd_blocks(int64_t rows, int per_sm);
+
+// ---- a block's other operators (add_norm.cu, grads.cu, state_cache.cu) ----
+
+// RMS norm of x + res (res NULL: of x); `ty` is the type of x, w, y and their gradients,
+// `stream_ty` that of res, h, dh and dr.  Forward: y (QUANT: e4m3, with scales of `group`
+// columns, 0: of a row) and h.  Backward: from h_in, dy and dh (or NULL) dx, dr (where the
+// types differ) and the blocks' sums part [blocks][D] of the weight's gradient.
+enum class AddNormKind { FWD, QUANT, BWD };
+struct AddNormCall {
+    int64_t rows;
+    int D, group;
+    int64_t x_stride, r_stride;  // r_stride: of res, of h_in in the backward
+    float eps;
+    const void *x, *res, *w;
+    void* h = nullptr;
+    void* y = nullptr;
+    float* scales = nullptr;
+    const void *h_in = nullptr, *dy = nullptr, *dh = nullptr;
+    void *dx = nullptr, *dr = nullptr;
+    float* part = nullptr;
+    int blocks = 0;
+};
+constexpr int kAddNormMost = 8192;  // columns
+cudaError_t launch_add_norm(const AddNormCall& c, InType ty, InType stream_ty, AddNormKind kind, cudaStream_t st);
+// Blocks of the backward; `wide`: bytes of an element of the wider type.
+int add_norm_bwd_blocks(int64_t rows, int D, int wide);
+
+// The gradients' norm and their scaling: partial sums (grad_parts(count) doubles at most)
+// first, *parts of them.
+size_t grad_parts(int64_t count);
+int64_t grad_tiles(int64_t n);  // at least as many as the tiles of n elements
+cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, double* part, int* parts, cudaStream_t st);
+cudaError_t launch_grad_norm(const double* part, int parts, float* norm, cudaStream_t st);
+cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const double* part, int parts, float max_norm,
+                              float* norm, cudaStream_t st);
+
+// States [B][rows][K] to and from the slots of a cache [slots][rows][K] with a scale a row.
+struct StateCall {
+    int B, K;
+    int64_t rows, slots;
+    const int32_t* slot_of;
+    const float* states;  // store
+    float* out;           // load
+    void* cache;
+    float* scales;
+};
+cudaError_t launch_state_cache(const StateCall& c, bool load, cudaStream_t st);
 
 }  // namespace gdn

@@ -1,0 +1,374 @@
+// grads.cu -- the norm of all of a model's gradients taken as one vector, and their
+// clipping to a largest norm.
+//
+//   norm = sqrt(sum over all tensors of g^2),    out = g min(1, max_norm / norm).
+//
+// Bound by reading the gradients, once for the norm and once for the scaling.  The tensors
+// come as kernel parameters (addresses, lengths, first tiles; up to kMany a launch), so that
+// a call copies nothing to the device and can be captured.  They are cut into tiles, which
+// the blocks share evenly, each block a run of neighbouring ones; the scaling takes a run
+// from its end, where what the norm read last may still be in L2.
+//
+// The sum: a thread adds the squares of its 32 elements of a tile in float32, and the tiles'
+// sums with their rounding errors kept (two float32 numbers); blocks and the call in float64,
+// in a fixed order, by every block of the scaling for itself.  So the norm of N elements
+// is within a few float32 roundings, whatever N, and equal calls give equal bits.  Squares
+// that leave float32's range, upward or downward, are added again in float64.
+
+#include <float.h>
+
+#include "gdn_internal.h"
+#include "rows.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace rows;
+
+constexpr int kTile = kThreads * 32;  // elements
+constexpr int kFew = 64, kMany = 1024;
+
+// A launch's tensors.  n: the length, with the types in its top bits.  tile0: the tiles of
+// the tensors before.
+template <int N>
+struct List {
+    const void* p[N];
+    void* out[N];
+    uint64_t n[N];
+    uint32_t tile0[N];
+    uint32_t tiles;
+    int count;
+};
+constexpr uint64_t kOutBf16 = 1ull << 63, kInBf16 = 1ull << 62, kLength = kInBf16 - 1;
+
+// A tensor as a block walks it.  Tiles begin at the 16-byte boundary before its first
+// element, `lead` elements earlier.
+struct Tensor {
+    const char* p;
+    char* out;
+    int64_t n;
+    uint32_t first, end;  // tiles
+    int lead;
+    bool in16, out16;
+    template <int N>
+    __device__ __forceinline__ void at(const List<N>& l, int i) {
+        p = (const char*)l.p[i];
+        out = (char*)l.out[i];
+        const uint64_t n_ = l.n[i];
+        n = (int64_t)(n_ & kLength);
+        in16 = n_ & kInBf16;
+        out16 = n_ & kOutBf16;
+        first = l.tile0[i];
+        end = i + 1 < l.count ? l.tile0[i + 1] : l.tiles;
+        lead = (int)((uintptr_t)p & 15) >> (in16 ? 1 : 2);
+    }
+};
+
+// The tensor that holds a tile: the last one that begins at or before it (empty tensors
+// have no tiles).
+template <int N>
+__device__ __forceinline__ int find(const List<N>& l, uint32_t tile) {
+    int lo = 0, hi = l.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (l.tile0[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float at1(const char* p, int64_t e, bool half) {
+    return half ? __bfloat162float(((const __nv_bfloat16*)p)[e]) : ((const float*)p)[e];
+}
+
+// 16 bytes from element e on (e a whole number of vectors behind the boundary): elements
+// outside the tensor are zeros.
+template <int VEC>
+__device__ __forceinline__ uint4 vector_at(const Tensor& t, int64_t e) {
+    constexpr bool kHalf = VEC == 8;
+    if (e >= 0 && e + VEC <= t.n) return *reinterpret_cast<const uint4*>(t.p + e * (16 / VEC));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        if (e + j < 0 || e + j >= t.n) continue;
+        if (kHalf) w[j / 2] |= (uint32_t)((const uint16_t*)t.p)[e + j] << (j % 2 * 16);
+        else w[j] = ((const uint32_t*)t.p)[e + j];
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A sum as two float32 numbers, the second what the first's roundings left out.
+struct Sum {
+    float s = 0.f, c = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, b = t - s;
+        c += (s - (t - b)) + (x - b);
+        s = t;
+    }
+};
+
+template <int VEC>
+__device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum, double& rest) {
+    constexpr int M = 32 / VEC;
+    uint4 v[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) v[j] = vector_at<VEC>(t, e + (int64_t)j * kThreads * VEC);
+    uint64_t ss[2] = {twice(0.f), twice(0.f)};
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        uint64_t f[VEC / 2];
+        get(v[j], f);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) ss[i & 1] = fma2(f[i], f[i], ss[i & 1]);
+    }
+    const float s = sum2(add2(ss[0], ss[1]));
+    // below 2^-100 a square may have been rounded to a subnormal or to 0; above 2^100 the
+    // sum of many tiles may not fit
+    if (s >= 7.888609e-31f && s <= 1.2676506e30f) {
+        sum.add(s);
+        return;
+    }
+    double d = 0.;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        uint64_t f[VEC / 2];
+        get(v[j], f);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            float a, b;
+            unpair(f[i], a, b);
+            if (a != 0.f) d += (double)a * a;
+            if (b != 0.f) d += (double)b * b;
+        }
+    }
+    rest += d;
+}
+
+// The sum of one double per thread, in a fixed order; the same in every thread.
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double part[kThreads / 32];
+    __syncthreads();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) x += part[i];
+    return x;
+}
+
+// Block b's tiles of `tiles`.
+__device__ __forceinline__ void run_of(uint32_t tiles, uint32_t& from, uint32_t& to) {
+    from = (uint32_t)((uint64_t)tiles * blockIdx.x / gridDim.x);
+    to = (uint32_t)((uint64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+}
+
+constexpr int kSumPerSm = 4, kScalePerSm = 4;
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, kSumPerSm)
+grad_sum_kernel(const __grid_constant__ List<N> l, double* __restrict__ part) {
+    await_previous();
+    uint32_t tile, to;
+    run_of(l.tiles, tile, to);
+    Sum sum;
+    double rest = 0.;
+    if (tile < to) {
+        int i = find(l, tile);
+        Tensor t;
+        t.at(l, i);
+        for (; tile < to; ++tile) {
+            while (tile >= t.end) t.at(l, ++i);
+            const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
+            if (t.in16) square_tile<8>(t, e + threadIdx.x * 8, sum, rest);
+            else square_tile<4>(t, e + threadIdx.x * 4, sum, rest);
+        }
+    }
+    const double all = block_sum((double)sum.s + (double)sum.c + rest);
+    if (threadIdx.x == 0) part[blockIdx.x] = all;
+}
+
+__device__ __forceinline__ double norm_of(const double* __restrict__ part, int parts) {
+    double x = 0.;
+    for (int i = threadIdx.x; i < parts; i += kThreads) x += part[i];
+    return sqrt(block_sum(x));
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __restrict__ part, int parts, float* norm) {
+    await_previous();
+    const double x = norm_of(part, parts);
+    if (threadIdx.x == 0) *norm = (float)x;
+}
+
+// VEC neighbouring results from element e on, whose address is a whole number of vectors;
+// none outside the tensor.
+template <int VEC, bool kHalf>
+__device__ __forceinline__ void put_vector(const Tensor& t, int64_t e, const uint64_t (&f)[VEC / 2]) {
+    if (e >= 0 && e + VEC <= t.n) {
+        if constexpr (kHalf && VEC == 8) {
+            *reinterpret_cast<uint4*>(t.out + e * 2) = put(f);
+        } else if constexpr (kHalf) {
+            *reinterpret_cast<uint2*>(t.out + e * 2) = make_uint2(pack2(f[0]), pack2(f[1]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const uint64_t g[2] = {f[2 * i], f[2 * i + 1]};
+                *reinterpret_cast<uint4*>(t.out + (e + 4 * i) * 4) = put(g);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        float a[2];
+        unpair(f[i], a[0], a[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t at = e + 2 * i + k;
+            if (at < 0 || at >= t.n) continue;
+            if (kHalf) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(a[k]);
+            else ((float*)t.out)[at] = a[k];
+        }
+    }
+}
+
+template <int VEC, bool kHalf>
+__device__ __forceinline__ void scale_tile(const Tensor& t, int64_t e, uint64_t by) {
+    constexpr int M = 32 / VEC;
+    uint4 v[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) v[j] = vector_at<VEC>(t, e + (int64_t)j * kThreads * VEC);
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        uint64_t f[VEC / 2];
+        get(v[j], f);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) f[i] = mul2(f[i], by);
+        put_vector<VEC, kHalf>(t, e + (int64_t)j * kThreads * VEC, f);
+    }
+}
+
+// Where the output's boundaries are not the input's: neighbouring threads take neighbouring
+// elements.
+__device__ __forceinline__ void scale_tile_apart(const Tensor& t, int64_t e, float by) {
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+        const int64_t at = e + threadIdx.x + j * kThreads;
+        if (at < 0 || at >= t.n) continue;
+        const float x = at1(t.p, at, t.in16) * by;
+        if (t.out16) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(x);
+        else ((float*)t.out)[at] = x;
+    }
+}
+
+// in_place: every tensor is its own output.
+template <int N>
+__global__ void __launch_bounds__(kThreads, kScalePerSm)
+grad_scale_kernel(const __grid_constant__ List<N> l, const double* __restrict__ part, int parts, float max_norm,
+                  float* norm, bool in_place) {
+    await_previous();
+    const double x = norm_of(part, parts);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)x;
+    // a norm that is not finite says nothing of how long the gradients are: they stay
+    const float by = x > (double)max_norm && x <= DBL_MAX ? (float)((double)max_norm / x) : 1.f;
+    if (in_place && by == 1.f) return;
+    uint32_t from, tile;
+    run_of(l.tiles, from, tile);
+    if (from >= tile) return;
+    int i = find(l, tile - 1);
+    Tensor t;
+    t.at(l, i);
+    while (tile-- > from) {
+        while (tile < t.first) t.at(l, --i);
+        const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
+        if (by == 1.f && t.out == t.p) continue;
+        const int vec = t.in16 ? 8 : 4;
+        const bool whole = ((uintptr_t)t.out - (uintptr_t)t.lead * (t.out16 ? 2 : 4)) % (t.out16 ? 2 * vec : 16) == 0;
+        if (!whole) scale_tile_apart(t, e, by);
+        else if (t.in16 && t.out16) scale_tile<8, true>(t, e + threadIdx.x * 8, twice(by));
+        else if (t.in16) scale_tile<8, false>(t, e + threadIdx.x * 8, twice(by));
+        else if (t.out16) scale_tile<4, true>(t, e + threadIdx.x * 4, twice(by));
+        else scale_tile<4, false>(t, e + threadIdx.x * 4, twice(by));
+    }
+}
+
+// One launch's list from tensors a .. b - 1.
+template <int N>
+void fill(List<N>& l, const gdn_grad* g, int64_t a, int64_t b) {
+    uint64_t tiles = 0;
+    l.count = (int)(b - a);
+    for (int64_t i = a; i < b; ++i) {
+        const bool in16 = g[i].dtype == GDN_BF16;
+        const int lead = (int)((uintptr_t)g[i].grad & 15) >> (in16 ? 1 : 2);
+        l.p[i - a] = g[i].grad;
+        l.out[i - a] = g[i].out;
+        l.n[i - a] = (uint64_t)g[i].n | (in16 ? kInBf16 : 0) | (g[i].out_dtype == GDN_BF16 ? kOutBf16 : 0);
+        l.tile0[i - a] = (uint32_t)tiles;
+        if (g[i].n) tiles += ((uint64_t)g[i].n + lead + kTile - 1) / kTile;
+    }
+    l.tiles = (uint32_t)tiles;
+}
+
+int grid_of(uint32_t tiles, int per_sm) {
+    const uint32_t cap = (uint32_t)(per_sm * sm_count());
+    return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
+}
+
+template <int N>
+cudaError_t sum(const gdn_grad* g, int64_t a, int64_t b, double* part, int* parts, cudaStream_t st) {
+    List<N> l;
+    fill(l, g, a, b);
+    const int grid = grid_of(l.tiles, kSumPerSm);
+    double* to = part + *parts;
+    *parts += grid;
+    return launch_dependent(grad_sum_kernel<N>, dim3(grid), kThreads, 0, st, l, to);
+}
+
+template <int N>
+cudaError_t scale(const gdn_grad* g, int64_t a, int64_t b, const double* part, int parts, float max_norm, float* norm,
+                  bool in_place, cudaStream_t st) {
+    List<N> l;
+    fill(l, g, a, b);
+    return launch_dependent(grad_scale_kernel<N>, dim3(grid_of(l.tiles, kScalePerSm)), kThreads, 0, st, l, part, parts,
+                            max_norm, norm, in_place);
+}
+
+}  // namespace
+
+int64_t grad_tiles(int64_t n) { return n / kTile + 2; }
+
+size_t grad_parts(int64_t count) {
+    const int64_t launches = count <= kMany ? 1 : (count + kMany - 1) / kMany;
+    return (size_t)launches * kSumPerSm * sm_count();
+}
+
+cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, double* part, int* parts, cudaStream_t st) {
+    *parts = 0;
+    cudaError_t e = cudaSuccess;
+    for (int64_t a = 0; e == cudaSuccess && (a == 0 || a < count); a += kMany) {
+        const int64_t b = count - a < kMany ? count : a + kMany;
+        e = b - a <= kFew ? sum<kFew>(g, a, b, part, parts, st) : sum<kMany>(g, a, b, part, parts, st);
+    }
+    return e;
+}
+
+cudaError_t launch_grad_norm(const double* part, int parts, float* norm, cudaStream_t st) {
+    return launch_dependent(grad_norm_kernel, dim3(1), kThreads, 0, st, part, parts, norm);
+}
+
+cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const double* part, int parts, float max_norm,
+                              float* norm, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    for (int64_t a = 0; e == cudaSuccess && (a == 0 || a < count); a += kMany) {
+        const int64_t b = count - a < kMany ? count : a + kMany;
+        bool in_place = true;
+        for (int64_t i = a; i < b; ++i) in_place = in_place && g[i].out == g[i].grad;
+        float* to = a == 0 ? norm : nullptr;
+        e = b - a <= kFew ? scale<kFew>(g, a, b, part, parts, max_norm, to, in_place, st)
+                          : scale<kMany>(g, a, b, part, parts, max_norm, to, in_place, st);
+    }
+    return e;
+}
+
+}  // namespace gdn

@@ -1,5 +1,5 @@
-// layer_binding.cpp -- the Python binding of the linear-attention layer's calls
-// (include/gdn.h) on torch tensors: the same checks, allocations and errors as gdn.py's,
+// layer_binding.cpp -- the Python binding of the linear-attention layer's calls and of those
+// around it in its block (include/gdn.h) on torch tensors: the same checks, allocations and errors as gdn.py's,
 // in C++.  A decode step's kernel takes a few microseconds; marshalling one call in
 // Python took 13 us on the benchmark's host, here it takes 3.4 (the launch is 2.5 of them;
 // 4.2 with a program's own Python between the calls).
@@ -24,6 +24,7 @@
 #include <cstdio>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "gdn.h"
 
@@ -36,8 +37,13 @@ struct Api {
     F(gdn_la_fwd) F(gdn_la_bwd) F(gdn_la_decode) F(gdn_qk_norm_rope_fwd)                                         \
     F(gdn_qk_norm_rope_bwd_workspace_bytes) F(gdn_qk_norm_rope_bwd) F(gdn_gated_norm_fwd)                        \
     F(gdn_gated_norm_bwd_workspace_bytes) F(gdn_gated_norm_bwd)
+// The block's, which a library of the layer alone lacks: their calls then raise.
+#define GDN_BLOCK_CALLS(F)                                                                                      \
+    F(gdn_qk_norm_rope_axes_fwd) F(gdn_qk_norm_rope_axes_bwd) F(gdn_add_norm_fwd) F(gdn_add_norm_quant)          \
+    F(gdn_add_norm_bwd_workspace_bytes) F(gdn_add_norm_bwd) F(gdn_grad_workspace_bytes) F(gdn_grad_norm)         \
+    F(gdn_clip_grads) F(gdn_state_store) F(gdn_state_load)
 #define GDN_FIELD(name) decltype(&::name) name = nullptr;
-    GDN_LAYER_CALLS(GDN_FIELD)
+    GDN_LAYER_CALLS(GDN_FIELD) GDN_BLOCK_CALLS(GDN_FIELD)
 #undef GDN_FIELD
 } api;
 
@@ -83,10 +89,11 @@ struct Like {
     at::Device device;
     at::ScalarType type;
     int code;
-    Like(const at::Tensor& t, const char* name) : device(t.device()), type(t.scalar_type()) {
+    Like(const at::Tensor& t, const char* name) : Like(t, name, t.dim() == 4, "four dimensions") {}
+    Like(const at::Tensor& t, const char* name, bool shaped, const char* expected)
+        : device(t.device()), type(t.scalar_type()) {
         if (!t.is_cuda()) invalid("inputs must be CUDA tensors");
-        if (t.dim() != 4)
-            invalid(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected four dimensions");
+        if (!shaped) invalid(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected " + expected);
         if (type == at::kFloat) code = GDN_F32;
         else if (type == at::kBFloat16) code = GDN_BF16;
         else fail(GDN_ERR_UNSUPPORTED, "dtype %s (use float32 or bfloat16)", c10::toString(type));
@@ -449,6 +456,345 @@ PyObject* gated_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ------------------------------------------- norm and rotation by several positions
+
+struct RopeAxes {
+    const at::Tensor &q, &k;
+    Like like;
+    at::DimVector ks;
+    gdn_rope_axes_problem p{};
+    const void *wq, *wk;
+    const float *cos = nullptr, *sin = nullptr;
+    const int32_t* positions;
+    // q, k, q_weight, k_weight, cos, sin, positions, sections, then eps, interleaved, alternating
+    RopeAxes(PyObject* const* a, PyObject* eps, PyObject* interleaved, PyObject* alternating)
+        : q(*tensor(a[0], "q")), k(*tensor(a[1], "k")), like(q, "q") {
+        Like(k, "k");
+        const int64_t B = q.size(0), T = q.size(1), D = q.size(3);
+        ks = {B, T, k.size(2), D};
+        const at::Tensor& c = *tensor(a[4], "cos");
+        if (c.dim() != 2) invalid("cos must be a [table_rows, R/2] tensor");
+        const int64_t table = c.size(0), pairs = c.size(1);
+        cos = (const float*)input(a[4], "cos", {table, pairs}, at::kFloat, like);
+        sin = (const float*)input(a[5], "sin", {table, pairs}, at::kFloat, like);
+        wq = input(a[2], "q_weight", {D}, like.type, like);
+        wk = input(a[3], "k_weight", {D}, like.type, like);
+        PyObject* parts = PySequence_Fast(a[7], "sections must be a sequence of whole numbers");
+        if (!parts) throw PythonError{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(parts);
+        bool whole = true;
+        for (Py_ssize_t i = 0; i < n && i < 4; ++i) {
+            const long x = PyLong_AsLong(PySequence_Fast_GET_ITEM(parts, i));
+            whole = whole && !(x == -1 && PyErr_Occurred());
+            p.sections[i] = x < -1 || x > 1 << 20 ? -1 : (int32_t)x;
+            if (!whole) break;
+        }
+        Py_DECREF(parts);
+        if (!whole) throw PythonError{};
+        if (n < 1 || n > 4) fail(GDN_ERR_UNSUPPORTED, "sections has %zd entries, expected 1 to 4", n);
+        p.axes = (int32_t)n;
+        positions = (const int32_t*)input(a[6], "positions", {(int64_t)n, B, T}, at::kInt, like);
+        const int inter = PyObject_IsTrue(interleaved), alt = PyObject_IsTrue(alternating);
+        if (inter < 0 || alt < 0) throw PythonError{};
+        p.alternating = alt;
+        p.rope = {B, T, q.size(2), k.size(2), D, 2 * pairs, table, rows(q, "q", q.sizes(), like),
+                  rows(k, "k", ks, like), as_float(eps), inter, like.code};
+    }
+};
+
+bool have_block() {
+    if (api.gdn_state_load) return true;
+    PyErr_SetString(PyExc_RuntimeError, "the library lacks the block's calls: build it again");
+    return false;
+}
+
+// q, k, q_weight, k_weight, cos, sin, positions, sections, eps, interleaved, alternating, q_out,
+// k_out, stream
+PyObject* rope_axes_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 14, [&] {
+        RopeAxes c(a, a[8], a[9], a[10]);
+        const OnStream stream(a[13], c.like);
+        const at::Tensor qo = output(a[11], "q_out", c.q.sizes(), c.like.type, c.like),
+                         ko = output(a[12], "k_out", c.ks, c.like.type, c.like);
+        done(api.gdn_qk_norm_rope_axes_fwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions,
+                                           qo.data_ptr(), ko.data_ptr(), stream.raw));
+        return results(qo, ko);
+    });
+}
+
+// q, k, q_weight, k_weight, cos, sin, positions, sections, dq_out, dk_out, eps, interleaved,
+// alternating, dq, dk, dq_weight, dk_weight, workspace, stream
+PyObject* rope_axes_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 19, [&] {
+        RopeAxes c(a, a[10], a[11], a[12]);
+        const OnStream stream(a[18], c.like);
+        const at::DimVector width{c.p.rope.D};
+        const void *dqo = input(a[8], "dq_out", c.q.sizes(), c.like.type, c.like),
+                   *dko = input(a[9], "dk_out", c.ks, c.like.type, c.like);
+        const at::Tensor dq = output(a[13], "dq", c.q.sizes(), c.like.type, c.like),
+                         dk = output(a[14], "dk", c.ks, c.like.type, c.like),
+                         dwq = output(a[15], "dq_weight", width, c.like.type, c.like),
+                         dwk = output(a[16], "dk_weight", width, c.like.type, c.like);
+        const Workspace ws(a[17], c.like, [&] { return api.gdn_qk_norm_rope_bwd_workspace_bytes(&c.p.rope); });
+        done(api.gdn_qk_norm_rope_axes_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions,
+                                           dqo, dko, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(),
+                                           ws.at, ws.bytes, stream.raw));
+        return results(dq, dk, dwq, dwk);
+    });
+}
+
+// ------------------------------------------------- residual addition and norm
+
+// A [..., D] tensor whose rows lie a fixed stride apart: that stride in elements (0: dense).
+int64_t row_step(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, const Like& like) {
+    check(t, name, shape, type, like.device);
+    if (t.is_contiguous() || t.numel() == 0) return 0;
+    const int64_t D = t.size(-1);
+    int64_t step = 0, count = 1;  // of the rows seen so far
+    bool even = D == 1 || t.stride(-1) == 1;
+    for (int64_t i = t.dim() - 2; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (count == 1) step = t.stride(i);
+        even = even && t.stride(i) == step * count;
+        count *= t.size(i);
+    }
+    if (!even || (count > 1 && step < D))
+        invalid(std::string(name) + " must be dense in its last dimension and its rows a fixed stride apart, got strides " +
+                shape_text(t.strides()));
+    return count > 1 ? step : 0;
+}
+
+at::ScalarType stream_type(const at::Tensor& t, const char* name, const Like& like) {
+    if (t.scalar_type() != like.type && t.scalar_type() != at::kFloat)
+        fail(GDN_ERR_UNSUPPORTED, "%s has dtype %s, expected %s or Float", name, c10::toString(t.scalar_type()),
+             c10::toString(like.type));
+    return t.scalar_type();
+}
+
+// x, residual, weight, and the call's problem.
+struct AddNorm {
+    const at::Tensor& x;
+    const at::Tensor* residual;
+    Like like;
+    at::ScalarType kept;  // h's type
+    const void* weight;
+    gdn_add_norm_problem p;
+    AddNorm(PyObject* const* a, PyObject* eps)
+        : x(*tensor(a[0], "x")), residual(tensor(a[1], "residual", true)),
+          like(x, "x", x.dim() > 0 && x.size(-1) > 0, "rows in the last dimension") {
+        kept = residual ? stream_type(*residual, "residual", like) : like.type;
+        const int64_t D = x.size(-1);
+        weight = input(a[2], "weight", {D}, like.type, like);
+        p = {x.numel() / D, D, row_step(x, "x", x.sizes(), like.type, like),
+             residual ? row_step(*residual, "residual", x.sizes(), kept, like) : 0, as_float(eps), like.code,
+             kept == at::kFloat ? GDN_F32 : GDN_BF16};
+    }
+    // The sum: none without a residual; the caller's, or a new one.
+    std::optional<at::Tensor> sum(PyObject* o) const {
+        if (!residual) {
+            if (o != Py_None) invalid("h is given without a residual: it would be x");
+            return std::nullopt;
+        }
+        return output(o, "h", x.sizes(), kept, like);
+    }
+};
+
+void* address(const std::optional<at::Tensor>& t) { return t ? t->data_ptr() : nullptr; }
+
+// x, residual, weight, eps, h, y, stream
+PyObject* add_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 7, [&] {
+        AddNorm c(a, a[3]);
+        const OnStream stream(a[6], c.like);
+        const auto h = c.sum(a[4]);
+        const at::Tensor y = output(a[5], "y", c.x.sizes(), c.like.type, c.like);
+        done(api.gdn_add_norm_fwd(&c.p, c.x.data_ptr(), c.residual ? c.residual->data_ptr() : nullptr, c.weight,
+                                  address(h), y.data_ptr(), stream.raw));
+        return results(y, h);
+    });
+}
+
+// x, residual, weight, eps, group, h, y, scales, stream
+PyObject* add_norm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 9, [&] {
+        AddNorm c(a, a[3]);
+        const OnStream stream(a[8], c.like);
+        const long group = PyLong_AsLong(a[4]);
+        if (group == -1 && PyErr_Occurred()) throw PythonError{};
+        if (group < 0 || group > 128 || (group && c.p.D % group))
+            fail(GDN_ERR_UNSUPPORTED, "group=%ld: must be 0, 32, 64 or 128 and divide D=%ld", group, (long)c.p.D);
+        const auto h = c.sum(a[5]);
+        const at::Tensor y = output(a[6], "y", c.x.sizes(), at::kFloat8_e4m3fn, c.like);
+        at::DimVector parts(c.x.sizes().begin(), c.x.sizes().end());
+        parts.back() = group ? c.p.D / group : 1;
+        const at::Tensor scales = output(a[7], "scales", parts, at::kFloat, c.like);
+        done(api.gdn_add_norm_quant(&c.p, (int32_t)group, c.x.data_ptr(), c.residual ? c.residual->data_ptr() : nullptr,
+                                    c.weight, address(h), y.data_ptr(), scales.data_ptr<float>(), stream.raw));
+        return results(y, scales, h);
+    });
+}
+
+// h, weight, dy, dh, eps, dx, d_residual, dweight, workspace, stream
+PyObject* add_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 10, [&] {
+        const at::Tensor &h = *tensor(a[0], "h"), &dy = *tensor(a[2], "dy");
+        const Like like(dy, "dy", dy.dim() > 0 && dy.size(-1) > 0, "rows in the last dimension");
+        const at::ScalarType kept = stream_type(h, "h", like);
+        const OnStream stream(a[9], like);
+        const int64_t D = dy.size(-1);
+        const gdn_add_norm_problem p = {dy.numel() / D, D, 0, row_step(h, "h", dy.sizes(), kept, like), as_float(a[4]),
+                                        like.code, kept == at::kFloat ? GDN_F32 : GDN_BF16};
+        dense(dy, "dy", dy.sizes(), like.type, like);
+        const void *w = input(a[1], "weight", {D}, like.type, like), *dh = input(a[3], "dh", dy.sizes(), kept, like, true);
+        const bool apart = kept != like.type;
+        const at::Tensor dx = output(a[5], "dx", dy.sizes(), like.type, like);
+        if (!apart && a[6] != Py_None && !tensor(a[6], "d_residual")->is_same(dx))
+            invalid("d_residual is given where the types agree: dx is both gradients");
+        const at::Tensor dr = apart ? output(a[6], "d_residual", dy.sizes(), kept, like) : dx;
+        const at::Tensor dw = output(a[7], "dweight", {D}, like.type, like);
+        const Workspace ws(a[8], like, [&] { return api.gdn_add_norm_bwd_workspace_bytes(&p); });
+        done(api.gdn_add_norm_bwd(&p, h.data_ptr(), w, dy.data_ptr(), dh, dx.data_ptr(), apart ? dr.data_ptr() : nullptr,
+                                  dw.data_ptr(), ws.at, ws.bytes, stream.raw));
+        return results(dx, dr, dw);
+    });
+}
+
+// ------------------------------------------------------- the gradients' norm
+
+// The tensors of a list (None is left out), with their outputs where there are some.
+struct Grads {
+    std::vector<gdn_grad> list;
+    std::vector<const at::Tensor*> written;
+    std::optional<Like> like;
+    PyObject *seq = nullptr, *outs = nullptr;
+    ~Grads() {
+        Py_XDECREF(seq);
+        Py_XDECREF(outs);
+    }
+    const at::Tensor& one(PyObject* o, const char* what) {
+        const at::Tensor& t = *tensor(o, what);
+        if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense())
+            invalid(std::string(what) + " must be dense in memory, got strides " +
+                    (t.layout() == at::kStrided ? shape_text(t.strides()) : "of another layout"));
+        const Like l(t, what, true, "");
+        if (!like) like = l;
+        else if (like->device != l.device) invalid(std::string(what) + " is on " + l.device.str() + ", expected " + like->device.str());
+        return t;
+    }
+    static int32_t code(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? GDN_F32 : GDN_BF16; }
+    Grads(PyObject* tensors, PyObject* out, bool write) {
+        if (THPVariable_Check(tensors)) invalid("grads must be a sequence of tensors");
+        if (!(seq = PySequence_Fast(tensors, "grads must be a sequence of tensors"))) throw PythonError{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+        if (out != Py_None) {
+            if (THPVariable_Check(out)) invalid("out must be a sequence of tensors");
+            if (!(outs = PySequence_Fast(out, "out must be a sequence of tensors"))) throw PythonError{};
+            if (PySequence_Fast_GET_SIZE(outs) != n)
+                fail(GDN_ERR_INVALID_ARG, "out has %zd tensors, expected %zd", PySequence_Fast_GET_SIZE(outs), n);
+        }
+        list.reserve(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            PyObject* o = PySequence_Fast_GET_ITEM(seq, i);
+            if (o == Py_None) continue;
+            const at::Tensor& g = one(o, "a gradient");
+            const at::Tensor& to = outs ? one(PySequence_Fast_GET_ITEM(outs, i), "an output") : g;
+            if (outs && (to.sizes() != g.sizes() || !(to.strides() == g.strides() || (to.is_contiguous() && g.is_contiguous()))))
+                invalid("an output has shape " + shape_text(to.sizes()) + " and strides " + shape_text(to.strides()) +
+                        ", its gradient " + shape_text(g.sizes()) + " and " + shape_text(g.strides()));
+            list.push_back({g.data_ptr(), to.data_ptr(), g.numel(), code(g), code(to)});
+            if (write) written.push_back(&to);
+        }
+    }
+};
+
+// The norm to fill: the caller's, or a new one on the gradients' device.
+at::Tensor norm_output(PyObject* o, const Grads& g) {
+    if (o != Py_None) {
+        const at::Tensor& t = *tensor(o, "norm");
+        const Like l(t, "norm", t.numel() == 1, "one element");
+        if (l.type != at::kFloat) fail(GDN_ERR_INVALID_ARG, "norm has dtype %s, expected Float", c10::toString(l.type));
+        if (g.like && g.like->device != l.device) invalid("norm is on " + l.device.str() + ", expected " + g.like->device.str());
+        return t;
+    }
+    if (!g.like) invalid("no gradients: their device is not known (give norm)");
+    return g.like->empty({}, at::kFloat);
+}
+
+PyObject* grads_call(PyObject* tensors, PyObject* out, const float* max_norm, PyObject* norm, PyObject* workspace,
+                     PyObject* on) {
+    Grads g(tensors, out, max_norm != nullptr);
+    if (!g.like && norm != Py_None) {
+        const at::Tensor& t = *tensor(norm, "norm");
+        g.like.emplace(t, "norm", true, "");
+    }
+    if (!g.like) invalid("no gradients: their device is not known (give norm)");
+    const OnStream stream(on, *g.like);
+    const at::Tensor to = norm_output(norm, g);
+    const int64_t count = (int64_t)g.list.size();
+    const Workspace ws(workspace, *g.like, [&] { return api.gdn_grad_workspace_bytes(count); });
+    done(max_norm ? api.gdn_clip_grads(g.list.data(), count, *max_norm, to.data_ptr<float>(), ws.at, ws.bytes, stream.raw)
+                  : api.gdn_grad_norm(g.list.data(), count, to.data_ptr<float>(), ws.at, ws.bytes, stream.raw));
+    for (const at::Tensor* t : g.written) changed(*t);
+    changed(to);
+    return wrap(to);
+}
+
+// grads, norm, workspace, stream
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 4, [&] { return grads_call(a[0], Py_None, nullptr, a[1], a[2], a[3]); });
+}
+
+// grads, max_norm, out, norm, workspace, stream
+PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 6, [&] {
+        const float most = as_float(a[1]);
+        return grads_call(a[0], a[2], &most, a[3], a[4], a[5]);
+    });
+}
+
+// ------------------------------------------------------- the cache of states
+
+struct StateCache {
+    const at::Tensor &cache, &scales, &slots;
+    Like like;
+    gdn_state_cache_problem p;
+    StateCache(PyObject* cache_, PyObject* scales_, PyObject* slots_)
+        : cache(*tensor(cache_, "cache")), scales(*tensor(scales_, "scales")), slots(*tensor(slots_, "slots")),
+          like(scales, "scales", scales.dim() == 3, "[slots, H, V]") {
+        if (cache.dim() != 4) invalid("cache has shape " + shape_text(cache.sizes()) + ", expected [slots, H, V, K]");
+        if (slots.dim() != 1) invalid("slots has shape " + shape_text(slots.sizes()) + ", expected [B]");
+        p = {slots.size(0), cache.size(1), cache.size(3), cache.size(2), cache.size(0)};
+        dense(cache, "cache", cache.sizes(), at::kChar, like);
+        dense(scales, "scales", {p.slots, p.H, p.V}, at::kFloat, like);
+        dense(slots, "slots", {p.B}, at::kInt, like);
+    }
+};
+
+// states, slots, cache, scales, stream
+PyObject* state_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 5, [&] {
+        const StateCache c(a[2], a[3], a[1]);
+        const OnStream stream(a[4], c.like);
+        const void* states = input(a[0], "states", {c.p.B, c.p.H, c.p.V, c.p.K}, at::kFloat, c.like);
+        done(api.gdn_state_store(&c.p, (const float*)states, c.slots.data_ptr<int32_t>(), c.cache.data_ptr(),
+                                 c.scales.data_ptr<float>(), stream.raw));
+        return results(c.cache, c.scales);
+    });
+}
+
+// cache, scales, slots, states, stream
+PyObject* state_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return !have_block() ? nullptr : call(n, 5, [&] {
+        const StateCache c(a[0], a[1], a[2]);
+        const OnStream stream(a[4], c.like);
+        const at::Tensor states = output(a[3], "states", {c.p.B, c.p.H, c.p.V, c.p.K}, at::kFloat, c.like);
+        done(api.gdn_state_load(&c.p, c.cache.data_ptr(), c.scales.data_ptr<float>(), c.slots.data_ptr<int32_t>(),
+                                states.data_ptr<float>(), stream.raw));
+        changed(states);
+        return wrap(states);
+    });
+}
+
 // load(path of libgdn.so, GdnError)
 PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 2 || !PyUnicode_Check(a[0]) || !PyType_Check(a[1])) {
@@ -461,6 +807,10 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define GDN_LOOK(name)                                                            \
     if (lib && !(found.name = (decltype(found.name))dlsym(lib, #name))) missing = #name;
     GDN_LAYER_CALLS(GDN_LOOK)
+#undef GDN_LOOK
+#define GDN_LOOK(name) \
+    if (lib) found.name = (decltype(found.name))dlsym(lib, #name);
+    GDN_BLOCK_CALLS(GDN_LOOK)
 #undef GDN_LOOK
     if (missing) {
         PyErr_Format(PyExc_RuntimeError, "%s: %s not found", PyUnicode_AsUTF8(a[0]), missing);
@@ -476,7 +826,10 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define GDN_METHOD(name) {#name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDN_METHOD(load),      GDN_METHOD(la_fwd),   GDN_METHOD(la_bwd),
                          GDN_METHOD(la_decode), GDN_METHOD(rope_fwd), GDN_METHOD(rope_bwd),
-                         GDN_METHOD(gated_fwd), GDN_METHOD(gated_bwd), {nullptr, nullptr, 0, nullptr}};
+                         GDN_METHOD(gated_fwd), GDN_METHOD(gated_bwd), GDN_METHOD(rope_axes_fwd),
+                         GDN_METHOD(rope_axes_bwd), GDN_METHOD(add_norm_fwd), GDN_METHOD(add_norm_quant),
+                         GDN_METHOD(add_norm_bwd), GDN_METHOD(grad_norm), GDN_METHOD(clip_grads),
+                         GDN_METHOD(state_store), GDN_METHOD(state_load), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

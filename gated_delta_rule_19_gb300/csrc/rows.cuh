@@ -92,6 +92,13 @@ struct Ring {
     __device__ __forceinline__ void copy8(int slot, int piece, int half, const void* src) const {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at(slot, piece) + 8 * half), "l"(src) : "memory");
     }
+    // 4 bytes, to the piece's word `word`
+    __device__ __forceinline__ void copy4(int slot, int piece, int word, const void* src) const {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at(slot, piece) + 4 * word), "l"(src) : "memory");
+    }
+    __device__ __forceinline__ void put4(int slot, int piece, int word, float x) const {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(slot, piece) + 4 * word), "f"(x) : "memory");
+    }
     __device__ __forceinline__ void put(int slot, int piece, float x) const {
         asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(at(slot, piece)), "f"(x) : "memory");
     }

@@ -52,6 +52,27 @@ class gdn_gated_norm_problem(ctypes.Structure):
                 ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+class gdn_rope_axes_problem(ctypes.Structure):
+    _fields_ = [("rope", gdn_rope_problem), ("axes", ctypes.c_int32), ("alternating", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4)]
+
+
+class gdn_add_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("stream_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32)]
+
+
+class gdn_grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class gdn_state_cache_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("K", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("slots", ctypes.c_int64)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
 
@@ -119,6 +140,20 @@ def load_library():
                      ("gdn_gated_norm_bwd_workspace_bytes", PG)):
         getattr(lib, fn).argtypes = [prob]
         getattr(lib, fn).restype = ctypes.c_size_t
+    PA, PN, PS = (ctypes.POINTER(t) for t in (gdn_rope_axes_problem, gdn_add_norm_problem, gdn_state_cache_problem))
+    i64, f32, size = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    for fn, args in (("gdn_qk_norm_rope_axes_fwd", [PA] + [_vp] * 10),
+                     ("gdn_qk_norm_rope_axes_bwd", [PA] + [_vp] * 14 + [size, _vp]),
+                     ("gdn_add_norm_fwd", [PN] + [_vp] * 6), ("gdn_add_norm_quant", [PN, ctypes.c_int32] + [_vp] * 7),
+                     ("gdn_add_norm_bwd", [PN] + [_vp] * 8 + [size, _vp]),
+                     ("gdn_grad_norm", [ctypes.POINTER(gdn_grad), i64, _vp, _vp, size, _vp]),
+                     ("gdn_clip_grads", [ctypes.POINTER(gdn_grad), i64, f32, _vp, _vp, size, _vp]),
+                     ("gdn_state_store", [PS] + [_vp] * 5), ("gdn_state_load", [PS] + [_vp] * 5)):
+        getattr(lib, fn).argtypes = args
+        getattr(lib, fn).restype = ctypes.c_int
+    for fn, arg in (("gdn_add_norm_bwd_workspace_bytes", PN), ("gdn_grad_workspace_bytes", i64)):
+        getattr(lib, fn).argtypes = [arg]
+        getattr(lib, fn).restype = size
     lib.gdn_count_nonfinite.argtypes = [_vp, ctypes.c_int64, ctypes.c_int, _vp, _vp]
     lib.gdn_count_nonfinite.restype = ctypes.c_int
     lib.gdn_set_sequence_split.argtypes = [ctypes.c_int]
@@ -150,7 +185,10 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_last_error", "gdn_fwd_works
             "gdn_test_set_wait_limit", "gdn_la_fwd_workspace_bytes", "gdn_la_saved_bytes",
             "gdn_la_bwd_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode",
             "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_bytes", "gdn_qk_norm_rope_bwd",
-            "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd")
+            "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd",
+            "gdn_qk_norm_rope_axes_fwd", "gdn_qk_norm_rope_axes_bwd", "gdn_add_norm_fwd", "gdn_add_norm_quant",
+            "gdn_add_norm_bwd_workspace_bytes", "gdn_add_norm_bwd", "gdn_grad_workspace_bytes", "gdn_grad_norm",
+            "gdn_clip_grads", "gdn_state_store", "gdn_state_load")
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -981,3 +1019,88 @@ def gdn_gated_norm_bwd(x, gate, weight, dy, *, eps: float = 1e-6, grads=None, wo
     Returns ``(dx, dgate, dweight)``."""
     dx, dgate, dw = grads if grads is not None else (None,) * 3
     return (_layer or _binding()).gated_bwd(x, gate, weight, dy, eps, dx, dgate, dw, workspace, _raw(stream))
+
+
+# ---- What surrounds the layer in its block: the rotation by several positions, the residual's
+# addition with the norm, the gradients' norm and clipping, the states of waiting sequences
+# (see include/gdn.h).
+
+
+def gdn_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, sections, *, eps: float = 1e-6,
+                              interleaved: bool = False, alternating: bool = False, q_out=None, k_out=None, stream=None):
+    """:func:`gdn_qk_norm_rope_fwd` for tokens with a position on each of 1 to 4 axes, as those
+    of images and videos (time, height, width; ``gdn_qk_norm_rope_axes_fwd``).  positions int32
+    [axes,B,T]; ``sections``: how many of the R/2 pairs each axis turns, one behind the other,
+    or with ``alternating`` in turn (pair i by axis i % axes while i // axes is below its
+    section, by axis 0 otherwise).  A pair's angle is in its own column of cos, sin [table_rows,
+    R/2], in the row of its axis's position; one outside the tables makes that axis's elements
+    of the token NaN.  Returns ``(q_out, k_out)``, dense."""
+    return (_layer or _binding()).rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, sections, eps,
+                                                interleaved, alternating, q_out, k_out, _raw(stream))
+
+
+def gdn_qk_norm_rope_axes_bwd(q, k, q_weight, k_weight, cos, sin, positions, sections, dq_out, dk_out, *,
+                              eps: float = 1e-6, interleaved: bool = False, alternating: bool = False, grads=None,
+                              workspace=None, stream=None):
+    """Backward of :func:`gdn_qk_norm_rope_axes_fwd` (``gdn_qk_norm_rope_axes_bwd``).
+    Returns ``(dq, dk, dq_weight, dk_weight)``."""
+    dq, dk, dwq, dwk = grads if grads is not None else (None,) * 4
+    return (_layer or _binding()).rope_axes_bwd(q, k, q_weight, k_weight, cos, sin, positions, sections, dq_out, dk_out,
+                                                eps, interleaved, alternating, dq, dk, dwq, dwk, workspace, _raw(stream))
+
+
+def gdn_add_norm_fwd(x, residual, weight, *, eps: float = 1e-6, h=None, y=None, stream=None):
+    """``h = x + residual`` and ``y = h weight / sqrt(mean(h^2) + eps)`` for every row of x
+    [..., D] (``gdn_add_norm_fwd``; D a multiple of 8, or of 4 in float32, up to 8192; rows may
+    lie a fixed stride apart).  residual: of x's shape, in x's type or float32, which is h's
+    type too, or None (``h`` is x).  The norm is that of the float32 sum.  ``h``: a tensor to
+    fill, which may be ``residual`` itself.  Returns ``(y, h)``, dense; h is None without a
+    residual."""
+    return (_layer or _binding()).add_norm_fwd(x, residual, weight, eps, h, y, _raw(stream))
+
+
+def gdn_add_norm_quant(x, residual, weight, *, eps: float = 1e-6, group: int = 0, h=None, y=None, scales=None,
+                       stream=None):
+    """:func:`gdn_add_norm_fwd` with y in 8 bits (``gdn_add_norm_quant``): y float8_e4m3fn and
+    float32 scales [..., D / group], ``y * scales`` being the norm; ``group`` is 32, 64 or 128
+    columns, or 0 for a scale a row (scales [..., 1]).  Returns ``(y, scales, h)``."""
+    return (_layer or _binding()).add_norm_quant(x, residual, weight, eps, group, h, y, scales, _raw(stream))
+
+
+def gdn_add_norm_bwd(h, weight, dy, dh=None, *, eps: float = 1e-6, grads=None, workspace=None, stream=None):
+    """Backward of :func:`gdn_add_norm_fwd` (``gdn_add_norm_bwd``) from the gradients of y and,
+    by the residual stream, of h (None: zeros); h as the forward returned it, or x where there
+    was no residual.  Returns ``(dx, d_residual, dweight)``: one gradient, in dy's type and in
+    h's, and the same tensor where these agree."""
+    dx, dr, dw = grads if grads is not None else (None,) * 3
+    return (_layer or _binding()).add_norm_bwd(h, weight, dy, dh, eps, dx, dr, dw, workspace, _raw(stream))
+
+
+def gdn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
+    """The norm of all elements of a sequence of gradients (``gdn_grad_norm``; float32 or
+    bfloat16 CUDA tensors, each dense in memory in any order of its dimensions; None is left
+    out).  Returns ``norm``, float32 on the device."""
+    return (_layer or _binding()).grad_norm(grads, norm, workspace, _raw(stream))
+
+
+def gdn_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace=None, stream=None):
+    """Scales the gradients by ``min(1, max_norm / norm)`` of :func:`gdn_grad_norm`, in place
+    or into ``out`` (a tensor for each, float32 or bfloat16, of the same shape and order;
+    ``gdn_clip_grads``).  Where the norm is NaN or infinite they are left as they were.
+    Returns ``norm``, that of the gradients before."""
+    return (_layer or _binding()).clip_grads(grads, max_norm, out, norm, workspace, _raw(stream))
+
+
+def gdn_state_store(states, slots, cache, scales, *, stream=None):
+    """Parks the states of waiting sequences in 8 bits (``gdn_state_store``): states float32
+    [B,H,V,K] into the slots (int32 [B]) of cache int8 [n,H,V,K] with scales float32 [n,H,V],
+    each row as the nearest whole numbers of 1/127 of its largest element.  A sequence whose
+    slot is outside the cache is not kept, and of several with one slot the last is.  Returns
+    ``(cache, scales)``."""
+    return (_layer or _binding()).state_store(states, slots, cache, scales, _raw(stream))
+
+
+def gdn_state_load(cache, scales, slots, *, states=None, stream=None):
+    """The states of ``slots`` as :func:`gdn_state_store` left them, float32 [B,H,V,K]
+    (``gdn_state_load``); zeros, a new sequence's, where a slot is outside the cache."""
+    return (_layer or _binding()).state_load(cache, scales, slots, states, _raw(stream))

@@ -510,6 +510,145 @@ gdn_status gdn_gated_norm_bwd(const gdn_gated_norm_problem* p, const void* x, co
                               size_t workspace_bytes, void* stream);
 
 /*
+ * ---- What surrounds the layer in its block ---------------------------------
+ *
+ * The rotation by several positions, the residual's addition with the norm, the
+ * gradients' norm and clipping, and the states of waiting sequences in 8 bits.  As
+ * above: errors before any launch, nothing allocated, asynchronous on `stream`.
+ */
+
+/* The q, k norm with a position on each of 1 to 4 axes (time, height and width of an
+ * image or a video).  sections[a]: how many of the R / 2 pairs take their angle by axis a;
+ * they sum to R / 2, and those behind `axes` are not read.  In blocks: the first
+ * sections[0] pairs by axis 0, the next sections[1] by axis 1, ...; alternating: pair i by
+ * axis i % axes while i / axes < sections[i % axes], by axis 0 otherwise (sections of which
+ * that rule does not give as many pairs to each axis are refused). */
+typedef struct {
+    gdn_rope_problem rope;
+    int32_t axes, alternating;
+    int32_t sections[4];
+} gdn_rope_axes_problem;
+
+/*
+ * gdn_qk_norm_rope_axes_fwd, gdn_qk_norm_rope_axes_bwd -- gdn_qk_norm_rope_fwd and _bwd
+ * with pair i of a token turned by the angle in column i of the tables' row
+ * positions[axis of i][b][t].
+ *   positions  int32 [axes,B,T], required (unless R = 0).  A position outside the tables
+ *              makes the elements of its axis's pairs NaN, and in the backward the
+ *              token's whole gradient rows.
+ * The workspace is that of gdn_qk_norm_rope_bwd for p->rope.
+ */
+gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
+                                     const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                     const int32_t* positions, void* q_out, void* k_out, void* stream);
+gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
+                                     const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                     const int32_t* positions, const void* dq_out, const void* dk_out, void* dq,
+                                     void* dk, void* dq_weight, void* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Sizes of the residual's addition with the norm.  rows <= 2^33 rows of D elements, D a
+ * multiple of 8 (4 where both types are float32), 8192 at most.  dtype: of x, weight, y and
+ * their gradients; stream_dtype: of the residual stream (residual, h and their gradients),
+ * dtype itself or GDN_F32.  x_stride, stream_stride: elements from row to row of x and of
+ * the residual (0: dense), multiples of 16 bytes. */
+typedef struct {
+    int64_t rows, D;
+    int64_t x_stride, stream_stride;
+    float eps;
+    int32_t dtype, stream_dtype;
+} gdn_add_norm_problem;
+
+/*
+ * gdn_add_norm_fwd -- for every row: h = x + residual, y = h w / sqrt(mean(h^2) + eps), the
+ * norm of the float32 sum, before it is rounded to h's type (squares are summed in float32:
+ * a row past 1e19 in size has no norm).
+ *   residual  NULL: h = x, and h has to be NULL (stream_dtype is dtype then).
+ *   h         dense; NULL: not kept; may be residual itself, where that is dense.
+ *   y         dense, in dtype.
+ */
+gdn_status gdn_add_norm_fwd(const gdn_add_norm_problem* p, const void* x, const void* residual, const void* weight,
+                            void* h, void* y, void* stream);
+
+/*
+ * gdn_add_norm_quant -- the same with y in 8 bits (e4m3: sign, 4 bits of exponent, 3 of
+ * mantissa), for a product that takes its operand so: scale = max|y| / 448 over each `group`
+ * columns of a row (32, 64 or 128, which divide D; 0: the whole row), 2^-126 at least, and
+ * y8 = y / scale rounded to nearest even.
+ *   y8      [rows, D] bytes.
+ *   scales  float32 [rows, D / group] ([rows] for a whole row's).  A group that holds NaN or
+ *           an infinity has a scale that is not finite: read back, it is NaN.
+ */
+gdn_status gdn_add_norm_quant(const gdn_add_norm_problem* p, int32_t group, const void* x, const void* residual,
+                              const void* weight, void* h, void* y8, float* scales, void* stream);
+
+/*
+ * gdn_add_norm_bwd -- from dy (of y) and dh (of h, NULL: zeros), both dense, with h as
+ * the forward left it (x itself where there was no residual; stream_stride is h's):
+ * the gradient of x, which is that of the residual too, and the weight's ([D], dtype; summed
+ * in float32 in a fixed order, so equal calls give equal bits).
+ *   dx          in dtype, dense.
+ *   d_residual  in stream_dtype, dense; NULL where the types agree (dx is both).
+ */
+size_t gdn_add_norm_bwd_workspace_bytes(const gdn_add_norm_problem* p);
+gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const void* weight, const void* dy,
+                            const void* dh, void* dx, void* d_residual, void* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* One tensor of a model's gradients: n elements, dense in memory, at an address that is a
+ * multiple of an element.  out: where its clipped values go, in out_dtype; may be grad itself
+ * (then of its type). */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t n;
+    int32_t dtype, out_dtype;
+} gdn_grad;
+
+/*
+ * gdn_grad_norm -- *norm = sqrt(sum of g^2 over all elements of all tensors), float32 on the
+ * device, 4-byte aligned.  The array (host memory, `count` <= 2^20) is read before the call
+ * returns; out and out_dtype are not used, and a tensor may be listed twice.  The sum keeps
+ * the float32 sums' rounding errors and squares that leave float32's range, so the norm is
+ * right to float32 for any number of finite elements; equal calls give equal bits.
+ * gdn_clip_grads -- the same, and out = g * min(1, max_norm / norm) for every tensor (in
+ * float32, rounded once).  Where norm is NaN or infinite the factor is 1: the caller
+ * sees it in *norm.  max_norm >= 0, infinity: no limit.  Outputs overlap neither each other
+ * nor a gradient other than their own.
+ *   norm       required by gdn_grad_norm; NULL: not kept.
+ *   workspace  gdn_grad_workspace_bytes(count) bytes, 16-byte aligned; calls in flight at
+ *              the same time need one each.
+ */
+size_t gdn_grad_workspace_bytes(int64_t count);
+gdn_status gdn_grad_norm(const gdn_grad* grads, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                         void* stream);
+gdn_status gdn_clip_grads(const gdn_grad* grads, int64_t count, float max_norm, float* norm, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Sizes of a cache of waiting sequences' states: K and V of 16, 32, 64 or 128, B and H as
+ * above, 0 <= slots < 2^31. */
+typedef struct {
+    int64_t B, H, K, V, slots;
+} gdn_state_cache_problem;
+
+/*
+ * gdn_state_store -- parks the states of B sequences in 8 bits: for every row s of K elements,
+ * scale = max|s| / 127 (2^-126 at least, float32) and code = the whole number nearest to
+ * s / scale, ties to even.
+ *   states  float32 [B,H,V,K].
+ *   slot    int32 [B], 4-byte aligned: where sequence b goes.  One outside the cache: it is
+ *           not kept.  Of sequences with the same slot the last one is.
+ *   cache   int8 [slots,H,V,K];  scales  float32 [slots,H,V].  Other slots stay as they are.
+ * A row that holds NaN or an infinity gets the scale NaN, and is read back as NaN.
+ * gdn_state_load -- resumes them: states = code * scale for slot[b], zeros (a new sequence's
+ * state) where slot[b] is outside the cache.
+ */
+gdn_status gdn_state_store(const gdn_state_cache_problem* p, const float* states, const int32_t* slot, void* cache,
+                           float* scales, void* stream);
+gdn_status gdn_state_load(const gdn_state_cache_problem* p, const void* cache, const float* scales,
+                          const int32_t* slot, float* states, void* stream);
+
+/*
  * gdn_count_nonfinite -- adds to *count the number of elements of x[0 .. n-1]
  * that are NaN or +-inf: a device-side check of inputs or results (for example,
  * the outputs of gdn_fwd after suspect inputs).  It does not synchronise: the
