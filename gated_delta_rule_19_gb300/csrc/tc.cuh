@@ -90,6 +90,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
     }
 }
 
+// The same for the forward scan's wait for its first product, which the test hook's limit
+// (limit_ns > 0) always ends: try_wait may itself suspend the thread for longer than the
+// kernels' short waits take, and %globaltimer may stand still for as long, so with a limit
+// this wait tests without blocking and counts clock cycles (two a nanosecond).  (In every
+// wait of these kernels the branch cost 0.65% of a training step; in this one nothing.)
+__device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity, int* err, int code,
+                                                 uint32_t limit_ns) {
+    if (!limit_ns) return mbar_wait(bar, parity, err, code);
+    const long long t0 = clock64();
+    while (!mbar_test_wait(bar, parity))
+        if (clock64() - t0 > 2ll * limit_ns) {
+            atomicOr(err, code);
+            return false;
+        }
+    return true;
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1) {

@@ -974,7 +974,7 @@ scan_fwd_tc(Dims d, const __grid_constant__ CUtensorMap tm_q, const __grid_const
             gr_prev = gr;
             if (urow) {
                 ok = mbar_wait(&tbar[stg], (c / NS) & 1, err, 8, d.wait_ns) && ok;  // Ut slice is read below
-                ok = mbar_wait(barXY, c & 1, err, 16, d.wait_ns) && ok;
+                ok = mbar_wait_strict(barXY, c & 1, err, 16, d.wait_ns) && ok;
                 __syncwarp();
                 fence_after_sync();
                 // U = Ut - X, Uh = e_r U  (row r, columns cb .. cb+HV)
