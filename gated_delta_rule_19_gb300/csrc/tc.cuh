@@ -101,7 +101,7 @@ __device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity,
     const long long t0 = clock64();
     while (!mbar_test_wait(bar, parity))
         if (clock64() - t0 > 2ll * limit_ns) {
-            atomicOr(err, code);
+            if (err) atomicOr(err, code);
             return false;
         }
     return true;
