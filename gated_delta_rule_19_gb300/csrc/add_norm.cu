@@ -2,7 +2,7 @@
 // 8-bit output, and the gradients: the step in front of a layer's projection.
 //
 // Row x of D elements, residual s, weight w; h = x + s, r = (mean h^2 + eps)^(-1/2):
-//   y = h r w,     y8 = e4m3(y / scale) with scale = max(|y|) / 448 over a group of columns.
+//   y = h r w,     y8 = e4m3(y / scale) with scale = max|y| / 448 over a group of columns.
 // Backward, from dy and the gradient dh that reaches h by the residual stream, with
 // hh = h r and t = dy w:
 //   d = r (t - hh mean(t hh)) + dh   (of x and of the residual),    dw = sum over rows of dy hh.
@@ -15,6 +15,8 @@
 // stores fill whole sectors; the row is read once, its sum of squares is made of registers.
 // Persistent blocks with a ring of asynchronous copies (rows.cuh) keep the next rows in
 // flight.
+
+#include <float.h>
 
 #include "gdn_internal.h"
 #include "rows.cuh"
@@ -30,11 +32,11 @@ constexpr int kPieces = 4, kStages = 2;
 template <typename T, int VEC>
 struct Piece {
     static constexpr int BYTES = VEC * (int)sizeof(T);
-    static __device__ __forceinline__ void copy(uint32_t at, const T* src, bool on) {
+    static __device__ __forceinline__ void copy(uint32_t at, const T* src) {
         if constexpr (BYTES == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(on ? 16 : 0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at), "l"(src), "r"(on ? 8 : 0) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(src) : "memory");
     }
     static __device__ __forceinline__ void unpack(const uint4& x, uint64_t (&f)[VEC / 2]) {
         if constexpr (BYTES == 16) get(x, f);
@@ -54,8 +56,8 @@ struct Piece {
         return make_uint4(x.x, x.y, 0, 0);
     }
     static __device__ __forceinline__ void store(T* p, const uint64_t (&f)[VEC / 2]) {
-        if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = put(f);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0]), pack2(f[1]));
+        if constexpr (BYTES == 16) __stcs(reinterpret_cast<uint4*>(p), put(f));
+        else __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack2(f[0]), pack2(f[1])));
     }
 };
 
@@ -82,21 +84,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+// max(|pair's two|, m)
 __device__ __forceinline__ float abs_max(const uint64_t& p, float m) {
-    float a, b;
+    float a, b, r;
     unpair(p, a, b);
-    return max_nan(m, max_nan(fabsf(a), fabsf(b)));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(m));
+    return r;
 }
 
-// A row's place: row `turn * gridDim.x * rows a block + ...`, its lane u of L.
+// A thread's place: its row of the block's in each turn, and in the row the columns c0 + p LV of
+// its pieces p < n.  Pieces behind the row's end and rows behind the last are not read,
+// computed or written; their lanes only take part in exchanges and barriers.
+template <int VEC>
 struct Place {
-    int L, u, per;       // lanes a row, this lane, rows a block
-    int64_t first, step;  // this thread's first row, and the rows that all blocks take in a turn
-    int turns;            // the same for every thread of a block: the sums' barriers are whole
-    __device__ __forceinline__ Place(int64_t rows, int L_, int n)
-        : L(L_), u(threadIdx.x & (L_ - 1)), per(n / L_), first((int64_t)blockIdx.x * per + threadIdx.x / L_),
-          step((int64_t)gridDim.x * per) {
+    int L, LV, c0, n;
+    int64_t row, step;  // this thread's first row, and the rows that all blocks take in a turn
+    int turns;          // the same for every thread of a block
+    __device__ __forceinline__ Place(int64_t rows, int D, int L_, int threads)
+        : L(L_), LV(L_ * VEC), c0((threadIdx.x & (L_ - 1)) * VEC), n(0) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) n += c0 + p * LV < D;
+        const int per = threads / L_;
         const int64_t base = (int64_t)blockIdx.x * per;
+        row = base + threadIdx.x / L_;
+        step = (int64_t)gridDim.x * per;
         turns = base < rows ? (int)((rows - base + step - 1) / step) : 0;
     }
 };
@@ -142,24 +153,114 @@ __device__ __forceinline__ uint32_t e4m3x2(uint64_t p) {
     return r;
 }
 
-// The scale of a group whose largest number is m: m / 448, so that e4m3's largest number
-// stands for it, but no subnormal one, whose inverse would be infinite.  NaN stays NaN, and
-// with an infinite scale the group is read back as NaN.
-__device__ __forceinline__ float scale_of(float m) {
-    const float s = m / 448.f;
-    return s < 1.17549435e-38f ? 1.17549435e-38f : s;
+constexpr float kLeast = 1.17549435e-38f;  // 2^-126, the least scale
+
+// The 8-bit form.  With t = h w and m = max|t| over the group, y / scale = 448 t / m: the
+// row's r is no part of it.  t (448 / m) in float32 is off by up to 8 of its last bits, which
+// matters next to the middle between two e4m3 numbers only, where the 20 mantissa bits that
+// e4m3 drops are near 10...0.  There (one element of 60000) 448 t is compared with the middle
+// times m, both exactly, so that y8 is the number nearest to the exact quotient.  (Below 2^-6
+// e4m3 drops more bits, and an element there may fall on either side of a middle that is
+// within float32's error.)  In float64 that comparison made the kernel 1.8 times slower,
+// rare as it is.
+// How far a quotient's low 20 bits are behind the first that are near (times 2^12, which
+// drops the other bits): up to kNear they are.
+constexpr uint32_t kNear = 16u << 12;
+__device__ __forceinline__ uint32_t behind(float q) { return __float_as_uint(q) * 4096u - (0x7fff8u << 12); }
+// (x + res) w as two float32 numbers, the second what the first's roundings left out.
+__device__ __forceinline__ float2 product_of(float x, float res, float w) {
+    const float h = x + res, b = h - x, left = (x - (h - b)) + (res - b);
+    const float t = h * w;
+    return make_float2(t, fmaf(left, w, fmaf(h, w, -t)));
+}
+// q, near a middle, moved to the side of it on which 448 t / m is (m = most + left).
+__device__ __forceinline__ float beside_middle(float q, float2 t, float most, float left) {
+    const uint32_t at = (__float_as_uint(q) & 0x7ff00000u) | 0x80000u;
+    const float middle = __uint_as_float(at), sign = copysignf(1.f, q);
+    const float a = 448.f * fabsf(t.x), a1 = fmaf(448.f, fabsf(t.x), -a), b = middle * most, b1 = fmaf(middle, most, -b);
+    const float d = (a - b) + ((a1 - b1) + fmaf(448.f, sign * t.y, -(middle * left)));
+    return copysignf(__uint_as_float(d > 0.f ? at + 1 : d < 0.f ? at - 1 : at), q);
+}
+
+// What is needed rarely is not inlined: it would take the registers of every row.  x and res
+// (0: no residual): the row's places in shared memory.
+// The piece's 8-bit numbers from its quotients q, those next to a middle decided exactly.
+template <typename TX, typename TR>
+__device__ __noinline__ uint2 exact_piece(uint32_t x, uint32_t res, uint4 w, float by, float most, float left) {
+    constexpr int VEC = 16 / (int)sizeof(TR);
+    uint64_t f[VEC / 2], g[VEC / 2], k[VEC / 2];
+    Piece<TX, VEC>::load(x, f);
+    if (res) Piece<TR, VEC>::load(res, g);
+    Piece<TX, VEC>::unpack(w, k);
+    uint32_t code[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        float xv[2], rv[2] = {0.f, 0.f}, wv[2], q[2];
+        unpair(f[j], xv[0], xv[1]);
+        if (res) unpair(g[j], rv[0], rv[1]);
+        unpair(k[j], wv[0], wv[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 t = product_of(xv[e], rv[e], wv[e]);
+            q[e] = t.x * by;
+            if (behind(q[e]) <= kNear) q[e] = beside_middle(q[e], t, most, left);
+        }
+        code[j] = e4m3x2(pair(q[0], q[1]));
+    }
+    return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
+// What float32's rounding left out of the largest |t|, of the piece's elements that are it.
+template <typename TX, typename TR>
+__device__ __noinline__ float left_of(uint32_t x, uint32_t res, uint4 w, float most, float left) {
+    constexpr int VEC = 16 / (int)sizeof(TR);
+    uint64_t f[VEC / 2], g[VEC / 2], k[VEC / 2];
+    Piece<TX, VEC>::load(x, f);
+    if (res) Piece<TR, VEC>::load(res, g);
+    Piece<TX, VEC>::unpack(w, k);
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        float xv[2], rv[2] = {0.f, 0.f}, wv[2];
+        unpair(f[j], xv[0], xv[1]);
+        if (res) unpair(g[j], rv[0], rv[1]);
+        unpair(k[j], wv[0], wv[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 t = product_of(xv[e], rv[e], wv[e]);
+            if (fabsf(t.x) == most) left = fmaxf(left, copysignf(1.f, t.x) * t.y);
+        }
+    }
+    return left;
+}
+
+struct Scale {
+    float scale;
+    uint64_t by;  // what takes t, or y where `plain`, to 8 bits
+    bool plain;   // m or the scale next to the end of float32's range, or not finite
+};
+// NaN stays NaN, and a group with an infinite scale is read back as NaN.
+__device__ __forceinline__ Scale scale_of(float m, float r) {
+    const float s = m * r * (1.f / 448.f);
+    Scale c;
+    c.scale = s < kLeast ? kLeast : s;
+    c.plain = !(m >= 7.888609e-31f && s >= kLeast && s <= 3.402823466e38f);
+    float inverse;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inverse) : "f"(c.plain ? c.scale : m));
+    c.by = twice(c.plain ? inverse : 448.f * inverse);
+    return c;
 }
 
 struct NormDims {
     int64_t rows, x_stride, r_stride;
-    int D, L, group;  // group: columns of a scale
+    int D, L;
+    int group, shift;  // columns of a scale (D: a row's), and for groups of 32 to 128 their logarithm
     float eps;
 };
 
+constexpr int kPerSm = 2;
 constexpr int kFwdSlots = 2 * kPieces, kBwdSlots = 3 * kPieces;
 
 template <typename TX, typename TR, int N, bool kQuant>
-__global__ void __launch_bounds__(N, N == 256 ? 3 : 1)
+__global__ void __launch_bounds__(N, N == 256 ? kPerSm : 1)
 add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const TX* __restrict__ w, TR* h,
                     void* __restrict__ y, float* __restrict__ scales) {
     constexpr int VEC = 16 / (int)sizeof(TR), S = kStages;
@@ -168,101 +269,175 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
     await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ float2 part[2][N / 32];
-    __shared__ float most[2][N / 32];
+    __shared__ float most[kQuant ? 4 : 1][N / 32];
     const Slots<kFwdSlots, S, N> ring(sm);
-    const Place at(d.rows, d.L, N);
+    const Place<VEC> at(d.rows, d.D, d.L, N);
     const float inv_d = 1.f / d.D;
-    auto live = [&](int p) { return (at.u + p * at.L) * VEC < d.D; };
-    auto column = [&](int p) { return (at.u + p * at.L) * VEC; };
-    int64_t now = at.first, next = now;
+    // where the thread's pieces of the row copied and of the row worked on are
+    const TX* x_next = x + at.row * d.x_stride + at.c0;
+    const TR* r_next = res ? res + at.row * d.r_stride + at.c0 : nullptr;
+    const int64_t x_step = at.step * d.x_stride, r_step = at.step * d.r_stride, step = at.step * d.D;
+    int64_t now = at.row, next = now, out = now * d.D + at.c0;
     auto issue = [&](int slot) {
-        const TX* xp = x + next * d.x_stride;
-        const TR* rp = res + next * d.r_stride;
+        if (next < d.rows) {
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
-            const bool on = next < d.rows && live(p);
-            PX::copy(ring.at(slot, p), on ? xp + column(p) : x, on);
-            if (res) PR::copy(ring.at(slot, kPieces + p), on ? rp + column(p) : res, on);
+            for (int p = 0; p < kPieces; ++p) {
+                if (p >= at.n) break;
+                PX::copy(ring.at(slot, p), x_next + p * at.LV);
+                if (res) PR::copy(ring.at(slot, kPieces + p), r_next + p * at.LV);
+            }
         }
         commit();
-        next += at.step;
+        next += at.step, x_next += x_step, r_next += r_step;
     };
     uint4 wv[kPieces];
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) wv[p] = live(p) ? PX::ldg(w + column(p)) : make_uint4(0, 0, 0, 0);
-    if (at.turns) issue(0);
-    for (int turn = 0, slot = 0; turn < at.turns; ++turn, slot ^= 1, now += at.step) {
-        issue(slot ^ 1);
+    for (int p = 0; p < kPieces; ++p) wv[p] = p < at.n ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
+    if (at.turns) {
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) issue(i);
+    }
+    for (int turn = 0, slot = 0, fill = S - 1; turn < at.turns; ++turn, now += at.step, out += step) {
+        issue(fill);
+        fill = fill + 1 == S ? 0 : fill + 1;
         wait_group<S - 1>();
+        const int n = now < d.rows ? at.n : 0;
         uint64_t a[kPieces][VEC / 2], ss = twice(0.f);
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
+            if (p >= n) break;
             PX::load(ring.at(slot, p), a[p]);
             if (res) {
                 uint64_t s[VEC / 2];
                 PR::load(ring.at(slot, kPieces + p), s);
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) a[p][j] = add2(a[p][j], s[j]);
-                if (h && now < d.rows && live(p)) PR::store(h + now * d.D + column(p), a[p]);
+                if (h) PR::store(h + out + p * at.LV, a[p]);
             }
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) ss = fma2(a[p][j], a[p][j], ss);
         }
         float sum = sum2(ss), none = 0.f;
         row_sums<N>(sum, none, at.L, part, turn);
-        const uint64_t r = twice(rsqrtf(fmaf(sum, inv_d, d.eps)));
-        float m = 0.f;
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
-            uint64_t f[VEC / 2];
-            PX::unpack(wv[p], f);
-#pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-                a[p][j] = mul2(mul2(a[p][j], r), f[j]);
-                if (kQuant) m = abs_max(a[p][j], m);
-            }
-            if constexpr (!kQuant) {
-                if (now < d.rows && live(p)) PX::store((TX*)y + now * d.D + column(p), a[p]);
-            } else if (d.group < d.D) {
-                // a group's lanes are neighbours: 4 to 32 of them
-                for (int off = d.group / VEC / 2; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float scale = scale_of(m);
-                const uint64_t by = twice(1.f / scale);
-#pragma unroll
-                for (int j = 0; j < VEC / 2; ++j) a[p][j] = mul2(a[p][j], by);
-                if (column(p) % d.group == 0 && now < d.rows && live(p))
-                    scales[now * (d.D / d.group) + column(p) / d.group] = scale;
-                m = 0.f;
-            }
-        }
-        if constexpr (kQuant) {
-            uint64_t by = twice(1.f);
-            if (d.group >= d.D) {
-                const float scale = scale_of(row_max<N>(m, at.L, most, turn));
-                by = twice(1.f / scale);
-                if (at.u == 0 && now < d.rows) scales[now] = scale;
-            }
+        const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
+        if constexpr (!kQuant) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                if (p * at.L * VEC >= d.D || now >= d.rows || !live(p)) break;
-                uint32_t q[VEC / 2];
+                if (p >= n) break;
+                uint64_t f[VEC / 2];
+                PX::unpack(wv[p], f);
 #pragma unroll
-                for (int j = 0; j < VEC / 2; ++j) q[j] = e4m3x2(mul2(a[p][j], by));
-                unsigned char* out = (unsigned char*)y + now * d.D + column(p);
-                if constexpr (VEC == 8) *reinterpret_cast<uint2*>(out) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                else *reinterpret_cast<uint32_t*>(out) = q[0] | q[1] << 16;
+                for (int j = 0; j < VEC / 2; ++j) a[p][j] = mul2(mul2(a[p][j], twice(r)), f[j]);
+                PX::store((TX*)y + out + p * at.LV, a[p]);
+            }
+        } else {
+            constexpr bool kWide = sizeof(TR) == 4;
+            auto place = [&](int p) { return res ? ring.at(slot, kPieces + p) : 0u; };
+            // the piece's t in the place of h, and its largest |t|
+            auto weighted = [&](int p) {
+                uint64_t f[VEC / 2];
+                PX::unpack(wv[p], f);
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    a[p][j] = mul2(a[p][j], f[j]);
+                    m = abs_max(a[p][j], m);
+                }
+                return m;
+            };
+            // (bf16's sums and products are exact, but for addends 2^16 apart)
+            auto left_out = [&](int p, float most, float left) {
+                bool is = false;
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    float t0, t1;
+                    unpair(a[p][j], t0, t1);
+                    is = is || fabsf(t0) == most || fabsf(t1) == most;
+                }
+                return is ? left_of<TX, TR>(ring.at(slot, p), place(p), wv[p], most, left) : left;
+            };
+            auto quantise = [&](int p, float most, float left, const Scale& c) {
+                uint32_t q[4] = {0, 0, 0, 0}, near = kNear + 1;
+                if (c.plain) {
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j) a[p][j] = mul2(a[p][j], twice(r));
+                }
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const uint64_t z = mul2(a[p][j], c.by);
+                    float z0, z1;
+                    unpair(z, z0, z1);
+                    near = min(near, min(behind(z0), behind(z1)));
+                    q[j] = e4m3x2(z);
+                }
+                uint2 code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                if (near <= kNear && !c.plain) {
+                    float by, same;
+                    unpair(c.by, by, same);
+                    code = exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], by, most, left);
+                }
+                unsigned char* to = (unsigned char*)y + out + p * at.LV;
+                if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = code;
+                else *reinterpret_cast<uint32_t*>(to) = code.x;
+            };
+            if (d.group < d.D) {
+                // the largest over a group's lanes, neighbours: 4 to 32 of them
+                const int lanes = d.group / VEC;
+                auto over_group = [&](float m) {
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    if (lanes > 4) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    if (lanes > 8) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    if (lanes > 16) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    return m;
+                };
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p * at.LV >= d.D) break;
+                    float m = p < n ? weighted(p) : 0.f, left = 0.f;
+                    m = over_group(m);
+                    if constexpr (kWide) left = over_group(p < n ? left_out(p, m, -FLT_MAX) : 0.f);
+                    if (p >= n) continue;
+                    const Scale c = scale_of(m, r);
+                    const int col = at.c0 + p * at.LV;
+                    if ((col & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
+                    quantise(p, m, left, c);
+                }
+            } else {
+                float m = 0.f, left = -FLT_MAX;
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p >= n) break;
+                    m = max_nan(m, weighted(p));
+                }
+                m = row_max<N>(m, at.L, most, turn);
+                if constexpr (kWide) {
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) {
+                        if (p >= n) break;
+                        left = left_out(p, m, left);
+                    }
+                    left = row_max<N>(left, at.L, most + 2, turn);
+                } else {
+                    left = 0.f;
+                }
+                const Scale c = scale_of(m, r);
+                if (at.c0 == 0 && n) scales[now] = c.scale;
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p >= n) break;
+                    quantise(p, m, left, c);
+                }
             }
         }
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
     wait_group<0>();  // no copy outlives the block
 }
 
 // Each block leaves one row of column sums in part [gridDim.x][D].
 template <typename TX, typename TR, int N>
-__global__ void __launch_bounds__(N, N == 256 ? 2 : 1)
+__global__ void __launch_bounds__(N, N == 256 ? kPerSm : 1)
 add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__ w, const TX* __restrict__ dy,
                     const TR* __restrict__ dh, TX* __restrict__ dx, TR* __restrict__ dr, float* __restrict__ sums) {
     constexpr int VEC = 16 / (int)sizeof(TR), S = kStages;
@@ -272,40 +447,45 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ float2 part[2][N / 32];
     const Slots<kBwdSlots, S, N> ring(sm);
-    const Place at(d.rows, d.L, N);
+    const Place<VEC> at(d.rows, d.D, d.L, N);
     const float inv_d = 1.f / d.D;
-    auto live = [&](int p) { return (at.u + p * at.L) * VEC < d.D; };
-    auto column = [&](int p) { return (at.u + p * at.L) * VEC; };
-    int64_t now = at.first, next = now;
+    const TR* h_next = h + at.row * d.r_stride + at.c0;
+    const int64_t h_step = at.step * d.r_stride, step = at.step * d.D;
+    int64_t now = at.row, next = now, out = now * d.D + at.c0, in = out;
     auto issue = [&](int slot) {
-        const TR* hp = h + next * d.r_stride;
+        if (next < d.rows) {
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
-            const bool on = next < d.rows && live(p);
-            PR::copy(ring.at(slot, p), on ? hp + column(p) : h, on);
-            PX::copy(ring.at(slot, kPieces + p), on ? dy + next * d.D + column(p) : dy, on);
-            if (dh) PR::copy(ring.at(slot, 2 * kPieces + p), on ? dh + next * d.D + column(p) : dh, on);
+            for (int p = 0; p < kPieces; ++p) {
+                if (p >= at.n) break;
+                PR::copy(ring.at(slot, p), h_next + p * at.LV);
+                PX::copy(ring.at(slot, kPieces + p), dy + in + p * at.LV);
+                if (dh) PR::copy(ring.at(slot, 2 * kPieces + p), dh + in + p * at.LV);
+            }
         }
         commit();
-        next += at.step;
+        next += at.step, h_next += h_step, in += step;
     };
     uint4 wv[kPieces];
     uint64_t acc[kPieces][VEC / 2];
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-        wv[p] = live(p) ? PX::ldg(w + column(p)) : make_uint4(0, 0, 0, 0);
+        wv[p] = p < at.n ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) acc[p][j] = twice(0.f);
     }
-    if (at.turns) issue(0);
-    for (int turn = 0, slot = 0; turn < at.turns; ++turn, slot ^= 1, now += at.step) {
-        issue(slot ^ 1);
+    if (at.turns) {
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) issue(i);
+    }
+    for (int turn = 0, slot = 0, fill = S - 1; turn < at.turns; ++turn, now += at.step, out += step) {
+        issue(fill);
+        fill = fill + 1 == S ? 0 : fill + 1;
         wait_group<S - 1>();
+        const int n = now < d.rows ? at.n : 0;
         uint64_t ss = twice(0.f), tx = ss;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
+            if (p >= n) break;
             uint64_t a[VEC / 2], g[VEC / 2], f[VEC / 2];
             PR::load(ring.at(slot, p), a);
             PX::load(ring.at(slot, kPieces + p), g);
@@ -318,15 +498,14 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         }
         float sq = sum2(ss), st = sum2(tx);
         row_sums<N>(sq, st, at.L, part, turn);
-        // 0 where there is no row: its zeros times 1 / sqrt(eps) are NaN for eps = 0
-        const float r = now < d.rows ? rsqrtf(fmaf(sq, inv_d, d.eps)) : 0.f;
+        const float r = rsqrtf(fmaf(sq, inv_d, d.eps));
         // mean(t hh) = r mean(t h), times r of hh
         const uint64_t m = twice(-st * r * r * inv_d), r2 = twice(r);
         // the pieces are read again from shared memory: held in registers over the sum they
         // would leave room for half of the warps
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            if (p * at.L * VEC >= d.D) break;
+            if (p >= n) break;
             uint64_t a[VEC / 2], g[VEC / 2], f[VEC / 2];
             PR::load(ring.at(slot, p), a);
             PX::load(ring.at(slot, kPieces + p), g);
@@ -341,24 +520,23 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) a[j] = add2(a[j], g[j]);
             }
-            if (now < d.rows && live(p)) {
-                PX::store(dx + now * d.D + column(p), a);
-                if constexpr (sizeof(TX) != sizeof(TR)) PR::store(dr + now * d.D + column(p), a);
-            }
+            PX::store(dx + out + p * at.LV, a);
+            if constexpr (sizeof(TX) != sizeof(TR)) PR::store(dr + out + p * at.LV, a);
         }
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
     wait_group<0>();
     // the block's rows of sums, one after the other: the same call gives the same bits
     __syncthreads();
     float* col = (float*)sm;
-    for (int g = 0; g < at.per; ++g) {
+    for (int g = 0; g < N / at.L; ++g) {
         if ((int)threadIdx.x / at.L == g) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                if (!live(p)) break;
+                if (p >= at.n) break;
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) {
-                    float* c = col + column(p) + 2 * j;
+                    float* c = col + at.c0 + p * at.LV + 2 * j;
                     float lo, hi;
                     unpair(acc[p][j], lo, hi);
                     c[0] = g ? c[0] + lo : lo;
@@ -385,7 +563,7 @@ cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    const int64_t want = (d.rows + N / d.L - 1) / (N / d.L), cap = (int64_t)sm_count() * (N == 256 ? 3 : 1);
+    const int64_t want = (d.rows + N / d.L - 1) / (N / d.L), cap = (int64_t)sm_count() * (N == 256 ? kPerSm : 1);
     return launch_dependent(kern, dim3((unsigned)(want < cap ? want : cap)), N, smem, st, d, (const TX*)c.x,
                             (const TR*)c.res, (const TX*)c.w, (TR*)c.h, c.y, c.scales);
 }
@@ -413,7 +591,8 @@ cudaError_t any(const AddNormCall& c, const NormDims& d, AddNormKind kind, cudaS
 
 template <typename TX, typename TR>
 cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
-    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR)), c.group ? c.group : c.D, c.eps};
+    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR)), c.group ? c.group : c.D,
+                     c.group == 32 ? 5 : c.group == 64 ? 6 : 7, c.eps};
     return d.L <= 256 ? any<TX, TR, 256>(c, d, kind, st) : any<TX, TR, 512>(c, d, kind, st);
 }
 
@@ -421,7 +600,7 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
 
 int add_norm_bwd_blocks(int64_t rows, int D, int wide) {
     const int L = lanes_of(D, 16 / wide), n = L <= 256 ? 256 : 512;
-    const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * (n == 256 ? 2 : 1);
+    const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * (n == 256 ? kPerSm : 1);
     return (int)(want < 1 ? 1 : want < cap ? want : cap);
 }
 

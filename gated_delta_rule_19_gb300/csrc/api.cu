@@ -2270,7 +2270,7 @@ gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, fl
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     cudaStream_t cs = (cudaStream_t)stream;
-    double* part = (double*)workspace;
+    gdn::GradPart* part = (gdn::GradPart*)workspace;
     int parts = 0;
     cudaError_t e = timed(gdn::KID_GRAD_SUM, cs, [&] { return gdn::launch_grad_sums(g, count, part, &parts, cs); });
     if (e == cudaSuccess && clip)
@@ -2389,7 +2389,7 @@ gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const 
 }
 
 size_t gdn_grad_workspace_bytes(int64_t count) {
-    return count < 0 || count > (int64_t)1 << 20 ? 0 : gdn::grad_parts(count) * sizeof(double);
+    return count < 0 || count > (int64_t)1 << 20 ? 0 : gdn::grad_parts(count) * sizeof(gdn::GradPart);
 }
 
 gdn_status gdn_grad_norm(const gdn_grad* g, int64_t count, float* norm, void* workspace, size_t workspace_bytes,

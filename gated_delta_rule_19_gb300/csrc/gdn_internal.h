@@ -482,13 +482,17 @@ cudaError_t launch_add_norm(const AddNormCall& c, InType ty, InType stream_ty, A
 // Blocks of the backward; `wide`: bytes of an element of the wider type.
 int add_norm_bwd_blocks(int64_t rows, int D, int wide);
 
-// The gradients' norm and their scaling: partial sums (grad_parts(count) doubles at most)
-// first, *parts of them.
+// The gradients' norm and their scaling: partial sums (grad_parts(count) of them at most)
+// first, *parts in the end.
+struct GradPart {
+    float s, c;
+    double rest;
+};
 size_t grad_parts(int64_t count);
 int64_t grad_tiles(int64_t n);  // at least as many as the tiles of n elements
-cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, double* part, int* parts, cudaStream_t st);
-cudaError_t launch_grad_norm(const double* part, int parts, float* norm, cudaStream_t st);
-cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const double* part, int parts, float max_norm,
+cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, GradPart* part, int* parts, cudaStream_t st);
+cudaError_t launch_grad_norm(const GradPart* part, int parts, float* norm, cudaStream_t st);
+cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const GradPart* part, int parts, float max_norm,
                               float* norm, cudaStream_t st);
 
 // States [B][rows][K] to and from the slots of a cache [slots][rows][K] with a scale a row.

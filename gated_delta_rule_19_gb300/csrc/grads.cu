@@ -10,10 +10,11 @@
 // from its end, where what the norm read last may still be in L2.
 //
 // The sum: a thread adds the squares of its 32 elements of a tile in float32, and the tiles'
-// sums with their rounding errors kept (two float32 numbers); blocks and the call in float64,
-// in a fixed order, by every block of the scaling for itself.  So the norm of N elements
+// sums, the blocks' and the call's with their rounding errors kept (two float32 numbers), in a
+// fixed order; the last by every block of the scaling for itself.  So the norm of N elements
 // is within a few float32 roundings, whatever N, and equal calls give equal bits.  Squares
-// that leave float32's range, upward or downward, are added again in float64.
+// that leave float32's range, upward or downward, are added again in float64 (always in
+// float64, a call of 1.3 M elements took 15.4 us).
 
 #include <float.h>
 
@@ -26,16 +27,20 @@ namespace {
 using namespace rows;
 
 constexpr int kTile = kThreads * 32;  // elements
-constexpr int kFew = 64, kMany = 1024;
+// Tensors of a launch: as many as fit 4 KB of parameters, or nearly 32 KB.
+constexpr int kFew = 120, kMany = 1000;
 
-// A launch's tensors.  n: the length, with the types in its top bits.  tile0: the tiles of
+// A tensor of a launch.  n: the length, with the types in its top bits.  tile0: the tiles of
 // the tensors before.
+struct Entry {
+    const void* p;
+    void* out;
+    uint64_t n;
+    uint32_t tile0;
+};
 template <int N>
 struct List {
-    const void* p[N];
-    void* out[N];
-    uint64_t n[N];
-    uint32_t tile0[N];
+    Entry e[N];
     uint32_t tiles;
     int count;
 };
@@ -52,14 +57,14 @@ struct Tensor {
     bool in16, out16;
     template <int N>
     __device__ __forceinline__ void at(const List<N>& l, int i) {
-        p = (const char*)l.p[i];
-        out = (char*)l.out[i];
-        const uint64_t n_ = l.n[i];
+        p = (const char*)l.e[i].p;
+        out = (char*)l.e[i].out;
+        const uint64_t n_ = l.e[i].n;
         n = (int64_t)(n_ & kLength);
         in16 = n_ & kInBf16;
         out16 = n_ & kOutBf16;
-        first = l.tile0[i];
-        end = i + 1 < l.count ? l.tile0[i + 1] : l.tiles;
+        first = l.e[i].tile0;
+        end = i + 1 < l.count ? l.e[i + 1].tile0 : l.tiles;
         lead = (int)((uintptr_t)p & 15) >> (in16 ? 1 : 2);
     }
 };
@@ -71,7 +76,7 @@ __device__ __forceinline__ int find(const List<N>& l, uint32_t tile) {
     int lo = 0, hi = l.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (l.tile0[mid] <= tile) lo = mid;
+        if (l.e[mid].tile0 <= tile) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -88,6 +93,7 @@ __device__ __forceinline__ uint4 vector_at(const Tensor& t, int64_t e) {
     constexpr bool kHalf = VEC == 8;
     if (e >= 0 && e + VEC <= t.n) return *reinterpret_cast<const uint4*>(t.p + e * (16 / VEC));
     uint32_t w[4] = {0, 0, 0, 0};
+    if (e >= t.n || e + VEC <= 0) return make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         if (e + j < 0 || e + j >= t.n) continue;
@@ -97,9 +103,11 @@ __device__ __forceinline__ uint4 vector_at(const Tensor& t, int64_t e) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A sum as two float32 numbers, the second what the first's roundings left out.
+// A sum as two float32 numbers, the second what the first's roundings left out; `rest` is what
+// float32's range does not take, nearly always 0.
 struct Sum {
     float s = 0.f, c = 0.f;
+    double rest = 0.;
     __device__ __forceinline__ void add(float x) {
         const float t = s + x, b = t - s;
         c += (s - (t - b)) + (x - b);
@@ -108,7 +116,7 @@ struct Sum {
 };
 
 template <int VEC>
-__device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum, double& rest) {
+__device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum) {
     constexpr int M = 32 / VEC;
     uint4 v[M];
 #pragma unroll
@@ -122,12 +130,16 @@ __device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum
         for (int i = 0; i < VEC / 2; ++i) ss[i & 1] = fma2(f[i], f[i], ss[i & 1]);
     }
     const float s = sum2(add2(ss[0], ss[1]));
-    // below 2^-100 a square may have been rounded to a subnormal or to 0; above 2^100 the
-    // sum of many tiles may not fit
-    if (s >= 7.888609e-31f && s <= 1.2676506e30f) {
+    // below 2^-100 a square may have been rounded to a subnormal or to 0; of sums above 2^85
+    // the 2^31 tiles' might not fit
+    if (s >= 7.888609e-31f && s <= 3.8685626e25f) {
         sum.add(s);
         return;
     }
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < M; ++j) any |= v[j].x | v[j].y | v[j].z | v[j].w;
+    if ((any & (VEC == 8 ? 0x7fff7fffu : 0x7fffffffu)) == 0) return;  // zeros, or no elements
     double d = 0.;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
@@ -141,20 +153,36 @@ __device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum
             if (b != 0.f) d += (double)b * b;
         }
     }
-    rest += d;
+    sum.rest += d;
 }
 
-// The sum of one double per thread, in a fixed order; the same in every thread.
-__device__ __forceinline__ double block_sum(double x) {
-    __shared__ double part[kThreads / 32];
-    __syncthreads();
+// The threads' sums added in a fixed order; the same in every thread.  Without float64
+// unless some thread has a rest: its operations run at a small part of float32's rate.
+__device__ __forceinline__ Sum block_sum(Sum x) {
+    __shared__ float2 part[kThreads / 32];
+    __shared__ double rests[kThreads / 32];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.;
+    for (int off = 16; off > 0; off >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, x.s, off), c = __shfl_xor_sync(0xffffffffu, x.c, off);
+        x.add(s);
+        x.c += c;
+    }
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(x.s, x.c);
+    const bool any = __syncthreads_or(x.rest != 0.);  // true of NaN
+    if (any) {
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) x += part[i];
+        for (int off = 16; off > 0; off >>= 1) x.rest += __shfl_xor_sync(0xffffffffu, x.rest, off);
+        if ((threadIdx.x & 31) == 0) rests[threadIdx.x >> 5] = x.rest;
+        __syncthreads();
+        x.rest = 0.;
+        for (int i = 0; i < kThreads / 32; ++i) x.rest += rests[i];
+    }
+    x.s = x.c = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        x.add(part[i].x);
+        x.c += part[i].y;
+    }
     return x;
 }
 
@@ -168,37 +196,59 @@ constexpr int kSumPerSm = 4, kScalePerSm = 4;
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kSumPerSm)
-grad_sum_kernel(const __grid_constant__ List<N> l, double* __restrict__ part) {
-    await_previous();
+grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) {
     uint32_t tile, to;
     run_of(l.tiles, tile, to);
     Sum sum;
-    double rest = 0.;
-    if (tile < to) {
-        int i = find(l, tile);
-        Tensor t;
-        t.at(l, i);
-        for (; tile < to; ++tile) {
-            while (tile >= t.end) t.at(l, ++i);
-            const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
-            if (t.in16) square_tile<8>(t, e + threadIdx.x * 8, sum, rest);
-            else square_tile<4>(t, e + threadIdx.x * 4, sum, rest);
-        }
-    }
-    const double all = block_sum((double)sum.s + (double)sum.c + rest);
-    if (threadIdx.x == 0) part[blockIdx.x] = all;
-}
-
-__device__ __forceinline__ double norm_of(const double* __restrict__ part, int parts) {
-    double x = 0.;
-    for (int i = threadIdx.x; i < parts; i += kThreads) x += part[i];
-    return sqrt(block_sum(x));
-}
-
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __restrict__ part, int parts, float* norm) {
+    int i = 0;
+    Tensor t;
+    if (tile < to) t.at(l, i = find(l, tile));
     await_previous();
-    const double x = norm_of(part, parts);
-    if (threadIdx.x == 0) *norm = (float)x;
+    for (; tile < to; ++tile) {
+        while (tile >= t.end) t.at(l, ++i);
+        const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
+        if (t.in16) square_tile<8>(t, e + threadIdx.x * 8, sum);
+        else square_tile<4>(t, e + threadIdx.x * 4, sum);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = {sum.s, sum.c, sum.rest};
+}
+
+// The norm from the blocks' sums, and the factor that takes it to max_norm; the same in every
+// thread.
+struct Norm {
+    float norm, by;
+};
+__device__ __forceinline__ Norm norm_of(const GradPart* __restrict__ part, int parts, float max_norm) {
+    __shared__ Norm all;
+    Sum x;
+    for (int i = threadIdx.x; i < parts; i += kThreads) {
+        const GradPart p = part[i];
+        x.add(p.s);
+        x.c += p.c;
+        x.rest += p.rest;
+    }
+    x = block_sum(x);
+    const float s = x.s + x.c;
+    if (x.rest == 0. && s <= FLT_MAX) {
+        // the root of s, and half of what its square leaves of the sum over itself
+        const float n = sqrtf(s), left = fmaf(-n, n, x.s) + x.c;
+        const float norm = s > 0.f ? n + 0.5f * left / n : 0.f;
+        return {norm, norm > max_norm ? max_norm / norm : 1.f};
+    }
+    if (threadIdx.x == 0) {
+        const double n = sqrt((double)x.s + (double)x.c + x.rest);
+        // a norm that is not finite says nothing of how long the gradients are: they stay
+        all = {(float)n, n > (double)max_norm && n <= DBL_MAX ? (float)((double)max_norm / n) : 1.f};
+    }
+    __syncthreads();
+    return all;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const GradPart* __restrict__ part, int parts, float* norm) {
+    await_previous();
+    const Norm x = norm_of(part, parts, 0.f);
+    if (threadIdx.x == 0) *norm = x.norm;
 }
 
 // VEC neighbouring results from element e on, whose address is a whole number of vectors;
@@ -265,20 +315,18 @@ __device__ __forceinline__ void scale_tile_apart(const Tensor& t, int64_t e, flo
 // in_place: every tensor is its own output.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kScalePerSm)
-grad_scale_kernel(const __grid_constant__ List<N> l, const double* __restrict__ part, int parts, float max_norm,
+grad_scale_kernel(const __grid_constant__ List<N> l, const GradPart* __restrict__ part, int parts, float max_norm,
                   float* norm, bool in_place) {
-    await_previous();
-    const double x = norm_of(part, parts);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)x;
-    // a norm that is not finite says nothing of how long the gradients are: they stay
-    const float by = x > (double)max_norm && x <= DBL_MAX ? (float)((double)max_norm / x) : 1.f;
-    if (in_place && by == 1.f) return;
     uint32_t from, tile;
     run_of(l.tiles, from, tile);
-    if (from >= tile) return;
-    int i = find(l, tile - 1);
+    int i = 0;
     Tensor t;
-    t.at(l, i);
+    if (from < tile) t.at(l, i = find(l, tile - 1));
+    await_previous();
+    const Norm x = norm_of(part, parts, max_norm);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
+    const float by = x.by;
+    if ((in_place && by == 1.f) || from >= tile) return;
     while (tile-- > from) {
         while (tile < t.first) t.at(l, --i);
         const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
@@ -301,10 +349,8 @@ void fill(List<N>& l, const gdn_grad* g, int64_t a, int64_t b) {
     for (int64_t i = a; i < b; ++i) {
         const bool in16 = g[i].dtype == GDN_BF16;
         const int lead = (int)((uintptr_t)g[i].grad & 15) >> (in16 ? 1 : 2);
-        l.p[i - a] = g[i].grad;
-        l.out[i - a] = g[i].out;
-        l.n[i - a] = (uint64_t)g[i].n | (in16 ? kInBf16 : 0) | (g[i].out_dtype == GDN_BF16 ? kOutBf16 : 0);
-        l.tile0[i - a] = (uint32_t)tiles;
+        l.e[i - a] = {g[i].grad, g[i].out, (uint64_t)g[i].n | (in16 ? kInBf16 : 0) | (g[i].out_dtype == GDN_BF16 ? kOutBf16 : 0),
+                      (uint32_t)tiles};
         if (g[i].n) tiles += ((uint64_t)g[i].n + lead + kTile - 1) / kTile;
     }
     l.tiles = (uint32_t)tiles;
@@ -316,17 +362,17 @@ int grid_of(uint32_t tiles, int per_sm) {
 }
 
 template <int N>
-cudaError_t sum(const gdn_grad* g, int64_t a, int64_t b, double* part, int* parts, cudaStream_t st) {
+cudaError_t sum(const gdn_grad* g, int64_t a, int64_t b, GradPart* part, int* parts, cudaStream_t st) {
     List<N> l;
     fill(l, g, a, b);
     const int grid = grid_of(l.tiles, kSumPerSm);
-    double* to = part + *parts;
+    GradPart* to = part + *parts;
     *parts += grid;
     return launch_dependent(grad_sum_kernel<N>, dim3(grid), kThreads, 0, st, l, to);
 }
 
 template <int N>
-cudaError_t scale(const gdn_grad* g, int64_t a, int64_t b, const double* part, int parts, float max_norm, float* norm,
+cudaError_t scale(const gdn_grad* g, int64_t a, int64_t b, const GradPart* part, int parts, float max_norm, float* norm,
                   bool in_place, cudaStream_t st) {
     List<N> l;
     fill(l, g, a, b);
@@ -343,7 +389,7 @@ size_t grad_parts(int64_t count) {
     return (size_t)launches * kSumPerSm * sm_count();
 }
 
-cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, double* part, int* parts, cudaStream_t st) {
+cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, GradPart* part, int* parts, cudaStream_t st) {
     *parts = 0;
     cudaError_t e = cudaSuccess;
     for (int64_t a = 0; e == cudaSuccess && (a == 0 || a < count); a += kMany) {
@@ -353,11 +399,11 @@ cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, double* part, int
     return e;
 }
 
-cudaError_t launch_grad_norm(const double* part, int parts, float* norm, cudaStream_t st) {
+cudaError_t launch_grad_norm(const GradPart* part, int parts, float* norm, cudaStream_t st) {
     return launch_dependent(grad_norm_kernel, dim3(1), kThreads, 0, st, part, parts, norm);
 }
 
-cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const double* part, int parts, float max_norm,
+cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const GradPart* part, int parts, float max_norm,
                               float* norm, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     for (int64_t a = 0; e == cudaSuccess && (a == 0 || a < count); a += kMany) {

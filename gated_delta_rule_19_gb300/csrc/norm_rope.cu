@@ -5,7 +5,7 @@
 namespace gdn {
 
 cudaError_t launch_qk_norm_rope(const RopeCall& c, InType ty, bool bwd, cudaStream_t st) {
-    return ty == InType::BF16 ? launch_t<__nv_bfloat16, false>(c, bwd, st) : launch_t<float, false>(c, bwd, st);
+    return ty == InType::BF16 ? launch_t<__nv_bfloat16, 0>(c, bwd, st) : launch_t<float, 0>(c, bwd, st);
 }
 
 }  // namespace gdn

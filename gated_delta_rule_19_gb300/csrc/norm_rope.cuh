@@ -13,9 +13,12 @@
 // both elements of a pair are in one lane, and likewise of the rest.  An item of a group
 // is kHeads heads of one token, which share the angles' pieces.
 //
-// With several axes (kAxes) a token has a position on each of up to four, and every pair
-// takes its angle from the tables' row of one of them.  The calls of one position
-// (norm_rope.cu) and of several (norm_rope_axes.cu) are compiled apart.
+// With several axes a token has a position on each of up to four, and every pair takes its
+// angle from the tables' row of one of them.  The calls of one position (norm_rope.cu,
+// kAxes 0) and of several (norm_rope_axes.cu) are compiled apart, and those in two forms:
+// where every unit of angles that lie together and are copied together belongs to one axis
+// (kAxes 1), a lane keeps the positions of its two units' axes; else (kAxes 2) those of all
+// axes.
 #pragma once
 
 #include "gdn_internal.h"
@@ -46,8 +49,8 @@ struct RopeDims {
 
 struct Tables {
     const float *cos, *sin;
-    const int32_t* pos;  // or NULL: the token's place in its sequence; kAxes: [axes][tokens]
-    int axes;            // kAxes: the positions of a token, and the pairs' axes
+    const int32_t* pos;  // or NULL: the token's place in its sequence; kAxes > 0: [axes][tokens]
+    int axes;            // kAxes > 0: the positions of a token, and the pairs' axes
     AxesMap map;
 };
 
@@ -64,26 +67,51 @@ __device__ __forceinline__ int pair_of(const RopeDims& d, int u, int j) {
     return u * (VEC / 2) + (j < VEC / 2 ? j : d.R / 4 + j - VEC / 2);
 }
 
-// Where a token's angles are: its row of the tables, or its rows, one for each axis, and the
-// axes of the lane's VEC pairs, two bits each.
-template <int VEC, bool kInter, bool kAxes>
+// Angles that are copied together: four, or the two that lie together of interleaved float32.
+template <int VEC, bool kInter>
+constexpr int kUnit = kInter && VEC == 4 ? 2 : 4;
+
+__device__ __forceinline__ uint32_t axis_of(const AxesMap& m, int pair) {
+    const int word = pair >> 5;
+    const uint64_t w = word < 2 ? word == 0 ? m.w[0] : m.w[1] : word == 2 ? m.w[2] : m.w[3];
+    return (uint32_t)(w >> (2 * (pair & 31))) & 3;
+}
+
+// Where a token's angles are.  One position: its row of the tables.
+template <int VEC, bool kInter, int kAxes>
 struct Where {
     int pos = 0;
     __device__ __forceinline__ Where(const RopeDims&, const Tables&, int, bool) {}
     __device__ __forceinline__ void move(const RopeDims& d, const Tables& t, int64_t tok) { pos = position(d, t, tok); }
 };
+// The rows of the lane's units.
 template <int VEC, bool kInter>
-struct Where<VEC, kInter, true> {
+struct Where<VEC, kInter, 1> {
+    static constexpr int N = VEC / kUnit<VEC, kInter>;
+    const int32_t* from[N];  // the axis's positions
+    int pos[N];
+    __device__ __forceinline__ Where(const RopeDims& d, const Tables& t, int u, bool turns) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            from[i] = t.pos;
+            pos[i] = 0;
+            if (turns) from[i] += axis_of(t.map, pair_of<VEC, kInter>(d, u, i * kUnit<VEC, kInter>)) * d.tokens;
+        }
+    }
+    __device__ __forceinline__ void move(const RopeDims&, const Tables&, int64_t tok) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) pos[i] = from[i][tok];
+    }
+};
+// The rows of all axes, and the axes of the lane's VEC pairs, two bits each.
+template <int VEC, bool kInter>
+struct Where<VEC, kInter, 2> {
     int pos[4] = {0, 0, 0, 0};
     uint32_t axis = 0;
     __device__ __forceinline__ Where(const RopeDims& d, const Tables& t, int u, bool turns) {
         if (!turns) return;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = pair_of<VEC, kInter>(d, u, j), word = c >> 5;
-            const uint64_t w = word < 2 ? word == 0 ? t.map.w[0] : t.map.w[1] : word == 2 ? t.map.w[2] : t.map.w[3];
-            axis |= (uint32_t)(w >> (2 * (c & 31)) & 3) << (2 * j);
-        }
+        for (int j = 0; j < VEC; ++j) axis |= axis_of(t.map, pair_of<VEC, kInter>(d, u, j)) << (2 * j);
     }
     __device__ __forceinline__ void move(const RopeDims& d, const Tables& t, int64_t tok) {
 #pragma unroll
@@ -97,12 +125,40 @@ struct Where<VEC, kInter, true> {
     }
 };
 
-// copy_angles (below) for several axes: four angles of one row that lie together in one copy
-// of 16 bytes, others by 4 bytes each (the four at the border of two axes' pairs, and all
-// where the axes take turns).  A position outside the tables gives its own pairs NaN.
+// copy_angles (below) for several axes.  A position outside the tables gives its own pairs
+// NaN.
 template <int VEC, bool kInter, typename R>
 __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, const RopeDims& d, const Tables& t,
-                                            const Where<VEC, kInter, true>& at, int u, bool turns) {
+                                            const Where<VEC, kInter, 1>& at, int u, bool turns) {
+    if (!turns) return;
+    const float nan = __int_as_float(0x7fc00000);
+    constexpr int U = kUnit<VEC, kInter>;
+#pragma unroll
+    for (int i = 0; i < VEC / U; ++i) {
+        const int row = at.pos[i], p = p0 + i * U / 4;
+        if (row < 0 || row >= d.rows) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                ring.put4(slot, p, i * U % 4 + j, nan);
+                ring.put4(slot, p + VEC / 4, i * U % 4 + j, nan);
+            }
+            continue;
+        }
+        const int64_t e = (int64_t)row * (d.R / 2) + pair_of<VEC, kInter>(d, u, i * U);
+        if constexpr (U == 4) {
+            ring.copy_shared(slot, p, t.cos + e);
+            ring.copy_shared(slot, p + VEC / 4, t.sin + e);
+        } else {
+            ring.copy8(slot, p, i, t.cos + e);
+            ring.copy8(slot, p + VEC / 4, i, t.sin + e);
+        }
+    }
+}
+// Four angles of one row that lie together in one copy, others by 4 bytes each: the four at
+// the border of two axes' pairs, and all where the axes take turns.
+template <int VEC, bool kInter, typename R>
+__device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, const RopeDims& d, const Tables& t,
+                                            const Where<VEC, kInter, 2>& at, int u, bool turns) {
     if (!turns) return;
     const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
@@ -141,7 +197,7 @@ __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, con
 // first piece come first, then those of the second, a quarter of the row behind.
 template <int VEC, bool kInter, typename R>
 __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, const RopeDims& d, const Tables& t,
-                                            const Where<VEC, kInter, false>& at, int u, bool turns) {
+                                            const Where<VEC, kInter, 0>& at, int u, bool turns) {
     if (!turns) return;
     const int pos = at.pos;
     if (pos < 0 || pos >= d.rows) {
@@ -237,7 +293,7 @@ using FwdRing = Ring<2 * kFwdHeads + kVec<T> / 2, kFwdStages>;
 template <typename T>
 using BwdRing = Ring<4 * kBwdHeads + kVec<T> / 2, kBwdStages>;
 
-template <typename T, int G, bool kInter, bool kAxes>
+template <typename T, int G, bool kInter, int kAxes>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_norm_rope_fwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab) {
     constexpr int VEC = kVec<T>, NH = kFwdHeads, S = kFwdStages;
@@ -317,7 +373,7 @@ qk_norm_rope_fwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab) {
 
 // Walks the queries' items, then the keys', and leaves one row of column sums per block
 // and side in part [2][gridDim.x][D].
-template <typename T, int G, bool kInter, bool kAxes>
+template <typename T, int G, bool kInter, int kAxes>
 __global__ void __launch_bounds__(kThreads, kRopeBwdPerSm)
 qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __restrict__ part) {
     constexpr int VEC = kVec<T>, NH = kBwdHeads, S = kBwdStages;
@@ -411,7 +467,7 @@ qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __r
     }
 }
 
-template <typename T, int G, bool kInter, bool kAxes>
+template <typename T, int G, bool kInter, int kAxes>
 cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T>& k, const Tables& tab, float* part,
                      int blocks, cudaStream_t st) {
     if (!bwd) {
@@ -433,14 +489,14 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
     }
 }
 
-template <typename T, int G, bool kAxes>
+template <typename T, int G, int kAxes>
 cudaError_t launch_g(const RopeDims& d, bool inter, bool bwd, Side<T> q, Side<T> k, const Tables& tab, float* part,
                      int blocks, cudaStream_t st) {
     return inter ? launch_k<T, G, true, kAxes>(d, bwd, q, k, tab, part, blocks, st)
                  : launch_k<T, G, false, kAxes>(d, bwd, q, k, tab, part, blocks, st);
 }
 
-template <typename T, bool kAxes>
+template <typename T, int kAxes>
 cudaError_t launch_t(const RopeCall& c, bool bwd, cudaStream_t st) {
     RopeDims d{c.tokens, c.T, c.D, c.R, c.rows, c.eps};
     const Tables tab{c.cos, c.sin, c.pos, c.axes, c.map};

@@ -633,8 +633,8 @@ typedef struct {
 
 /*
  * gdn_state_store -- parks the states of B sequences in 8 bits: for every row s of K elements,
- * scale = max|s| / 127 (2^-126 at least, float32) and code = the whole number nearest to
- * s / scale, ties to even.
+ * scale = max|s| * (1/127) in float32 (2^-126 at least) and code = the whole number nearest
+ * to s / scale, ties to even.
  *   states  float32 [B,H,V,K].
  *   slot    int32 [B], 4-byte aligned: where sequence b goes.  One outside the cache: it is
  *           not kept.  Of sequences with the same slot the last one is.

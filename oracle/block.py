@@ -80,8 +80,9 @@ def clip(grads, max_norm):
 
 
 def park(states):
-    """(codes, scales) of float32 rows; the scales are float32 numbers, and the codes count
-    those."""
+    """(codes, scales) of float32 rows; the scales are the float32 products by 1/127, and the
+    codes count those."""
     x = np.asarray(states, dtype=np.float64)
-    s = np.maximum((np.abs(x).max(-1) / 127.0).astype(np.float32).astype(np.float64), LEAST)
+    s = np.abs(x).max(-1).astype(np.float32) * (np.float32(1) / np.float32(127))
+    s = np.maximum(s.astype(np.float64), LEAST)
     return np.rint(x / s[..., None]), s

@@ -153,6 +153,27 @@ def test_quant(rows, D, dtype, stream, slices, group):
     assert torch.equal(h, h2)
 
 
+@pytest.mark.parametrize("rows,D,dtype,stream,group", [
+    (4000, 768, "bf16", "bf16", 128), (4000, 768, "bf16", "f32", 128), (4000, 768, "f32", "f32", 64), (900, 4096, "bf16", "bf16", 0),
+    (900, 4096, "f32", "f32", 0), (900, 4096, "bf16", "f32", 0), (3000, 1000, "f32", "f32", 0), (3000, 992, "bf16", "bf16", 32)])
+def test_quant_gives_the_nearest_number(rows, D, dtype, stream, group):
+    """Every 8-bit number is the one nearest to the exact quotient 448 t / max|t| of the group
+    (t = (x + residual) w; the row's norm divides out): of 3 million elements not one is on the
+    wrong side of a middle.  Below 2^-6 a middle may be decided by float32's error: within 2^-20
+    of it either side is taken."""
+    x, r, w, _, _ = _inputs(rows, D, dtype, stream, False, seed=9)
+    y, _, _ = gdn.gdn_add_norm_quant(x, r, w, eps=EPS, group=group)
+    torch.cuda.synchronize()
+    t = ((_np(x) + _np(r)) * _np(w)).reshape(rows, -1, group or D)
+    exact = t * 448.0 / np.abs(t).max(-1, keepdims=True)
+    want, got = block.e4m3(exact), _np(y.float()).reshape(t.shape)
+    wrong = want != got
+    low = np.abs(exact) < 2.0 ** -6
+    assert not (wrong & ~low).any()
+    middle = (want + got) / 2
+    assert (np.abs(exact - middle) <= 2.0 ** -20 * np.abs(middle))[wrong].all()
+
+
 def test_quant_of_no_residual_and_of_the_least_numbers():
     """Rows of zeros and of numbers so small that their scale would be subnormal."""
     x = torch.zeros(4, 256, device="cuda")

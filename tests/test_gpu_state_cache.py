@@ -102,10 +102,11 @@ def test_ties_and_next_to_them():
             x = base.astype(np.float32)
             x = x if shift == 0 else np.nextafter(x, np.float32(np.inf if shift > 0 else -np.inf))
             rows.append(np.concatenate([[np.float32(np.float64(s) * 127)], x, [0.0]]).astype(np.float32))
+    part = np.float32(1) / np.float32(127)
     r = np.random.default_rng(0)
     while len(rows) < 16 * 20:  # random steps, quotients next to a middle
         top = np.float32(np.exp(r.normal() * 20))
-        s = np.float32(top / np.float32(127))
+        s = top * part
         x = ((r.integers(-126, 126, 62) + 0.5) * np.float64(s)).astype(np.float32)
         x = np.where(r.random(62) < 0.5, np.nextafter(x, np.float32(np.inf)), x)
         rows.append(np.concatenate([[top], x, [-top]]).astype(np.float32))
