@@ -239,7 +239,7 @@ const char* const kKernelNames[gdn::KID_COUNT] = {
     "la_states", "la_link_kernel", "la_scan", "la_decode_kernel", "qk_norm_rope_fwd_kernel", "qk_norm_rope_bwd_kernel",
     "gated_norm_fwd_kernel", "gated_norm_bwd_kernel", "weight_sum_kernel", "qk_norm_rope_fwd_kernel(axes)",
     "qk_norm_rope_bwd_kernel(axes)", "add_norm_fwd_kernel", "add_norm_fwd_kernel(8 bits)", "add_norm_bwd_kernel",
-    "grad_sum_kernel", "grad_norm_kernel", "grad_scale_kernel", "state_store_kernel", "state_load_kernel"};
+    "grad_sum_kernel", "grad_norm_kernel", "grad_scale_kernel", "grad_clip_kernel", "state_store_kernel", "state_load_kernel"};
 
 template <typename F>
 cudaError_t timed(int kid, cudaStream_t st, F&& launch) {
@@ -1988,6 +1988,10 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
     return rope_fwd(p, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream);
 }
 
+// Whether the blocks of a backward are one cluster, which needs neither memory for its sums nor
+// the launch that adds them up (several axes; the calls of one position keep their two launches).
+static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && c.blocks <= gdn::kMostCluster; }
+
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p) {
     gdn::RopeCall c{};
     return rope_problem(p, &c) == GDN_OK ? (size_t)2 * c.blocks * c.D * sizeof(float) : 0;
@@ -2000,7 +2004,8 @@ static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
     gdn_status st = rope_problem(p, &c);
     if (st != GDN_OK) return st;
     const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
-    const size_t need = gdn_qk_norm_rope_bwd_workspace_bytes(p);
+    const bool cluster = rope_cluster(c);
+    const size_t need = cluster ? 0 : gdn_qk_norm_rope_bwd_workspace_bytes(p);
     const int64_t wq = p->Hq * p->D, wk = p->Hk * p->D;
     const size_t nq = (size_t)c.tokens * wq * es, nk = (size_t)c.tokens * wk * es;
     const Span ins[] = {{q, row_span(c.tokens, c.q_stride, wq, p->dtype), "q"},
@@ -2022,12 +2027,13 @@ static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
     if (c.tokens && (st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
     c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
     c.qo = dq, c.ko = dk, c.dqo = dq_out, c.dko = dk_out, c.part = (float*)workspace;
+    if (cluster) c.dwq = dq_weight, c.dwk = dk_weight;
     cudaStream_t cs = (cudaStream_t)stream;
     const gdn::InType ty = elem_type(p->dtype);
     cudaError_t e = timed(c.axes ? gdn::KID_NORM_AXES_BWD : gdn::KID_NORM_ROPE_BWD, cs, [&] {
         return c.axes ? gdn::launch_qk_norm_rope_axes(c, ty, true, cs) : gdn::launch_qk_norm_rope(c, ty, true, cs);
     });
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !cluster)
         e = timed(gdn::KID_WEIGHT_SUM, cs,
                   [&] { return gdn::launch_weight_sum(2, c.blocks, c.D, ty, c.part, dq_weight, dk_weight, cs); });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "q, k norm and rotation gradient kernel");
@@ -2107,7 +2113,7 @@ gdn_status gdn_gated_norm_bwd(const gdn_gated_norm_problem* p, const void* x, co
 namespace {
 
 // The axes' part of a call: which axis turns each pair.
-gdn_status axes_map(const gdn_rope_axes_problem* p, const int32_t* positions, gdn::RopeCall* c) {
+gdn_status axes_map(const gdn_rope_axes_problem* p, const int32_t* positions, gdn::RopeCall* c, bool call = true) {
     if (!p) return fail(GDN_ERR_INVALID_ARG, "problem pointer is NULL");
     const int64_t pairs = p->rope.R / 2;
     if (p->axes < 1 || p->axes > 4) return fail(GDN_ERR_UNSUPPORTED, "axes=%d: must be 1 to 4", (int)p->axes);
@@ -2139,7 +2145,7 @@ gdn_status axes_map(const gdn_rope_axes_problem* p, const int32_t* positions, gd
         if (counts[a] != p->sections[a])
             return fail(GDN_ERR_INVALID_ARG, "sections[%d]=%d: %d of the alternating pairs fall to this axis", a,
                         (int)p->sections[a], counts[a]);
-    if (pairs && p->rope.B > 0 && p->rope.T > 0) {
+    if (call && pairs && p->rope.B > 0 && p->rope.T > 0) {
         if (!positions) return fail(GDN_ERR_INVALID_ARG, "positions is NULL");
         if ((uintptr_t)positions % 4 != 0) return fail(GDN_ERR_INVALID_ARG, "positions is not 4-byte aligned");
     }
@@ -2201,7 +2207,8 @@ gdn_status add_norm(const gdn_add_norm_problem* p, gdn::AddNormKind kind, int32_
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "residual norm kernel");
 }
 
-size_t add_norm_part(const gdn::AddNormCall& c) { return (size_t)c.blocks * c.D * sizeof(float); }
+// A cluster needs no memory for its sums.
+size_t add_norm_part(const gdn::AddNormCall& c) { return c.grid.cluster ? 0 : (size_t)c.grid.blocks * c.D * sizeof(float); }
 
 // The tensors of a gradient call; with `write` their outputs too, which must lie apart.
 gdn_status check_grads(const gdn_grad* g, int64_t count, bool write, const Span* others, int nothers) {
@@ -2264,7 +2271,7 @@ gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, fl
     if (clip && !(max_norm >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "max_norm=%g is negative", (double)max_norm);
     gdn_status st;
     if ((!clip || norm) && (st = check_word_ptr(norm, "norm")) != GDN_OK) return st;
-    const size_t need = gdn_grad_workspace_bytes(count < 0 ? 0 : count);
+    const size_t need = count > 0 && !g ? 0 : gdn_grad_workspace_bytes(g, count);
     const Span others[] = {{norm, sizeof(float), "norm"}, {workspace, need, "workspace"}};
     if ((st = check_grads(g, count, clip, others, 2)) != GDN_OK || (st = check_ptr(others[1], true)) != GDN_OK) return st;
     if (workspace_bytes < need)
@@ -2272,6 +2279,11 @@ gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, fl
     cudaStream_t cs = (cudaStream_t)stream;
     gdn::GradPart* part = (gdn::GradPart*)workspace;
     int parts = 0;
+    if (const int blocks = gdn::grad_cluster(g, count, clip)) {
+        cudaError_t e = timed(gdn::KID_GRAD_CLIP, cs,
+                              [&] { return gdn::launch_grad_cluster(g, count, blocks, max_norm, norm, clip, cs); });
+        return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gradient clipping kernel");
+    }
     cudaError_t e = timed(gdn::KID_GRAD_SUM, cs, [&] { return gdn::launch_grad_sums(g, count, part, &parts, cs); });
     if (e == cudaSuccess && clip)
         e = timed(gdn::KID_GRAD_SCALE, cs,
@@ -2322,6 +2334,12 @@ gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void*
     return st == GDN_OK ? rope_fwd(&p->rope, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream) : st;
 }
 
+size_t gdn_qk_norm_rope_axes_bwd_workspace_bytes(const gdn_rope_axes_problem* p) {
+    gdn::RopeCall c{};
+    if (axes_map(p, nullptr, &c, false) != GDN_OK || rope_problem(&p->rope, &c) != GDN_OK || rope_cluster(c)) return 0;
+    return gdn_qk_norm_rope_bwd_workspace_bytes(&p->rope);
+}
+
 gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                                      const int32_t* positions, const void* dq_out, const void* dk_out, void* dq,
@@ -2348,7 +2366,7 @@ gdn_status gdn_add_norm_quant(const gdn_add_norm_problem* p, int32_t group, cons
 size_t gdn_add_norm_bwd_workspace_bytes(const gdn_add_norm_problem* p) {
     gdn::AddNormCall c{};
     if (add_norm_problem(p, &c) != GDN_OK) return 0;
-    c.blocks = gdn::add_norm_bwd_blocks(c.rows, c.D, (int)elem_size(p->stream_dtype));
+    c.grid = gdn::add_norm_bwd_grid(c.rows, c.D, (int)elem_size(p->stream_dtype));
     return add_norm_part(c);
 }
 
@@ -2361,7 +2379,7 @@ gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const 
     if (st != GDN_OK) return st;
     const bool apart = p->dtype != p->stream_dtype;
     const size_t es = elem_size(p->dtype), er = elem_size(p->stream_dtype), n = (size_t)p->rows * p->D;
-    c.blocks = gdn::add_norm_bwd_blocks(c.rows, c.D, (int)er);
+    c.grid = gdn::add_norm_bwd_grid(c.rows, c.D, (int)er);
     const size_t need = add_norm_part(c);
     if (!apart && d_residual)
         return fail(GDN_ERR_INVALID_ARG, "d_residual is given where the types agree: dx is both gradients");
@@ -2376,20 +2394,21 @@ gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const 
     if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 0, nullptr, nullptr)) != GDN_OK) return st;
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-    c.h_in = h, c.w = weight, c.dy = dy, c.dh = dh, c.dx = dx, c.dr = d_residual, c.part = (float*)workspace;
+    c.h_in = h, c.w = weight, c.dy = dy, c.dh = dh, c.dx = dx, c.dr = d_residual, c.dw = dweight, c.part = (float*)workspace;
     cudaStream_t cs = (cudaStream_t)stream;
     const gdn::InType ty = elem_type(p->dtype);
     cudaError_t e = timed(gdn::KID_ADD_NORM_BWD, cs, [&] {
         return gdn::launch_add_norm(c, ty, elem_type(p->stream_dtype), gdn::AddNormKind::BWD, cs);
     });
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !c.grid.cluster)
         e = timed(gdn::KID_WEIGHT_SUM, cs,
-                  [&] { return gdn::launch_weight_sum(1, c.blocks, c.D, ty, c.part, dweight, dweight, cs); });
+                  [&] { return gdn::launch_weight_sum(1, c.grid.blocks, c.D, ty, c.part, dweight, dweight, cs); });
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "residual norm gradient kernel");
 }
 
-size_t gdn_grad_workspace_bytes(int64_t count) {
-    return count < 0 || count > (int64_t)1 << 20 ? 0 : gdn::grad_parts(count) * sizeof(gdn::GradPart);
+size_t gdn_grad_workspace_bytes(const gdn_grad* g, int64_t count) {
+    if (count < 0 || count > (int64_t)1 << 20 || (count && !g) || gdn::grad_cluster(g, count, true)) return 0;
+    return gdn::grad_parts(count) * sizeof(gdn::GradPart);
 }
 
 gdn_status gdn_grad_norm(const gdn_grad* g, int64_t count, float* norm, void* workspace, size_t workspace_bytes,

@@ -181,9 +181,6 @@ gated_norm_bwd_kernel(GatedDims d, const T* __restrict__ x, const T* __restrict_
     block_columns<G, VEC>(acc, c0, c0 + half, live, d.D, (float*)sm, part + (int64_t)blockIdx.x * d.D);
 }
 
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
 // dw[c] = sum over the blocks' rows of part, in a fixed order: a warp takes 32 columns'
 // rows w, w + 32, ..., the warps' sums are added in order.  blockIdx.y picks the side
 // (part and dw of the queries, then of the keys).  Bound by latency: 32 warps a block, so

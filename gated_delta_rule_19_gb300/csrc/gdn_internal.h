@@ -163,6 +163,7 @@ enum KernelId {
     KID_GRAD_SUM,        // grad_sum_kernel
     KID_GRAD_NORM,       // grad_norm_kernel
     KID_GRAD_SCALE,      // grad_scale_kernel
+    KID_GRAD_CLIP,       // grad_clip_kernel: a few tiles' norm and scaling
     KID_STATE_STORE,     // state_store_kernel
     KID_STATE_LOAD,      // state_load_kernel
     KID_COUNT
@@ -378,7 +379,22 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
 #ifdef __CUDACC__
 // The kernels before this one in the stream are complete, and what they wrote is visible.
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A cluster's blocks: all threads have arrived, and see what the others' blocks wrote in
+// shared memory; a word of rank's.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_word(const float* mine, uint32_t rank) {
+    uint32_t at;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
 #endif
+// Blocks of the largest cluster (above 8 a kernel has to be allowed it).
+constexpr int kMostCluster = 16;
 
 // Launches a kernel that may start while the one before it in the stream drains (a call
 // of one kernel takes 1.6 us less behind another one): it calls await_previous() before it
@@ -396,6 +412,36 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, 
     a[0].val.programmaticStreamSerializationAllowed = 1;
     c.attrs = a;
     c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// The same for a grid of one cluster.  `done`: as in allow_smem.
+template <typename... P, typename... A>
+cudaError_t launch_one_cluster(void (*kernel)(P...), int blocks, unsigned threads, size_t smem,
+                               std::atomic<uint64_t>& done, cudaStream_t st, const A&... args) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute a[2];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    a[1].id = cudaLaunchAttributeClusterDimension;
+    a[1].val.clusterDim.x = (unsigned)blocks;
+    a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+    c.attrs = a;
+    c.numAttrs = 2;
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
@@ -429,8 +475,11 @@ struct RopeCall {
     const void *dqo = nullptr, *dko = nullptr;
     float* part = nullptr;
     int blocks = 0;
-    int axes = 0;  // launch_qk_norm_rope_axes: pos is [axes][tokens]
+    // launch_qk_norm_rope_axes: pos is [axes][tokens]; in a backward whose blocks are one
+    // cluster the weights' gradients (part is not used then)
+    int axes = 0;
     AxesMap map = {};
+    void *dwq = nullptr, *dwk = nullptr;
 };
 cudaError_t launch_qk_norm_rope(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
 cudaError_t launch_qk_norm_rope_axes(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
@@ -461,7 +510,15 @@ int rows_bwd_blocks(int64_t rows, int per_sm);
 // RMS norm of x + res (res NULL: of x); `ty` is the type of x, w, y and their gradients,
 // `stream_ty` that of res, h, dh and dr.  Forward: y (QUANT: e4m3, with scales of `group`
 // columns, 0: of a row) and h.  Backward: from h_in, dy and dh (or NULL) dx, dr (where the
-// types differ) and the blocks' sums part [blocks][D] of the weight's gradient.
+// types differ), and of the weight's gradient dw itself (a cluster) or the blocks' sums part
+// [blocks][D].
+// Blocks of the backward, and whether they are one cluster, which makes the weight's gradient
+// itself; `wide`: bytes of an element of the wider type.
+struct AddNormGrid {
+    int blocks;
+    bool cluster;
+};
+AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide);
 enum class AddNormKind { FWD, QUANT, BWD };
 struct AddNormCall {
     int64_t rows;
@@ -473,14 +530,12 @@ struct AddNormCall {
     void* y = nullptr;
     float* scales = nullptr;
     const void *h_in = nullptr, *dy = nullptr, *dh = nullptr;
-    void *dx = nullptr, *dr = nullptr;
+    void *dx = nullptr, *dr = nullptr, *dw = nullptr;
     float* part = nullptr;
-    int blocks = 0;
+    AddNormGrid grid = {0, false};
 };
 constexpr int kAddNormMost = 8192;  // columns
 cudaError_t launch_add_norm(const AddNormCall& c, InType ty, InType stream_ty, AddNormKind kind, cudaStream_t st);
-// Blocks of the backward; `wide`: bytes of an element of the wider type.
-int add_norm_bwd_blocks(int64_t rows, int D, int wide);
 
 // The gradients' norm and their scaling: partial sums (grad_parts(count) of them at most)
 // first, *parts in the end.
@@ -491,6 +546,10 @@ struct GradPart {
 size_t grad_parts(int64_t count);
 int64_t grad_tiles(int64_t n);  // at least as many as the tiles of n elements
 cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, GradPart* part, int* parts, cudaStream_t st);
+// Few tiles: the blocks of a cluster that does it all (0: too many), and its launch.
+int grad_cluster(const gdn_grad* g, int64_t count, bool clip);
+cudaError_t launch_grad_cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm, float* norm, bool clip,
+                                cudaStream_t st);
 cudaError_t launch_grad_norm(const GradPart* part, int parts, float* norm, cudaStream_t st);
 cudaError_t launch_grad_scale(const gdn_grad* g, int64_t count, const GradPart* part, int parts, float max_norm,
                               float* norm, cudaStream_t st);

@@ -116,7 +116,7 @@ struct Sum {
 };
 
 template <int VEC>
-__device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum) {
+__device__ __forceinline__ void square_vectors(const Tensor& t, int64_t e, Sum& sum) {
     constexpr int M = 32 / VEC;
     uint4 v[M];
 #pragma unroll
@@ -156,11 +156,19 @@ __device__ __forceinline__ void square_tile(const Tensor& t, int64_t e, Sum& sum
     sum.rest += d;
 }
 
-// The threads' sums added in a fixed order; the same in every thread.  Without float64
-// unless some thread has a rest: its operations run at a small part of float32's rate.
+// A tile's squares, by kThreads threads.
+__device__ __forceinline__ void square_tile(const Tensor& t, uint32_t tile, int thread, Sum& sum) {
+    const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
+    if (t.in16) square_vectors<8>(t, e + thread * 8, sum);
+    else square_vectors<4>(t, e + thread * 4, sum);
+}
+
+// The sums of a block's T threads added in a fixed order; the same in every thread.  Without
+// float64 unless some thread has a rest: its operations run at a small part of float32's rate.
+template <int T>
 __device__ __forceinline__ Sum block_sum(Sum x) {
-    __shared__ float2 part[kThreads / 32];
-    __shared__ double rests[kThreads / 32];
+    __shared__ float2 part[T / 32];
+    __shared__ double rests[T / 32];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float s = __shfl_xor_sync(0xffffffffu, x.s, off), c = __shfl_xor_sync(0xffffffffu, x.c, off);
@@ -175,21 +183,21 @@ __device__ __forceinline__ Sum block_sum(Sum x) {
         if ((threadIdx.x & 31) == 0) rests[threadIdx.x >> 5] = x.rest;
         __syncthreads();
         x.rest = 0.;
-        for (int i = 0; i < kThreads / 32; ++i) x.rest += rests[i];
+        for (int i = 0; i < T / 32; ++i) x.rest += rests[i];
     }
     x.s = x.c = 0.f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < T / 32; ++i) {
         x.add(part[i].x);
         x.c += part[i].y;
     }
     return x;
 }
 
-// Block b's tiles of `tiles`.
-__device__ __forceinline__ void run_of(uint32_t tiles, uint32_t& from, uint32_t& to) {
-    from = (uint32_t)((uint64_t)tiles * blockIdx.x / gridDim.x);
-    to = (uint32_t)((uint64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+// Worker b's tiles, of n workers.
+__device__ __forceinline__ void run_of(uint32_t tiles, uint32_t b, uint32_t n, uint32_t& from, uint32_t& to) {
+    from = (uint32_t)((uint64_t)tiles * b / n);
+    to = (uint32_t)((uint64_t)tiles * (b + 1) / n);
 }
 
 constexpr int kSumPerSm = 4, kScalePerSm = 4;
@@ -198,7 +206,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kSumPerSm)
 grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) {
     uint32_t tile, to;
-    run_of(l.tiles, tile, to);
+    run_of(l.tiles, blockIdx.x, gridDim.x, tile, to);
     Sum sum;
     int i = 0;
     Tensor t;
@@ -206,11 +214,9 @@ grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) 
     await_previous();
     for (; tile < to; ++tile) {
         while (tile >= t.end) t.at(l, ++i);
-        const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
-        if (t.in16) square_tile<8>(t, e + threadIdx.x * 8, sum);
-        else square_tile<4>(t, e + threadIdx.x * 4, sum);
+        square_tile(t, tile, threadIdx.x, sum);
     }
-    sum = block_sum(sum);
+    sum = block_sum<kThreads>(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = {sum.s, sum.c, sum.rest};
 }
 
@@ -219,16 +225,10 @@ grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) 
 struct Norm {
     float norm, by;
 };
-__device__ __forceinline__ Norm norm_of(const GradPart* __restrict__ part, int parts, float max_norm) {
+template <int T>
+__device__ __forceinline__ Norm norm_of(Sum x, float max_norm) {
     __shared__ Norm all;
-    Sum x;
-    for (int i = threadIdx.x; i < parts; i += kThreads) {
-        const GradPart p = part[i];
-        x.add(p.s);
-        x.c += p.c;
-        x.rest += p.rest;
-    }
-    x = block_sum(x);
+    x = block_sum<T>(x);
     const float s = x.s + x.c;
     if (x.rest == 0. && s <= FLT_MAX) {
         // the root of s, and half of what its square leaves of the sum over itself
@@ -244,10 +244,20 @@ __device__ __forceinline__ Norm norm_of(const GradPart* __restrict__ part, int p
     __syncthreads();
     return all;
 }
+__device__ __forceinline__ Sum parts_of(const GradPart* __restrict__ part, int parts) {
+    Sum x;
+    for (int i = threadIdx.x; i < parts; i += kThreads) {
+        const GradPart p = part[i];
+        x.add(p.s);
+        x.c += p.c;
+        x.rest += p.rest;
+    }
+    return x;
+}
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const GradPart* __restrict__ part, int parts, float* norm) {
     await_previous();
-    const Norm x = norm_of(part, parts, 0.f);
+    const Norm x = norm_of<kThreads>(parts_of(part, parts), 0.f);
     if (threadIdx.x == 0) *norm = x.norm;
 }
 
@@ -284,7 +294,7 @@ __device__ __forceinline__ void put_vector(const Tensor& t, int64_t e, const uin
 }
 
 template <int VEC, bool kHalf>
-__device__ __forceinline__ void scale_tile(const Tensor& t, int64_t e, uint64_t by) {
+__device__ __forceinline__ void scale_vectors(const Tensor& t, int64_t e, uint64_t by) {
     constexpr int M = 32 / VEC;
     uint4 v[M];
 #pragma unroll
@@ -301,15 +311,28 @@ __device__ __forceinline__ void scale_tile(const Tensor& t, int64_t e, uint64_t 
 
 // Where the output's boundaries are not the input's: neighbouring threads take neighbouring
 // elements.
-__device__ __forceinline__ void scale_tile_apart(const Tensor& t, int64_t e, float by) {
+__device__ __forceinline__ void scale_apart(const Tensor& t, int64_t e, float by) {
 #pragma unroll 8
     for (int j = 0; j < 32; ++j) {
-        const int64_t at = e + threadIdx.x + j * kThreads;
+        const int64_t at = e + j * kThreads;
         if (at < 0 || at >= t.n) continue;
         const float x = at1(t.p, at, t.in16) * by;
         if (t.out16) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(x);
         else ((float*)t.out)[at] = x;
     }
+}
+
+// A tile times `by`, by kThreads threads.
+__device__ __forceinline__ void scale_tile(const Tensor& t, uint32_t tile, int thread, float by) {
+    if (by == 1.f && t.out == t.p) return;
+    const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
+    const int vec = t.in16 ? 8 : 4;
+    const bool whole = ((uintptr_t)t.out - (uintptr_t)t.lead * (t.out16 ? 2 : 4)) % (t.out16 ? 2 * vec : 16) == 0;
+    if (!whole) scale_apart(t, e + thread, by);
+    else if (t.in16 && t.out16) scale_vectors<8, true>(t, e + thread * 8, twice(by));
+    else if (t.in16) scale_vectors<8, false>(t, e + thread * 8, twice(by));
+    else if (t.out16) scale_vectors<4, true>(t, e + thread * 4, twice(by));
+    else scale_vectors<4, false>(t, e + thread * 4, twice(by));
 }
 
 // in_place: every tensor is its own output.
@@ -318,26 +341,60 @@ __global__ void __launch_bounds__(kThreads, kScalePerSm)
 grad_scale_kernel(const __grid_constant__ List<N> l, const GradPart* __restrict__ part, int parts, float max_norm,
                   float* norm, bool in_place) {
     uint32_t from, tile;
-    run_of(l.tiles, from, tile);
+    run_of(l.tiles, blockIdx.x, gridDim.x, from, tile);
     int i = 0;
     Tensor t;
     if (from < tile) t.at(l, i = find(l, tile - 1));
     await_previous();
-    const Norm x = norm_of(part, parts, max_norm);
+    const Norm x = norm_of<kThreads>(parts_of(part, parts), max_norm);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
     const float by = x.by;
     if ((in_place && by == 1.f) || from >= tile) return;
     while (tile-- > from) {
         while (tile < t.first) t.at(l, --i);
-        const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
-        if (by == 1.f && t.out == t.p) continue;
-        const int vec = t.in16 ? 8 : 4;
-        const bool whole = ((uintptr_t)t.out - (uintptr_t)t.lead * (t.out16 ? 2 : 4)) % (t.out16 ? 2 * vec : 16) == 0;
-        if (!whole) scale_tile_apart(t, e, by);
-        else if (t.in16 && t.out16) scale_tile<8, true>(t, e + threadIdx.x * 8, twice(by));
-        else if (t.in16) scale_tile<8, false>(t, e + threadIdx.x * 8, twice(by));
-        else if (t.out16) scale_tile<4, true>(t, e + threadIdx.x * 4, twice(by));
-        else scale_tile<4, false>(t, e + threadIdx.x * 4, twice(by));
+        scale_tile(t, tile, threadIdx.x, by);
+    }
+}
+
+// Both passes of a few tiles in one launch: the blocks of one cluster, kWorkers workers of
+// kThreads threads each, hand their sums around through shared memory, and the second pass reads
+// what the first left in L2.  Without `clip` the norm alone.
+constexpr int kWorkers = 3;
+template <int N>
+__global__ void __launch_bounds__(kThreads * kWorkers, 1)
+grad_clip_kernel(const __grid_constant__ List<N> l, float max_norm, float* norm, bool clip) {
+    __shared__ GradPart mine;
+    const uint32_t worker = blockIdx.x * kWorkers + threadIdx.x / kThreads;
+    const int thread = threadIdx.x % kThreads;
+    uint32_t from, to;
+    run_of(l.tiles, worker, gridDim.x * kWorkers, from, to);
+    Sum sum;
+    int i = 0;
+    Tensor t;
+    if (from < to) t.at(l, i = find(l, from));
+    await_previous();
+    for (uint32_t tile = from; tile < to; ++tile) {
+        while (tile >= t.end) t.at(l, ++i);
+        square_tile(t, tile, thread, sum);
+    }
+    sum = block_sum<kThreads * kWorkers>(sum);
+    if (threadIdx.x == 0) mine = {sum.s, sum.c, sum.rest};
+    cluster_sync();
+    Sum all;
+    if (threadIdx.x < gridDim.x) {
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = cluster_word((const float*)&mine + k, threadIdx.x);
+        all.s = w[0], all.c = w[1];
+        all.rest = __hiloint2double(__float_as_int(w[3]), __float_as_int(w[2]));
+    }
+    cluster_sync();  // no block leaves before the others have read its sum
+    const Norm x = norm_of<kThreads * kWorkers>(all, max_norm);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
+    if (!clip) return;
+    for (uint32_t tile = to; tile-- > from;) {
+        while (tile < t.first) t.at(l, --i);
+        scale_tile(t, tile, thread, x.by);
     }
 }
 
@@ -380,6 +437,19 @@ cudaError_t scale(const gdn_grad* g, int64_t a, int64_t b, const GradPart* part,
                             max_norm, norm, in_place);
 }
 
+template <int N>
+cudaError_t cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm, float* norm, bool clip, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    List<N> l;
+    fill(l, g, 0, count);
+    return launch_one_cluster(grad_clip_kernel<N>, blocks, kThreads * kWorkers, 0, done, st, l, max_norm, norm, clip);
+}
+
+// Tiles that one cluster takes, to clip them or for their norm alone: a call of bf16 clips 1 to
+// 48 tiles in 5.0 to 6.3 us, 96 in 8.0, in two launches 6.9 to 7.2 any of them; the norm
+// of 144 takes 6.5 us either way, of 48 5.2 and 6.4.
+constexpr int64_t kClusterTiles = 48, kClusterNormTiles = 144;
+
 }  // namespace
 
 int64_t grad_tiles(int64_t n) { return n / kTile + 2; }
@@ -387,6 +457,21 @@ int64_t grad_tiles(int64_t n) { return n / kTile + 2; }
 size_t grad_parts(int64_t count) {
     const int64_t launches = count <= kMany ? 1 : (count + kMany - 1) / kMany;
     return (size_t)launches * kSumPerSm * sm_count();
+}
+
+int grad_cluster(const gdn_grad* g, int64_t count, bool clip) {
+    if (count > kFew) return 0;
+    int64_t tiles = 0;
+    for (int64_t i = 0; i < count; ++i) tiles += (g[i].n + kTile - 1) / kTile;
+    if (tiles > (clip ? kClusterTiles : kClusterNormTiles)) return 0;
+    int blocks = 1;
+    while (blocks < kMostCluster && blocks * kWorkers < tiles) blocks *= 2;
+    return blocks;
+}
+
+cudaError_t launch_grad_cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm, float* norm, bool clip,
+                                cudaStream_t st) {
+    return cluster<kFew>(g, count, blocks, max_norm, norm, clip, st);
 }
 
 cudaError_t launch_grad_sums(const gdn_grad* g, int64_t count, GradPart* part, int* parts, cudaStream_t st) {

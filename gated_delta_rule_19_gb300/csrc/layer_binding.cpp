@@ -39,7 +39,8 @@ struct Api {
     F(gdn_gated_norm_bwd_workspace_bytes) F(gdn_gated_norm_bwd)
 // The block's, which a library of the layer alone lacks: their calls then raise.
 #define GDN_BLOCK_CALLS(F)                                                                                      \
-    F(gdn_qk_norm_rope_axes_fwd) F(gdn_qk_norm_rope_axes_bwd) F(gdn_add_norm_fwd) F(gdn_add_norm_quant)          \
+    F(gdn_qk_norm_rope_axes_fwd) F(gdn_qk_norm_rope_axes_bwd_workspace_bytes) F(gdn_qk_norm_rope_axes_bwd)      \
+    F(gdn_add_norm_fwd) F(gdn_add_norm_quant)                                                                   \
     F(gdn_add_norm_bwd_workspace_bytes) F(gdn_add_norm_bwd) F(gdn_grad_workspace_bytes) F(gdn_grad_norm)         \
     F(gdn_clip_grads) F(gdn_state_store) F(gdn_state_load)
 #define GDN_FIELD(name) decltype(&::name) name = nullptr;
@@ -535,7 +536,7 @@ PyObject* rope_axes_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          dk = output(a[14], "dk", c.ks, c.like.type, c.like),
                          dwq = output(a[15], "dq_weight", width, c.like.type, c.like),
                          dwk = output(a[16], "dk_weight", width, c.like.type, c.like);
-        const Workspace ws(a[17], c.like, [&] { return api.gdn_qk_norm_rope_bwd_workspace_bytes(&c.p.rope); });
+        const Workspace ws(a[17], c.like, [&] { return api.gdn_qk_norm_rope_axes_bwd_workspace_bytes(&c.p); });
         done(api.gdn_qk_norm_rope_axes_bwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions,
                                            dqo, dko, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(),
                                            ws.at, ws.bytes, stream.raw));
@@ -731,7 +732,7 @@ PyObject* grads_call(PyObject* tensors, PyObject* out, const float* max_norm, Py
     const OnStream stream(on, *g.like);
     const at::Tensor to = norm_output(norm, g);
     const int64_t count = (int64_t)g.list.size();
-    const Workspace ws(workspace, *g.like, [&] { return api.gdn_grad_workspace_bytes(count); });
+    const Workspace ws(workspace, *g.like, [&] { return api.gdn_grad_workspace_bytes(g.list.data(), count); });
     done(max_norm ? api.gdn_clip_grads(g.list.data(), count, *max_norm, to.data_ptr<float>(), ws.at, ws.bytes, stream.raw)
                   : api.gdn_grad_norm(g.list.data(), count, to.data_ptr<float>(), ws.at, ws.bytes, stream.raw));
     for (const at::Tensor* t : g.written) changed(*t);

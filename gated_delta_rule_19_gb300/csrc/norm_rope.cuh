@@ -37,6 +37,7 @@ struct Side {
     const T* w;   // [D]
     const T* dy;  // backward: [tokens, H, D]
     T* out;       // y or dx, [tokens, H, D]
+    T* dw;        // backward in one cluster (kAxes > 0): the weight's gradient; else NULL
     int64_t stride;
     int H, blocks, per;
 };
@@ -372,7 +373,8 @@ qk_norm_rope_fwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab) {
 }
 
 // Walks the queries' items, then the keys', and leaves one row of column sums per block
-// and side in part [2][gridDim.x][D].
+// and side in part [2][gridDim.x][D]; the blocks of a cluster add theirs up themselves, in the
+// order of the blocks as the sum behind this kernel does.
 template <typename T, int G, bool kInter, int kAxes>
 __global__ void __launch_bounds__(kThreads, kRopeBwdPerSm)
 qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __restrict__ part) {
@@ -462,8 +464,23 @@ qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __r
             }
             ring.wait_all();  // the ring's memory serves the sums next
         }
-        block_columns<G, VEC>(acc, sl.c0, sl.c1, sl.live, d.D, (float*)sm,
-                              part + ((int64_t)side * gridDim.x + blockIdx.x) * d.D);
+        float* to = part + ((int64_t)side * gridDim.x + blockIdx.x) * d.D;
+        if constexpr (kAxes > 0) {
+            __shared__ float mine[256];
+            if (sd.dw) to = mine;
+            block_columns<G, VEC>(acc, sl.c0, sl.c1, sl.live, d.D, (float*)sm, to);
+            if (sd.dw) {
+                cluster_sync();
+                for (int col = blockIdx.x * kThreads + threadIdx.x; col < d.D; col += gridDim.x * kThreads) {
+                    float sum = 0.f;
+                    for (uint32_t b = 0; b < gridDim.x; ++b) sum += cluster_word(mine + col, b);
+                    store1(sd.dw + col, sum);
+                }
+                cluster_sync();  // no block takes its sums back, or leaves, before the others have read them
+            }
+        } else {
+            block_columns<G, VEC>(acc, sl.c0, sl.c1, sl.live, d.D, (float*)sm, to);
+        }
     }
 }
 
@@ -482,7 +499,8 @@ cudaError_t launch_k(const RopeDims& d, bool bwd, const Side<T>& q, const Side<T
         auto kern = qk_norm_rope_bwd_kernel<T, G, kInter, kAxes>;
         constexpr int smem = BwdRing<T>::BYTES;
         static_assert(smem >= (kThreads / 32) * 256 * 4, "the column sums fit the ring");
-        static std::atomic<uint64_t> done{0};
+        static std::atomic<uint64_t> done{0}, done1{0};
+        if (kAxes > 0 && q.dw) return launch_one_cluster(kern, blocks, kThreads, smem, done1, st, d, q, k, tab, part);
         cudaError_t e = allow_smem(kern, smem, done);
         if (e != cudaSuccess) return e;
         return launch_dependent(kern, dim3((unsigned)blocks), kThreads, smem, st, d, q, k, tab, part);
@@ -501,11 +519,11 @@ cudaError_t launch_t(const RopeCall& c, bool bwd, cudaStream_t st) {
     RopeDims d{c.tokens, c.T, c.D, c.R, c.rows, c.eps};
     const Tables tab{c.cos, c.sin, c.pos, c.axes, c.map};
     const int nh = bwd ? kBwdHeads : kFwdHeads;
-    auto side = [&](const void* x, const void* w, const void* dy, void* out, int64_t stride, int H) {
+    auto side = [&](const void* x, const void* w, const void* dy, void* out, void* dw, int64_t stride, int H) {
         const int blocks = (H + nh - 1) / nh;
-        return Side<T>{(const T*)x, (const T*)w, (const T*)dy, (T*)out, stride, H, blocks, blocks ? (H + blocks - 1) / blocks : 0};
+        return Side<T>{(const T*)x, (const T*)w, (const T*)dy, (T*)out, (T*)dw, stride, H, blocks, blocks ? (H + blocks - 1) / blocks : 0};
     };
-    const Side<T> q = side(c.q, c.wq, c.dqo, c.qo, c.q_stride, c.Hq), k = side(c.k, c.wk, c.dko, c.ko, c.k_stride, c.Hk);
+    const Side<T> q = side(c.q, c.wq, c.dqo, c.qo, c.dwq, c.q_stride, c.Hq), k = side(c.k, c.wk, c.dko, c.ko, c.dwk, c.k_stride, c.Hk);
     switch (lanes_for(c.D, kVec<T>)) {
         case 1: return launch_g<T, 1, kAxes>(d, c.interleaved, bwd, q, k, tab, c.part, c.blocks, st);
         case 2: return launch_g<T, 2, kAxes>(d, c.interleaved, bwd, q, k, tab, c.part, c.blocks, st);

@@ -140,6 +140,9 @@ template <typename T>
 __device__ __forceinline__ void sts16(T* p, const uint4& x) {
     __stcs(reinterpret_cast<uint4*>(p), x);
 }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
 // Sum over aligned groups of G lanes.
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {

@@ -151,8 +151,9 @@ def load_library():
                      ("gdn_state_store", [PS] + [_vp] * 5), ("gdn_state_load", [PS] + [_vp] * 5)):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = ctypes.c_int
-    for fn, arg in (("gdn_add_norm_bwd_workspace_bytes", PN), ("gdn_grad_workspace_bytes", i64)):
-        getattr(lib, fn).argtypes = [arg]
+    for fn, args in (("gdn_add_norm_bwd_workspace_bytes", [PN]), ("gdn_qk_norm_rope_axes_bwd_workspace_bytes", [PA]),
+                     ("gdn_grad_workspace_bytes", [ctypes.POINTER(gdn_grad), i64])):
+        getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = size
     lib.gdn_count_nonfinite.argtypes = [_vp, ctypes.c_int64, ctypes.c_int, _vp, _vp]
     lib.gdn_count_nonfinite.restype = ctypes.c_int
@@ -186,7 +187,8 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_last_error", "gdn_fwd_works
             "gdn_la_bwd_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode",
             "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_bytes", "gdn_qk_norm_rope_bwd",
             "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd",
-            "gdn_qk_norm_rope_axes_fwd", "gdn_qk_norm_rope_axes_bwd", "gdn_add_norm_fwd", "gdn_add_norm_quant",
+            "gdn_qk_norm_rope_axes_fwd", "gdn_qk_norm_rope_axes_bwd_workspace_bytes",
+            "gdn_qk_norm_rope_axes_bwd", "gdn_add_norm_fwd", "gdn_add_norm_quant",
             "gdn_add_norm_bwd_workspace_bytes", "gdn_add_norm_bwd", "gdn_grad_workspace_bytes", "gdn_grad_norm",
             "gdn_clip_grads", "gdn_state_store", "gdn_state_load")
 

@@ -536,11 +536,11 @@ typedef struct {
  *   positions  int32 [axes,B,T], required (unless R = 0).  A position outside the tables
  *              makes the elements of its axis's pairs NaN, and in the backward the
  *              token's whole gradient rows.
- * The workspace is that of gdn_qk_norm_rope_bwd for p->rope.
  */
 gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                                      const int32_t* positions, void* q_out, void* k_out, void* stream);
+size_t gdn_qk_norm_rope_axes_bwd_workspace_bytes(const gdn_rope_axes_problem* p);
 gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                                      const int32_t* positions, const void* dq_out, const void* dk_out, void* dq,
@@ -616,10 +616,10 @@ typedef struct {
  * sees it in *norm.  max_norm >= 0, infinity: no limit.  Outputs overlap neither each other
  * nor a gradient other than their own.
  *   norm       required by gdn_grad_norm; NULL: not kept.
- *   workspace  gdn_grad_workspace_bytes(count) bytes, 16-byte aligned; calls in flight at
- *              the same time need one each.
+ *   workspace  gdn_grad_workspace_bytes(grads, count) bytes (0 for a few tensors), 16-byte
+ *              aligned; calls in flight at the same time need one each.
  */
-size_t gdn_grad_workspace_bytes(int64_t count);
+size_t gdn_grad_workspace_bytes(const gdn_grad* grads, int64_t count);
 gdn_status gdn_grad_norm(const gdn_grad* grads, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
                          void* stream);
 gdn_status gdn_clip_grads(const gdn_grad* grads, int64_t count, float max_norm, float* norm, void* workspace,

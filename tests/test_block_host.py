@@ -32,7 +32,7 @@ ROPE_FWD = ("q", "k", "q_weight", "k_weight", "cos", "sin", "positions", "q_out"
 ROPE_BWD = ROPE_FWD[:7] + ("dq_out", "dk_out", "dq", "dk", "dq_weight", "dk_weight", "workspace")
 
 
-def _axes(lib, sections=(8, 12, 12), alternating=0, axes=None, B=2, T=10, D=128, R=64, rows=10, dtype=1):
+def _axes(lib, sections=(8, 12, 12), alternating=0, axes=None, B=2, T=1000, D=128, R=64, rows=1000, dtype=1):
     rope = lib.gdn_rope_problem(B, T, 4, 2, D, R, rows, 0, 0, 1e-6, 0, dtype)
     return lib.gdn_rope_axes_problem(rope, len(sections) if axes is None else axes, alternating,
                                      (ctypes.c_int32 * 4)(*sections[:4]))
@@ -59,6 +59,9 @@ def test_axes_refused(lib):
     assert both(ok, positions=FAKE + 2) == {INVALID}
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", ok, ROPE_FWD, k_out=FAKE + 16) == INVALID
     assert _call(lib, "gdn_qk_norm_rope_axes_bwd", ok, ROPE_BWD, sized=16) == WS
+    need = lib.load_library().gdn_qk_norm_rope_axes_bwd_workspace_bytes
+    assert need(ctypes.byref(ok)) > 0 and need(ctypes.byref(_axes(lib, T=10))) == 0  # few tokens: one cluster
+    assert need(ctypes.byref(_axes(lib, axes=5))) == 0
     assert lib.load_library().gdn_qk_norm_rope_axes_fwd(None, *[None] * 10) == INVALID
     # nothing to do: nothing is needed
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", _axes(lib, T=0), ROPE_FWD, q=None, k=None, positions=None, q_out=None,
@@ -72,7 +75,7 @@ QUANT = ("x", "residual", "weight", "h", "y", "scales")
 BWD = ("h", "weight", "dy", "dh", "dx", "d_residual", "dweight", "workspace")
 
 
-def _norm(lib, rows=100, D=512, sx=0, ss=0, eps=1e-6, dtype=1, stream=1):
+def _norm(lib, rows=10000, D=512, sx=0, ss=0, eps=1e-6, dtype=1, stream=1):
     return lib.gdn_add_norm_problem(rows, D, sx, ss, eps, dtype, stream)
 
 
@@ -107,6 +110,8 @@ def test_add_norm_problems_refused(lib):
         assert "group" in lib.gdn_last_error()
     assert _quant(lib, _norm(lib, D=1000), 64) == UNSUP  # does not divide
     assert _bwd(lib, _norm(lib), sized=64) == WS
+    need = lib.load_library().gdn_add_norm_bwd_workspace_bytes
+    assert need(ctypes.byref(_norm(lib))) > 0 and need(ctypes.byref(_norm(lib, rows=40))) == 0  # few rows: one cluster
 
 
 def test_add_norm_pointers_refused(lib):
@@ -157,7 +162,7 @@ def _length(lib, rows, count=None, norm=FAKE + 90 * GAP, ws=FAKE + 91 * GAP, siz
 
 def test_grads_refused(lib):
     A, B, C = FAKE, FAKE + GAP, FAKE + 2 * GAP
-    ok = (A, A, 1000, 0, 0)
+    ok = (A, A, 1 << 22, 0, 0)  # more than one cluster takes: with a workspace
     for call in (_clip, _length):
         for row, status, word in (((A, A, -1, 0, 0), INVALID, "negative"), ((A, A, (1 << 43) + 1, 0, 0), UNSUP, "2^43"),
                                   ((A, A, 8, 2, 0), UNSUP, "dtype 2"), ((None, None, 8, 0, 0), INVALID, "NULL"),
@@ -178,7 +183,7 @@ def test_grads_refused(lib):
     assert _clip(lib, [(A, B, 8, 0, 5)]) == UNSUP
     # outputs on one another, on another gradient, or on a part of their own
     for rows in ([ok, ok], [(A, C, 1000, 0, 0), (B, C + 3996, 1000, 0, 0)], [(A, B, 1000, 0, 0), (B, C, 1000, 0, 0)],
-                 [(A, A + 16, 1000, 0, 0)], [(A, C, 1000, 0, 1), (B, C + 1998, 1000, 0, 1)],
+                 [(A, A + 16, 1 << 22, 0, 0)], [(A, C, 1000, 0, 1), (B, C + 1998, 1000, 0, 1)],
                  [(A, B, 1 << 20, 1, 1), (C, C, 9, 0, 0), (B + 1024, B + 1024, 4, 1, 1)]):
         assert _clip(lib, rows) == INVALID, rows
         assert "overlaps" in lib.gdn_last_error()
@@ -187,8 +192,9 @@ def test_grads_refused(lib):
         assert "max_norm" in lib.gdn_last_error()
     h = lib.load_library()
     assert h.gdn_clip_grads(None, 3, 1.0, None, None, 0, None) == INVALID
-    assert h.gdn_grad_workspace_bytes(-1) == 0 and h.gdn_grad_workspace_bytes(0) > 0
-    assert h.gdn_grad_workspace_bytes(5000) > h.gdn_grad_workspace_bytes(1)
+    size = lambda *rows, **kw: h.gdn_grad_workspace_bytes(_grads(lib, *rows), kw.get("count", len(rows)))  # noqa: E731
+    assert size(ok, count=-1) == 0 and size() == 0 and h.gdn_grad_workspace_bytes(None, 3) == 0
+    assert size((A, A, 1000, 0, 0)) == 0 and 0 < size(ok) == size(ok, ok) < size(*[ok] * 5000)
 
 
 # -------------------------------------------------------------- state cache

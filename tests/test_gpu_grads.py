@@ -55,6 +55,8 @@ LISTS = {
     "layer": ([(512, 64), (64, 128), (32,), (32,), (32,), (64,)], "bbbbbb"),
     "empty": ([(0,), (5,), (0, 3), (0,), (70000,), (0,)], "bffbbf"),
     "many": ([(1 + 37 * i % 301,) for i in range(64)] + [(40000,)], "bf" * 32 + "b"),
+    "cluster": ([(250000,), (300, 1000), (500000,), (1 << 19,)], "bfbf"),
+    "past the cluster": ([(250000,), (300, 1000), (500000,), (1 << 19,), (8192,)], "bfbfb"),
     "thousands": ([(1 + 7 * i % 13,) for i in range(2500)] + [(9000, 3)], "fb" * 1250 + "f"),
 }
 
@@ -293,7 +295,7 @@ def test_refusals():
                  lambda: gdn.gdn_clip_grads([g], 1.0, out=g), lambda: gdn.gdn_clip_grads([g], float("nan")), lambda: gdn.gdn_grad_norm(g),
                  lambda: gdn.gdn_grad_norm([g], norm=torch.empty(2, device="cuda")), lambda: gdn.gdn_grad_norm([g], norm=torch.empty(1)),
                  lambda: gdn.gdn_grad_norm([g], norm=h[:1]), lambda: gdn.gdn_grad_norm([g], norm=g[5]),
-                 lambda: gdn.gdn_grad_norm([g], workspace=torch.empty(8, device="cuda")),
+                 lambda: gdn.gdn_grad_norm([torch.zeros(1 << 21, device="cuda")], workspace=torch.empty(8, device="cuda")),
                  lambda: gdn.gdn_grad_norm([g.to_sparse()]), lambda: gdn.gdn_grad_norm([g, g.cpu()])):
         with pytest.raises(gdn.GdnError):
             call()

@@ -391,9 +391,12 @@ def test_refusals():
     ok = dict(h=r, weight=w, dy=dy, dh=dh)
     for over in (dict(h=r[:5]), dict(dy=None), dict(dy=dy.float()), dict(dh=dh.float()), dict(dh=dh[:, :8]), dict(weight=None),
                  dict(dy=_inputs(20, 512, "bf16", "bf16", True)[0]), dict(h=r.half()), dict(grads=(r, None, None)),
-                 dict(grads=(None, torch.empty_like(r), None)), dict(workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+                 dict(grads=(None, torch.empty_like(r), None))):
         with pytest.raises(gdn.GdnError):
             gdn.gdn_add_norm_bwd(**{**ok, **over})
+    many = torch.zeros(3000, 512, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(gdn.GdnError, match="workspace"):
+        gdn.gdn_add_norm_bwd(many, w, many, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError):
         gdn.gdn_add_norm_fwd(1, r, w)
     gdn.gdn_add_norm_bwd(**ok)

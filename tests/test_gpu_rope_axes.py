@@ -187,6 +187,8 @@ def test_refusals():
     with pytest.raises(gdn.GdnError):
         gdn.gdn_qk_norm_rope_axes_bwd(**ok, dq_out=dqo, dk_out=None)
     with pytest.raises(gdn.GdnError):
-        gdn.gdn_qk_norm_rope_axes_bwd(**ok, dq_out=dqo, dk_out=dko, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        many = dict(zip(("q", "k", "q_weight", "k_weight", "cos", "sin", "positions", "dq_out", "dk_out"),
+                        _inputs(2, 500, 4, 2, 64, 32, "bf16", False, 3)))
+        gdn.gdn_qk_norm_rope_axes_bwd(**many, sections=(6, 5, 5), workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     gdn.gdn_qk_norm_rope_axes_fwd(**ok)
     torch.cuda.synchronize()
