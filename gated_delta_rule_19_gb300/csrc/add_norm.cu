@@ -551,11 +551,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         for (int c = threadIdx.x; c < d.D; c += N) sums[(int64_t)blockIdx.x * d.D + c] = col[c];
     } else {
         cluster_sync();
-        for (int c = blockIdx.x * N + threadIdx.x; c < d.D; c += gridDim.x * N) {
-            float s = 0.f;
-            for (uint32_t b = 0; b < gridDim.x; ++b) s += cluster_word(col + c, b);
-            store1(dw + c, s);
-        }
+        for (int c = blockIdx.x * N + threadIdx.x; c < d.D; c += gridDim.x * N) store1(dw + c, cluster_sum(col + c));
         cluster_sync();  // no block leaves before the others have read its sums
     }
 }

@@ -1953,9 +1953,20 @@ gdn_status gated_problem(const gdn_gated_norm_problem* p, gdn::GatedCall* c) {
 
 extern "C" {
 
+// Whether the blocks of a backward are one cluster, which needs neither memory for its sums nor
+// the launch that adds them up (several axes; the calls of one position keep their two launches).
+static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && c.blocks <= gdn::kMostCluster; }
+
+// Room for the tokens' gathered angles, where a call of several axes gathers them.
+static size_t rope_gathered(const gdn_rope_problem* p, const gdn::RopeCall& c) {
+    if (!c.axes || c.R == 0 || c.tokens > INT32_MAX || c.tokens * (c.Hq + c.Hk) < gdn::kRopeGatherRows) return 0;
+    return gdn::rope_whole_units(c, elem_type(p->dtype)) ? 0 : (size_t)c.tokens * c.R * sizeof(float);
+}
+
 static gdn_status rope_fwd(const gdn_rope_problem* p, gdn::RopeCall& c, const void* q, const void* k,
                            const void* q_weight, const void* k_weight, const float* cos, const float* sin,
-                           const int32_t* positions, void* q_out, void* k_out, void* stream) {
+                           const int32_t* positions, void* q_out, void* k_out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
     gdn_status st = rope_problem(p, &c);
     if (st != GDN_OK) return st;
     const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
@@ -1966,12 +1977,17 @@ static gdn_status rope_fwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
                         {k_weight, p->D * es, "k_weight"},
                         {cos, table, "cos"},
                         {sin, table, "sin"}};
-    const Span outs[] = {{q_out, (size_t)c.tokens * wq * es, "q_out"}, {k_out, (size_t)c.tokens * wk * es, "k_out"}};
-    if ((st = check_spans(ins, 6, 1u << 4 | 1u << 5, outs, 2, 0, nullptr, nullptr)) != GDN_OK) return st;
+    const size_t need = rope_gathered(p, c);
+    const Span outs[] = {{q_out, (size_t)c.tokens * wq * es, "q_out"},
+                         {k_out, (size_t)c.tokens * wk * es, "k_out"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_spans(ins, 6, 1u << 4 | 1u << 5, outs, need ? 3 : 2, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     if (c.tokens == 0 || p->Hq + p->Hk == 0) return GDN_OK;
     if ((st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
     c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
-    c.qo = q_out, c.ko = k_out;
+    c.qo = q_out, c.ko = k_out, c.gathered = need ? (float*)workspace : nullptr;
     cudaStream_t cs = (cudaStream_t)stream;
     const gdn::InType ty = elem_type(p->dtype);
     cudaError_t e = timed(c.axes ? gdn::KID_NORM_AXES_FWD : gdn::KID_NORM_ROPE_FWD, cs, [&] {
@@ -1985,12 +2001,8 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
                                 void* q_out, void* k_out, void* stream) {
     g_err[0] = 0;
     gdn::RopeCall c{};
-    return rope_fwd(p, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream);
+    return rope_fwd(p, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, nullptr, 0, stream);
 }
-
-// Whether the blocks of a backward are one cluster, which needs neither memory for its sums nor
-// the launch that adds them up (several axes; the calls of one position keep their two launches).
-static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && c.blocks <= gdn::kMostCluster; }
 
 size_t gdn_qk_norm_rope_bwd_workspace_bytes(const gdn_rope_problem* p) {
     gdn::RopeCall c{};
@@ -2005,7 +2017,7 @@ static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
     if (st != GDN_OK) return st;
     const size_t es = elem_size(p->dtype), table = (size_t)p->table_rows * (p->R / 2) * sizeof(float);
     const bool cluster = rope_cluster(c);
-    const size_t need = cluster ? 0 : gdn_qk_norm_rope_bwd_workspace_bytes(p);
+    const size_t angles = rope_gathered(p, c), need = angles + (cluster ? 0 : gdn_qk_norm_rope_bwd_workspace_bytes(p));
     const int64_t wq = p->Hq * p->D, wk = p->Hk * p->D;
     const size_t nq = (size_t)c.tokens * wq * es, nk = (size_t)c.tokens * wk * es;
     const Span ins[] = {{q, row_span(c.tokens, c.q_stride, wq, p->dtype), "q"},
@@ -2026,7 +2038,8 @@ static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     if (c.tokens && (st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
     c.q = q, c.k = k, c.wq = q_weight, c.wk = k_weight, c.cos = cos, c.sin = sin, c.pos = positions;
-    c.qo = dq, c.ko = dk, c.dqo = dq_out, c.dko = dk_out, c.part = (float*)workspace;
+    c.qo = dq, c.ko = dk, c.dqo = dq_out, c.dko = dk_out;
+    c.part = (float*)((char*)workspace + angles), c.gathered = angles ? (float*)workspace : nullptr;
     if (cluster) c.dwq = dq_weight, c.dwk = dk_weight;
     cudaStream_t cs = (cudaStream_t)stream;
     const gdn::InType ty = elem_type(p->dtype);
@@ -2327,17 +2340,25 @@ extern "C" {
 
 gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
-                                     const int32_t* positions, void* q_out, void* k_out, void* stream) {
+                                     const int32_t* positions, void* q_out, void* k_out, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
     g_err[0] = 0;
     gdn::RopeCall c{};
     const gdn_status st = axes_map(p, positions, &c);
-    return st == GDN_OK ? rope_fwd(&p->rope, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, stream) : st;
+    return st == GDN_OK ? rope_fwd(&p->rope, c, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out, workspace,
+                                   workspace_bytes, stream)
+                        : st;
+}
+
+size_t gdn_qk_norm_rope_axes_fwd_workspace_bytes(const gdn_rope_axes_problem* p) {
+    gdn::RopeCall c{};
+    return axes_map(p, nullptr, &c, false) == GDN_OK && rope_problem(&p->rope, &c) == GDN_OK ? rope_gathered(&p->rope, c) : 0;
 }
 
 size_t gdn_qk_norm_rope_axes_bwd_workspace_bytes(const gdn_rope_axes_problem* p) {
     gdn::RopeCall c{};
-    if (axes_map(p, nullptr, &c, false) != GDN_OK || rope_problem(&p->rope, &c) != GDN_OK || rope_cluster(c)) return 0;
-    return gdn_qk_norm_rope_bwd_workspace_bytes(&p->rope);
+    if (axes_map(p, nullptr, &c, false) != GDN_OK || rope_problem(&p->rope, &c) != GDN_OK) return 0;
+    return rope_gathered(&p->rope, c) + (rope_cluster(c) ? 0 : gdn_qk_norm_rope_bwd_workspace_bytes(&p->rope));
 }
 
 gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,

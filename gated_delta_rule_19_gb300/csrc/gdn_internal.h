@@ -380,6 +380,11 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
 // The kernels before this one in the stream are complete, and what they wrote is visible.
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+#endif
+// Blocks of the largest cluster (above 8 a kernel has to be allowed it).
+constexpr int kMostCluster = 16;
+
+#ifdef __CUDACC__
 // A cluster's blocks: all threads have arrived, and see what the others' blocks wrote in
 // shared memory; a word of rank's.
 __device__ __forceinline__ void cluster_sync() {
@@ -392,9 +397,17 @@ __device__ __forceinline__ float cluster_word(const float* mine, uint32_t rank) 
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
     return x;
 }
+// The same word of the grid's blocks, all of one cluster, added up in their order; the loads
+// are in flight together.
+__device__ __forceinline__ float cluster_sum(const float* mine) {
+    float w[kMostCluster], s = 0.f;
+#pragma unroll
+    for (int b = 0; b < kMostCluster; ++b) w[b] = b < (int)gridDim.x ? cluster_word(mine, b) : 0.f;
+#pragma unroll
+    for (int b = 0; b < kMostCluster; ++b) s += w[b];
+    return s;
+}
 #endif
-// Blocks of the largest cluster (above 8 a kernel has to be allowed it).
-constexpr int kMostCluster = 16;
 
 // Launches a kernel that may start while the one before it in the stream drains (a call
 // of one kernel takes 1.6 us less behind another one): it calls await_previous() before it
@@ -475,14 +488,23 @@ struct RopeCall {
     const void *dqo = nullptr, *dko = nullptr;
     float* part = nullptr;
     int blocks = 0;
-    // launch_qk_norm_rope_axes: pos is [axes][tokens]; in a backward whose blocks are one
-    // cluster the weights' gradients (part is not used then)
+    // launch_qk_norm_rope_axes: pos is [axes][tokens]; room for the tokens' gathered angles
+    // [2][tokens][R / 2], or NULL; in a backward whose blocks are one cluster the weights'
+    // gradients (part is not used then)
     int axes = 0;
     AxesMap map = {};
+    float* gathered = nullptr;
     void *dwq = nullptr, *dwk = nullptr;
 };
 cudaError_t launch_qk_norm_rope(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
 cudaError_t launch_qk_norm_rope_axes(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
+cudaError_t launch_qk_norm_rope_apart(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
+bool rope_whole_units(const RopeCall& c, InType ty);
+// Rows of queries and keys from which on angles that have to be copied one by one are gathered
+// in front (rows of 128, forward and backward, us a call one by one and gathered: 16384 of bf16
+// 5.7 + 15.2 and 6.9 + 13.5, 32768 9.1 + 15.6 and 8.4 + 14.4, 65536 13.8 + 23.0 and 11.9 + 19.2; of
+// float32 5.8 + 11.0 and 7.1 + 11.9, 8.5 + 14.5 and 9.1 + 14.7, 15.0 + 20.5 and 14.5 + 19.7).
+constexpr int64_t kRopeGatherRows = 32768;
 
 // RMS norm of x times silu(z); backward: part [blocks][D].
 struct GatedCall {

@@ -39,7 +39,8 @@ struct Api {
     F(gdn_gated_norm_bwd_workspace_bytes) F(gdn_gated_norm_bwd)
 // The block's, which a library of the layer alone lacks: their calls then raise.
 #define GDN_BLOCK_CALLS(F)                                                                                      \
-    F(gdn_qk_norm_rope_axes_fwd) F(gdn_qk_norm_rope_axes_bwd_workspace_bytes) F(gdn_qk_norm_rope_axes_bwd)      \
+    F(gdn_qk_norm_rope_axes_fwd_workspace_bytes) F(gdn_qk_norm_rope_axes_fwd)                                    \
+    F(gdn_qk_norm_rope_axes_bwd_workspace_bytes) F(gdn_qk_norm_rope_axes_bwd)                                    \
     F(gdn_add_norm_fwd) F(gdn_add_norm_quant)                                                                   \
     F(gdn_add_norm_bwd_workspace_bytes) F(gdn_add_norm_bwd) F(gdn_grad_workspace_bytes) F(gdn_grad_norm)         \
     F(gdn_clip_grads) F(gdn_state_store) F(gdn_state_load)
@@ -510,15 +511,16 @@ bool have_block() {
 }
 
 // q, k, q_weight, k_weight, cos, sin, positions, sections, eps, interleaved, alternating, q_out,
-// k_out, stream
+// k_out, workspace, stream
 PyObject* rope_axes_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return !have_block() ? nullptr : call(n, 14, [&] {
+    return !have_block() ? nullptr : call(n, 15, [&] {
         RopeAxes c(a, a[8], a[9], a[10]);
-        const OnStream stream(a[13], c.like);
+        const OnStream stream(a[14], c.like);
         const at::Tensor qo = output(a[11], "q_out", c.q.sizes(), c.like.type, c.like),
                          ko = output(a[12], "k_out", c.ks, c.like.type, c.like);
+        const Workspace ws(a[13], c.like, [&] { return api.gdn_qk_norm_rope_axes_fwd_workspace_bytes(&c.p); });
         done(api.gdn_qk_norm_rope_axes_fwd(&c.p, c.q.data_ptr(), c.k.data_ptr(), c.wq, c.wk, c.cos, c.sin, c.positions,
-                                           qo.data_ptr(), ko.data_ptr(), stream.raw));
+                                           qo.data_ptr(), ko.data_ptr(), ws.at, ws.bytes, stream.raw));
         return results(qo, ko);
     });
 }

@@ -15,10 +15,11 @@
 //
 // With several axes a token has a position on each of up to four, and every pair takes its
 // angle from the tables' row of one of them.  The calls of one position (norm_rope.cu,
-// kAxes 0) and of several (norm_rope_axes.cu) are compiled apart, and those in two forms:
-// where every unit of angles that lie together and are copied together belongs to one axis
-// (kAxes 1), a lane keeps the positions of its two units' axes; else (kAxes 2) those of all
-// axes.
+// kAxes 0) and of several (norm_rope_axes.cu) are compiled apart, and those in three forms.
+// Where every unit of angles that lie together and are copied together belongs to one axis
+// (kAxes 1), a lane keeps the positions of its two units' axes.  Else a lane of a few tokens'
+// calls keeps those of all axes and copies angle by angle (kAxes 2), and for many tokens a
+// kernel in front gathers each token's angles, once for all of its heads (kAxes 3).
 #pragma once
 
 #include "gdn_internal.h"
@@ -84,6 +85,13 @@ struct Where {
     int pos = 0;
     __device__ __forceinline__ Where(const RopeDims&, const Tables&, int, bool) {}
     __device__ __forceinline__ void move(const RopeDims& d, const Tables& t, int64_t tok) { pos = position(d, t, tok); }
+};
+// Gathered angles: the token's own row.
+template <int VEC, bool kInter>
+struct Where<VEC, kInter, 3> {
+    int pos = 0;
+    __device__ __forceinline__ Where(const RopeDims&, const Tables&, int, bool) {}
+    __device__ __forceinline__ void move(const RopeDims&, const Tables&, int64_t tok) { pos = (int)tok; }
 };
 // The rows of the lane's units.
 template <int VEC, bool kInter>
@@ -196,9 +204,10 @@ __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, con
 // position outside the tables gives NaN, so that the token's rows show it.  In the
 // first order pair j is elements j of the two pieces; interleaved, the pairs of the
 // first piece come first, then those of the second, a quarter of the row behind.
-template <int VEC, bool kInter, typename R>
+template <int VEC, bool kInter, typename R, int A>
 __device__ __forceinline__ void copy_angles(const R& ring, int slot, int p0, const RopeDims& d, const Tables& t,
-                                            const Where<VEC, kInter, 0>& at, int u, bool turns) {
+                                            const Where<VEC, kInter, A>& at, int u, bool turns) {
+    static_assert(A == 0 || A == 3, "one row for all pairs");
     if (!turns) return;
     const int pos = at.pos;
     if (pos < 0 || pos >= d.rows) {
@@ -471,11 +480,8 @@ qk_norm_rope_bwd_kernel(RopeDims d, Side<T> q, Side<T> k, Tables tab, float* __r
             block_columns<G, VEC>(acc, sl.c0, sl.c1, sl.live, d.D, (float*)sm, to);
             if (sd.dw) {
                 cluster_sync();
-                for (int col = blockIdx.x * kThreads + threadIdx.x; col < d.D; col += gridDim.x * kThreads) {
-                    float sum = 0.f;
-                    for (uint32_t b = 0; b < gridDim.x; ++b) sum += cluster_word(mine + col, b);
-                    store1(sd.dw + col, sum);
-                }
+                for (int col = blockIdx.x * kThreads + threadIdx.x; col < d.D; col += gridDim.x * kThreads)
+                    store1(sd.dw + col, cluster_sum(mine + col));
                 cluster_sync();  // no block takes its sums back, or leaves, before the others have read them
             }
         } else {

@@ -142,7 +142,7 @@ def load_library():
         getattr(lib, fn).restype = ctypes.c_size_t
     PA, PN, PS = (ctypes.POINTER(t) for t in (gdn_rope_axes_problem, gdn_add_norm_problem, gdn_state_cache_problem))
     i64, f32, size = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-    for fn, args in (("gdn_qk_norm_rope_axes_fwd", [PA] + [_vp] * 10),
+    for fn, args in (("gdn_qk_norm_rope_axes_fwd", [PA] + [_vp] * 10 + [size, _vp]),
                      ("gdn_qk_norm_rope_axes_bwd", [PA] + [_vp] * 14 + [size, _vp]),
                      ("gdn_add_norm_fwd", [PN] + [_vp] * 6), ("gdn_add_norm_quant", [PN, ctypes.c_int32] + [_vp] * 7),
                      ("gdn_add_norm_bwd", [PN] + [_vp] * 8 + [size, _vp]),
@@ -151,7 +151,8 @@ def load_library():
                      ("gdn_state_store", [PS] + [_vp] * 5), ("gdn_state_load", [PS] + [_vp] * 5)):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = ctypes.c_int
-    for fn, args in (("gdn_add_norm_bwd_workspace_bytes", [PN]), ("gdn_qk_norm_rope_axes_bwd_workspace_bytes", [PA]),
+    for fn, args in (("gdn_add_norm_bwd_workspace_bytes", [PN]), ("gdn_qk_norm_rope_axes_fwd_workspace_bytes", [PA]),
+                     ("gdn_qk_norm_rope_axes_bwd_workspace_bytes", [PA]),
                      ("gdn_grad_workspace_bytes", [ctypes.POINTER(gdn_grad), i64])):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = size
@@ -187,7 +188,8 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_last_error", "gdn_fwd_works
             "gdn_la_bwd_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode",
             "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_bytes", "gdn_qk_norm_rope_bwd",
             "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd",
-            "gdn_qk_norm_rope_axes_fwd", "gdn_qk_norm_rope_axes_bwd_workspace_bytes",
+            "gdn_qk_norm_rope_axes_fwd_workspace_bytes", "gdn_qk_norm_rope_axes_fwd",
+            "gdn_qk_norm_rope_axes_bwd_workspace_bytes",
             "gdn_qk_norm_rope_axes_bwd", "gdn_add_norm_fwd", "gdn_add_norm_quant",
             "gdn_add_norm_bwd_workspace_bytes", "gdn_add_norm_bwd", "gdn_grad_workspace_bytes", "gdn_grad_norm",
             "gdn_clip_grads", "gdn_state_store", "gdn_state_load")
@@ -1029,7 +1031,8 @@ def gdn_gated_norm_bwd(x, gate, weight, dy, *, eps: float = 1e-6, grads=None, wo
 
 
 def gdn_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, sections, *, eps: float = 1e-6,
-                              interleaved: bool = False, alternating: bool = False, q_out=None, k_out=None, stream=None):
+                              interleaved: bool = False, alternating: bool = False, q_out=None, k_out=None,
+                              workspace=None, stream=None):
     """:func:`gdn_qk_norm_rope_fwd` for tokens with a position on each of 1 to 4 axes, as those
     of images and videos (time, height, width; ``gdn_qk_norm_rope_axes_fwd``).  positions int32
     [axes,B,T]; ``sections``: how many of the R/2 pairs each axis turns, one behind the other,
@@ -1038,7 +1041,7 @@ def gdn_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, sec
     R/2], in the row of its axis's position; one outside the tables makes that axis's elements
     of the token NaN.  Returns ``(q_out, k_out)``, dense."""
     return (_layer or _binding()).rope_axes_fwd(q, k, q_weight, k_weight, cos, sin, positions, sections, eps,
-                                                interleaved, alternating, q_out, k_out, _raw(stream))
+                                                interleaved, alternating, q_out, k_out, workspace, _raw(stream))
 
 
 def gdn_qk_norm_rope_axes_bwd(q, k, q_weight, k_weight, cos, sin, positions, sections, dq_out, dk_out, *,

@@ -536,10 +536,13 @@ typedef struct {
  *   positions  int32 [axes,B,T], required (unless R = 0).  A position outside the tables
  *              makes the elements of its axis's pairs NaN, and in the backward the
  *              token's whole gradient rows.
+ *   workspace  the *_workspace_bytes(p) bytes, which may be 0.
  */
+size_t gdn_qk_norm_rope_axes_fwd_workspace_bytes(const gdn_rope_axes_problem* p);
 gdn_status gdn_qk_norm_rope_axes_fwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
-                                     const int32_t* positions, void* q_out, void* k_out, void* stream);
+                                     const int32_t* positions, void* q_out, void* k_out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 size_t gdn_qk_norm_rope_axes_bwd_workspace_bytes(const gdn_rope_axes_problem* p);
 gdn_status gdn_qk_norm_rope_axes_bwd(const gdn_rope_axes_problem* p, const void* q, const void* k,
                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,

@@ -10,6 +10,7 @@ from test_layer_binding_host import FAKE, ROOT, RUN
 MORE = r"""
 extern "C" {
 SIZE(gdn_add_norm_bwd_workspace_bytes) SIZE(gdn_grad_workspace_bytes) SIZE(gdn_qk_norm_rope_axes_bwd_workspace_bytes)
+SIZE(gdn_qk_norm_rope_axes_fwd_workspace_bytes)
 CALL(gdn_qk_norm_rope_axes_fwd) CALL(gdn_qk_norm_rope_axes_bwd) CALL(gdn_add_norm_fwd) CALL(gdn_add_norm_quant)
 CALL(gdn_add_norm_bwd) CALL(gdn_grad_norm) CALL(gdn_clip_grads) CALL(gdn_state_store) CALL(gdn_state_load)
 }

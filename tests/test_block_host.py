@@ -28,7 +28,7 @@ def _call(lib, fn, p, names, sized=None, first=(), **over):
 
 # ------------------------------------------------------------ rotation by axes
 
-ROPE_FWD = ("q", "k", "q_weight", "k_weight", "cos", "sin", "positions", "q_out", "k_out")
+ROPE_FWD = ("q", "k", "q_weight", "k_weight", "cos", "sin", "positions", "q_out", "k_out", "workspace")
 ROPE_BWD = ROPE_FWD[:7] + ("dq_out", "dk_out", "dq", "dk", "dq_weight", "dk_weight", "workspace")
 
 
@@ -39,7 +39,7 @@ def _axes(lib, sections=(8, 12, 12), alternating=0, axes=None, B=2, T=1000, D=12
 
 
 def test_axes_refused(lib):
-    both = lambda p, **o: {_call(lib, "gdn_qk_norm_rope_axes_fwd", p, ROPE_FWD, **o),  # noqa: E731
+    both = lambda p, **o: {_call(lib, "gdn_qk_norm_rope_axes_fwd", p, ROPE_FWD, sized=1 << 40, **o),  # noqa: E731
                            _call(lib, "gdn_qk_norm_rope_axes_bwd", p, ROPE_BWD, sized=1 << 40, **o)}
     for kw, status, word in ((dict(axes=0), UNSUP, "axes=0"), (dict(axes=5), UNSUP, "axes=5"),
                              (dict(sections=(8, 12, 11)), INVALID, "sum"), (dict(sections=(40, -4, -4)), INVALID, "sections[0]"),
@@ -57,14 +57,22 @@ def test_axes_refused(lib):
         assert both(ok, **{n: None}) == {INVALID}, n
         assert n in lib.gdn_last_error()
     assert both(ok, positions=FAKE + 2) == {INVALID}
-    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", ok, ROPE_FWD, k_out=FAKE + 16) == INVALID
+    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", ok, ROPE_FWD, sized=0, k_out=FAKE + 16) == INVALID
+    # pairs that are copied one by one, of many tokens: their angles are gathered first
+    turns = _axes(lib, sections=(12, 10, 10), alternating=1)
+    need = lib.load_library().gdn_qk_norm_rope_axes_fwd_workspace_bytes
+    assert need(ctypes.byref(ok)) == 0 and need(ctypes.byref(_axes(lib, sections=(12, 10, 10), alternating=1, T=10))) == 0
+    assert need(ctypes.byref(turns)) == 2 * 1000 * 64 * 4
+    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1000) == WS
+    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1 << 40, workspace=None) == INVALID
+    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1 << 40, workspace=FAKE + GAP) == INVALID
     assert _call(lib, "gdn_qk_norm_rope_axes_bwd", ok, ROPE_BWD, sized=16) == WS
     need = lib.load_library().gdn_qk_norm_rope_axes_bwd_workspace_bytes
     assert need(ctypes.byref(ok)) > 0 and need(ctypes.byref(_axes(lib, T=10))) == 0  # few tokens: one cluster
     assert need(ctypes.byref(_axes(lib, axes=5))) == 0
-    assert lib.load_library().gdn_qk_norm_rope_axes_fwd(None, *[None] * 10) == INVALID
+    assert lib.load_library().gdn_qk_norm_rope_axes_fwd(None, *[None] * 10, 0, None) == INVALID
     # nothing to do: nothing is needed
-    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", _axes(lib, T=0), ROPE_FWD, q=None, k=None, positions=None, q_out=None,
+    assert _call(lib, "gdn_qk_norm_rope_axes_fwd", _axes(lib, T=0), ROPE_FWD, sized=0, q=None, k=None, positions=None, q_out=None,
                  k_out=None) == 0
 
 
