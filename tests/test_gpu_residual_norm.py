@@ -84,6 +84,11 @@ CASES = [
     (3000, 96, "bf16", "bf16", False),
     (2500, 512, "f32", "f32", False),
     (1900, 1536, "bf16", "f32", False),
+    # a backward of one cluster of 2, 11, 15 and 16 blocks of eight rows, and one block more; of
+    # 16 blocks of a row
+    (9, 512, "bf16", "bf16", False), (88, 256, "bf16", "bf16", False), (115, 1000, "bf16", "bf16", False),
+    (128, 512, "f32", "f32", False), (129, 768, "bf16", "bf16", False),
+    (16, 8192, "f32", "f32", False), (15, 8192, "bf16", "bf16", False), (17, 8192, "bf16", "f32", False),
 ]
 
 

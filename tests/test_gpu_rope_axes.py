@@ -64,6 +64,17 @@ CASES = [
     (1, 2000, 6, 6, 128, 128, "bf16", False, True, (16, 24, 24), False),
     (2, 700, 7, 7, 128, 128, "f32", False, False, (23, 20, 21), False),
     (2, 50, 4, 3, 64, 0, "bf16", False, False, (0,), False),
+    # as many rows as have their angles gathered in front
+    (1, 3001, 6, 6, 128, 128, "bf16", False, True, (23, 20, 21), False),
+    (2, 1111, 12, 4, 128, 128, "f32", True, False, (24, 20, 20), True),
+    (3, 2749, 3, 1, 96, 32, "bf16", True, False, (5, 4, 3, 4), False),
+    (1, 4100, 8, 8, 64, 64, "f32", False, True, (14, 9, 9), True),
+    # a backward of one cluster, of 1, 2, 15 and 16 blocks, and one block more
+    (1, 16, 1, 1, 128, 128, "bf16", False, False, (16, 24, 24), False),
+    (1, 17, 1, 1, 128, 128, "f32", False, False, (16, 24, 24), False),
+    (1, 240, 1, 1, 64, 64, "bf16", False, False, (8, 12, 12), False),
+    (1, 64, 4, 4, 256, 256, "f32", False, False, (32, 48, 48), False),
+    (1, 257, 1, 1, 128, 128, "bf16", False, False, (16, 24, 24), False),
 ]
 
 
@@ -107,11 +118,12 @@ def test_axes(B, T, Hq, Hk, D, R, dtype, interleaved, slices, sections, alternat
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("sections,alternating", [((16, 24, 24), False), ((23, 20, 21), False), ((24, 20, 20), True), ((64,), False)])
-def test_equal_positions_are_one(dtype, interleaved, sections, alternating):
+@pytest.mark.parametrize("T", [7, 45, 1900])
+def test_equal_positions_are_one(dtype, interleaved, sections, alternating, T):
     """Text among images has the same position on every axis: the call of one position, bit
     for bit."""
-    q, k, wq, wk, cos, sin, pos, dqo, dko = _inputs(2, 45, 6, 3, 128, 128, dtype, True, 1)
-    many = pos.expand(len(sections), 2, 45).contiguous()
+    q, k, wq, wk, cos, sin, pos, dqo, dko = _inputs(2, T, 6, 3, 128, 128, dtype, True, 1)
+    many = pos.expand(len(sections), 2, T).contiguous()
     one = (q, k, wq, wk, cos, sin, pos[0])
     all_ = (q, k, wq, wk, cos, sin, many, sections)
     how = dict(interleaved=interleaved)
@@ -124,16 +136,17 @@ def test_equal_positions_are_one(dtype, interleaved, sections, alternating):
 
 @pytest.mark.parametrize("sections,alternating", [((8, 4, 4), False), ((7, 5, 4), False), ((6, 5, 5), True)])
 @pytest.mark.parametrize("interleaved", [False, True])
-def test_positions_outside_the_tables(interleaved, sections, alternating):
+@pytest.mark.parametrize("T", [4, 4100])
+def test_positions_outside_the_tables(interleaved, sections, alternating, T):
     """They show in their own axis's pairs of their own token."""
-    q, k, wq, wk, cos, sin, pos, dqo, dko = _inputs(2, 4, 3, 1, 64, 32, "bf16", False, 3)
+    q, k, wq, wk, cos, sin, pos, dqo, dko = _inputs(2, T, 3, 1, 64, 32, "bf16", False, 3)
     pos[0, 0, 1], pos[2, 1, 2], pos[1, 0, 3] = -1, cos.shape[0], -2 ** 31
     yq, yk = gdn.gdn_qk_norm_rope_axes_fwd(q, k, wq, wk, cos, sin, pos, sections, interleaved=interleaved, alternating=alternating)
     g = gdn.gdn_qk_norm_rope_axes_bwd(q, k, wq, wk, cos, sin, pos, sections, dqo, dko, interleaved=interleaved, alternating=alternating)
     torch.cuda.synchronize()
     axis = torch.from_numpy(block.axis_of_pair(sections, alternating))
     first, second = layer._pairs(32, interleaved)
-    bad = torch.zeros(2, 4, 64, dtype=torch.bool)
+    bad = torch.zeros(2, T, 64, dtype=torch.bool)
     for a, b, t in ((0, 0, 1), (2, 1, 2), (1, 0, 3)):
         on = (axis == a).nonzero().flatten().numpy()
         bad[b, t, first[on]] = bad[b, t, second[on]] = True
