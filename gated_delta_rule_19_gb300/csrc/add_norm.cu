@@ -256,11 +256,12 @@ struct NormDims {
     float eps;
 };
 
-constexpr int kPerSm = 2;
+// Blocks of N threads an SM holds.
+constexpr int per_sm(int N) { return 512 / N; }
 constexpr int kFwdSlots = 2 * kPieces, kBwdSlots = 3 * kPieces;
 
 template <typename TX, typename TR, int N, bool kQuant>
-__global__ void __launch_bounds__(N, N == 256 ? kPerSm : 1)
+__global__ void __launch_bounds__(N, per_sm(N))
 add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const TX* __restrict__ w, TR* h,
                     void* __restrict__ y, float* __restrict__ scales) {
     constexpr int VEC = 16 / (int)sizeof(TR), S = kStages;
@@ -438,7 +439,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
 // Each block leaves one row of column sums in sums [gridDim.x][D]; the blocks of a cluster
 // (kCluster, the whole grid) add theirs up to dw, each some columns.
 template <typename TX, typename TR, int N, bool kCluster>
-__global__ void __launch_bounds__(N, N == 256 ? kPerSm : 1)
+__global__ void __launch_bounds__(N, per_sm(N))
 add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__ w, const TX* __restrict__ dy,
                     const TR* __restrict__ dh, TX* __restrict__ dx, TR* __restrict__ dr, TX* __restrict__ dw, float* __restrict__ sums) {
     constexpr int VEC = 16 / (int)sizeof(TR), S = kStages;
@@ -570,7 +571,7 @@ cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    const int64_t want = (d.rows + N / d.L - 1) / (N / d.L), cap = (int64_t)sm_count() * (N == 256 ? kPerSm : 1);
+    const int64_t want = (d.rows + N / d.L - 1) / (N / d.L), cap = (int64_t)sm_count() * per_sm(N);
     return launch_dependent(kern, dim3((unsigned)(want < cap ? want : cap)), N, smem, st, d, (const TX*)c.x,
                             (const TR*)c.res, (const TX*)c.w, (TR*)c.h, c.y, c.scales);
 }
@@ -592,20 +593,21 @@ cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
                             (TX*)c.dw, c.part);
 }
 
-template <typename TX, typename TR, int N>
-cudaError_t any(const AddNormCall& c, const NormDims& d, AddNormKind kind, cudaStream_t st) {
-    switch (kind) {
-        case AddNormKind::FWD: return fwd<TX, TR, N, false>(c, d, st);
-        case AddNormKind::QUANT: return fwd<TX, TR, N, true>(c, d, st);
-        default: return bwd<TX, TR, N>(c, d, st);
-    }
+template <typename TX, typename TR, bool kQuant>
+cudaError_t fwd_n(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
+    return d.L <= 128 ? fwd<TX, TR, 128, kQuant>(c, d, st) : d.L == 256 ? fwd<TX, TR, 256, kQuant>(c, d, st)
+                                                                       : fwd<TX, TR, 512, kQuant>(c, d, st);
 }
 
 template <typename TX, typename TR>
 cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
     const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR)), c.group ? c.group : c.D,
                      c.group == 32 ? 5 : c.group == 64 ? 6 : 7, c.eps};
-    return d.L <= 256 ? any<TX, TR, 256>(c, d, kind, st) : any<TX, TR, 512>(c, d, kind, st);
+    switch (kind) {
+        case AddNormKind::FWD: return fwd_n<TX, TR, false>(c, d, st);
+        case AddNormKind::QUANT: return fwd_n<TX, TR, true>(c, d, st);
+        default: return d.L <= 256 ? bwd<TX, TR, 256>(c, d, st) : bwd<TX, TR, 512>(c, d, st);
+    }
 }
 
 }  // namespace
@@ -615,7 +617,7 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
 // 6.0 to 6.4; with two turns 6.0 to 6.8.
 AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide) {
     const int L = lanes_of(D, 16 / wide), n = L <= 256 ? 256 : 512;
-    const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * (n == 256 ? kPerSm : 1);
+    const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * per_sm(n);
     if (want <= kMostCluster) return {(int)(want < 1 ? 1 : want), true};
     return {(int)(want < cap ? want : cap), false};
 }
