@@ -200,7 +200,11 @@ __device__ __forceinline__ void run_of(uint32_t tiles, uint32_t b, uint32_t n, u
     to = (uint32_t)((uint64_t)tiles * (b + 1) / n);
 }
 
-constexpr int kSumPerSm = 4, kScalePerSm = 4;
+// Blocks an SM holds (252 M float32 into bf16, a whole call: 3 for the scaling 375 us, 4 391; where
+// boundaries are apart, 22 M: 41 and 35).
+constexpr int kSumPerSm = 4;
+template <bool kApart>
+constexpr int kScalePerSm = kApart ? 4 : 3;
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kSumPerSm)
@@ -309,35 +313,105 @@ __device__ __forceinline__ void scale_vectors(const Tensor& t, int64_t e, uint64
     }
 }
 
-// Where the output's boundaries are not the input's: neighbouring threads take neighbouring
-// elements.
-__device__ __forceinline__ void scale_apart(const Tensor& t, int64_t e, float by) {
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) {
-        const int64_t at = e + j * kThreads;
-        if (at < 0 || at >= t.n) continue;
-        const float x = at1(t.p, at, t.in16) * by;
-        if (t.out16) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(x);
-        else ((float*)t.out)[at] = x;
+// N bf16 elements from the address p on, in words and not beyond them but for the halves of the
+// first and the last word.
+template <int N>
+struct Halves {
+    uint32_t w[N / 2 + 1];
+    __device__ __forceinline__ void load(const char* p) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) w[k] = q[k];
+        w[N / 2] = (uintptr_t)p & 2 ? q[N / 2] : 0;
+    }
+    __device__ __forceinline__ void get(bool odd, uint64_t (&f)[N / 2]) const {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) f[k] = bf16_pair(odd ? __funnelshift_r(w[k], w[k + 1], 16) : w[k]);
+    }
+};
+
+// Where the output's 16-byte boundaries are not the input's, as in a flat buffer: vectors of
+// whole 16 bytes of the output, whose elements are read one by one (bf16: by words).  A tile
+// takes the vectors that begin in it, but for the last at its end and with the one before its
+// begin; the tensor's last tile takes one more.  (Elements one by one on both sides: 22 M bf16
+// in odd places of a flat buffer 61 us a call, so 23.)
+template <bool kIn16, bool kOut16>
+__device__ __forceinline__ void scale_apart(const Tensor& t, uint32_t tile, int thread, float by) {
+    constexpr int VEC = kOut16 ? 8 : 4, M = 32 / VEC;
+    const int64_t e0 = (int64_t)(tile - t.first) * kTile - t.lead;
+    const int lead = (int)((uintptr_t)t.out & 15) >> (kOut16 ? 1 : 2);
+    const int64_t first = e0 - ((e0 + lead) & (VEC - 1)), e = first + thread * VEC;
+    const uint64_t by2 = twice(by);
+    if (first >= 1 && first + kTile < t.n) {  // a word more on either side is the tensor's
+        uint64_t f[M][VEC / 2];
+        if constexpr (kIn16) {
+            const bool odd = ((uintptr_t)t.p + 2 * e) & 2;
+            Halves<VEC> h[M];
+#pragma unroll
+            for (int j = 0; j < M; ++j) h[j].load(t.p + 2 * (e + j * kThreads * VEC));
+#pragma unroll
+            for (int j = 0; j < M; ++j) h[j].get(odd, f[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+                const float* q = (const float*)t.p + e + j * kThreads * VEC;
+#pragma unroll
+                for (int k = 0; k < VEC / 2; ++k) f[j][k] = pair(q[2 * k], q[2 * k + 1]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+#pragma unroll
+            for (int k = 0; k < VEC / 2; ++k) f[j][k] = mul2(f[j][k], by2);
+            put_vector<VEC, kOut16>(t, e + j * kThreads * VEC, f[j]);
+        }
+    } else {
+        auto one = [&](int64_t at) {
+            for (int k = 0; k < VEC; ++k, ++at) {
+                if (at < 0 || at >= t.n) continue;
+                const float x = at1(t.p, at, kIn16) * by;
+                if (kOut16) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(x);
+                else ((float*)t.out)[at] = x;
+            }
+        };
+        for (int j = 0; j < M; ++j) one(e + j * kThreads * VEC);
+    }
+    if (tile + 1 == t.end && thread == 0) {
+        const int64_t at = first + kTile;
+        for (int k = 0; k < VEC; ++k) {
+            if (at + k >= t.n) break;
+            const float x = at1(t.p, at + k, kIn16) * by;
+            if (kOut16) ((__nv_bfloat16*)t.out)[at + k] = __float2bfloat16_rn(x);
+            else ((float*)t.out)[at + k] = x;
+        }
     }
 }
 
-// A tile times `by`, by kThreads threads.
+// Whether a tensor's output has its boundaries where the input has.
+__host__ __device__ __forceinline__ bool together(uintptr_t in, uintptr_t out, bool in16, bool out16) {
+    const uintptr_t lead = (in & 15) >> (in16 ? 1 : 2);
+    return (out - lead * (out16 ? 2 : 4)) % (in16 && out16 ? 16 : out16 ? 8 : 16) == 0;
+}
+
+// A tile times `by`, by kThreads threads.  kApart: some tensor's boundaries are apart.
+template <bool kApart>
 __device__ __forceinline__ void scale_tile(const Tensor& t, uint32_t tile, int thread, float by) {
     if (by == 1.f && t.out == t.p) return;
     const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
-    const int vec = t.in16 ? 8 : 4;
-    const bool whole = ((uintptr_t)t.out - (uintptr_t)t.lead * (t.out16 ? 2 : 4)) % (t.out16 ? 2 * vec : 16) == 0;
-    if (!whole) scale_apart(t, e + thread, by);
-    else if (t.in16 && t.out16) scale_vectors<8, true>(t, e + thread * 8, twice(by));
+    if (kApart && !together((uintptr_t)t.p, (uintptr_t)t.out, t.in16, t.out16)) {
+        if (t.in16 && t.out16) scale_apart<true, true>(t, tile, thread, by);
+        else if (t.in16) scale_apart<true, false>(t, tile, thread, by);
+        else if (t.out16) scale_apart<false, true>(t, tile, thread, by);
+        else scale_apart<false, false>(t, tile, thread, by);
+    } else if (t.in16 && t.out16) scale_vectors<8, true>(t, e + thread * 8, twice(by));
     else if (t.in16) scale_vectors<8, false>(t, e + thread * 8, twice(by));
     else if (t.out16) scale_vectors<4, true>(t, e + thread * 4, twice(by));
     else scale_vectors<4, false>(t, e + thread * 4, twice(by));
 }
 
 // in_place: every tensor is its own output.
-template <int N>
-__global__ void __launch_bounds__(kThreads, kScalePerSm)
+template <int N, bool kApart>
+__global__ void __launch_bounds__(kThreads, kScalePerSm<kApart>)
 grad_scale_kernel(const __grid_constant__ List<N> l, const GradPart* __restrict__ part, int parts, float max_norm,
                   float* norm, bool in_place) {
     uint32_t from, tile;
@@ -352,7 +426,7 @@ grad_scale_kernel(const __grid_constant__ List<N> l, const GradPart* __restrict_
     if ((in_place && by == 1.f) || from >= tile) return;
     while (tile-- > from) {
         while (tile < t.first) t.at(l, --i);
-        scale_tile(t, tile, threadIdx.x, by);
+        scale_tile<kApart>(t, tile, threadIdx.x, by);
     }
 }
 
@@ -394,7 +468,7 @@ grad_clip_kernel(const __grid_constant__ List<N> l, float max_norm, float* norm,
     if (!clip) return;
     for (uint32_t tile = to; tile-- > from;) {
         while (tile < t.first) t.at(l, --i);
-        scale_tile(t, tile, thread, x.by);
+        scale_tile<true>(t, tile, thread, x.by);
     }
 }
 
@@ -433,8 +507,12 @@ cudaError_t scale(const gdn_grad* g, int64_t a, int64_t b, const GradPart* part,
                   bool in_place, cudaStream_t st) {
     List<N> l;
     fill(l, g, a, b);
-    return launch_dependent(grad_scale_kernel<N>, dim3(grid_of(l.tiles, kScalePerSm)), kThreads, 0, st, l, part, parts,
-                            max_norm, norm, in_place);
+    bool apart = false;
+    for (int64_t i = a; i < b; ++i)
+        apart = apart || (g[i].n && !together((uintptr_t)g[i].grad, (uintptr_t)g[i].out, g[i].dtype == GDN_BF16, g[i].out_dtype == GDN_BF16));
+    const dim3 grid(grid_of(l.tiles, apart ? kScalePerSm<true> : kScalePerSm<false>));
+    return apart ? launch_dependent(grad_scale_kernel<N, true>, grid, kThreads, 0, st, l, part, parts, max_norm, norm, in_place)
+                 : launch_dependent(grad_scale_kernel<N, false>, grid, kThreads, 0, st, l, part, parts, max_norm, norm, in_place);
 }
 
 template <int N>

@@ -104,11 +104,11 @@ def test_same_call_same_bits_and_generators():
 
 
 @pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
-@pytest.mark.parametrize("first,behind", [(0, 0), (1, 0), (0, 1), (3, 3), (2, 5), (5, 2), (4, 8), (7, 7)])
+@pytest.mark.parametrize("first,behind", [(0, 0), (1, 0), (0, 1), (3, 3), (2, 5), (5, 2), (4, 8), (7, 7), (0, 3), (6, 1), (1, 6), (4, 5), (0, 6), (7, 0)])
 def test_parts_of_one_buffer(dtype, out, first, behind):
     """Tensors that begin anywhere in a buffer, outputs anywhere in another; what lies between
     stays."""
-    sizes = [1, 9000, 6, 8192, 33, 20000]
+    sizes = [1, 9000, 6, 8192, 33, 20000, 8191, 16390, 0, 24571]
     flat, = _tensors([(sum(sizes) + 64,)], [dtype], seed=first)
     to = torch.full((sum(sizes) + 64,), 7.0, device="cuda", dtype=DT[out])
     grads, outs, at = [], [], 0
