@@ -10,9 +10,9 @@
 // The sum is normalised as it stands in float32; h is what the residual stream keeps, in
 // its own type, and what the backward reads.
 //
-// Bound by reading and writing the rows.  A row is held by L lanes (a power of two, a warp
-// at least), each with kPieces pieces of it a stride of L apart, so that a warp's loads and
-// stores fill whole sectors; the row is read once, its sum of squares is made of registers.
+// Bound by reading and writing the rows.  A row is held by L lanes (a power of two from 8 on),
+// each with kPieces pieces of it a stride of L apart, so that a warp's loads and stores fill
+// whole sectors; the row is read once, its sum of squares is made of registers.
 // Persistent blocks with a ring of asynchronous copies (rows.cuh) keep the next rows in
 // flight.
 
@@ -112,13 +112,24 @@ struct Place {
     }
 };
 
-// Sums of two values over the L lanes of a row; `part` has two halves, used in turn, so that
-// one barrier a turn is enough.
+// Over the L lanes of a row, or those of them that are in this warp.
+template <typename F>
+__device__ __forceinline__ float over_lanes(float x, int L, F&& both) {
+    x = both(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    x = both(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    if (L > 4) x = both(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    if (L > 8) x = both(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    if (L > 16) x = both(x, __shfl_xor_sync(0xffffffffu, x, 16));
+    return x;
+}
+// Sums of two values over a row; `part` has two halves, used in turn, so that one barrier a
+// turn is enough.
 template <int N>
 __device__ __forceinline__ void row_sums(float& a, float& b, int L, float2 (*part)[N / 32], int turn) {
-    a = group_sum<32>(a);
-    b = group_sum<32>(b);
-    if (L == 32) return;
+    auto plus = [](float x, float y) { return x + y; };
+    a = over_lanes(a, L, plus);
+    b = over_lanes(b, L, plus);
+    if (L <= 32) return;
     float2* p = part[turn & 1];
     const int warp = threadIdx.x >> 5, w = L / 32, first = warp & ~(w - 1);
     if ((threadIdx.x & 31) == 0) p[warp] = make_float2(a, b);
@@ -132,9 +143,8 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int L, float2 (*par
 }
 template <int N>
 __device__ __forceinline__ float row_max(float m, int L, float (*part)[N / 32], int turn) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (L == 32) return m;
+    m = over_lanes(m, L, max_nan);
+    if (L <= 32) return m;
     float* p = part[turn & 1];
     const int warp = threadIdx.x >> 5, w = L / 32, first = warp & ~(w - 1);
     if ((threadIdx.x & 31) == 0) p[warp] = m;
@@ -346,7 +356,9 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 }
                 return m;
             };
-            // (bf16's sums and products are exact, but for addends 2^16 apart)
+            // What the float32 t leave out of the group's largest |t|: sums and products of bf16
+            // are exact (but for addends 2^16 apart), of float32 it is taken from the elements
+            // that are the largest, where a quotient next to a middle asks for it.
             auto left_out = [&](int p, float most, float left) {
                 bool is = false;
 #pragma unroll
@@ -357,7 +369,8 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 }
                 return is ? left_of<TX, TR>(ring.at(slot, p), place(p), wv[p], most, left) : left;
             };
-            auto quantise = [&](int p, float most, float left, const Scale& c) {
+            // the piece's numbers, and whether a quotient is next to a middle
+            auto coded = [&](int p, const Scale& c, uint2& code) {
                 uint32_t q[4] = {0, 0, 0, 0}, near = kNear + 1;
                 if (c.plain) {
 #pragma unroll
@@ -371,63 +384,83 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     near = min(near, min(behind(z0), behind(z1)));
                     q[j] = e4m3x2(z);
                 }
-                uint2 code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                if (near <= kNear && !c.plain) {
-                    float by, same;
-                    unpair(c.by, by, same);
-                    code = exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], by, most, left);
-                }
+                code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                return near <= kNear && !c.plain;
+            };
+            auto exact = [&](int p, float most, float left, const Scale& c) {
+                float by, same;
+                unpair(c.by, by, same);
+                return exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], by, most, left);
+            };
+            auto store = [&](int p, const uint2& code) {
                 unsigned char* to = (unsigned char*)y + out + p * at.LV;
                 if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = code;
                 else *reinterpret_cast<uint32_t*>(to) = code.x;
             };
             if (d.group < d.D) {
-                // the largest over a group's lanes, neighbours: 4 to 32 of them
-                const int lanes = d.group / VEC;
-                auto over_group = [&](float m) {
-                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    if (lanes > 4) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    if (lanes > 8) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    if (lanes > 16) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    return m;
-                };
+                const int lanes = d.group / VEC;  // a group's, neighbours: 4 to 32 of them
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
                     if (p * at.LV >= d.D) break;
-                    float m = p < n ? weighted(p) : 0.f, left = 0.f;
-                    m = over_group(m);
-                    if constexpr (kWide) left = over_group(p < n ? left_out(p, m, -FLT_MAX) : 0.f);
-                    if (p >= n) continue;
+                    const float m = over_lanes(p < n ? weighted(p) : 0.f, lanes, max_nan);
+                    if (!kWide && p >= n) continue;
                     const Scale c = scale_of(m, r);
-                    const int col = at.c0 + p * at.LV;
-                    if ((col & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
-                    quantise(p, m, left, c);
+                    uint2 code;
+                    if constexpr (kWide) {
+                        const bool near = p < n && coded(p, c, code);
+                        if (__any_sync(0xffffffffu, near)) {
+                            const float left = over_lanes(p < n ? left_out(p, m, -FLT_MAX) : -FLT_MAX, lanes, max_nan);
+                            if (near) code = exact(p, m, left, c);
+                        }
+                        if (p >= n) continue;
+                    }
+                    if (((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
+                    if (!kWide && coded(p, c, code)) code = exact(p, m, 0.f, c);
+                    store(p, code);
                 }
             } else {
-                float m = 0.f, left = -FLT_MAX;
+                float m = 0.f;
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= n) break;
                     m = max_nan(m, weighted(p));
                 }
                 m = row_max<N>(m, at.L, most, turn);
+                const Scale c = scale_of(m, r);
+                if (at.c0 == 0 && n) scales[now] = c.scale;
                 if constexpr (kWide) {
+                    uint2 code[kPieces];
+                    uint32_t near = 0;  // a bit a piece
 #pragma unroll
                     for (int p = 0; p < kPieces; ++p) {
                         if (p >= n) break;
-                        left = left_out(p, m, left);
+                        near |= (uint32_t)coded(p, c, code[p]) << p;
                     }
-                    left = row_max<N>(left, at.L, most + 2, turn);
-                } else {
-                    left = 0.f;
-                }
-                const Scale c = scale_of(m, r);
-                if (at.c0 == 0 && n) scales[now] = c.scale;
+                    if (at.L > 32 ? __syncthreads_or(near) : __any_sync(0xffffffffu, near)) {
+                        float left = -FLT_MAX;
 #pragma unroll
-                for (int p = 0; p < kPieces; ++p) {
-                    if (p >= n) break;
-                    quantise(p, m, left, c);
+                        for (int p = 0; p < kPieces; ++p) {
+                            if (p >= n) break;
+                            left = left_out(p, m, left);
+                        }
+                        left = row_max<N>(left, at.L, most + 2, turn);
+#pragma unroll
+                        for (int p = 0; p < kPieces; ++p)
+                            if (near >> p & 1) code[p] = exact(p, m, left, c);
+                    }
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) {
+                        if (p >= n) break;
+                        store(p, code[p]);
+                    }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) {
+                        if (p >= n) break;
+                        uint2 code;
+                        if (coded(p, c, code)) code = exact(p, m, 0.f, c);
+                        store(p, code);
+                    }
                 }
             }
         }
@@ -528,11 +561,29 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         slot = slot + 1 == S ? 0 : slot + 1;
     }
     wait_group<0>();
-    // the block's rows of sums, one after the other: the same call gives the same bits
+    // the sums of a warp's rows, then those of the block's, one after the other: the same call
+    // gives the same bits
+    const bool part_warp = at.L < 32;
+    if (part_warp) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                float lo, hi;
+                unpair(acc[p][j], lo, hi);
+                for (int off = at.L; off < 32; off *= 2) {
+                    lo += __shfl_xor_sync(0xffffffffu, lo, off);
+                    hi += __shfl_xor_sync(0xffffffffu, hi, off);
+                }
+                acc[p][j] = pair(lo, hi);
+            }
+    }
     __syncthreads();
     float* col = (float*)sm;
-    for (int g = 0; g < N / at.L; ++g) {
-        if ((int)threadIdx.x / at.L == g) {
+    const int wide = part_warp ? 32 : at.L;
+    const bool adds = !part_warp || (int)(threadIdx.x & 31) < at.L;
+    for (int g = 0; g < N / wide; ++g) {
+        if ((int)threadIdx.x / wide == g && adds) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 if (p >= at.n) break;
@@ -557,9 +608,16 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     }
 }
 
-// Lanes a row takes: pieces of VEC elements, kPieces a lane, a warp at least.
-int lanes_of(int D, int vec) {
-    int L = 32;
+// Lanes a row of pieces of VEC elements takes, kPieces a lane: a warp at least, or two pieces
+// a lane of fewer (35 x 1755 rows of 512 bf16 with 16 lanes 86.3 us forward and backward, with
+// 32 83.3).  The 8-bit form, which computes more, takes kPieces from 8 lanes on (29 x 1429 rows
+// of 272 with 16 lanes 15.9 us, with 32 23.2), but all of a group of columns with a scale.
+int lanes_of(int D, int vec, bool quant, int group) {
+    int L = 8;
+    if (quant)
+        while (L * vec < group) L *= 2;
+    else
+        while (L < 32 && L * 2 * vec < D) L *= 2;
     while (L * kPieces * vec < D) L *= 2;
     return L;
 }
@@ -601,7 +659,7 @@ cudaError_t fwd_n(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
 
 template <typename TX, typename TR>
 cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
-    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR)), c.group ? c.group : c.D,
+    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR), kind == AddNormKind::QUANT, c.group), c.group ? c.group : c.D,
                      c.group == 32 ? 5 : c.group == 64 ? 6 : 7, c.eps};
     switch (kind) {
         case AddNormKind::FWD: return fwd_n<TX, TR, false>(c, d, st);
@@ -616,7 +674,7 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
 // launch: 1 to 16 blocks of rows of 768 to 4096 elements 4.6 to 5.3 us a call, as two launches
 // 6.0 to 6.4; with two turns 6.0 to 6.8.
 AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide) {
-    const int L = lanes_of(D, 16 / wide), n = L <= 256 ? 256 : 512;
+    const int L = lanes_of(D, 16 / wide, false, 0), n = L <= 256 ? 256 : 512;
     const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * per_sm(n);
     if (want <= kMostCluster) return {(int)(want < 1 ? 1 : want), true};
     return {(int)(want < cap ? want : cap), false};

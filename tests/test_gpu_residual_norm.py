@@ -88,6 +88,7 @@ CASES = [
     # 16 blocks of a row
     (9, 512, "bf16", "bf16", False), (88, 256, "bf16", "bf16", False), (115, 1000, "bf16", "bf16", False),
     (128, 512, "f32", "f32", False), (129, 768, "bf16", "bf16", False),
+    (1000, 24, "bf16", "bf16", False), (777, 40, "f32", "f32", False), (500, 200, "bf16", "f32", False),
     (16, 8192, "f32", "f32", False), (15, 8192, "bf16", "bf16", False), (17, 8192, "bf16", "f32", False),
 ]
 
@@ -137,7 +138,9 @@ def test_without_residual_or_its_gradient(rows, D, dtype, stream, slices):
     (17, 256, "bf16", "bf16", True, 64), (9, 260, "f32", "f32", True, 0), (100, 768, "bf16", "bf16", False, 128),
     (33, 1000, "bf16", "f32", True, 0), (31, 992, "bf16", "f32", False, 32), (8, 2048, "f32", "f32", False, 128),
     (6, 2176, "bf16", "f32", False, 64), (7, 4096, "bf16", "bf16", False, 0), (3, 4224, "f32", "f32", True, 32),
-    (3, 8192, "bf16", "bf16", False, 128), (2, 8192, "bf16", "f32", False, 0), (3000, 96, "bf16", "bf16", False, 32)])
+    (3, 8192, "bf16", "bf16", False, 128), (2, 8192, "bf16", "f32", False, 0), (3000, 96, "bf16", "bf16", False, 32),
+    (70, 256, "f32", "f32", False, 128), (70, 256, "f32", "f32", False, 32), (129, 256, "bf16", "bf16", False, 128),
+    (129, 512, "bf16", "f32", False, 0), (333, 64, "bf16", "bf16", False, 0), (333, 128, "bf16", "f32", False, 32), (5, 24, "bf16", "bf16", False, 0)])
 def test_quant(rows, D, dtype, stream, slices, group):
     x, r, w, _, _ = _inputs(rows, D, dtype, stream, slices)
     out = torch.full((rows, D), 0x7f, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # NaN
@@ -160,7 +163,8 @@ def test_quant(rows, D, dtype, stream, slices, group):
 
 @pytest.mark.parametrize("rows,D,dtype,stream,group", [
     (4000, 768, "bf16", "bf16", 128), (4000, 768, "bf16", "f32", 128), (4000, 768, "f32", "f32", 64), (900, 4096, "bf16", "bf16", 0),
-    (900, 4096, "f32", "f32", 0), (900, 4096, "bf16", "f32", 0), (3000, 1000, "f32", "f32", 0), (3000, 992, "bf16", "bf16", 32)])
+    (900, 4096, "f32", "f32", 0), (900, 4096, "bf16", "f32", 0), (3000, 1000, "f32", "f32", 0), (3000, 992, "bf16", "bf16", 32),
+    (20000, 128, "f32", "f32", 0), (20000, 192, "bf16", "f32", 64), (700, 4960, "f32", "f32", 32)])
 def test_quant_gives_the_nearest_number(rows, D, dtype, stream, group):
     """Every 8-bit number is the one nearest to the exact quotient 448 t / max|t| of the group
     (t = (x + residual) w; the row's norm divides out): of 3 million elements not one is on the
