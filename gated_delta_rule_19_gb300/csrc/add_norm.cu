@@ -194,9 +194,12 @@ __device__ __forceinline__ float beside_middle(float q, float2 t, float most, fl
 
 // What is needed rarely is not inlined: it would take the registers of every row.  x and res
 // (0: no residual): the row's places in shared memory.
-// The piece's 8-bit numbers from its quotients q, those next to a middle decided exactly.
+// The piece's 8-bit numbers from its quotients, those next to a middle decided exactly.
+struct Quotients {
+    uint64_t z[4];
+};
 template <typename TX, typename TR>
-__device__ __noinline__ uint2 exact_piece(uint32_t x, uint32_t res, uint4 w, float by, float most, float left) {
+__device__ __noinline__ uint2 exact_piece(uint32_t x, uint32_t res, uint4 w, Quotients q, float most, float left) {
     constexpr int VEC = 16 / (int)sizeof(TR);
     uint64_t f[VEC / 2], g[VEC / 2], k[VEC / 2];
     Piece<TX, VEC>::load(x, f);
@@ -205,17 +208,15 @@ __device__ __noinline__ uint2 exact_piece(uint32_t x, uint32_t res, uint4 w, flo
     uint32_t code[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
-        float xv[2], rv[2] = {0.f, 0.f}, wv[2], q[2];
+        float xv[2], rv[2] = {0.f, 0.f}, wv[2], z[2];
         unpair(f[j], xv[0], xv[1]);
         if (res) unpair(g[j], rv[0], rv[1]);
         unpair(k[j], wv[0], wv[1]);
+        unpair(q.z[j], z[0], z[1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float2 t = product_of(xv[e], rv[e], wv[e]);
-            q[e] = t.x * by;
-            if (behind(q[e]) <= kNear) q[e] = beside_middle(q[e], t, most, left);
-        }
-        code[j] = e4m3x2(pair(q[0], q[1]));
+        for (int e = 0; e < 2; ++e)
+            if (behind(z[e]) <= kNear) z[e] = beside_middle(z[e], product_of(xv[e], rv[e], wv[e]), most, left);
+        code[j] = e4m3x2(pair(z[0], z[1]));
     }
     return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
 }
@@ -370,7 +371,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 return is ? left_of<TX, TR>(ring.at(slot, p), place(p), wv[p], most, left) : left;
             };
             // the piece's numbers, and whether a quotient is next to a middle
-            auto coded = [&](int p, const Scale& c, uint2& code) {
+            auto coded = [&](int p, const Scale& c, uint2& code, Quotients& z) {
                 uint32_t q[4] = {0, 0, 0, 0}, near = kNear + 1;
                 if (c.plain) {
 #pragma unroll
@@ -378,19 +379,17 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 }
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) {
-                    const uint64_t z = mul2(a[p][j], c.by);
+                    z.z[j] = mul2(a[p][j], c.by);
                     float z0, z1;
-                    unpair(z, z0, z1);
+                    unpair(z.z[j], z0, z1);
                     near = min(near, min(behind(z0), behind(z1)));
-                    q[j] = e4m3x2(z);
+                    q[j] = e4m3x2(z.z[j]);
                 }
                 code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
                 return near <= kNear && !c.plain;
             };
-            auto exact = [&](int p, float most, float left, const Scale& c) {
-                float by, same;
-                unpair(c.by, by, same);
-                return exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], by, most, left);
+            auto exact = [&](int p, float most, float left, const Quotients& z) {
+                return exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], z, most, left);
             };
             auto store = [&](int p, const uint2& code) {
                 unsigned char* to = (unsigned char*)y + out + p * at.LV;
@@ -406,16 +405,17 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     if (!kWide && p >= n) continue;
                     const Scale c = scale_of(m, r);
                     uint2 code;
+                    Quotients z;
                     if constexpr (kWide) {
-                        const bool near = p < n && coded(p, c, code);
+                        const bool near = p < n && coded(p, c, code, z);
                         if (__any_sync(0xffffffffu, near)) {
                             const float left = over_lanes(p < n ? left_out(p, m, -FLT_MAX) : -FLT_MAX, lanes, max_nan);
-                            if (near) code = exact(p, m, left, c);
+                            if (near) code = exact(p, m, left, z);
                         }
                         if (p >= n) continue;
                     }
                     if (((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
-                    if (!kWide && coded(p, c, code)) code = exact(p, m, 0.f, c);
+                    if (!kWide && coded(p, c, code, z)) code = exact(p, m, 0.f, z);
                     store(p, code);
                 }
             } else {
@@ -434,7 +434,8 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
 #pragma unroll
                     for (int p = 0; p < kPieces; ++p) {
                         if (p >= n) break;
-                        near |= (uint32_t)coded(p, c, code[p]) << p;
+                        Quotients z;
+                        near |= (uint32_t)coded(p, c, code[p], z) << p;
                     }
                     if (at.L > 32 ? __syncthreads_or(near) : __any_sync(0xffffffffu, near)) {
                         float left = -FLT_MAX;
@@ -445,8 +446,12 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                         }
                         left = row_max<N>(left, at.L, most + 2, turn);
 #pragma unroll
-                        for (int p = 0; p < kPieces; ++p)
-                            if (near >> p & 1) code[p] = exact(p, m, left, c);
+                        for (int p = 0; p < kPieces; ++p) {
+                            if (!(near >> p & 1)) continue;
+                            Quotients z;
+                            coded(p, c, code[p], z);
+                            code[p] = exact(p, m, left, z);
+                        }
                     }
 #pragma unroll
                     for (int p = 0; p < kPieces; ++p) {
@@ -458,7 +463,8 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     for (int p = 0; p < kPieces; ++p) {
                         if (p >= n) break;
                         uint2 code;
-                        if (coded(p, c, code)) code = exact(p, m, 0.f, c);
+                        Quotients z;
+                        if (coded(p, c, code, z)) code = exact(p, m, 0.f, z);
                         store(p, code);
                     }
                 }
