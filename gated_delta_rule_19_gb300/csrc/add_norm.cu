@@ -10,8 +10,7 @@
 // The sum is normalised as it stands in float32; h is what the residual stream keeps, in
 // its own type, and what the backward reads.
 //
-// Bound by reading and writing the rows.  A row is held by L lanes (a power of two from 8 on),
-// each with kPieces pieces of it a stride of L apart, so that a warp's loads and stores fill
+// Bound by reading and writing the rows.  A row is held by L lanes (8 to 512), each with kPieces pieces of it a stride of L apart, so that a warp's loads and stores fill
 // whole sectors; the row is read once, its sum of squares is made of registers.
 // Persistent blocks with a ring of asynchronous copies (rows.cuh) keep the next rows in
 // flight.
@@ -98,15 +97,17 @@ __device__ __forceinline__ float abs_max(const uint64_t& p, float m) {
 template <int VEC>
 struct Place {
     int L, LV, c0, n;
+    int warps, first;   // of a row that takes whole warps: how many, and the first
     int64_t row, step;  // this thread's first row, and the rows that all blocks take in a turn
     int turns;          // the same for every thread of a block
-    __device__ __forceinline__ Place(int64_t rows, int D, int L_, int threads)
-        : L(L_), LV(L_ * VEC), c0((threadIdx.x & (L_ - 1)) * VEC), n(0) {
+    __device__ __forceinline__ Place(int64_t rows, int D, int L_) : L(L_), LV(L_ * VEC), n(0), warps(L_ / 32) {
+        const int per = blockDim.x / L_, mine = threadIdx.x / L_;
+        c0 = ((int)threadIdx.x - mine * L_) * VEC;
+        first = mine * warps;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) n += c0 + p * LV < D;
-        const int per = threads / L_;
         const int64_t base = (int64_t)blockIdx.x * per;
-        row = base + threadIdx.x / L_;
+        row = base + mine;
         step = (int64_t)gridDim.x * per;
         turns = base < rows ? (int)((rows - base + step - 1) / step) : 0;
     }
@@ -124,33 +125,31 @@ __device__ __forceinline__ float over_lanes(float x, int L, F&& both) {
 }
 // Sums of two values over a row; `part` has two halves, used in turn, so that one barrier a
 // turn is enough.
-template <int N>
-__device__ __forceinline__ void row_sums(float& a, float& b, int L, float2 (*part)[N / 32], int turn) {
+template <int N, int VEC>
+__device__ __forceinline__ void row_sums(float& a, float& b, const Place<VEC>& at, float2 (*part)[N / 32], int turn) {
     auto plus = [](float x, float y) { return x + y; };
-    a = over_lanes(a, L, plus);
-    b = over_lanes(b, L, plus);
-    if (L <= 32) return;
+    a = over_lanes(a, at.L, plus);
+    b = over_lanes(b, at.L, plus);
+    if (at.L <= 32) return;
     float2* p = part[turn & 1];
-    const int warp = threadIdx.x >> 5, w = L / 32, first = warp & ~(w - 1);
-    if ((threadIdx.x & 31) == 0) p[warp] = make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
     a = b = 0.f;
-    for (int i = 0; i < w; ++i) {
-        const float2 s = p[first + i];
+    for (int i = 0; i < at.warps; ++i) {
+        const float2 s = p[at.first + i];
         a += s.x;
         b += s.y;
     }
 }
-template <int N>
-__device__ __forceinline__ float row_max(float m, int L, float (*part)[N / 32], int turn) {
-    m = over_lanes(m, L, max_nan);
-    if (L <= 32) return m;
+template <int N, int VEC>
+__device__ __forceinline__ float row_max(float m, const Place<VEC>& at, float (*part)[N / 32], int turn) {
+    m = over_lanes(m, at.L, max_nan);
+    if (at.L <= 32) return m;
     float* p = part[turn & 1];
-    const int warp = threadIdx.x >> 5, w = L / 32, first = warp & ~(w - 1);
-    if ((threadIdx.x & 31) == 0) p[warp] = m;
+    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = p[first];
-    for (int i = 1; i < w; ++i) m = max_nan(m, p[first + i]);
+    m = p[at.first];
+    for (int i = 1; i < at.warps; ++i) m = max_nan(m, p[at.first + i]);
     return m;
 }
 
@@ -267,8 +266,9 @@ struct NormDims {
     float eps;
 };
 
-// Blocks of N threads an SM holds.
-constexpr int per_sm(int N) { return 512 / N; }
+// Threads an SM holds, and blocks of N of them.
+constexpr int kPerSm = 512;
+constexpr int per_sm(int N) { return kPerSm / N; }
 constexpr int kFwdSlots = 2 * kPieces, kBwdSlots = 3 * kPieces;
 
 template <typename TX, typename TR, int N, bool kQuant>
@@ -283,7 +283,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
     __shared__ float2 part[2][N / 32];
     __shared__ float most[kQuant ? 4 : 1][N / 32];
     const Slots<kFwdSlots, S, N> ring(sm);
-    const Place<VEC> at(d.rows, d.D, d.L, N);
+    const Place<VEC> at(d.rows, d.D, d.L);
     const float inv_d = 1.f / d.D;
     // where the thread's pieces of the row copied and of the row worked on are
     const TX* x_next = x + at.row * d.x_stride + at.c0;
@@ -330,7 +330,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
             for (int j = 0; j < VEC / 2; ++j) ss = fma2(a[p][j], a[p][j], ss);
         }
         float sum = sum2(ss), none = 0.f;
-        row_sums<N>(sum, none, at.L, part, turn);
+        row_sums<N>(sum, none, at, part, turn);
         const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
         if constexpr (!kQuant) {
 #pragma unroll
@@ -425,7 +425,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     if (p >= n) break;
                     m = max_nan(m, weighted(p));
                 }
-                m = row_max<N>(m, at.L, most, turn);
+                m = row_max<N>(m, at, most, turn);
                 const Scale c = scale_of(m, r);
                 if (at.c0 == 0 && n) scales[now] = c.scale;
                 if constexpr (kWide) {
@@ -444,7 +444,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                             if (p >= n) break;
                             left = left_out(p, m, left);
                         }
-                        left = row_max<N>(left, at.L, most + 2, turn);
+                        left = row_max<N>(left, at, most + 2, turn);
 #pragma unroll
                         for (int p = 0; p < kPieces; ++p) {
                             if (!(near >> p & 1)) continue;
@@ -488,7 +488,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ float2 part[2][N / 32];
     const Slots<kBwdSlots, S, N> ring(sm);
-    const Place<VEC> at(d.rows, d.D, d.L, N);
+    const Place<VEC> at(d.rows, d.D, d.L);
     const float inv_d = 1.f / d.D;
     const TR* h_next = h + at.row * d.r_stride + at.c0;
     const int64_t h_step = at.step * d.r_stride, step = at.step * d.D;
@@ -538,7 +538,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
             }
         }
         float sq = sum2(ss), st = sum2(tx);
-        row_sums<N>(sq, st, at.L, part, turn);
+        row_sums<N>(sq, st, at, part, turn);
         const float r = rsqrtf(fmaf(sq, inv_d, d.eps));
         // mean(t hh) = r mean(t h), times r of hh
         const uint64_t m = twice(-st * r * r * inv_d), r2 = twice(r);
@@ -618,14 +618,23 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
 // a lane of fewer (35 x 1755 rows of 512 bf16 with 16 lanes 86.3 us forward and backward, with
 // 32 83.3).  The 8-bit form, which computes more, takes kPieces from 8 lanes on (29 x 1429 rows
 // of 272 with 16 lanes 15.9 us, with 32 23.2), but all of a group of columns with a scale.
-int lanes_of(int D, int vec, bool quant, int group) {
+// Past a warp: a power of two, but where `most`, the most that let an SM hold as many rows as
+// the fewest would: 96 of them hold 288 or 384 pieces in five rows where 128 hold four.  Of 25 M
+// elements in the 8-bit form rows of 2304 bf16 so take 64 -> 71% of the copy rate with groups
+// of 128 and 71 -> 78% without, of 2304 float32 62 -> 73 and 71 -> 88; of 6144 bf16 with 192
+// lanes 66% and with 256, the most of two rows, 70.  Rows without a residual, which have less in
+// flight, gain (2304 bf16 80 -> 87%); those with one lose (88 -> 84%), and so does the backward
+// (2304 bf16 with a float32 stream 91 -> 83%).
+int lanes_of(int D, int vec, bool quant, int group, bool most) {
     int L = 8;
     if (quant)
         while (L * vec < group) L *= 2;
     else
         while (L < 32 && L * 2 * vec < D) L *= 2;
-    while (L * kPieces * vec < D) L *= 2;
-    return L;
+    while ((L < 32 || !most) && L * kPieces * vec < D) L *= 2;
+    if (L * kPieces * vec >= D) return L;
+    const int warp = 32 * kPieces * vec, fewest = (D + warp - 1) / warp * 32, rows = kPerSm / fewest;
+    return kPerSm / rows / 32 * 32;
 }
 
 template <typename TX, typename TR, int N, bool kQuant>
@@ -635,8 +644,9 @@ cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    const int64_t want = (d.rows + N / d.L - 1) / (N / d.L), cap = (int64_t)sm_count() * per_sm(N);
-    return launch_dependent(kern, dim3((unsigned)(want < cap ? want : cap)), N, smem, st, d, (const TX*)c.x,
+    const int per = d.L < N ? N / d.L : 1, threads = per * d.L;
+    const int64_t want = (d.rows + per - 1) / per, cap = (int64_t)sm_count() * per_sm(threads);
+    return launch_dependent(kern, dim3((unsigned)(want < cap ? want : cap)), threads, smem, st, d, (const TX*)c.x,
                             (const TR*)c.res, (const TX*)c.w, (TR*)c.h, c.y, c.scales);
 }
 
@@ -659,14 +669,15 @@ cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
 
 template <typename TX, typename TR, bool kQuant>
 cudaError_t fwd_n(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
-    return d.L <= 128 ? fwd<TX, TR, 128, kQuant>(c, d, st) : d.L == 256 ? fwd<TX, TR, 256, kQuant>(c, d, st)
+    return d.L <= 128 ? fwd<TX, TR, 128, kQuant>(c, d, st) : d.L <= 256 ? fwd<TX, TR, 256, kQuant>(c, d, st)
                                                                        : fwd<TX, TR, 512, kQuant>(c, d, st);
 }
 
 template <typename TX, typename TR>
 cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
-    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR), kind == AddNormKind::QUANT, c.group), c.group ? c.group : c.D,
-                     c.group == 32 ? 5 : c.group == 64 ? 6 : 7, c.eps};
+    const bool quant = kind == AddNormKind::QUANT, most = quant || (kind == AddNormKind::FWD && !c.res);
+    const NormDims d{c.rows, c.x_stride, c.r_stride, c.D, lanes_of(c.D, 16 / (int)sizeof(TR), quant, c.group, most),
+                     c.group ? c.group : c.D, c.group == 32 ? 5 : c.group == 64 ? 6 : 7, c.eps};
     switch (kind) {
         case AddNormKind::FWD: return fwd_n<TX, TR, false>(c, d, st);
         case AddNormKind::QUANT: return fwd_n<TX, TR, true>(c, d, st);
@@ -680,7 +691,7 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
 // launch: 1 to 16 blocks of rows of 768 to 4096 elements 4.6 to 5.3 us a call, as two launches
 // 6.0 to 6.4; with two turns 6.0 to 6.8.
 AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide) {
-    const int L = lanes_of(D, 16 / wide, false, 0), n = L <= 256 ? 256 : 512;
+    const int L = lanes_of(D, 16 / wide, false, 0, false), n = L <= 256 ? 256 : 512;
     const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * per_sm(n);
     if (want <= kMostCluster) return {(int)(want < 1 ? 1 : want), true};
     return {(int)(want < cap ? want : cap), false};

@@ -410,3 +410,31 @@ def test_refusals():
         gdn.gdn_add_norm_fwd(1, r, w)
     gdn.gdn_add_norm_bwd(**ok)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,D,dtype,stream,group,ones", [
+    (1700, 2304, "bf16", "bf16", 128, False), (1700, 1152, "f32", "f32", 32, False), (1601, 1280, "bf16", "f32", 128, True),
+    (803, 3000, "bf16", "bf16", 0, False), (1000, 2560, "f32", "f32", 0, True), (931, 5120, "bf16", "bf16", 128, True),
+    (1403, 1032, "bf16", "f32", 0, False), (400, 2052, "f32", "f32", 0, False)])
+def test_rows_of_three_or_five_warps(rows, D, dtype, stream, group, ones):
+    """Rows that neither one, two, four nor more powers of two of warps hold well, some turns a
+    block: 8-bit numbers to the last one, also where exact ties are frequent (a weight of ones),
+    and the norm without a residual."""
+    x, r, w, _, _ = _inputs(rows, D, dtype, stream, True, seed=4)
+    if ones:
+        w = torch.ones_like(w)
+    y, s, h = gdn.gdn_add_norm_quant(x, r, w, eps=EPS, group=group)
+    plain, _ = gdn.gdn_add_norm_fwd(x, None, w, eps=EPS)
+    torch.cuda.synchronize()
+    rh = _np(x) + _np(r)
+    _within("h", h, rh, f=2.0 ** -23)
+    ry, _ = block.add_norm_fwd(_np(x), _np(r), _np(w), EPS)
+    _within("scales", s, block.quantise(ry, group)[1])
+    t = (rh * _np(w)).reshape(rows, -1, group or D)
+    exact = t * 448.0 / np.abs(t).max(-1, keepdims=True)
+    want, got = block.e4m3(exact), _np(y.float()).reshape(t.shape)
+    wrong = want != got
+    assert not (wrong & (np.abs(exact) >= 2.0 ** -6)).any()
+    middle = (want + got) / 2
+    assert (np.abs(exact - middle) <= 2.0 ** -20 * np.abs(middle))[wrong].all()
+    _within("y", plain, block.add_norm_fwd(_np(x), None, _np(w), EPS)[0])
