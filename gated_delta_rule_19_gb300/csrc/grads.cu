@@ -242,7 +242,8 @@ __device__ __forceinline__ Norm norm_of(Sum x, float max_norm) {
     }
     if (threadIdx.x == 0) {
         const double n = sqrt((double)x.s + (double)x.c + x.rest);
-        // a norm that is not finite says nothing of how long the gradients are: they stay
+        // where an element is not finite the norm says nothing of how long the gradients are: they
+        // stay; finite ones whose norm leaves float32's range are clipped by the float64 norm
         all = {(float)n, n > (double)max_norm && n <= DBL_MAX ? (float)((double)max_norm / n) : 1.f};
     }
     __syncthreads();

@@ -1091,8 +1091,8 @@ def gdn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
 def gdn_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace=None, stream=None):
     """Scales the gradients by ``min(1, max_norm / norm)`` of :func:`gdn_grad_norm`, in place
     or into ``out`` (a tensor for each, float32 or bfloat16, of the same shape and order;
-    ``gdn_clip_grads``).  Where the norm is NaN or infinite they are left as they were.
-    Returns ``norm``, that of the gradients before."""
+    ``gdn_clip_grads``).  Where one of their elements is NaN or infinite they are left as
+    they were.  Returns ``norm``, that of the gradients before."""
     return (_layer or _binding()).clip_grads(grads, max_norm, out, norm, workspace, _raw(stream))
 
 
