@@ -59,10 +59,10 @@ def test_axes_refused(lib):
     assert both(ok, positions=FAKE + 2) == {INVALID}
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", ok, ROPE_FWD, sized=0, k_out=FAKE + 16) == INVALID
     # pairs that are copied one by one, of many tokens: their angles are gathered first
-    turns = _axes(lib, sections=(12, 10, 10), alternating=1)
+    turns = _axes(lib, sections=(12, 10, 10), alternating=1, T=10000)
     need = lib.load_library().gdn_qk_norm_rope_axes_fwd_workspace_bytes
     assert need(ctypes.byref(ok)) == 0 and need(ctypes.byref(_axes(lib, sections=(12, 10, 10), alternating=1, T=10))) == 0
-    assert need(ctypes.byref(turns)) == 2 * 1000 * 64 * 4
+    assert need(ctypes.byref(turns)) == 2 * 10000 * 64 * 4
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1000) == WS
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1 << 40, workspace=None) == INVALID
     assert _call(lib, "gdn_qk_norm_rope_axes_fwd", turns, ROPE_FWD, sized=1 << 40, workspace=FAKE + GAP) == INVALID
