@@ -123,27 +123,44 @@ __device__ __forceinline__ float over_lanes(float x, int L, F&& both) {
     if (L > 16) x = both(x, __shfl_xor_sync(0xffffffffu, x, 16));
     return x;
 }
-// Sums of two values over a row; `part` has two halves, used in turn, so that one barrier a
-// turn is enough.
-template <int N, int VEC>
-__device__ __forceinline__ void row_sums(float& a, float& b, const Place<VEC>& at, float2 (*part)[N / 32], int turn) {
-    auto plus = [](float x, float y) { return x + y; };
-    a = over_lanes(a, at.L, plus);
-    b = over_lanes(b, at.L, plus);
+struct Plus {
+    __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
+};
+struct Max {
+    __device__ __forceinline__ float operator()(float x, float y) const { return max_nan(x, y); }
+};
+// Over a row the sum of a, and of b what F makes of it; `part` has two halves, used in turn, so
+// that one barrier a turn is enough.
+template <int N, typename F, int VEC>
+__device__ __forceinline__ void row_both(float& a, float& b, F f, const Place<VEC>& at, float2 (*part)[N / 32], int turn) {
+    a = over_lanes(a, at.L, Plus());
+    b = over_lanes(b, at.L, f);
     if (at.L <= 32) return;
     float2* p = part[turn & 1];
     if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    a = b = 0.f;
-    for (int i = 0; i < at.warps; ++i) {
+    const float2 s = p[at.first];
+    a = s.x, b = s.y;
+    for (int i = 1; i < at.warps; ++i) {
         const float2 s = p[at.first + i];
         a += s.x;
-        b += s.y;
+        b = f(b, s.y);
     }
 }
 template <int N, int VEC>
+__device__ __forceinline__ float row_sum(float a, const Place<VEC>& at, float2 (*part)[N / 32], int turn) {
+    a = over_lanes(a, at.L, Plus());
+    if (at.L <= 32) return a;
+    float2* p = part[turn & 1];
+    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5].x = a;
+    __syncthreads();
+    a = p[at.first].x;
+    for (int i = 1; i < at.warps; ++i) a += p[at.first + i].x;
+    return a;
+}
+template <int N, int VEC>
 __device__ __forceinline__ float row_max(float m, const Place<VEC>& at, float (*part)[N / 32], int turn) {
-    m = over_lanes(m, at.L, max_nan);
+    m = over_lanes(m, at.L, Max());
     if (at.L <= 32) return m;
     float* p = part[turn & 1];
     if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = m;
@@ -281,7 +298,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
     await_previous();
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ float2 part[2][N / 32];
-    __shared__ float most[kQuant ? 4 : 1][N / 32];
+    __shared__ float lefts[kQuant && sizeof(TR) == 4 ? 2 : 1][N / 32];
     const Slots<kFwdSlots, S, N> ring(sm);
     const Place<VEC> at(d.rows, d.D, d.L);
     const float inv_d = 1.f / d.D;
@@ -329,10 +346,8 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) ss = fma2(a[p][j], a[p][j], ss);
         }
-        float sum = sum2(ss), none = 0.f;
-        row_sums<N>(sum, none, at, part, turn);
-        const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
         if constexpr (!kQuant) {
+            const float r = rsqrtf(fmaf(row_sum<N>(sum2(ss), at, part, turn), inv_d, d.eps));
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 if (p >= n) break;
@@ -371,7 +386,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 return is ? left_of<TX, TR>(ring.at(slot, p), place(p), wv[p], most, left) : left;
             };
             // the piece's numbers, and whether a quotient is next to a middle
-            auto coded = [&](int p, const Scale& c, uint2& code, Quotients& z) {
+            auto coded = [&](int p, const Scale& c, float r, uint2& code, Quotients& z) {
                 uint32_t q[4] = {0, 0, 0, 0}, near = kNear + 1;
                 if (c.plain) {
 #pragma unroll
@@ -397,6 +412,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 else *reinterpret_cast<uint32_t*>(to) = code.x;
             };
             if (d.group < d.D) {
+                const float r = rsqrtf(fmaf(row_sum<N>(sum2(ss), at, part, turn), inv_d, d.eps));
                 const int lanes = d.group / VEC;  // a group's, neighbours: 4 to 32 of them
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
@@ -407,7 +423,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     uint2 code;
                     Quotients z;
                     if constexpr (kWide) {
-                        const bool near = p < n && coded(p, c, code, z);
+                        const bool near = p < n && coded(p, c, r, code, z);
                         if (__any_sync(0xffffffffu, near)) {
                             const float left = over_lanes(p < n ? left_out(p, m, -FLT_MAX) : -FLT_MAX, lanes, max_nan);
                             if (near) code = exact(p, m, left, z);
@@ -415,7 +431,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                         if (p >= n) continue;
                     }
                     if (((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
-                    if (!kWide && coded(p, c, code, z)) code = exact(p, m, 0.f, z);
+                    if (!kWide && coded(p, c, r, code, z)) code = exact(p, m, 0.f, z);
                     store(p, code);
                 }
             } else {
@@ -425,7 +441,10 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     if (p >= n) break;
                     m = max_nan(m, weighted(p));
                 }
-                m = row_max<N>(m, at, most, turn);
+                // the largest |t| needs nothing of the row's norm: both in one exchange
+                float sum = sum2(ss);
+                row_both<N>(sum, m, Max(), at, part, turn);
+                const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
                 const Scale c = scale_of(m, r);
                 if (at.c0 == 0 && n) scales[now] = c.scale;
                 if constexpr (kWide) {
@@ -435,7 +454,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                     for (int p = 0; p < kPieces; ++p) {
                         if (p >= n) break;
                         Quotients z;
-                        near |= (uint32_t)coded(p, c, code[p], z) << p;
+                        near |= (uint32_t)coded(p, c, r, code[p], z) << p;
                     }
                     if (at.L > 32 ? __syncthreads_or(near) : __any_sync(0xffffffffu, near)) {
                         float left = -FLT_MAX;
@@ -444,12 +463,12 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                             if (p >= n) break;
                             left = left_out(p, m, left);
                         }
-                        left = row_max<N>(left, at, most + 2, turn);
+                        left = row_max<N>(left, at, lefts, turn);
 #pragma unroll
                         for (int p = 0; p < kPieces; ++p) {
                             if (!(near >> p & 1)) continue;
                             Quotients z;
-                            coded(p, c, code[p], z);
+                            coded(p, c, r, code[p], z);
                             code[p] = exact(p, m, left, z);
                         }
                     }
@@ -464,7 +483,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                         if (p >= n) break;
                         uint2 code;
                         Quotients z;
-                        if (coded(p, c, code, z)) code = exact(p, m, 0.f, z);
+                        if (coded(p, c, r, code, z)) code = exact(p, m, 0.f, z);
                         store(p, code);
                     }
                 }
@@ -538,7 +557,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
             }
         }
         float sq = sum2(ss), st = sum2(tx);
-        row_sums<N>(sq, st, at, part, turn);
+        row_both<N>(sq, st, Plus(), at, part, turn);
         const float r = rsqrtf(fmaf(sq, inv_d, d.eps));
         // mean(t hh) = r mean(t h), times r of hh
         const uint64_t m = twice(-st * r * r * inv_d), r2 = twice(r);
