@@ -596,8 +596,8 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         slot = slot + 1 == S ? 0 : slot + 1;
     }
     wait_group<0>();
-    // the sums of a warp's rows, then those of the block's, one after the other: the same call
-    // gives the same bits
+    // the sums of a warp's rows; then each warp or row of warps leaves its own, and a thread adds
+    // four columns' in a fixed order: the same call gives the same bits
     const bool part_warp = at.L < 32;
     if (part_warp) {
 #pragma unroll
@@ -615,28 +615,29 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     }
     __syncthreads();
     float* col = (float*)sm;
-    const int wide = part_warp ? 32 : at.L;
-    const bool adds = !part_warp || (int)(threadIdx.x & 31) < at.L;
-    for (int g = 0; g < N / wide; ++g) {
-        if ((int)threadIdx.x / wide == g && adds) {
+    const int wide = part_warp ? 32 : at.L, parts = N / wide;
+    if (!part_warp || (int)(threadIdx.x & 31) < at.L) {
+        float* to = col + (int)threadIdx.x / wide * d.D + at.c0;
 #pragma unroll
-            for (int p = 0; p < kPieces; ++p) {
-                if (p >= at.n) break;
+        for (int p = 0; p < kPieces; ++p) {
+            if (p >= at.n) break;
 #pragma unroll
-                for (int j = 0; j < VEC / 2; ++j) {
-                    float* c = col + at.c0 + p * at.LV + 2 * j;
-                    float lo, hi;
-                    unpair(acc[p][j], lo, hi);
-                    c[0] = g ? c[0] + lo : lo;
-                    c[1] = g ? c[1] + hi : hi;
-                }
+            for (int j = 0; j < VEC / 4; ++j) {
+                const uint64_t four[2] = {acc[p][2 * j], acc[p][2 * j + 1]};
+                *reinterpret_cast<uint4*>(to + p * at.LV + 4 * j) = put(four);
             }
         }
-        __syncthreads();
     }
-    if constexpr (!kCluster) {
-        for (int c = threadIdx.x; c < d.D; c += N) sums[(int64_t)blockIdx.x * d.D + c] = col[c];
-    } else {
+    __syncthreads();
+    for (int c = 4 * threadIdx.x; c < d.D; c += 4 * N) {
+        float4 s = *reinterpret_cast<const float4*>(col + c);
+        for (int i = 1; i < parts; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(col + i * d.D + c);
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+        *reinterpret_cast<float4*>(kCluster ? col + c : sums + (int64_t)blockIdx.x * d.D + c) = s;
+    }
+    if constexpr (kCluster) {
         cluster_sync();
         for (int c = blockIdx.x * N + threadIdx.x; c < d.D; c += gridDim.x * N) store1(dw + c, cluster_sum(col + c));
         cluster_sync();  // no block leaves before the others have read its sums
@@ -682,7 +683,7 @@ cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
 template <typename TX, typename TR, int N>
 cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     constexpr int smem = Slots<kBwdSlots, kStages, N>::BYTES;
-    static_assert(smem >= kAddNormMost * 4, "the column sums fit the ring");
+    static_assert(smem >= N * kPieces * (16 / (int)sizeof(TR)) * 4, "every thread's column sums fit the ring");
     static std::atomic<uint64_t> done{0}, done1{0};
     const TR *h = (const TR*)c.h_in, *dh = (const TR*)c.dh;
     const TX *w = (const TX*)c.w, *dy = (const TX*)c.dy;
