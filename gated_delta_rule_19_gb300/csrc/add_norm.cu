@@ -137,6 +137,25 @@ __device__ __forceinline__ float over_lanes(float x, int L, Max both) {
     if (L >= 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
     return over_lanes<Max>(x, L, static_cast<Max&&>(both));
 }
+// The largest of each piece over the groups of `lanes` lanes that hold the columns of a scale.
+__device__ __forceinline__ void over_groups(float (&m)[kPieces], int lanes, int D, int LV) {
+    auto all = [&](auto&& f) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            if (p * LV >= D) break;
+            m[p] = f(m[p]);
+        }
+    };
+    auto with = [](int off) { return [off](float x) { return max_nan(x, __shfl_xor_sync(0xffffffffu, x, off)); }; };
+    if (lanes == 32) {
+        all([](float x) { return over_lanes(x, 32, Max()); });
+        return;
+    }
+    all(with(1));
+    all(with(2));
+    if (lanes > 4) all(with(4));
+    if (lanes > 8) all(with(8));
+}
 // Over a row the sum of a, and of b what F makes of it; `part` has two halves, used in turn, so
 // that one barrier a turn is enough.
 template <int N, typename F, int VEC>
@@ -419,30 +438,50 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = code;
                 else *reinterpret_cast<uint32_t*>(to) = code.x;
             };
+            // With a float32 stream quotients next to a middle are decided behind all pieces: a call
+            // between two keeps them from being worked on together (25 M elements in groups of
+            // 128, 2048 columns: 82 to 91% of the copy rate, of float32 2304 84 to 93).  The wider
+            // pieces of bf16 have enough to do each, and lose by it (1 to 2%).
+            uint32_t near = 0;  // a bit a piece
+            auto first = [&](int p, const Scale& c, float r, float most) {
+                uint2 code;
+                Quotients z;
+                const bool is = coded(p, c, r, code, z);
+                if constexpr (kWide) near |= (uint32_t)is << p;
+                else if (is) code = exact(p, most, 0.f, z);
+                store(p, code);
+            };
+            auto again = [&](int p, const Scale& c, float r, float most, float left) {
+                uint2 code;
+                Quotients z;
+                coded(p, c, r, code, z);
+                store(p, exact(p, most, left, z));
+            };
             if (d.group < d.D) {
-                const float r = rsqrtf(fmaf(row_sum<N>(sum2(ss), at, part, turn), inv_d, d.eps));
                 const int lanes = d.group / VEC;  // a group's, neighbours: 4 to 32 of them
+                float m[kPieces];
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) m[p] = p < n ? weighted(p) : 0.f;
+                over_groups(m, lanes, d.D, at.LV);
+                const float r = rsqrtf(fmaf(row_sum<N>(sum2(ss), at, part, turn), inv_d, d.eps));
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
-                    if (p * at.LV >= d.D) break;
-                    float m = p < n ? weighted(p) : 0.f;
-                    if constexpr (kWide) m = over_lanes(m, lanes, Max());
-                    else m = over_lanes(m, lanes, max_nan);  // of half a warp at most
-                    if (!kWide && p >= n) continue;
-                    const Scale c = scale_of(m, r);
-                    uint2 code;
-                    Quotients z;
-                    if constexpr (kWide) {
-                        const bool near = p < n && coded(p, c, r, code, z);
-                        if (__any_sync(0xffffffffu, near)) {
-                            const float left = over_lanes(p < n ? left_out(p, m, -FLT_MAX) : -FLT_MAX, lanes, max_nan);
-                            if (near) code = exact(p, m, left, z);
-                        }
-                        if (p >= n) continue;
-                    }
+                    if (p >= n) break;
+                    const Scale c = scale_of(m[p], r);
                     if (((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
-                    if (!kWide && coded(p, c, r, code, z)) code = exact(p, m, 0.f, z);
-                    store(p, code);
+                    first(p, c, r, m[p]);
+                }
+                if (kWide ? __any_sync(0xffffffffu, near) : near) {
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) {
+                        const bool mine = near >> p & 1;
+                        float left = 0.f;
+                        if constexpr (kWide) {
+                            if (!__any_sync(0xffffffffu, mine)) continue;
+                            left = over_lanes(p < n ? left_out(p, m[p], -FLT_MAX) : -FLT_MAX, lanes, max_nan);
+                        }
+                        if (mine) again(p, scale_of(m[p], r), r, m[p], left);
+                    }
                 }
             } else {
                 float m = 0.f;
@@ -457,45 +496,27 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
                 const Scale c = scale_of(m, r);
                 if (at.c0 == 0 && n) scales[now] = c.scale;
-                if constexpr (kWide) {
-                    uint2 code[kPieces];
-                    uint32_t near = 0;  // a bit a piece
 #pragma unroll
-                    for (int p = 0; p < kPieces; ++p) {
-                        if (p >= n) break;
-                        Quotients z;
-                        near |= (uint32_t)coded(p, c, r, code[p], z) << p;
-                    }
+                for (int p = 0; p < kPieces; ++p) {
+                    if (p >= n) break;
+                    first(p, c, r, m);
+                }
+                float left = 0.f;
+                if constexpr (kWide) {
                     if (at.L > 32 ? __syncthreads_or(near) : __any_sync(0xffffffffu, near)) {
-                        float left = -FLT_MAX;
+                        left = -FLT_MAX;
 #pragma unroll
                         for (int p = 0; p < kPieces; ++p) {
                             if (p >= n) break;
                             left = left_out(p, m, left);
                         }
                         left = row_max<N>(left, at, lefts, turn);
-#pragma unroll
-                        for (int p = 0; p < kPieces; ++p) {
-                            if (!(near >> p & 1)) continue;
-                            Quotients z;
-                            coded(p, c, r, code[p], z);
-                            code[p] = exact(p, m, left, z);
-                        }
                     }
+                }
+                if (near) {
 #pragma unroll
-                    for (int p = 0; p < kPieces; ++p) {
-                        if (p >= n) break;
-                        store(p, code[p]);
-                    }
-                } else {
-#pragma unroll
-                    for (int p = 0; p < kPieces; ++p) {
-                        if (p >= n) break;
-                        uint2 code;
-                        Quotients z;
-                        if (coded(p, c, r, code, z)) code = exact(p, m, 0.f, z);
-                        store(p, code);
-                    }
+                    for (int p = 0; p < kPieces; ++p)
+                        if (near >> p & 1) again(p, c, r, m, left);
                 }
             }
         }
