@@ -2292,7 +2292,7 @@ gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, fl
     cudaStream_t cs = (cudaStream_t)stream;
     gdn::GradPart* part = (gdn::GradPart*)workspace;
     int parts = 0;
-    if (const int blocks = gdn::grad_cluster(g, count, clip)) {
+    if (const int blocks = gdn::grad_cluster(g, count)) {
         cudaError_t e = timed(gdn::KID_GRAD_CLIP, cs,
                               [&] { return gdn::launch_grad_cluster(g, count, blocks, max_norm, norm, clip, cs); });
         return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gradient clipping kernel");
@@ -2428,7 +2428,7 @@ gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const 
 }
 
 size_t gdn_grad_workspace_bytes(const gdn_grad* g, int64_t count) {
-    if (count < 0 || count > (int64_t)1 << 20 || (count && !g) || gdn::grad_cluster(g, count, true)) return 0;
+    if (count < 0 || count > (int64_t)1 << 20 || (count && !g) || gdn::grad_cluster(g, count)) return 0;
     return gdn::grad_parts(count) * sizeof(gdn::GradPart);
 }
 

@@ -524,10 +524,11 @@ cudaError_t cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm
     return launch_one_cluster(grad_clip_kernel<N>, blocks, kThreads * kWorkers, 0, done, st, l, max_norm, norm, clip);
 }
 
-// Tiles that one cluster takes, to clip them or for their norm alone: a call of bf16 clips 1 to
-// 48 tiles in 5.0 to 6.3 us, 96 in 8.0, in two launches 6.9 to 7.2 any of them; the norm
-// of 144 takes 6.5 us either way, of 48 5.2 and 6.4.
-constexpr int64_t kClusterTiles = 48, kClusterNormTiles = 144;
+// Tiles that one cluster takes, to clip them or for their norm alone.  Calls one behind the
+// other take 4.2 to 5.6 us of 1 to 48 tiles, as two launches, bound by the host, 5.8 to 8.0; the
+// GPU alone needs 4.6 to 6.0, and of two launches 3.4 to 5.2.  With 96 tiles the host's
+// time is even, and the GPU's 6.2 to 6.9 against 3.6 to 4.5.
+constexpr int64_t kClusterTiles = 48;
 
 }  // namespace
 
@@ -538,11 +539,11 @@ size_t grad_parts(int64_t count) {
     return (size_t)launches * kSumPerSm * sm_count();
 }
 
-int grad_cluster(const gdn_grad* g, int64_t count, bool clip) {
+int grad_cluster(const gdn_grad* g, int64_t count) {
     if (count > kFew) return 0;
     int64_t tiles = 0;
     for (int64_t i = 0; i < count; ++i) tiles += (g[i].n + kTile - 1) / kTile;
-    if (tiles > (clip ? kClusterTiles : kClusterNormTiles)) return 0;
+    if (tiles > kClusterTiles) return 0;
     int blocks = 1;
     while (blocks < kMostCluster && blocks * kWorkers < tiles) blocks *= 2;
     return blocks;
