@@ -399,9 +399,11 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 }
                 return m;
             };
-            // What the float32 t leave out of the group's largest |t|: sums and products of bf16
-            // are exact (but for addends 2^16 apart), of float32 it is taken from the elements
-            // that are the largest, where a quotient next to a middle asks for it.
+            // What the float32 t leave out of the group's largest |t|: with a float32 stream it is
+            // taken from the elements that are the largest, where a quotient next to a middle
+            // asks for it.  Of bf16, whose sums and products mostly need no more bits than
+            // float32 has, the largest counts as float32 holds it: where it is rounded, by up to
+            // 2^-24, a quotient as close as that to a middle may fall on either side.
             auto left_out = [&](int p, float most, float left) {
                 bool is = false;
 #pragma unroll

@@ -169,7 +169,8 @@ def test_quant_gives_the_nearest_number(rows, D, dtype, stream, group):
     """Every 8-bit number is the one nearest to the exact quotient 448 t / max|t| of the group
     (t = (x + residual) w; the row's norm divides out): of 3 million elements not one is on the
     wrong side of a middle.  Below 2^-6 a middle may be decided by float32's error: within 2^-20
-    of it either side is taken."""
+    of it either side is taken.  (In bf16 the largest t is a float32, off by up to 2^-24: these
+    cases have no quotient that close to a middle but exact ties.)"""
     x, r, w, _, _ = _inputs(rows, D, dtype, stream, False, seed=9)
     y, _, _ = gdn.gdn_add_norm_quant(x, r, w, eps=EPS, group=group)
     torch.cuda.synchronize()
@@ -434,7 +435,8 @@ def test_rows_of_three_or_five_warps(rows, D, dtype, stream, group, ones):
     exact = t * 448.0 / np.abs(t).max(-1, keepdims=True)
     want, got = block.e4m3(exact), _np(y.float()).reshape(t.shape)
     wrong = want != got
-    assert not (wrong & (np.abs(exact) >= 2.0 ** -6)).any()
     middle = (want + got) / 2
-    assert (np.abs(exact - middle) <= 2.0 ** -20 * np.abs(middle))[wrong].all()
+    # bf16: the largest t is rounded to float32, by up to 2^-24 (and 2^-53 of float64's own)
+    near = np.where(np.abs(exact) < 2.0 ** -6, 2.0 ** -20, 1.01 * 2.0 ** -24 if stream == "bf16" else 0.0)
+    assert (np.abs(exact - middle) <= near * np.abs(middle))[wrong].all()
     _within("y", plain, block.add_norm_fwd(_np(x), None, _np(w), EPS)[0])
