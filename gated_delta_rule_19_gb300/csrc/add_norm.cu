@@ -138,11 +138,12 @@ __device__ __forceinline__ float over_lanes(float x, int L, Max both) {
     return over_lanes<Max>(x, L, static_cast<Max&&>(both));
 }
 // The largest of each piece over the groups of `lanes` lanes that hold the columns of a scale.
+template <int K>
 __device__ __forceinline__ void over_groups(float (&m)[kPieces], int lanes, int D, int LV) {
     auto all = [&](auto&& f) {
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            if (p * LV >= D) break;
+            if (K ? p >= K : p * LV >= D) break;
             m[p] = f(m[p]);
         }
     };
@@ -315,7 +316,11 @@ constexpr int kPerSm = 512;
 constexpr int per_sm(int N) { return kPerSm / N; }
 constexpr int kFwdSlots = 2 * kPieces, kBwdSlots = 3 * kPieces;
 
-template <typename TX, typename TR, int N, bool kQuant>
+// K: every lane holds K pieces of its row (0: as many as it has, some fewer than others).  Without
+// branches between pieces they are worked on together; rows behind the last are computed from
+// what lies in the ring, but not written.  (25 M elements in 8 bits, groups of 128, of the
+// copy rate: 2048 columns of bf16 79 to 84%, 5120 75 to 83; a float32 stream 8192 78 to 88.)
+template <typename TX, typename TR, int N, bool kQuant, int K>
 __global__ void __launch_bounds__(N, per_sm(N))
 add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const TX* __restrict__ w, TR* h,
                     void* __restrict__ y, float* __restrict__ scales) {
@@ -338,7 +343,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
         if (next < d.rows) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                if (p >= at.n) break;
+                if (K ? p >= K : p >= at.n) break;
                 PX::copy(ring.at(slot, p), x_next + p * at.LV);
                 if (res) PR::copy(ring.at(slot, kPieces + p), r_next + p * at.LV);
             }
@@ -348,7 +353,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
     };
     uint4 wv[kPieces];
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) wv[p] = p < at.n ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
+    for (int p = 0; p < kPieces; ++p) wv[p] = (K ? p < K : p < at.n) ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
     if (at.turns) {
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) issue(i);
@@ -357,7 +362,8 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
         issue(fill);
         fill = fill + 1 == S ? 0 : fill + 1;
         wait_group<S - 1>();
-        const int n = now < d.rows ? at.n : 0;
+        const bool live = now < d.rows;
+        const int n = K ? K : live ? at.n : 0;
         uint64_t a[kPieces][VEC / 2], ss = twice(0.f);
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
@@ -368,7 +374,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 PR::load(ring.at(slot, kPieces + p), s);
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) a[p][j] = add2(a[p][j], s[j]);
-                if (h) PR::store(h + out + p * at.LV, a[p]);
+                if (h && (!K || live)) PR::store(h + out + p * at.LV, a[p]);
             }
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) ss = fma2(a[p][j], a[p][j], ss);
@@ -382,7 +388,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 PX::unpack(wv[p], f);
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) a[p][j] = mul2(mul2(a[p][j], twice(r)), f[j]);
-                PX::store((TX*)y + out + p * at.LV, a[p]);
+                if (!K || live) PX::store((TX*)y + out + p * at.LV, a[p]);
             }
         } else {
             constexpr bool kWide = sizeof(TR) == 4;
@@ -436,20 +442,21 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 return exact_piece<TX, TR>(ring.at(slot, p), place(p), wv[p], z, most, left);
             };
             auto store = [&](int p, const uint2& code) {
+                if (K && !live) return;
                 unsigned char* to = (unsigned char*)y + out + p * at.LV;
                 if constexpr (VEC == 8) *reinterpret_cast<uint2*>(to) = code;
                 else *reinterpret_cast<uint32_t*>(to) = code.x;
             };
-            // With a float32 stream quotients next to a middle are decided behind all pieces: a call
-            // between two keeps them from being worked on together (25 M elements in groups of
-            // 128, 2048 columns: 82 to 91% of the copy rate, of float32 2304 84 to 93).  The wider
-            // pieces of bf16 have enough to do each, and lose by it (1 to 2%).
+            // Quotients next to a middle are decided behind all pieces: a call between two keeps
+            // them from being worked on together (25 M elements of a float32 stream in groups of
+            // 128, 2048 columns: 82 to 91% of the copy rate).  Only bf16 in lanes of different
+            // numbers of pieces, which branch between them all the same, loses by it (1 to 2%).
             uint32_t near = 0;  // a bit a piece
             auto first = [&](int p, const Scale& c, float r, float most) {
                 uint2 code;
                 Quotients z;
                 const bool is = coded(p, c, r, code, z);
-                if constexpr (kWide) near |= (uint32_t)is << p;
+                if constexpr (kWide || K) near |= (uint32_t)is << p;
                 else if (is) code = exact(p, most, 0.f, z);
                 store(p, code);
             };
@@ -464,13 +471,13 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 float m[kPieces];
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) m[p] = p < n ? weighted(p) : 0.f;
-                over_groups(m, lanes, d.D, at.LV);
+                over_groups<K>(m, lanes, d.D, at.LV);
                 const float r = rsqrtf(fmaf(row_sum<N>(sum2(ss), at, part, turn), inv_d, d.eps));
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= n) break;
                     const Scale c = scale_of(m[p], r);
-                    if (((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
+                    if ((!K || live) && ((at.c0 + p * at.LV) & (d.group - 1)) == 0) scales[(out + p * at.LV) >> d.shift] = c.scale;
                     first(p, c, r, m[p]);
                 }
                 if (kWide ? __any_sync(0xffffffffu, near) : near) {
@@ -497,7 +504,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
                 row_both<N>(sum, m, Max(), at, part, turn);
                 const float r = rsqrtf(fmaf(sum, inv_d, d.eps));
                 const Scale c = scale_of(m, r);
-                if (at.c0 == 0 && n) scales[now] = c.scale;
+                if (at.c0 == 0 && (K ? live : n > 0)) scales[now] = c.scale;
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
                     if (p >= n) break;
@@ -529,7 +536,7 @@ add_norm_fwd_kernel(NormDims d, const TX* __restrict__ x, const TR* res, const T
 
 // Each block leaves one row of column sums in sums [gridDim.x][D]; the blocks of a cluster
 // (kCluster, the whole grid) add theirs up to dw, each some columns.
-template <typename TX, typename TR, int N, bool kCluster>
+template <typename TX, typename TR, int N, bool kCluster, int K>
 __global__ void __launch_bounds__(N, per_sm(N))
 add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__ w, const TX* __restrict__ dy,
                     const TR* __restrict__ dh, TX* __restrict__ dx, TR* __restrict__ dr, TX* __restrict__ dw, float* __restrict__ sums) {
@@ -549,7 +556,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         if (next < d.rows) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                if (p >= at.n) break;
+                if (K ? p >= K : p >= at.n) break;
                 PR::copy(ring.at(slot, p), h_next + p * at.LV);
                 PX::copy(ring.at(slot, kPieces + p), dy + in + p * at.LV);
                 if (dh) PR::copy(ring.at(slot, 2 * kPieces + p), dh + in + p * at.LV);
@@ -562,7 +569,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     uint64_t acc[kPieces][VEC / 2];
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-        wv[p] = p < at.n ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
+        wv[p] = (K ? p < K : p < at.n) ? PX::ldg(w + at.c0 + p * at.LV) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) acc[p][j] = twice(0.f);
     }
@@ -574,7 +581,8 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         issue(fill);
         fill = fill + 1 == S ? 0 : fill + 1;
         wait_group<S - 1>();
-        const int n = now < d.rows ? at.n : 0;
+        const bool live = now < d.rows;
+        const int n = K ? K : live ? at.n : 0;
         uint64_t ss = twice(0.f), tx = ss;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
@@ -598,7 +606,7 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
         // would leave room for half of the warps
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            if (p >= n) break;
+            if (K ? !live || p >= K : p >= n) break;
             uint64_t a[VEC / 2], g[VEC / 2], f[VEC / 2];
             PR::load(ring.at(slot, p), a);
             PX::load(ring.at(slot, kPieces + p), g);
@@ -667,6 +675,9 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
     }
 }
 
+// Whether every lane has three pieces, or every lane four (lane: a piece of all).
+bool even(int D, int lane) { return D == 3 * lane || D == 4 * lane; }
+
 // Lanes a row of pieces of VEC elements takes, kPieces a lane: a warp at least, or two pieces
 // a lane of fewer (35 x 1755 rows of 512 bf16 with 16 lanes 86.3 us forward and backward, with
 // 32 83.3).  The 8-bit form, which computes more, takes kPieces from 8 lanes on (29 x 1429 rows
@@ -675,7 +686,8 @@ add_norm_bwd_kernel(NormDims d, const TR* __restrict__ h, const TX* __restrict__
 // the fewest would: 96 of them hold 288 or 384 pieces in five rows where 128 hold four.  Of 25 M
 // elements in the 8-bit form rows of 2304 bf16 so take 73% of the copy rate for 66 in groups of
 // 128 and 84 for 80 without, with a float32 stream 84 for 69 and 87 for 73, of float32 91 for 82;
-// of 6144 bf16 192 lanes take 84% and 256, the most of two rows, 87.  Rows without a residual,
+// of 6144 bf16 192 lanes take 84% and 256, the most of two rows, 87.  Lanes that share the pieces
+// evenly come before more lanes (4608 float32 78 to 86%, 7168 bf16 73 to 78).  Rows without a residual,
 // which have less in flight, gain (2304 bf16 85 to 94%); those with one lose (89 to 85%), and
 // so does the backward (2304 bf16 with a float32 stream 91 to 83%).
 int lanes_of(int D, int vec, bool quant, int group, bool most) {
@@ -687,12 +699,15 @@ int lanes_of(int D, int vec, bool quant, int group, bool most) {
     while ((L < 32 || !most) && L * kPieces * vec < D) L *= 2;
     if (L * kPieces * vec >= D) return L;
     const int warp = 32 * kPieces * vec, fewest = (D + warp - 1) / warp * 32, rows = kPerSm / fewest;
-    return kPerSm / rows / 32 * 32;
+    const int widest = kPerSm / rows / 32 * 32;
+    for (int L = widest; L >= fewest; L -= 32)
+        if (even(D, L * vec)) return L;
+    return widest;
 }
 
-template <typename TX, typename TR, int N, bool kQuant>
-cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
-    auto kern = add_norm_fwd_kernel<TX, TR, N, kQuant>;
+template <typename TX, typename TR, int N, bool kQuant, int K>
+cudaError_t fwd_k(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
+    auto kern = add_norm_fwd_kernel<TX, TR, N, kQuant, K>;
     constexpr int smem = Slots<kFwdSlots, kStages, N>::BYTES;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
@@ -703,6 +718,13 @@ cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
                             (const TR*)c.res, (const TX*)c.w, (TR*)c.h, c.y, c.scales);
 }
 
+template <typename TX, typename TR, int N, bool kQuant>
+cudaError_t fwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
+    const int lane = 16 / (int)sizeof(TR) * d.L;
+    if (!even(d.D, lane)) return fwd_k<TX, TR, N, kQuant, 0>(c, d, st);
+    return d.D == 3 * lane ? fwd_k<TX, TR, N, kQuant, 3>(c, d, st) : fwd_k<TX, TR, N, kQuant, 4>(c, d, st);
+}
+
 template <typename TX, typename TR, int N>
 cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     constexpr int smem = Slots<kBwdSlots, kStages, N>::BYTES;
@@ -711,13 +733,19 @@ cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
     const TR *h = (const TR*)c.h_in, *dh = (const TR*)c.dh;
     const TX *w = (const TX*)c.w, *dy = (const TX*)c.dy;
     if (c.grid.cluster)
-        return launch_one_cluster(add_norm_bwd_kernel<TX, TR, N, true>, c.grid.blocks, N, smem, done1, st, d, h, w, dy, dh,
+        return launch_one_cluster(add_norm_bwd_kernel<TX, TR, N, true, 0>, c.grid.blocks, N, smem, done1, st, d, h, w, dy, dh,
                                   (TX*)c.dx, (TR*)c.dr, (TX*)c.dw, c.part);
-    auto kern = add_norm_bwd_kernel<TX, TR, N, false>;
-    cudaError_t e = allow_smem(kern, smem, done);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3((unsigned)c.grid.blocks), N, smem, st, d, h, w, dy, dh, (TX*)c.dx, (TR*)c.dr,
-                            (TX*)c.dw, c.part);
+    auto launch = [&](auto kern, std::atomic<uint64_t>& done) {
+        cudaError_t e = allow_smem(kern, smem, done);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(kern, dim3((unsigned)c.grid.blocks), N, smem, st, d, h, w, dy, dh, (TX*)c.dx, (TR*)c.dr,
+                                (TX*)c.dw, c.part);
+    };
+    static std::atomic<uint64_t> done3{0}, done4{0};
+    const int lane = 16 / (int)sizeof(TR) * d.L;
+    if (!even(d.D, lane)) return launch(add_norm_bwd_kernel<TX, TR, N, false, 0>, done);
+    return d.D == 3 * lane ? launch(add_norm_bwd_kernel<TX, TR, N, false, 3>, done3)
+                           : launch(add_norm_bwd_kernel<TX, TR, N, false, 4>, done4);
 }
 
 template <typename TX, typename TR, bool kQuant>
