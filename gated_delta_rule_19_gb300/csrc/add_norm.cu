@@ -684,12 +684,13 @@ bool even(int D, int lane) { return D == 3 * lane || D == 4 * lane; }
 // of 272 with 16 lanes 15.9 us, with 32 23.2), but all of a group of columns with a scale.
 // Past a warp: a power of two, but where `most`, the most that let an SM hold as many rows as
 // the fewest would: 96 of them hold 288 or 384 pieces in five rows where 128 hold four.  Of 25 M
-// elements in the 8-bit form rows of 2304 bf16 so take 73% of the copy rate for 66 in groups of
-// 128 and 84 for 80 without, with a float32 stream 84 for 69 and 87 for 73, of float32 91 for 82;
-// of 6144 bf16 192 lanes take 84% and 256, the most of two rows, 87.  Lanes that share the pieces
-// evenly come before more lanes (4608 float32 78 to 86%, 7168 bf16 73 to 78).  Rows without a residual,
-// which have less in flight, gain (2304 bf16 85 to 94%); those with one lose (89 to 85%), and
-// so does the backward (2304 bf16 with a float32 stream 91 to 83%).
+// elements in the 8-bit form rows of 2304 bf16 so take 81% of the copy rate for 66 in groups of
+// 128 and 87 for 80 without, with a float32 stream 83 for 69 and 88 for 73, of float32 91 for 82;
+// of 6144 bf16 192 lanes take 79 and 85% and 256, the most of two rows, 82 and 86.  Lanes that share
+// the pieces evenly come before more lanes (4608 float32 78 to 86%, 7168 bf16 73 to 78).  Rows
+// without a residual, which have less in flight, gain (2304 bf16 85 to 107%, partly from L2);
+// those with one lose (89 to 86%), and so does the backward (2304 bf16 with a float32 stream 91
+// to 83%).
 int lanes_of(int D, int vec, bool quant, int group, bool most) {
     int L = 8;
     if (quant)
