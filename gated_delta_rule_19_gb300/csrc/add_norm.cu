@@ -751,8 +751,10 @@ cudaError_t bwd(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
 
 template <typename TX, typename TR, bool kQuant>
 cudaError_t fwd_n(const AddNormCall& c, const NormDims& d, cudaStream_t st) {
-    return d.L <= 128 ? fwd<TX, TR, 128, kQuant>(c, d, st) : d.L <= 256 ? fwd<TX, TR, 256, kQuant>(c, d, st)
-                                                                       : fwd<TX, TR, 512, kQuant>(c, d, st);
+    static_assert(kAddNormMost <= 256 * kPieces * 8, "rows of bf16 take 256 lanes at most");
+    if constexpr (sizeof(TR) == 4)
+        if (d.L > 256) return fwd<TX, TR, 512, kQuant>(c, d, st);
+    return d.L <= 128 ? fwd<TX, TR, 128, kQuant>(c, d, st) : fwd<TX, TR, 256, kQuant>(c, d, st);
 }
 
 template <typename TX, typename TR>
@@ -763,7 +765,10 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
     switch (kind) {
         case AddNormKind::FWD: return fwd_n<TX, TR, false>(c, d, st);
         case AddNormKind::QUANT: return fwd_n<TX, TR, true>(c, d, st);
-        default: return d.L <= 256 ? bwd<TX, TR, 256>(c, d, st) : bwd<TX, TR, 512>(c, d, st);
+        default:
+            if constexpr (sizeof(TR) == 4)
+                if (d.L > 256) return bwd<TX, TR, 512>(c, d, st);
+            return bwd<TX, TR, 256>(c, d, st);
     }
 }
 
