@@ -22,6 +22,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <memory>
 #include <optional>
 #include <string>
 #include <vector>
@@ -664,16 +665,19 @@ PyObject* add_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ------------------------------------------------------- the gradients' norm
 
+// A reference of its own to a Python object: a member, so that a constructor that throws gives
+// it back.
+struct Release {
+    void operator()(PyObject* o) const { Py_DECREF(o); }
+};
+using Owned = std::unique_ptr<PyObject, Release>;
+
 // The tensors of a list (None is left out), with their outputs where there are some.
 struct Grads {
     std::vector<gdn_grad> list;
     std::vector<const at::Tensor*> written;
     std::optional<Like> like;
-    PyObject *seq = nullptr, *outs = nullptr;
-    ~Grads() {
-        Py_XDECREF(seq);
-        Py_XDECREF(outs);
-    }
+    Owned seq, outs;
     const at::Tensor& one(PyObject* o, const char* what) {
         const at::Tensor& t = *tensor(o, what);
         if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense())
@@ -687,20 +691,22 @@ struct Grads {
     static int32_t code(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? GDN_F32 : GDN_BF16; }
     Grads(PyObject* tensors, PyObject* out, bool write) {
         if (THPVariable_Check(tensors)) invalid("grads must be a sequence of tensors");
-        if (!(seq = PySequence_Fast(tensors, "grads must be a sequence of tensors"))) throw PythonError{};
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+        seq.reset(PySequence_Fast(tensors, "grads must be a sequence of tensors"));
+        if (!seq) throw PythonError{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.get());
         if (out != Py_None) {
             if (THPVariable_Check(out)) invalid("out must be a sequence of tensors");
-            if (!(outs = PySequence_Fast(out, "out must be a sequence of tensors"))) throw PythonError{};
-            if (PySequence_Fast_GET_SIZE(outs) != n)
-                fail(GDN_ERR_INVALID_ARG, "out has %zd tensors, expected %zd", PySequence_Fast_GET_SIZE(outs), n);
+            outs.reset(PySequence_Fast(out, "out must be a sequence of tensors"));
+            if (!outs) throw PythonError{};
+            if (PySequence_Fast_GET_SIZE(outs.get()) != n)
+                fail(GDN_ERR_INVALID_ARG, "out has %zd tensors, expected %zd", PySequence_Fast_GET_SIZE(outs.get()), n);
         }
         list.reserve(n);
         for (Py_ssize_t i = 0; i < n; ++i) {
-            PyObject* o = PySequence_Fast_GET_ITEM(seq, i);
+            PyObject* o = PySequence_Fast_GET_ITEM(seq.get(), i);
             if (o == Py_None) continue;
             const at::Tensor& g = one(o, "a gradient");
-            const at::Tensor& to = outs ? one(PySequence_Fast_GET_ITEM(outs, i), "an output") : g;
+            const at::Tensor& to = outs ? one(PySequence_Fast_GET_ITEM(outs.get(), i), "an output") : g;
             if (outs && (to.sizes() != g.sizes() || !(to.strides() == g.strides() || (to.is_contiguous() && g.is_contiguous()))))
                 invalid("an output has shape " + shape_text(to.sizes()) + " and strides " + shape_text(to.strides()) +
                         ", its gradient " + shape_text(g.sizes()) + " and " + shape_text(g.strides()));
