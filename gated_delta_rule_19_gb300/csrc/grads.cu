@@ -224,10 +224,23 @@ grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) 
     if (threadIdx.x == 0) part[blockIdx.x] = {sum.s, sum.c, sum.rest};
 }
 
+// What the gradients are multiplied by: the product of two numbers.  A factor below 2^-126, of which
+// one float32 number would keep few bits or none, is first * 2^-126 with a normal first (below
+// 2^-252, which takes a max_norm below 2^-102, no result is more than a subnormal); all others
+// are first * 1.  The product by `first`, below 1, overflows for no finite gradient.
+struct Factor {
+    float first, then;
+    __device__ __forceinline__ bool one() const { return first == 1.f && then == 1.f; }
+    __device__ __forceinline__ float of(float x) const { return x * first * then; }
+    __device__ __forceinline__ uint64_t of(uint64_t x) const { return mul2(mul2(x, twice(first)), twice(then)); }
+};
+constexpr float kLeast = 1.17549435e-38f, kMost = 8.507059e37f;  // 2^-126, 2^126
+
 // The norm from the blocks' sums, and the factor that takes it to max_norm; the same in every
 // thread.
 struct Norm {
-    float norm, by;
+    float norm;
+    Factor by;
 };
 template <int T>
 __device__ __forceinline__ Norm norm_of(Sum x, float max_norm) {
@@ -238,13 +251,18 @@ __device__ __forceinline__ Norm norm_of(Sum x, float max_norm) {
         // the root of s, and half of what its square leaves of the sum over itself
         const float n = sqrtf(s), left = fmaf(-n, n, x.s) + x.c;
         const float norm = s > 0.f ? n + 0.5f * left / n : 0.f;
-        return {norm, norm > max_norm ? max_norm / norm : 1.f};
+        if (!(norm > max_norm)) return {norm, {1.f, 1.f}};
+        const float by = max_norm / norm;
+        if (by >= kLeast) return {norm, {by, 1.f}};
+        return {norm, {max_norm * kMost / norm, kLeast}};  // max_norm is below 2^-62 here
     }
     if (threadIdx.x == 0) {
         const double n = sqrt((double)x.s + (double)x.c + x.rest);
         // where an element is not finite the norm says nothing of how long the gradients are: they
         // stay; finite ones whose norm leaves float32's range are clipped by the float64 norm
-        all = {(float)n, n > (double)max_norm && n <= DBL_MAX ? (float)((double)max_norm / n) : 1.f};
+        const double by = n > (double)max_norm && n <= DBL_MAX ? (double)max_norm / n : 1.;
+        const bool small = by < (double)kLeast;
+        all = {(float)n, {(float)(small ? by * (double)kMost : by), small ? kLeast : 1.f}};
     }
     __syncthreads();
     return all;
@@ -299,7 +317,7 @@ __device__ __forceinline__ void put_vector(const Tensor& t, int64_t e, const uin
 }
 
 template <int VEC, bool kHalf>
-__device__ __forceinline__ void scale_vectors(const Tensor& t, int64_t e, uint64_t by) {
+__device__ __forceinline__ void scale_vectors(const Tensor& t, int64_t e, const Factor& by) {
     constexpr int M = 32 / VEC;
     uint4 v[M];
 #pragma unroll
@@ -309,7 +327,7 @@ __device__ __forceinline__ void scale_vectors(const Tensor& t, int64_t e, uint64
         uint64_t f[VEC / 2];
         get(v[j], f);
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) f[i] = mul2(f[i], by);
+        for (int i = 0; i < VEC / 2; ++i) f[i] = by.of(f[i]);
         put_vector<VEC, kHalf>(t, e + (int64_t)j * kThreads * VEC, f);
     }
 }
@@ -337,12 +355,11 @@ struct Halves {
 // begin; the tensor's last tile takes one more.  (Elements one by one on both sides: 22 M bf16
 // in odd places of a flat buffer 61 us a call, so 23.)
 template <bool kIn16, bool kOut16>
-__device__ __forceinline__ void scale_apart(const Tensor& t, uint32_t tile, int thread, float by) {
+__device__ __forceinline__ void scale_apart(const Tensor& t, uint32_t tile, int thread, const Factor& by) {
     constexpr int VEC = kOut16 ? 8 : 4, M = 32 / VEC;
     const int64_t e0 = (int64_t)(tile - t.first) * kTile - t.lead;
     const int lead = (int)((uintptr_t)t.out & 15) >> (kOut16 ? 1 : 2);
     const int64_t first = e0 - ((e0 + lead) & (VEC - 1)), e = first + thread * VEC;
-    const uint64_t by2 = twice(by);
     if (first >= 1 && first + kTile < t.n) {  // a word more on either side is the tensor's
         uint64_t f[M][VEC / 2];
         if constexpr (kIn16) {
@@ -363,14 +380,14 @@ __device__ __forceinline__ void scale_apart(const Tensor& t, uint32_t tile, int 
 #pragma unroll
         for (int j = 0; j < M; ++j) {
 #pragma unroll
-            for (int k = 0; k < VEC / 2; ++k) f[j][k] = mul2(f[j][k], by2);
+            for (int k = 0; k < VEC / 2; ++k) f[j][k] = by.of(f[j][k]);
             put_vector<VEC, kOut16>(t, e + j * kThreads * VEC, f[j]);
         }
     } else {
         auto one = [&](int64_t at) {
             for (int k = 0; k < VEC; ++k, ++at) {
                 if (at < 0 || at >= t.n) continue;
-                const float x = at1(t.p, at, kIn16) * by;
+                const float x = by.of(at1(t.p, at, kIn16));
                 if (kOut16) ((__nv_bfloat16*)t.out)[at] = __float2bfloat16_rn(x);
                 else ((float*)t.out)[at] = x;
             }
@@ -381,7 +398,7 @@ __device__ __forceinline__ void scale_apart(const Tensor& t, uint32_t tile, int 
         const int64_t at = first + kTile;
         for (int k = 0; k < VEC; ++k) {
             if (at + k >= t.n) break;
-            const float x = at1(t.p, at + k, kIn16) * by;
+            const float x = by.of(at1(t.p, at + k, kIn16));
             if (kOut16) ((__nv_bfloat16*)t.out)[at + k] = __float2bfloat16_rn(x);
             else ((float*)t.out)[at + k] = x;
         }
@@ -396,18 +413,18 @@ __host__ __device__ __forceinline__ bool together(uintptr_t in, uintptr_t out, b
 
 // A tile times `by`, by kThreads threads.  kApart: some tensor's boundaries are apart.
 template <bool kApart>
-__device__ __forceinline__ void scale_tile(const Tensor& t, uint32_t tile, int thread, float by) {
-    if (by == 1.f && t.out == t.p) return;
+__device__ __forceinline__ void scale_tile(const Tensor& t, uint32_t tile, int thread, const Factor& by) {
+    if (by.one() && t.out == t.p) return;
     const int64_t e = (int64_t)(tile - t.first) * kTile - t.lead;
     if (kApart && !together((uintptr_t)t.p, (uintptr_t)t.out, t.in16, t.out16)) {
         if (t.in16 && t.out16) scale_apart<true, true>(t, tile, thread, by);
         else if (t.in16) scale_apart<true, false>(t, tile, thread, by);
         else if (t.out16) scale_apart<false, true>(t, tile, thread, by);
         else scale_apart<false, false>(t, tile, thread, by);
-    } else if (t.in16 && t.out16) scale_vectors<8, true>(t, e + thread * 8, twice(by));
-    else if (t.in16) scale_vectors<8, false>(t, e + thread * 8, twice(by));
-    else if (t.out16) scale_vectors<4, true>(t, e + thread * 4, twice(by));
-    else scale_vectors<4, false>(t, e + thread * 4, twice(by));
+    } else if (t.in16 && t.out16) scale_vectors<8, true>(t, e + thread * 8, by);
+    else if (t.in16) scale_vectors<8, false>(t, e + thread * 8, by);
+    else if (t.out16) scale_vectors<4, true>(t, e + thread * 4, by);
+    else scale_vectors<4, false>(t, e + thread * 4, by);
 }
 
 // in_place: every tensor is its own output.
@@ -423,8 +440,8 @@ grad_scale_kernel(const __grid_constant__ List<N> l, const GradPart* __restrict_
     await_previous();
     const Norm x = norm_of<kThreads>(parts_of(part, parts), max_norm);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
-    const float by = x.by;
-    if ((in_place && by == 1.f) || from >= tile) return;
+    const Factor by = x.by;
+    if ((in_place && by.one()) || from >= tile) return;
     while (tile-- > from) {
         while (tile < t.first) t.at(l, --i);
         scale_tile<kApart>(t, tile, threadIdx.x, by);

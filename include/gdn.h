@@ -615,7 +615,7 @@ typedef struct {
  * the float32 sums' rounding errors and squares that leave float32's range, so the norm is
  * right to float32 for any number of finite elements; equal calls give equal bits.
  * gdn_clip_grads -- the same, and out = g * min(1, max_norm / norm) for every tensor (in
- * float32, rounded once).  Where an element is NaN or infinite the factor is 1: the caller
+ * float32, rounded once, and for a factor below float32's normal numbers too).  Where an element is NaN or infinite the factor is 1: the caller
  * sees it in *norm.  (Of finite elements whose norm is past float32's range *norm is
  * infinite too, and they are clipped.)  max_norm >= 0, infinity: no limit.  Outputs overlap neither each other
  * nor a gradient other than their own.
