@@ -611,14 +611,16 @@ typedef struct {
 /*
  * gdn_grad_norm -- *norm = sqrt(sum of g^2 over all elements of all tensors), float32 on the
  * device, 4-byte aligned.  The array (host memory, `count` <= 2^20) is read before the call
- * returns; out and out_dtype are not used, and a tensor may be listed twice.  The sum keeps
- * the float32 sums' rounding errors and squares that leave float32's range, so the norm is
- * right to float32 for any number of finite elements; equal calls give equal bits.
+ * returns; out and out_dtype are not used, and a tensor may be listed twice.  32 squares at a
+ * time are added in float32, their sums with the rounding errors kept, and squares that leave
+ * float32's range in float64: of any number of finite elements the norm is within 6e-7 of its
+ * value (where float32 holds it as a normal number).  Equal calls give equal bits.
  * gdn_clip_grads -- the same, and out = g * min(1, max_norm / norm) for every tensor (in
- * float32, rounded once, and for a factor below float32's normal numbers too).  Where an element is NaN or infinite the factor is 1: the caller
- * sees it in *norm.  (Of finite elements whose norm is past float32's range *norm is
- * infinite too, and they are clipped.)  max_norm >= 0, infinity: no limit.  Outputs overlap neither each other
- * nor a gradient other than their own.
+ * float32, also where that factor is below float32's normal numbers; rounded to out_dtype).
+ * Where an element is NaN or infinite the factor is 1: the caller sees it in *norm.  (Of
+ * finite elements whose norm is past float32's range *norm is infinite too, and they are
+ * clipped.)  max_norm >= 0, infinity: no limit.  Outputs overlap neither each other nor a
+ * gradient other than their own.
  *   norm       required by gdn_grad_norm; NULL: not kept.
  *   workspace  gdn_grad_workspace_bytes(grads, count) bytes (0 for a few tensors), 16-byte
  *              aligned; calls in flight at the same time need one each.
