@@ -1957,6 +1957,14 @@ extern "C" {
 // the launch that adds them up (several axes; the calls of one position keep their two launches).
 static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && c.blocks <= gdn::kMostCluster; }
 
+// The positions that a call reads, which no output may overlap (4-byte aligned, so not one of
+// the spans of 16).
+static gdn_status check_positions(const gdn::RopeCall& c, const int32_t* positions, const Span* outs, int nout) {
+    const size_t n = c.R ? (size_t)c.tokens * (c.axes ? c.axes : 1) * sizeof(int32_t) : 0;
+    const Span at = {positions, n, "positions"};
+    return check_overlaps(&at, 1, outs, nout, nullptr, nullptr);
+}
+
 // Room for the tokens' gathered angles, where a call of several axes gathers them.
 static size_t rope_gathered(const gdn_rope_problem* p, const gdn::RopeCall& c) {
     if (!c.axes || c.R == 0 || c.tokens > INT32_MAX || c.tokens * (c.Hq + c.Hk) < gdn::kRopeGatherRows) return 0;
@@ -1982,6 +1990,7 @@ static gdn_status rope_fwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
                          {k_out, (size_t)c.tokens * wk * es, "k_out"},
                          {workspace, need, "workspace"}};
     if ((st = check_spans(ins, 6, 1u << 4 | 1u << 5, outs, need ? 3 : 2, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if ((st = check_positions(c, positions, outs, need ? 3 : 2)) != GDN_OK) return st;
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     if (c.tokens == 0 || p->Hq + p->Hk == 0) return GDN_OK;
@@ -2034,6 +2043,7 @@ static gdn_status rope_bwd(const gdn_rope_problem* p, gdn::RopeCall& c, const vo
                          {dk_weight, p->D * es, "dk_weight"},
                          {workspace, need, "workspace"}};
     if ((st = check_spans(ins, 8, 1u << 6 | 1u << 7, outs, 5, 0, nullptr, nullptr)) != GDN_OK) return st;
+    if ((st = check_positions(c, positions, outs, 5)) != GDN_OK) return st;
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     if (c.tokens && (st = rope_tables(p, cos, sin, positions)) != GDN_OK) return st;
