@@ -197,12 +197,15 @@ gdn_status check_ptr(const Span& s, bool required) {
 }
 
 // Every output must be disjoint from every input and from every other output;
-// `allow_same` lists (output, input) pairs that may be the identical buffer.
+// the output same_out and the input same_in (and, with same_name, no other input at its
+// address) may be the identical buffer.
 gdn_status check_overlaps(const Span* ins, int nin, const Span* outs, int nout,
-                          const void* same_out, const void* same_in) {
+                          const void* same_out, const void* same_in, const char* same_name = nullptr) {
     for (int i = 0; i < nout; ++i) {
         for (int j = 0; j < nin; ++j) {
-            if (outs[i].p && outs[i].p == same_out && ins[j].p == same_in) continue;
+            if (outs[i].p && outs[i].p == same_out && ins[j].p == same_in &&
+                (!same_name || strcmp(ins[j].name, same_name) == 0))
+                continue;
             if (overlap(outs[i], ins[j]))
                 return fail(GDN_ERR_INVALID_ARG, "output %s overlaps input %s", outs[i].name,
                             ins[j].name);
@@ -1665,14 +1668,15 @@ gdn_status check_word_ptr(const void* p, const char* name) {
 }
 
 gdn_status check_spans(const Span* ins, int nin, unsigned optional_ins, const Span* outs, int nout,
-                       unsigned optional_outs, const void* same_out, const void* same_in) {
+                       unsigned optional_outs, const void* same_out, const void* same_in,
+                       const char* same_name = nullptr) {
     gdn_status st;
     for (int i = 0; i < nin; ++i)
         if ((st = check_ptr(ins[i], !(optional_ins >> i & 1))) != GDN_OK) return st;
     for (int i = 0; i < nout; ++i)
         if ((st = check_ptr(outs[i], !(optional_outs >> i & 1))) != GDN_OK) return st;
     const bool same = same_out && same_out == same_in;  // the very same buffer, not a part of it
-    return check_overlaps(ins, nin, outs, nout, same ? same_out : nullptr, same ? same_in : nullptr);
+    return check_overlaps(ins, nin, outs, nout, same ? same_out : nullptr, same ? same_in : nullptr, same_name);
 }
 
 struct LaCall {
@@ -2212,7 +2216,10 @@ gdn_status add_norm(const gdn_add_norm_problem* p, gdn::AddNormKind kind, int32_
     if (!residual && p->stream_dtype != p->dtype)
         return fail(GDN_ERR_INVALID_ARG, "stream_dtype differs from dtype without a residual");
     const size_t es = elem_size(p->dtype), er = elem_size(p->stream_dtype), n = (size_t)p->rows * p->D;
-    const Span ins[] = {{x, row_span(p->rows, c.x_stride, p->D, p->dtype), "x"},
+    // h over the residual may lie over x too where x is the residual: a row is read before it is written
+    const bool over_x = h && h == residual && x == residual && p->dtype == p->stream_dtype &&
+                        (p->rows <= 1 || c.x_stride == c.r_stride);
+    const Span ins[] = {{x, over_x ? 0 : row_span(p->rows, c.x_stride, p->D, p->dtype), "x"},
                         {residual, row_span(p->rows, c.r_stride, p->D, p->stream_dtype), "residual"},
                         {weight, p->D * es, "weight"}};
     const Span outs[] = {{y, n * (quant ? 1 : es), "y"},
@@ -2220,7 +2227,7 @@ gdn_status add_norm(const gdn_add_norm_problem* p, gdn::AddNormKind kind, int32_
                          {scales, quant ? (size_t)p->rows * (group ? p->D / group : 1) * sizeof(float) : 0, "scales"}};
     if (h && h == residual && p->rows > 1 && c.r_stride != p->D)
         return fail(GDN_ERR_INVALID_ARG, "h is the residual, which is not dense");
-    if ((st = check_spans(ins, 3, 1u << 1, outs, 3, 1u << 1, h, residual)) != GDN_OK) return st;
+    if ((st = check_spans(ins, 3, 1u << 1, outs, 3, 1u << 1, h, residual, "residual")) != GDN_OK) return st;
     if (p->rows == 0) return GDN_OK;
     c.x = x, c.res = residual, c.w = weight, c.h = h, c.y = y, c.scales = scales, c.group = group;
     cudaStream_t cs = (cudaStream_t)stream;

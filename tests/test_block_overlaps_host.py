@@ -40,3 +40,33 @@ def test_outputs_over_one_axis_positions(lib):  # noqa: F811
         assert "overlaps input positions" in lib.gdn_last_error()
     assert _call(lib, "gdn_qk_norm_rope_fwd", p, names, q_out=at + 2 * 1000 * 4) not in (0, INVALID)
     assert _call(lib, "gdn_qk_norm_rope_fwd", p, names, positions=None) not in (0, INVALID)
+
+
+def test_a_sum_over_a_residual_that_x_lies_over(lib):  # noqa: F811
+    """h may be the residual; x at the same address is only the same rows where it has the residual's
+    type and stride.  Else rows of h lie over rows of x that are still to be read."""
+    at = FAKE + FWD.index("residual") * GAP
+
+    def norm(**kw):
+        d = dict(rows=10, D=512, sx=0, ss=0, dtype=1, stream=1)
+        d.update(kw)
+        return lib.gdn_add_norm_problem(d["rows"], d["D"], d["sx"], d["ss"], 1e-6, d["dtype"], d["stream"])
+
+    def both(p, **over):
+        return [_call(lib, "gdn_add_norm_fwd", p, FWD, **over), _call(lib, "gdn_add_norm_quant", p, QUANT, first=(0,), **over)]
+
+    for p in (norm(sx=1024), norm(stream=0), norm(rows=2, sx=1536, stream=0), norm(rows=1, stream=0), norm(rows=2, sx=520)):
+        assert both(p, x=at, h=at) == [INVALID] * 2
+        assert "overlaps input x" in lib.gdn_last_error(), lib.gdn_last_error()
+    # the same rows: each is read before it is written
+    for p in (norm(), norm(dtype=0, stream=0), norm(rows=1, sx=1024)):
+        assert not set(both(p, x=at, h=at)) & {0, INVALID}
+    # the weight there
+    assert both(norm(), weight=at, h=at) == [INVALID] * 2
+    assert "overlaps input weight" in lib.gdn_last_error()
+    # x elsewhere, and a part of the residual
+    assert not set(both(norm(), h=at)) & {0, INVALID}
+    assert both(norm(), x=at + 512, h=at) == [INVALID] * 2
+    # no address is not an address that agrees
+    assert both(norm(), x=None, residual=None, h=None) == [INVALID] * 2
+    assert both(norm(), x=None, h=at) == [INVALID] * 2
