@@ -1780,7 +1780,8 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
                          {final_state, nstate, "final_state"},
                          {saved, nsaved, "saved"},
                          {workspace, need, "workspace"}};
-    if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 1u << 1 | 1u << 2, final_state, initial_state)) != GDN_OK)
+    if ((st = check_spans(ins, 4, 1u << 3, outs, 4, 1u << 1 | 1u << 2, final_state, initial_state, "initial_state")) !=
+        GDN_OK)
         return st;
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -1828,8 +1829,8 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
                          {dv, (size_t)c.tokens * wv * es, "dv"},
                          {d_initial_state, nstate, "d_initial_state"},
                          {workspace, need, "workspace"}};
-    if ((st = check_spans(ins, 7, 1u << 4 | 1u << 5 | 1u << 6, outs, 5, 1u << 3, d_initial_state, d_final_state)) !=
-        GDN_OK)
+    if ((st = check_spans(ins, 7, 1u << 4 | 1u << 5 | 1u << 6, outs, 5, 1u << 3, d_initial_state, d_final_state,
+                          "d_final_state")) != GDN_OK)
         return st;
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);

@@ -70,3 +70,19 @@ def test_a_sum_over_a_residual_that_x_lies_over(lib):  # noqa: F811
     # no address is not an address that agrees
     assert both(norm(), x=None, residual=None, h=None) == [INVALID] * 2
     assert both(norm(), x=None, h=at) == [INVALID] * 2
+
+
+def test_linear_attention_states_over_other_inputs(lib):  # noqa: F811
+    """The final state may be the initial one, the initial state's gradient the final state's: that
+    allows no other input at their address."""
+    p = lib.gdn_la_problem(1, 65536, 4, 128, 128, 0, 0, 0, 1)  # with saved sums
+    fwd = ("q", "k", "v", "log_decay", "initial_state", "o", "final_state", "saved", "workspace")
+    bwd = ("q", "k", "v", "log_decay", "initial_state", "saved", "d_o", "d_final_state", "dq", "dk", "dv", "d_initial_state", "workspace")
+    at = FAKE + 50 * GAP
+    for fn, names, pair, others in (("gdn_la_fwd", fwd, ("initial_state", "final_state"), ("q", "k", "v")),
+                                    ("gdn_la_bwd", bwd, ("d_final_state", "d_initial_state"), ("q", "v", "d_o", "initial_state", "saved"))):
+        same = dict.fromkeys(pair, at)
+        assert _call(lib, fn, p, names, sized=1 << 40, **same) not in (0, INVALID), fn
+        for n in others:
+            assert _call(lib, fn, p, names, sized=1 << 40, **same, **{n: at}) == INVALID, (fn, n)
+            assert f"overlaps input {n}" in lib.gdn_last_error(), lib.gdn_last_error()
