@@ -781,8 +781,48 @@ cudaError_t launch_t(const AddNormCall& c, AddNormKind kind, cudaStream_t st) {
 AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide) {
     const int L = lanes_of(D, 16 / wide, false, 0, false), n = L <= 256 ? 256 : 512;
     const int64_t per = n / L, want = (rows + per - 1) / per, cap = (int64_t)sm_count() * per_sm(n);
-    if (want <= kMostCluster) return {(int)(want < 1 ? 1 : want), true};
+    if (one_cluster(want)) return {(int)(want < 1 ? 1 : want), true};
     return {(int)(want < cap ? want : cap), false};
+}
+
+std::atomic<int> test_cluster_limit{0};
+
+// Asked of the kernel that takes most of an SM (512 threads and 192 KB; as all that run in one
+// cluster it has an SM to itself), once for a context.  Where no GPU answers, the largest.  (This
+// GPU as a whole: 16; a green context of 8, 16 or 32 of its SMs: 8.)
+int cluster_limit() {
+    if (const int n = test_cluster_limit.load(std::memory_order_relaxed)) return n;
+    static std::atomic<uint64_t> known[4];  // a context's number times 256, and its limit
+    const uint64_t context = context_number();
+    std::atomic<uint64_t>& mine = known[context & 3];
+    const uint64_t was = mine.load(std::memory_order_relaxed);
+    if (context && was >> 8 == context) return (int)(was & 255);
+    auto kern = add_norm_bwd_kernel<float, float, 512, true, 0>;
+    constexpr int smem = Slots<kBwdSlots, kStages, 512>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return kMostCluster;
+    }
+    int n = kMostCluster;
+    for (; n > 1; n /= 2) {
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3((unsigned)n);
+        c.blockDim = dim3(512);
+        c.dynamicSmemBytes = smem;
+        cudaLaunchAttribute a;
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = (unsigned)n;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        c.attrs = &a;
+        c.numAttrs = 1;
+        int placed = 0;
+        if (cudaOccupancyMaxActiveClusters(&placed, kern, &c) != cudaSuccess) cudaGetLastError();
+        else if (placed > 0) break;
+    }
+    if (context) mine.store(context << 8 | (uint64_t)n, std::memory_order_relaxed);
+    return n;
 }
 
 cudaError_t launch_add_norm(const AddNormCall& c, InType ty, InType stream_ty, AddNormKind kind, cudaStream_t st) {

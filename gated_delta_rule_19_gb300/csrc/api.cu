@@ -509,6 +509,13 @@ gdn_status gdn_test_set_wait_limit(uint32_t ns) {
     return GDN_OK;
 }
 
+gdn_status gdn_test_set_cluster_limit(int32_t blocks) {
+    if (blocks < 0 || blocks > gdn::kMostCluster)
+        return fail(GDN_ERR_INVALID_ARG, "blocks=%d: must be 0 to %d", (int)blocks, gdn::kMostCluster);
+    gdn::test_cluster_limit = blocks;
+    return GDN_OK;
+}
+
 size_t gdn_fwd_workspace_bytes(const gdn_problem* p) {
     gdn::Dims d{};
     if (check_problem(p, &d) != GDN_OK) return 0;
@@ -1960,7 +1967,7 @@ extern "C" {
 
 // Whether the blocks of a backward are one cluster, which needs neither memory for its sums nor
 // the launch that adds them up (several axes; the calls of one position keep their two launches).
-static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && c.blocks <= gdn::kMostCluster; }
+static bool rope_cluster(const gdn::RopeCall& c) { return c.axes && gdn::one_cluster(c.blocks); }
 
 // The positions that a call reads, which no output may overlap (4-byte aligned, so not one of
 // the spans of 16).
@@ -2296,13 +2303,21 @@ gdn_status check_grads(const gdn_grad* g, int64_t count, bool write, const Span*
     return GDN_OK;
 }
 
+// The blocks of the cluster that takes the call (0: two launches), and the workspace with that.
+bool grads_listed(const gdn_grad* g, int64_t count) { return count >= 0 && count <= (int64_t)1 << 20 && (!count || g); }
+int grad_blocks(const gdn_grad* g, int64_t count) { return grads_listed(g, count) ? gdn::grad_cluster(g, count) : 0; }
+size_t grad_need(const gdn_grad* g, int64_t count, int blocks) {
+    return blocks || !grads_listed(g, count) ? 0 : gdn::grad_parts(count) * sizeof(gdn::GradPart);
+}
+
 gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, float* norm, void* workspace,
                  size_t workspace_bytes, void* stream) {
     g_err[0] = 0;
     if (clip && !(max_norm >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "max_norm=%g is negative", (double)max_norm);
     gdn_status st;
     if ((!clip || norm) && (st = check_word_ptr(norm, "norm")) != GDN_OK) return st;
-    const size_t need = count > 0 && !g ? 0 : gdn_grad_workspace_bytes(g, count);
+    const int blocks = grad_blocks(g, count);  // asked once: it decides the workspace and the launches
+    const size_t need = grad_need(g, count, blocks);
     const Span others[] = {{norm, sizeof(float), "norm"}, {workspace, need, "workspace"}};
     if ((st = check_grads(g, count, clip, others, 2)) != GDN_OK || (st = check_ptr(others[1], true)) != GDN_OK) return st;
     if (workspace_bytes < need)
@@ -2310,7 +2325,7 @@ gdn_status grads(const gdn_grad* g, int64_t count, bool clip, float max_norm, fl
     cudaStream_t cs = (cudaStream_t)stream;
     gdn::GradPart* part = (gdn::GradPart*)workspace;
     int parts = 0;
-    if (const int blocks = gdn::grad_cluster(g, count)) {
+    if (blocks) {
         cudaError_t e = timed(gdn::KID_GRAD_CLIP, cs,
                               [&] { return gdn::launch_grad_cluster(g, count, blocks, max_norm, norm, clip, cs); });
         return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gradient clipping kernel");
@@ -2445,10 +2460,7 @@ gdn_status gdn_add_norm_bwd(const gdn_add_norm_problem* p, const void* h, const 
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "residual norm gradient kernel");
 }
 
-size_t gdn_grad_workspace_bytes(const gdn_grad* g, int64_t count) {
-    if (count < 0 || count > (int64_t)1 << 20 || (count && !g) || gdn::grad_cluster(g, count)) return 0;
-    return gdn::grad_parts(count) * sizeof(gdn::GradPart);
-}
+size_t gdn_grad_workspace_bytes(const gdn_grad* g, int64_t count) { return grad_need(g, count, grad_blocks(g, count)); }
 
 gdn_status gdn_grad_norm(const gdn_grad* g, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
                          void* stream) {

@@ -206,6 +206,9 @@ bool tmap_rows_bthd(CUtensorMap* m, const void* ptr, int B, int T, int H, int D,
 bool tma_available();
 int sm_count();
 
+// The current context's number, which no other context has; 0 where there is none yet.
+uint64_t context_number();
+
 // Tensor-core forward (tc_fwd.cu).  tc_fwd_supported: shape/dtype test only.
 bool tc_fwd_supported(const Dims& d, InType ty);
 // Packed sequences on the flat chunk layout (B = 1; every sequence starts a new
@@ -381,8 +384,15 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 #endif
-// Blocks of the largest cluster (above 8 a kernel has to be allowed it).
+// Blocks of the largest cluster (above 8 a kernel has to be allowed it), and of the largest that
+// the current context can place where each block takes an SM: a part of the GPU (a green
+// context, an instance) may have fewer SMs together.  test_cluster_limit: the test hook's, or 0.
 constexpr int kMostCluster = 16;
+int cluster_limit();
+extern std::atomic<int> test_cluster_limit;
+inline bool one_cluster(int64_t blocks) {
+    return blocks <= 1 || (blocks <= kMostCluster && blocks <= cluster_limit());
+}
 
 #ifdef __CUDACC__
 // A cluster's blocks: all threads have arrived, and see what the others' blocks wrote in

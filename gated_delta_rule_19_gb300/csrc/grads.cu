@@ -563,7 +563,7 @@ int grad_cluster(const gdn_grad* g, int64_t count) {
     if (tiles > kClusterTiles) return 0;
     int blocks = 1;
     while (blocks < kMostCluster && blocks * kWorkers < tiles) blocks *= 2;
-    return blocks;
+    return one_cluster(blocks) ? blocks : 0;
 }
 
 cudaError_t launch_grad_cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm, float* norm, bool clip,

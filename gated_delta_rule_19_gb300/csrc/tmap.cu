@@ -1,6 +1,6 @@
 // tmap.cu -- host helpers of the tensor-core path: TMA tensor-map encoding
-// (through the driver entry point, so the library does not link libcuda) and
-// the SM count.
+// (through the driver entry point, so the library does not link libcuda), the
+// SM count and the current context's number.
 #include <cudaTypedefs.h>
 
 #include "gdn_internal.h"
@@ -57,6 +57,19 @@ bool tmap_rows(CUtensorMap* m, const void* ptr, int64_t rows, int cols) {
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, str, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t context_number() {
+    static PFN_cuCtxGetId_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (PFN_cuCtxGetId_v12000)p;
+    }();
+    unsigned long long id = 0;
+    return fn && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
 }
 
 int sm_count() {

@@ -162,6 +162,8 @@ def load_library():
     lib.gdn_set_sequence_split.restype = ctypes.c_int
     lib.gdn_test_set_wait_limit.argtypes = [ctypes.c_uint32]
     lib.gdn_test_set_wait_limit.restype = ctypes.c_int
+    lib.gdn_test_set_cluster_limit.argtypes = [ctypes.c_int32]
+    lib.gdn_test_set_cluster_limit.restype = ctypes.c_int
     lib.gdn_get_sequence_split.restype = ctypes.c_int
     lib.gdn_num_kernels.restype = ctypes.c_int
     lib.gdn_kernel_name.argtypes = [ctypes.c_int]
@@ -184,7 +186,7 @@ EXPORTED = ("gdn_version", "gdn_status_string", "gdn_last_error", "gdn_fwd_works
             "gdn_prologue_fwd", "gdn_prologue_bwd", "gdn_varlen_fwd_workspace_bytes",
             "gdn_varlen_bwd_workspace_bytes", "gdn_varlen_saved_bytes", "gdn_varlen_fwd", "gdn_varlen_bwd",
             "gdn_set_sequence_split", "gdn_get_sequence_split", "gdn_count_nonfinite",
-            "gdn_test_set_wait_limit", "gdn_la_fwd_workspace_bytes", "gdn_la_saved_bytes",
+            "gdn_test_set_wait_limit", "gdn_test_set_cluster_limit", "gdn_la_fwd_workspace_bytes", "gdn_la_saved_bytes",
             "gdn_la_bwd_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode",
             "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_bytes", "gdn_qk_norm_rope_bwd",
             "gdn_gated_norm_fwd", "gdn_gated_norm_bwd_workspace_bytes", "gdn_gated_norm_bwd",
@@ -478,6 +480,12 @@ def gdn_test_set_wait_limit(ns: int) -> None:
     """Test hook: limit, in nanoseconds, of the tensor-core kernels' bounded waits
     in the calls that follow (0 restores the default of 2 s); see include/gdn.h."""
     _check(load_library().gdn_test_set_wait_limit(int(ns)))
+
+
+def gdn_test_set_cluster_limit(blocks: int) -> None:
+    """Test hook: the most blocks of a cluster that small calls run as, 1 to 16 (0 restores
+    what the context can place); see include/gdn.h."""
+    _check(load_library().gdn_test_set_cluster_limit(int(blocks)))
 
 
 def gdn_get_sequence_split() -> int:

@@ -686,6 +686,17 @@ gdn_status gdn_count_nonfinite(const void* x, int64_t n, gdn_dtype dtype, int64_
 gdn_status gdn_test_set_wait_limit(uint32_t ns);
 
 /*
+ * gdn_test_set_cluster_limit -- test hook for the calls that run as one cluster of blocks where
+ * they are small (gdn_add_norm_bwd, gdn_qk_norm_rope_axes_bwd, gdn_grad_norm, gdn_clip_grads).
+ * They do so in clusters that the current context can place (a green context or an instance
+ * may have fewer SMs together than a cluster has blocks), and else in two launches with a
+ * workspace: the *_workspace_bytes queries and the calls are made in the same context.  This
+ * call takes `blocks` (1 to 16; 0 restores the context's own limit) for the largest cluster,
+ * for the whole process.
+ */
+gdn_status gdn_test_set_cluster_limit(int32_t blocks);
+
+/*
  * Optional launch timer, for benchmarks.  While started, every kernel launch of
  * gdn_fwd/gdn_bwd is bracketed by two CUDA events recorded on the call's stream
  * (up to `capacity` launches; later launches are not timed).  The events are
