@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -2464,7 +2465,7 @@ size_t gdn_grad_workspace_bytes(const gdn_grad* g, int64_t count) { return grad_
 
 gdn_status gdn_grad_norm(const gdn_grad* g, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
                          void* stream) {
-    return grads(g, count, false, 0.f, norm, workspace, workspace_bytes, stream);
+    return grads(g, count, false, HUGE_VALF, norm, workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_clip_grads(const gdn_grad* g, int64_t count, float max_norm, float* norm, void* workspace,

@@ -252,9 +252,9 @@ __device__ __forceinline__ Norm norm_of(Sum x, float max_norm) {
         const float n = sqrtf(s), left = fmaf(-n, n, x.s) + x.c;
         const float norm = s > 0.f ? n + 0.5f * left / n : 0.f;
         if (!(norm > max_norm)) return {norm, {1.f, 1.f}};
-        const float by = max_norm / norm;
-        if (by >= kLeast) return {norm, {by, 1.f}};
-        return {norm, {max_norm * kMost / norm, kLeast}};  // max_norm is below 2^-62 here
+        // a quotient near 2^-126 or below (max_norm is below 2^-60 then)
+        const bool small = max_norm < norm * (2.f * kLeast);
+        return {norm, {(small ? max_norm * kMost : max_norm) / norm, small ? kLeast : 1.f}};
     }
     if (threadIdx.x == 0) {
         const double n = sqrt((double)x.s + (double)x.c + x.rest);
@@ -280,7 +280,7 @@ __device__ __forceinline__ Sum parts_of(const GradPart* __restrict__ part, int p
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const GradPart* __restrict__ part, int parts, float* norm) {
     await_previous();
-    const Norm x = norm_of<kThreads>(parts_of(part, parts), 0.f);
+    const Norm x = norm_of<kThreads>(parts_of(part, parts), __int_as_float(0x7f800000));  // no limit
     if (threadIdx.x == 0) *norm = x.norm;
 }
 
