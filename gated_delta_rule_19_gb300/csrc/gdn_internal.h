@@ -511,9 +511,17 @@ cudaError_t launch_qk_norm_rope_axes(const RopeCall& c, InType ty, bool bwd, cud
 cudaError_t launch_qk_norm_rope_apart(const RopeCall& c, InType ty, bool bwd, cudaStream_t st);
 bool rope_whole_units(const RopeCall& c, InType ty);
 // Rows of queries and keys from which on angles that have to be copied one by one are gathered
-// in front (rows of 128, forward and backward, us a call one by one and gathered: 16384 of bf16
-// 5.7 + 15.2 and 6.9 + 13.5, 32768 9.1 + 15.6 and 8.4 + 14.4, 65536 13.8 + 23.0 and 11.9 + 19.2; of
-// float32 5.8 + 11.0 and 7.1 + 11.9, 8.5 + 14.5 and 9.1 + 14.7, 15.0 + 20.5 and 14.5 + 19.7).
+// in front.  Rows of 128, forward and backward together, us on the GPU one by one and gathered:
+//   heads            16384 rows     32768          65536          131072
+//   bf16     1 + 1   22.7, 21.1     33.2, 29.1     51.9, 44.4     94.7, 75.2
+//            2 + 2   21.1, 19.1     24.0, 22.1     35.0, 30.1     56.8, 47.9
+//            6 + 6   20.1, 18.2     22.3, 20.1     32.1, 26.4     50.6, 39.9
+//   float32  1 + 1   22.1, 22.6     33.3, 32.0     57.9, 52.8     110.1, 93.0
+//            2 + 2   16.7, 17.4     23.1, 23.4     36.6, 35.7     66.3, 63.7
+//            6 + 6   15.9, 16.5     21.8, 21.2     33.2, 31.8     57.9, 54.8
+// Single heads gain too, although no other head shares a token's angles: a lane's four become
+// one copy.  What 16384 rows of bf16 gain on the GPU, 1.6 to 2 us a pair of calls, the host pays
+// with two launches of 1.2.
 constexpr int64_t kRopeGatherRows = 32768;
 
 // RMS norm of x times silu(z); backward: part [blocks][D].
@@ -539,11 +547,6 @@ int rows_bwd_blocks(int64_t rows, int per_sm);
 
 // ---- a block's other operators (add_norm.cu, grads.cu, state_cache.cu) ----
 
-// RMS norm of x + res (res NULL: of x); `ty` is the type of x, w, y and their gradients,
-// `stream_ty` that of res, h, dh and dr.  Forward: y (QUANT: e4m3, with scales of `group`
-// columns, 0: of a row) and h.  Backward: from h_in, dy and dh (or NULL) dx, dr (where the
-// types differ), and of the weight's gradient dw itself (a cluster) or the blocks' sums part
-// [blocks][D].
 // Blocks of the backward, and whether they are one cluster, which makes the weight's gradient
 // itself; `wide`: bytes of an element of the wider type.
 struct AddNormGrid {
@@ -552,6 +555,11 @@ struct AddNormGrid {
 };
 AddNormGrid add_norm_bwd_grid(int64_t rows, int D, int wide);
 enum class AddNormKind { FWD, QUANT, BWD };
+// RMS norm of x + res (res NULL: of x); `ty` is the type of x, w, y and their gradients,
+// `stream_ty` that of res, h, dh and dr.  Forward: y (QUANT: e4m3, with scales of `group`
+// columns, 0: of a row) and h.  Backward: from h_in, dy and dh (or NULL) dx, dr (where the
+// types differ), and of the weight's gradient dw itself (a cluster) or the blocks' sums part
+// [blocks][D].
 struct AddNormCall {
     int64_t rows;
     int D, group;

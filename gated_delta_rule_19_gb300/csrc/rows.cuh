@@ -143,6 +143,19 @@ __device__ __forceinline__ void sts16(T* p, const uint4& x) {
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// 1 / x within one unit of float32's last place.
+__device__ __forceinline__ float inverse_of(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Sum over aligned groups of G lanes.
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {

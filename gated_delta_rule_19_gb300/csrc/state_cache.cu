@@ -34,17 +34,6 @@ __device__ __forceinline__ int code_of(float x, float step, float inverse) {
     return (int)c;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float inverse_of(float x) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // The four codes of a vector, one a byte; `near` takes the largest distance of a quotient
 // from its code.  1.5 * 2^23 added to a quotient leaves its nearest whole number in the
 // sum's low bits.
