@@ -541,9 +541,9 @@ cudaError_t cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm
     return launch_one_cluster(grad_clip_kernel<N>, blocks, kThreads * kWorkers, 0, done, st, l, max_norm, norm, clip);
 }
 
-// Tiles that one cluster takes, to clip them or for their norm alone.  Calls one behind the
-// other take 4.2 to 5.6 us of 1 to 48 tiles, as two launches, bound by the host, 5.8 to 8.0; the
-// GPU alone needs 4.6 to 6.0, and of two launches 3.4 to 5.2.  With 96 tiles the host's
+// Tiles that one cluster takes, to clip them or for their norm alone.  Of 4 to 48 tiles calls one
+// behind the other take 5.3 to 6.5 us and 4.5 to 5.2, as two launches, bound by the host, 6.6
+// and 6.1; the GPU alone needs as long, and of two launches 4.1 to 4.6 and 3.1 to 3.4.  With 96 tiles the host's
 // time is even, and the GPU's 6.2 to 6.9 against 3.6 to 4.5.
 constexpr int64_t kClusterTiles = 48;
 
