@@ -227,7 +227,8 @@ grad_sum_kernel(const __grid_constant__ List<N> l, GradPart* __restrict__ part) 
 // What the gradients are multiplied by: the product of two numbers.  A factor below 2^-126, of which
 // one float32 number would keep few bits or none, is first * 2^-126 with a normal first (below
 // 2^-252, which takes a max_norm below 2^-102, no result is more than a subnormal); all others
-// are first * 1.  The product by `first`, below 1, overflows for no finite gradient.
+// are first * 1.  The product by `first` overflows for no finite gradient: it is below 1 where the
+// norm is past 2^65, and below 2 elsewhere.
 struct Factor {
     float first, then;
     __device__ __forceinline__ bool one() const { return first == 1.f && then == 1.f; }
@@ -543,8 +544,8 @@ cudaError_t cluster(const gdn_grad* g, int64_t count, int blocks, float max_norm
 
 // Tiles that one cluster takes, to clip them or for their norm alone.  Of 4 to 48 tiles calls one
 // behind the other take 5.3 to 6.5 us and 4.5 to 5.2, as two launches, bound by the host, 6.6
-// and 6.1; the GPU alone needs as long, and of two launches 4.1 to 4.6 and 3.1 to 3.4.  With 96 tiles the host's
-// time is even, and the GPU's 6.2 to 6.9 against 3.6 to 4.5.
+// and 6.1; the GPU alone needs as long, and of two launches 4.1 to 4.6 and 3.1 to 3.4.  With
+// 96 tiles the host's time is even, and the GPU's 6.2 to 6.9 against 3.6 to 4.5.
 constexpr int64_t kClusterTiles = 48;
 
 }  // namespace
@@ -559,7 +560,7 @@ size_t grad_parts(int64_t count) {
 int grad_cluster(const gdn_grad* g, int64_t count) {
     if (count > kFew) return 0;
     int64_t tiles = 0;
-    for (int64_t i = 0; i < count; ++i) tiles += (g[i].n + kTile - 1) / kTile;
+    for (int64_t i = 0; i < count; ++i) tiles += g[i].n / kTile + (g[i].n % kTile != 0);
     if (tiles > kClusterTiles) return 0;
     int blocks = 1;
     while (blocks < kMostCluster && blocks * kWorkers < tiles) blocks *= 2;
